@@ -569,6 +569,130 @@ moe_status moe_rms_carry(const uint16_t* y, int T, int H, float eps, uint16_t* x
                          cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Element types of the tensors of the calls below (void pointers).  Rows of
+ * 2-D tensors may be strided: ld_* is the distance between rows in elements
+ * (>= the row length); elements of a row are adjacent.
+ * ------------------------------------------------------------------------- */
+enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2 };
+
+/* ---------------------------------------------------------------------------
+ * Routing to experts with a balance bias and expert groups.  For every token t
+ * with logits l[e]:
+ *   eligible   l[e] neither NaN nor -inf, and token_mask (device uint8 [T], may
+ *              be NULL) nonzero for t; a masked token's logits are not used
+ *   score s[e] MOE_SCORE_SOFTMAX: e^(l - max) / sum, the sum over the eligible
+ *              experts taken in neighbouring pairs (a binary tree over
+ *              e / 2, e / 4, ...) in fp32; MOE_SCORE_SIGMOID: 1 / (1 + e^-l),
+ *              0 where e^-l is past fp32's range
+ *   key[e]     bias NULL: l[e]; else s[e] + bias[e] (device fp32 [E]; used for
+ *              choosing only, never in the weights)
+ *   groups     with topk_group < n_group (E / n_group neighbouring experts to a
+ *              group, n_group <= 32 dividing E) only the topk_group groups of
+ *              largest value take part: MOE_GROUP_MAX the largest key,
+ *              MOE_GROUP_TOP2 the sum of the group's two largest s + bias (s
+ *              without bias; the largest alone where only one is eligible);
+ *              ties to the lower group
+ *   topk_ids   device int32 [T, k] out: the k largest keys in descending order,
+ *              ties to the lower id; -1 where fewer than k experts are left
+ *              (moe_slot_ensure and the expert forwards skip those)
+ *   topk_w     device fp32 [T, k] out: scale * s, renorm != 0: scale * s over
+ *              the sum of the kept s (softmax: the softmax over the kept
+ *              logits); 0 where the id is -1 or every kept s is 0
+ *   load       device int32 [E] or NULL: += the times each expert was chosen
+ *              (the caller clears it; what the bias is moved by)
+ * Keys are compared in fp32 with every operation rounded to nearest.
+ * 1 <= E <= 2048, 1 <= k <= min(E, 32), 1 <= topk_group <= n_group, T >= 0
+ * (T == 0 launches nothing).
+ * ------------------------------------------------------------------------- */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+moe_status moe_route(const void* logits, int dtype, int64_t ld_logits, int T, int E, int k, int score,
+                     const float* bias, int n_group, int topk_group, int group_score, int renorm, float scale,
+                     const uint8_t* token_mask, int32_t* topk_ids, float* topk_w, int32_t* load,
+                     cudaStream_t stream);
+
+/* Gradient of moe_route's weights with respect to the logits, the choice held
+ * fixed: with g = d_w (device fp32 [T, k]), s the scores and q the renormalised
+ * kept scores,
+ *   renorm:  d_l[id_j] = scale q_j c_j (g_j - sum_i q_i g_i), c = 1 (softmax),
+ *            1 - s (sigmoid); 0 for every other expert
+ *   plain sigmoid: d_l[id_j] = scale g_j s_j (1 - s_j); 0 for every other expert
+ *   plain softmax: d_l[e] = scale s[e] ([e kept] g - sum_j g_j s_j), every e
+ * topk_ids as moe_route wrote them (distinct in a row; an id outside [0, E)
+ * counts as -1).  d_logits device [T, E] of the logits' type, every element
+ * written (rows of masked tokens with 0). */
+moe_status moe_route_backward(const void* logits, int dtype, int64_t ld_logits, int T, int E, int k, int score,
+                              int renorm, float scale, const uint8_t* token_mask, const int32_t* topk_ids,
+                              const float* d_w, void* d_logits, int64_t ld_d_logits, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms before and after a block, with the block's gate and residual scale.
+ * With x [T, H] the residual stream, y [T, H] the block's output and, for a
+ * row z, n(z) = z / sqrt(mean(z^2) + eps):
+ *   u = residual_scale * x + gate * (n(y) * post_weight)     (written to x_out)
+ *   h = n(u) * next_weight                                   (the next block's input)
+ * computed in fp32 and rounded once to x's type (x_out) and y's type (h); h is
+ * taken from u before its rounding.
+ *   y            NULL: u = residual_scale * x (the norm before a first block)
+ *   post_weight  [H] or NULL: y is added without a norm
+ *   gate         MOE_GATE_NONE (NULL); MOE_GATE_CHANNEL [H]; MOE_GATE_TOKEN [T]
+ *   next_weight  [H] or NULL: h is not computed (a last block)
+ *   x_out        NULL: not written; may be x itself (in place)
+ * x and x_out have x_dtype, y and h y_dtype, the weights and the gate w_dtype;
+ * x_dtype equals y_dtype or is MOE_DT_F32.  1 <= H <= 16384, T >= 0.
+ * ------------------------------------------------------------------------- */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+moe_status moe_block_norm(int T, int H, int x_dtype, int y_dtype, int w_dtype, const void* x, int64_t ld_x,
+                          const void* y, int64_t ld_y, const void* post_weight, const void* gate, int gate_mode,
+                          float residual_scale, const void* next_weight, float eps, void* x_out, int64_t ld_x_out,
+                          void* h, int64_t ld_h, cudaStream_t stream);
+
+/* Gradient of moe_block_norm.  d_x_out (x's type; NULL: 0) and d_h (y's type;
+ * given exactly when next_weight is) come in; out go d_x (x's type), d_y (y's
+ * type, with y), and in fp32, each NULL where it is not wanted, d_post_weight
+ * [H], d_gate ([H] or [T] by gate_mode) and d_next_weight [H], overwritten (0
+ * for T == 0).  d_x may be d_x_out and d_y may be d_h (in place, same ld).
+ * Sums over tokens are taken in a fixed order: equal calls give equal bits.
+ * workspace: device memory of moe_block_norm_backward_workspace bytes (16-byte
+ * aligned; queried on the device that will run it). */
+size_t moe_block_norm_backward_workspace(int T, int H);
+moe_status moe_block_norm_backward(int T, int H, int x_dtype, int y_dtype, int w_dtype, const void* x, int64_t ld_x,
+                                   const void* y, int64_t ld_y, const void* d_x_out, int64_t ld_d_x_out,
+                                   const void* d_h, int64_t ld_d_h, const void* post_weight, const void* gate,
+                                   int gate_mode, float residual_scale, const void* next_weight, float eps,
+                                   void* d_x, int64_t ld_d_x, void* d_y, int64_t ld_d_y, float* d_post_weight,
+                                   float* d_gate, float* d_next_weight, void* workspace, size_t workspace_bytes,
+                                   cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A shared projection with low-rank adapters of many requests beside it:
+ *   out[t] = W x[t] + scale[a] * B[a] (A[a] x[t]),  a = adapter_ids[t]
+ * for the router's logits (N = E, fp32 out) or any dense projection.
+ *   x           device [T, H], W device [N, H]; lora_a device [n, R, H] and
+ *               lora_b device [n, N, R] dense; all of `dtype` (bf16 or f16)
+ *   adapter_ids device int32 [T]; negative: the token has no adapter.  An id
+ *               >= n counts as none and, when d_error (device int32, may be
+ *               NULL) is given, sets *d_error to MOE_ERR_INVALID (the caller
+ *               clears it)
+ *   lora_scale  device fp32 [n] or NULL (all 1)
+ *   out         device [T, N] of out_dtype (`dtype` or MOE_DT_F32)
+ * n_adapters == 0: the projection alone (the adapter pointers are not read).
+ * Products of the projection and of A x are exact in fp32 and summed in fp32;
+ * A x stays fp32 for the second product.
+ * H a multiple of 8, R a multiple of 8 up to 128, x, W, lora_a and lora_b
+ * 16-byte aligned, ld_x and ld_w multiples of 8; T >= 0, N >= 1.
+ * workspace: device memory of moe_adapter_linear_workspace bytes (16-byte
+ * aligned; may be NULL where that is 0; queried on the device that runs it).
+ * A wait that gave up sets *d_error to MOE_ERR_TIMEOUT.
+ * ------------------------------------------------------------------------- */
+size_t moe_adapter_linear_workspace(int T, int H, int N, int n_adapters, int R);
+moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out_dtype, const void* x, int64_t ld_x,
+                              const void* W, int64_t ld_w, int n_adapters, int R, const void* lora_a,
+                              const void* lora_b, const int32_t* adapter_ids, const float* lora_scale, void* out,
+                              int64_t ld_out, void* workspace, size_t workspace_bytes, int32_t* d_error,
+                              cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Per-kernel timing: when enabled, every kernel the library launches is
  * bracketed by two CUDA events recorded on its launching stream.
  * moe_profile_enable(1) clears the record and starts collecting; (0) stops.
@@ -583,7 +707,8 @@ moe_status moe_rms_carry(const uint16_t* y, int T, int H, float eps, uint16_t* x
  * ------------------------------------------------------------------------- */
 enum {
   MOE_K_ROUTER = 0, MOE_K_ENSURE, MOE_K_LADDER, MOE_K_GROUP, MOE_K_PLAN, MOE_K_GATEUP,
-  MOE_K_DOWN, MOE_K_COMBINE, MOE_K_CARRY, MOE_K_GEMM_GATEUP, MOE_K_GEMM_DOWN, MOE_K_COPY, MOE_K_COUNT
+  MOE_K_DOWN, MOE_K_COMBINE, MOE_K_CARRY, MOE_K_GEMM_GATEUP, MOE_K_GEMM_DOWN, MOE_K_COPY,
+  MOE_K_ROUTE, MOE_K_ROUTE_BWD, MOE_K_NORM, MOE_K_NORM_BWD, MOE_K_LINEAR, MOE_K_COUNT
 };
 moe_status moe_profile_enable(int enable);
 moe_status moe_profile_query(int kernel, double* total_ms, int* launches);

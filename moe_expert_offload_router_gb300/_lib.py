@@ -19,9 +19,15 @@ MOE_TAG_FP4, MOE_TAG_INT2, MOE_TAG_DROP = 0, 1, 2
 MOE_POOL_FP4, MOE_POOL_INT2, MOE_POOL_SHARED = 0, 1, 2
 MOE_W1, MOE_W3, MOE_W2 = 0, 1, 2
 (MOE_K_ROUTER, MOE_K_ENSURE, MOE_K_LADDER, MOE_K_GROUP, MOE_K_PLAN, MOE_K_GATEUP, MOE_K_DOWN,
- MOE_K_COMBINE, MOE_K_CARRY, MOE_K_GEMM_GATEUP, MOE_K_GEMM_DOWN, MOE_K_COPY, MOE_K_COUNT) = range(13)
+ MOE_K_COMBINE, MOE_K_CARRY, MOE_K_GEMM_GATEUP, MOE_K_GEMM_DOWN, MOE_K_COPY, MOE_K_ROUTE, MOE_K_ROUTE_BWD, MOE_K_NORM, MOE_K_NORM_BWD,
+ MOE_K_LINEAR, MOE_K_COUNT) = range(18)
 KERNEL_NAMES = ["router", "ensure", "ladder", "group_pairs", "plan", "gateup", "down", "combine",
-                "rms_carry", "gemm_gateup", "gemm_down", "copy_device"]
+                "rms_carry", "gemm_gateup", "gemm_down", "copy_device", "route", "route_backward", "block_norm",
+                "block_norm_backward", "adapter_linear"]
+MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID", 2: "MOE_ERR_CAPACITY", 3: "MOE_ERR_CUDA",
                 4: "MOE_ERR_TIMEOUT", 5: "MOE_ERR_NOMEM"}
 
@@ -37,6 +43,7 @@ if not os.path.exists(LIB_PATH):
 _lib = C.CDLL(LIB_PATH)
 
 vp, i32, sz, f32, u64 = C.c_void_p, C.c_int, C.c_size_t, C.c_float, C.c_uint64
+i64 = C.c_int64
 P_i32, P_u64 = C.POINTER(C.c_int32), C.POINTER(C.c_uint64)
 
 
@@ -96,6 +103,16 @@ _SIGS = {
                                       vp]),
     "moe_mx_quantize": (i32, [vp, i32, i32, vp, vp, vp]),
     "moe_rms_carry": (i32, [vp, i32, i32, f32, vp, vp]),
+    "moe_route": (i32, [vp, i32, i64, i32, i32, i32, i32, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp]),
+    "moe_route_backward": (i32, [vp, i32, i64, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp, i64, vp]),
+    "moe_block_norm": (i32, [i32, i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, i32, f32, vp, f32, vp, i64, vp,
+                             i64, vp]),
+    "moe_block_norm_backward_workspace": (sz, [i32, i32]),
+    "moe_block_norm_backward": (i32, [i32, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i32,
+                                      f32, vp, f32, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]),
+    "moe_adapter_linear_workspace": (sz, [i32, i32, i32, i32, i32]),
+    "moe_adapter_linear": (i32, [i32, i32, i32, i32, i32, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, i64, vp,
+                                 sz, vp, vp]),
     "moe_selftest": (i32, []),
     "moe_debug_timeout_probe": (i32, [C.c_int64, vp, vp]),
     "moe_profile_enable": (i32, [i32]),
@@ -479,6 +496,209 @@ def moe_dequant_debug(views: moe_expert_views, pool: int, slot: int, matrix: int
 def moe_rms_carry(y, eps: float, x_next, stream=None):
     T, H = y.shape
     _check(_lib.moe_rms_carry(_p(y), T, H, eps, _p(x_next), _s(stream)))
+
+
+_DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16,
+       torch.int16: MOE_DT_BF16}   # int16: bf16 bits, as the expert calls take them
+
+
+def _dt(t) -> int:
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise ValueError(f"unsupported tensor type {t.dtype}") from None
+
+
+def _rows(t, T: int, n: int, what: str):
+    """(pointer, row distance) of a [T, n] tensor whose rows may be strided."""
+    if t.shape != (T, n):
+        raise ValueError(f"{what} must be [{T}, {n}], got {tuple(t.shape)}")
+    sr, sc = t.stride()
+    if sc != 1 and n > 1:
+        raise ValueError(f"{what}: the elements of a row must be adjacent (strides {t.stride()})")
+    if sr < n:
+        if T > 1:
+            raise ValueError(f"{what}: rows overlap (strides {t.stride()})")
+        sr = n
+    return t.data_ptr(), sr
+
+
+def _vec(t, shape, dtypes, what: str):
+    """Pointer of a dense tensor of the given shape and one of the types, or None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype not in dtypes:
+        raise ValueError(f"{what} must be {list(shape)} of {[str(d) for d in dtypes]}, got {tuple(t.shape)} of {t.dtype}")
+    return _p(t)
+
+
+def _scratch(nbytes: int, dev, stream):
+    """A workspace for one call on `stream`: freed for that stream's later use."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return ws
+
+
+_I32, _F32, _U8 = (torch.int32,), (torch.float32,), (torch.uint8, torch.bool)
+
+
+def moe_route(logits, k: int, score: int = MOE_SCORE_SOFTMAX, bias=None, n_group: int = 1, topk_group: int = 1,
+              group_score: int = MOE_GROUP_TOP2, renorm: bool = True, scale: float = 1.0, token_mask=None,
+              topk_ids=None, topk_w=None, load=None, stream=None):
+    """(topk_ids, topk_w) of logits [T, E] (fp32, bf16 or f16; rows may be strided)."""
+    T, E = logits.shape
+    dev = logits.device
+    if topk_ids is None:
+        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    p, ld = _rows(logits, T, E, "logits")
+    _check(_lib.moe_route(p, _dt(logits), ld, T, E, k, score, _vec(bias, (E,), _F32, "bias"), n_group, topk_group,
+                          group_score, int(bool(renorm)), scale, _vec(token_mask, (T,), _U8, "token_mask"),
+                          _vec(topk_ids, (T, k), _I32, "topk_ids"), _vec(topk_w, (T, k), _F32, "topk_w"),
+                          _vec(load, (E,), _I32, "load"), _s(stream)))
+    return topk_ids, topk_w
+
+
+def moe_route_backward(logits, topk_ids, d_w, score: int = MOE_SCORE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
+                       token_mask=None, d_logits=None, stream=None):
+    """d_logits [T, E] (the logits' type) from d_w [T, k], the choice topk_ids held fixed."""
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    if d_logits is None:
+        d_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    if d_logits.dtype != logits.dtype:
+        raise ValueError(f"d_logits must be of the logits' type {logits.dtype}, got {d_logits.dtype}")
+    p, ld = _rows(logits, T, E, "logits")
+    pd, ldd = _rows(d_logits, T, E, "d_logits")
+    _check(_lib.moe_route_backward(p, _dt(logits), ld, T, E, k, score, int(bool(renorm)), scale,
+                                   _vec(token_mask, (T,), _U8, "token_mask"), _vec(topk_ids, (T, k), _I32, "topk_ids"),
+                                   _vec(d_w, (T, k), _F32, "d_w"), pd, ldd, _s(stream)))
+    return d_logits
+
+
+def _norm_weights(T, H, x, post_weight, gate, next_weight):
+    """(w_dtype, post pointer, gate pointer, gate mode, next pointer)."""
+    w_dtype, given = MOE_DT_F32, None
+    for t in (post_weight, gate, next_weight):
+        if t is not None:
+            if given is not None and t.dtype != given:
+                raise ValueError(f"post_weight, gate and next_weight must be of one type, got {given} and {t.dtype}")
+            given, w_dtype = t.dtype, _dt(t)
+    own = (given,)
+    mode = MOE_GATE_NONE
+    if gate is not None:   # [H]: for each channel; [T, 1]: for each token
+        mode = MOE_GATE_CHANNEL if gate.dim() == 1 else MOE_GATE_TOKEN
+    return (w_dtype, _vec(post_weight, (H,), own, "post_weight"),
+            _vec(gate, (H,) if mode == MOE_GATE_CHANNEL else (T, 1), own, "gate"), mode,
+            _vec(next_weight, (H,), own, "next_weight"))
+
+
+def moe_block_norm(x, y=None, post_weight=None, gate=None, residual_scale: float = 1.0, next_weight=None,
+                   eps: float = 1e-6, x_out=None, h=None, stream=None):
+    """(x_out, h) = (residual_scale x + gate n(y) post_weight, n(x_out) next_weight).
+
+    x [T, H] is the residual stream, y [T, H] a block's output (None: the norm
+    before a first block alone, no x_out unless one is given); gate [H] (each
+    channel) or [T, 1] (each token).  Without next_weight h is None."""
+    T, H = x.shape
+    w_dtype, pp, pg, mode, pn = _norm_weights(T, H, x, post_weight, gate, next_weight)
+    px, ldx = _rows(x, T, H, "x")
+    py, ldy = (None, 0) if y is None else _rows(y, T, H, "y")
+    like = x if y is None and h is None else (h if y is None else y)
+    if x_out is None and y is not None:
+        x_out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    if h is None and next_weight is not None:
+        h = torch.empty((T, H), dtype=like.dtype, device=x.device)
+    for t, of, what in ((x_out, x, "x_out"), (h, like, "h")):
+        if t is not None and t.dtype != of.dtype:
+            raise ValueError(f"{what} must be of type {of.dtype}, got {t.dtype}")
+    po, ldo = (None, 0) if x_out is None else _rows(x_out, T, H, "x_out")
+    ph, ldh = (None, 0) if h is None else _rows(h, T, H, "h")
+    _check(_lib.moe_block_norm(T, H, _dt(x), _dt(like), w_dtype, px, ldx, py, ldy, pp, pg, mode, residual_scale, pn,
+                               eps, po, ldo, ph, ldh, _s(stream)))
+    return x_out, h
+
+
+def moe_block_norm_backward_workspace(T: int, H: int) -> int:
+    return _lib.moe_block_norm_backward_workspace(T, H)
+
+
+def moe_block_norm_backward(x, y, d_x_out, d_h, post_weight=None, gate=None, residual_scale: float = 1.0,
+                            next_weight=None, eps: float = 1e-6, d_x=None, d_y=None, d_post_weight=None, d_gate=None,
+                            d_next_weight=None, workspace=None, stream=None):
+    """(d_x, d_y, d_post_weight, d_gate, d_next_weight) of moe_block_norm; the weights'
+    gradients are fp32, and None where the weight is not given."""
+    T, H = x.shape
+    dev = x.device
+    w_dtype, pp, pg, mode, pn = _norm_weights(T, H, x, post_weight, gate, next_weight)
+    px, ldx = _rows(x, T, H, "x")
+    py, ldy = (None, 0) if y is None else _rows(y, T, H, "y")
+    pu, ldu = (None, 0) if d_x_out is None else _rows(d_x_out, T, H, "d_x_out")
+    ph, ldh = (None, 0) if d_h is None else _rows(d_h, T, H, "d_h")
+    like = y if y is not None else (d_h if d_h is not None else x)
+    if d_x is None:
+        d_x = torch.empty((T, H), dtype=x.dtype, device=dev)
+    if d_y is None and y is not None:
+        d_y = torch.empty((T, H), dtype=y.dtype, device=dev)
+    for t, of, what in ((d_x_out, x, "d_x_out"), (d_h, like, "d_h"), (d_x, x, "d_x"), (d_y, like, "d_y")):
+        if t is not None and t.dtype != of.dtype:
+            raise ValueError(f"{what} must be of type {of.dtype}, got {t.dtype}")
+    if d_post_weight is None and post_weight is not None:
+        d_post_weight = torch.empty(H, dtype=torch.float32, device=dev)
+    if d_gate is None and gate is not None:
+        d_gate = torch.empty(gate.shape, dtype=torch.float32, device=dev)
+    if d_next_weight is None and next_weight is not None:
+        d_next_weight = torch.empty(H, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _scratch(_lib.moe_block_norm_backward_workspace(T, H), dev, stream)
+    pdx, lddx = _rows(d_x, T, H, "d_x")
+    pdy, lddy = (None, 0) if d_y is None else _rows(d_y, T, H, "d_y")
+    _check(_lib.moe_block_norm_backward(
+        T, H, _dt(x), _dt(like), w_dtype, px, ldx, py, ldy, pu, ldu, ph, ldh, pp, pg, mode, residual_scale, pn, eps,
+        pdx, lddx, pdy, lddy, _vec(d_post_weight, (H,), _F32, "d_post_weight"),
+        None if d_gate is None else _vec(d_gate, tuple(gate.shape), _F32, "d_gate"),
+        _vec(d_next_weight, (H,), _F32, "d_next_weight"), _p(workspace),
+        workspace.numel() * workspace.element_size(), _s(stream)))
+    return d_x, d_y, d_post_weight, d_gate, d_next_weight
+
+
+def moe_adapter_linear_workspace(T: int, H: int, N: int, n_adapters: int, R: int) -> int:
+    return _lib.moe_adapter_linear_workspace(T, H, N, n_adapters, R)
+
+
+def moe_adapter_linear(x, weight, lora_a=None, lora_b=None, adapter_ids=None, lora_scale=None, out=None,
+                       out_dtype=None, workspace=None, d_error=None, stream=None):
+    """out [T, N] = x weight^T + lora_scale[a] (x lora_a[a]^T) lora_b[a]^T, a = adapter_ids[t] (< 0: none).
+
+    x [T, H] and weight [N, H] (rows may be strided), lora_a [n, R, H], lora_b
+    [n, N, R], all bf16 or all f16; out of x's type or fp32.  Without lora_a the
+    projection alone."""
+    T, H = x.shape
+    N = weight.shape[0]
+    px, ldx = _rows(x, T, H, "x")
+    pw, ldw = _rows(weight, N, H, "weight")
+    if weight.dtype != x.dtype:
+        raise ValueError(f"weight must be of x's type {x.dtype}, got {weight.dtype}")
+    n = R = 0
+    pa = pb = pi = None
+    if lora_a is not None:
+        n, R = lora_a.shape[0], lora_a.shape[1]
+        pa = _vec(lora_a, (n, R, H), (x.dtype,), "lora_a")
+        pb = _vec(lora_b, (n, N, R), (x.dtype,), "lora_b")
+        pi = _vec(adapter_ids, (T,), _I32, "adapter_ids")
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype or x.dtype, device=x.device)
+    po, ldo = _rows(out, T, N, "out")
+    if workspace is None:
+        nb = _lib.moe_adapter_linear_workspace(T, H, N, n, R)
+        workspace = _scratch(nb, x.device, stream) if nb else None
+    _check(_lib.moe_adapter_linear(T, H, N, _dt(x), _dt(out), px, ldx, pw, ldw, n, R, pa, pb, pi,
+                                   _vec(lora_scale, (n,), _F32, "lora_scale"), po, ldo, _p(workspace),
+                                   0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                   _p(d_error), _s(stream)))
+    return out
 
 
 def moe_debug_timeout_probe(limit_ns: int, d_status, stream=None):

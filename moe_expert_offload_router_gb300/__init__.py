@@ -15,9 +15,12 @@ def __getattr__(name):
     if name in _SUBMODULES or name.startswith("__"):
         raise AttributeError(name)   # the import system then loads the submodule
     if name in ("DecodeLayerRunner", "PrefillStreamer"):
-        return getattr(importlib.import_module(__name__ + ".layer"), name)
-    lib = importlib.import_module(__name__ + "._lib")
-    try:
-        return getattr(lib, name)
-    except AttributeError:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}") from None
+        found = getattr(importlib.import_module(__name__ + ".layer"), name)
+    else:
+        lib = importlib.import_module(__name__ + "._lib")
+        try:
+            found = getattr(lib, name)
+        except AttributeError:
+            raise AttributeError(f"module {__name__!r} has no attribute {name!r}") from None
+    globals()[name] = found   # later uses find it without coming here (this costs microseconds a call)
+    return found

@@ -149,8 +149,8 @@ def _p(t):
 
 
 def _s(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # torch.cuda.current_stream().cuda_stream without the stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -503,10 +503,10 @@ _DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MO
 
 
 def _dt(t) -> int:
-    try:
-        return _DT[t.dtype]
-    except KeyError:
-        raise ValueError(f"unsupported tensor type {t.dtype}") from None
+    d = _DT.get(t.dtype)
+    if d is None:
+        raise ValueError(f"unsupported tensor type {t.dtype}")
+    return d
 
 
 def _rows(t, T: int, n: int, what: str):
@@ -527,7 +527,7 @@ def _vec(t, shape, dtypes, what: str):
     """Pointer of a dense tensor of the given shape and one of the types, or None."""
     if t is None:
         return None
-    if tuple(t.shape) != shape or t.dtype not in dtypes:
+    if t.shape != shape or t.dtype not in dtypes:
         raise ValueError(f"{what} must be {list(shape)} of {[str(d) for d in dtypes]}, got {tuple(t.shape)} of {t.dtype}")
     return _p(t)
 

@@ -1,11 +1,21 @@
 // A shared projection with low-rank adapters of many requests beside it:
-//   out[t] = W x[t] + scale[a] B[a] (A[a] x[t]),  a = adapter_ids[t].
+//   out[t] = W x[t] + B[a] u[t],  u[t] = scale[a] A[a] x[t],  a = adapter_ids[t].
 //
-// A first kernel takes u[t] = scale[a] A[a] x[t] (fp32 [T, R], one warp per
-// token); the projection's kernel adds B[a] u[t] to its sums before rounding.
+// u (fp32 [T, R]) comes from a first kernel; the projection's kernel starts
+// beside it (programmatic dependent launch) and waits for it only before its
+// epilogue, where B[a] u is added in fp32 token by token: an adapter touches
+// the tokens that name it and no others, whoever shares their tile.
+//
+// The projection runs on tcgen05 (kind::f16, fp32 accumulators in tensor
+// memory) with the operands swapped: W's rows are the MMA's 128 rows and the
+// tokens its N columns, so a decode batch of 16 tokens is one N = 16 tile and
+// no row of the tensor core is spent on padding.
 #include <math.h>
 
+#include <type_traits>
+
 #include "dtype.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 
@@ -21,78 +31,458 @@ struct LinearArgs {
 };
 
 template <typename TE>
-__global__ void __launch_bounds__(128) adapter_shrink_kernel(const LinearArgs a) {
-  const int t = (int)((blockIdx.x * (size_t)blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+struct Pair;   // two packed elements as fp32
+template <>
+struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 f32(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+};
+template <>
+struct Pair<__half> {
+  static __device__ __forceinline__ float2 f32(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+};
+
+// ------------------------------------------------------------ u = scale A x --
+
+// Few tokens: a warp takes kDots ranks of one token, each lane 16-byte chunks
+// of x and of the A rows.  Every token reads its own R x H of A (from L2 where
+// tokens share an adapter).
+constexpr int kDots = 2;
+template <typename TE>
+__global__ void __launch_bounds__(128) adapter_dot_kernel(const LinearArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();   // after the wait: the projection may read x from its start
+  const int per = a.R / kDots;
+  const long long w = (blockIdx.x * 128LL + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  const long long t = w / per;
   if (t >= a.T) return;
+  const int r0 = (int)(w % per) * kDots;
   const int id = a.ids[t];
   if (id >= a.n && a.err && lane == 0) atomicCAS(a.err, MOE_OK, MOE_ERR_INVALID);
   if (id < 0 || id >= a.n) return;
-  const TE* x = reinterpret_cast<const TE*>(a.x) + t * a.ld_x;
-  const float c = a.scale ? a.scale[id] : 1.f;
-  for (int r = 0; r < a.R; ++r) {
-    const TE* row = reinterpret_cast<const TE*>(a.A) + ((long long)id * a.R + r) * a.H;
-    float s = 0.f;
-    for (int i = lane; i < a.H; i += 32) s = fmaf(to_f32(row[i]), to_f32(x[i]), s);
+  const uint4* x = reinterpret_cast<const uint4*>(reinterpret_cast<const TE*>(a.x) + t * a.ld_x);
+  const int nc = a.H / 8;
+  const uint4* A[kDots];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) a.u[(long long)t * a.R + r] = c * s;
+  for (int r = 0; r < kDots; ++r)
+    A[r] = reinterpret_cast<const uint4*>(reinterpret_cast<const TE*>(a.A) + ((long long)id * a.R + r0 + r) * a.H);
+  float s[kDots] = {};
+#pragma unroll 4
+  for (int c = lane; c < nc; c += 32) {
+    const uint4 xv = x[c];
+    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+    for (int r = 0; r < kDots; ++r) {
+      const uint4 av = A[r][c];
+      const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = Pair<TE>::f32(xw[i]), q = Pair<TE>::f32(aw[i]);
+        s[r] = fmaf(p.x, q.x, fmaf(p.y, q.y, s[r]));
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int r = 0; r < kDots; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+  if (lane < kDots) {
+    float v = s[0];
+#pragma unroll
+    for (int r = 1; r < kDots; ++r) v = lane == r ? s[r] : v;
+    a.u[t * a.R + r0 + lane] = (a.scale ? a.scale[id] : 1.f) * v;
   }
 }
 
-// 64 tokens x 64 outputs per block of 256 threads, 4 x 4 per thread.
 template <typename TE>
-__global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a) {
-  __shared__ float xs[16][65], ws[16][65];
-  const int t0 = blockIdx.y * 64, n0 = blockIdx.x * 64, tid = threadIdx.x;
-  const int tx = tid % 16, ty = tid / 16;
+__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (sizeof(TE) == 2 && std::is_same<TE, __nv_bfloat16>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Many tokens: a block takes 16 tokens and goes through the adapters that they
+// name (one, mostly: a prompt's tokens share theirs), its eight warps splitting
+// H.  x and A rows go straight to MMA fragments: lane (g, c) loads 16 bytes at
+// k = 32 i + 8 c of rows g and g + 8 and uses them as the k16 steps 2 i and
+// 2 i + 1; both operands take k in that same order.
+template <typename TE, int RT>
+__global__ void __launch_bounds__(256) adapter_mma_kernel(const LinearArgs a) {
+  extern __shared__ float red[];   // [8 warps][16 tokens][R]
+  __shared__ int s_id[16];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int t0 = blockIdx.x * 16, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  if (threadIdx.x < 16) {
+    int id = t0 + (int)threadIdx.x < a.T ? a.ids[t0 + threadIdx.x] : -1;
+    if (id >= a.n) {
+      if (a.err && blockIdx.y == 0) atomicCAS(a.err, MOE_OK, MOE_ERR_INVALID);
+      id = -1;
+    }
+    s_id[threadIdx.x] = id;
+  }
+  __syncthreads();
+  const int mine = s_id[lane & 15];
+  bool first = lane < 16 && mine >= 0;
+  for (int i = 0; i < (lane & 15); ++i) first = first && s_id[i] != mine;
+  uint32_t todo = __ballot_sync(0xffffffffu, first);   // the tokens that name an adapter first
+  for (int i = 0; i < (int)blockIdx.y; ++i) todo &= todo - 1;
   const TE* x = reinterpret_cast<const TE*>(a.x);
-  const TE* W = reinterpret_cast<const TE*>(a.W);
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < a.H; k0 += 16) {
-    for (int i = tid; i < 64 * 16; i += 256) {
-      const int r = i / 16, c = i % 16;
-      xs[c][r] = t0 + r < a.T && k0 + c < a.H ? to_f32(x[(t0 + r) * a.ld_x + k0 + c]) : 0.f;
-      ws[c][r] = n0 + r < a.N && k0 + c < a.H ? to_f32(W[(n0 + r) * a.ld_w + k0 + c]) : 0.f;
+  const int ta = t0 + g < a.T ? t0 + g : a.T - 1, tb = t0 + g + 8 < a.T ? t0 + g + 8 : a.T - 1;
+  const uint4* xa = reinterpret_cast<const uint4*>(x + ta * a.ld_x);
+  const uint4* xb = reinterpret_cast<const uint4*>(x + tb * a.ld_x);
+  const int nc = a.H / 8;
+  while (todo) {
+    const int id = s_id[__ffs(todo) - 1];
+    const TE* A = reinterpret_cast<const TE*>(a.A) + (long long)id * a.R * a.H;
+    float acc[RT][4] = {};
+#pragma unroll 2
+    for (int i = warp; 4 * i < nc; i += 8) {
+      const int ch = 4 * i + c;
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      const uint4 p = ch < nc ? xa[ch] : z, q = ch < nc ? xb[ch] : z;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (8 * r >= a.R) break;
+        const uint4 b = ch < nc ? reinterpret_cast<const uint4*>(A + (long long)(8 * r + g) * a.H)[ch] : z;
+        mma16816<TE>(acc[r], p.x, q.x, p.y, q.y, b.x, b.y);
+        mma16816<TE>(acc[r], p.z, q.z, p.w, q.w, b.z, b.w);
+      }
+    }
+    __syncthreads();   // the sums before these have been read
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if (8 * r >= a.R) break;
+      float* d = red + (warp * 16 + g) * a.R + 8 * r + 2 * c;
+      d[0] = acc[r][0], d[1] = acc[r][1];
+      d[8 * a.R] = acc[r][2], d[8 * a.R + 1] = acc[r][3];
     }
     __syncthreads();
-    for (int c = 0; c < 16; ++c)
+    const float sc = a.scale ? a.scale[id] : 1.f;
+    for (int i = threadIdx.x; i < 16 * a.R; i += 256) {
+      const int t = i / a.R;
+      if (s_id[t] != id) continue;
+      float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[c][ty * 4 + i], ws[c][tx * 4 + j], acc[i][j]);
-    __syncthreads();
+      for (int w = 0; w < 8; ++w) s += red[w * 16 * a.R + i];
+      a.u[(long long)t0 * a.R + i] = sc * s;
+    }
+    for (int i = 0; i < (int)gridDim.y && todo; ++i) todo &= todo - 1;
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + ty * 4 + i;
-    if (t >= a.T) continue;
-    const int id = a.n ? a.ids[t] : -1;
+}
+
+// -------------------------------------------------------------- projection --
+
+// D [128 x n] (fp32 in tensor memory) += A [128 x 64] B [n x 64]^T, four K = 16
+// MMAs by one elected lane of a converged warp, then a commit that arrives on
+// `bar` when they have completed.
+__device__ __forceinline__ void mma_kstep(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                          uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 aa, bb;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 aa, %1, 2;\n\tadd.s64 bb, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], aa, bb, %3, t;\n\t"
+      "add.s64 aa, %1, 4;\n\tadd.s64 bb, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], aa, bb, %3, t;\n\t"
+      "add.s64 aa, %1, 6;\n\tadd.s64 bb, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], aa, bb, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(su32(bar))
+      : "memory");
+}
+// kind::f16, D fp32, A and B of one 16-bit type, both K-major, M = 128.
+__device__ __forceinline__ uint32_t idesc_f16(int n, bool bf16) {
+  const uint32_t t = bf16 ? 1u : 0u;
+  return (1u << 4) | (t << 7) | (t << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(r)
+               : "memory");
+  return v;
+}
+
+constexpr int kRows = 128;          // outputs (W rows) of a tile
+constexpr int kATile = kRows * 128; // bytes of a 64-wide K step of W
+
+template <int NT>
+struct SplitCfg {
+  static constexpr int kStage = kATile + NT * 128;
+  static constexpr int kStages = NT <= 64 ? 8 : NT == 128 ? 6 : 4;
+  static constexpr int kSmem = kStages * kStage + 1024;
+  static constexpr int kCols = NT < 32 ? 32 : NT;
+  static_assert(NT * kRows * 4 <= kStages * kStage, "the partial sums fit the stages");
+};
+
+// acc += B[a][n..n+3] . u[t] in fp32.
+template <typename TE>
+__device__ __forceinline__ void add_adapter4(const LinearArgs& a, int id, long long t, int n, float* acc) {
+  const float4* u = reinterpret_cast<const float4*>(a.u + t * a.R);
+  const TE* B = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + n) * a.R;
+  for (int r = 0; r < a.R; r += 8) {
+    const float4 u0 = u[r / 4], u1 = u[r / 4 + 1];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx * 4 + j;
-      if (n >= a.N) continue;
-      float s = acc[i][j];
-      if (id >= 0 && id < a.n) {
-        const TE* b = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + n) * a.R;
-        for (int r = 0; r < a.R; ++r) s = fmaf(to_f32(b[r]), a.u[(long long)t * a.R + r], s);
-      }
-      const long long o = t * a.ld_out + n;
-      if (a.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(a.out)[o] = s;
-      else reinterpret_cast<TE*>(a.out)[o] = from_f32<TE>(s);
+      if (n + j >= a.N) break;
+      const uint4 b = *reinterpret_cast<const uint4*>(B + (long long)j * a.R + r);
+      float2 p = Pair<TE>::f32(b.x);
+      float s = fmaf(p.x, u0.x, p.y * u0.y);
+      p = Pair<TE>::f32(b.y);
+      s = fmaf(p.x, u0.z, fmaf(p.y, u0.w, s));
+      p = Pair<TE>::f32(b.z);
+      s = fmaf(p.x, u1.x, fmaf(p.y, u1.y, s));
+      p = Pair<TE>::f32(b.w);
+      s = fmaf(p.x, u1.z, fmaf(p.y, u1.w, s));
+      acc[j] += s;
     }
   }
 }
 
 template <typename TE>
-static moe_status launch_linear(const LinearArgs& a, cudaStream_t s) {
+__device__ __forceinline__ void store4(const LinearArgs& a, long long t, int n, const float* v) {
+  if (a.out_dtype == MOE_DT_F32) {
+    float* o = reinterpret_cast<float*>(a.out) + t * a.ld_out + n;
+    if (n + 4 <= a.N && ((uintptr_t)o & 15) == 0) {
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      for (int j = 0; j < 4 && n + j < a.N; ++j) o[j] = v[j];
+    }
+  } else {
+    TE* o = reinterpret_cast<TE*>(a.out) + t * a.ld_out + n;
+    if (n + 4 <= a.N && ((uintptr_t)o & 7) == 0) {
+      TE e[4] = {from_f32<TE>(v[0]), from_f32<TE>(v[1]), from_f32<TE>(v[2]), from_f32<TE>(v[3])};
+      *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(e);
+    } else {
+      for (int j = 0; j < 4 && n + j < a.N; ++j) o[j] = from_f32<TE>(v[j]);
+    }
+  }
+}
+
+// One tile of 128 outputs x NT tokens per cluster, whose blocks split H: each
+// brings its share of W and x by TMA (as many 64-wide steps in flight as the
+// stages hold: with H / cluster <= 512 the whole share), multiplies it, puts its
+// fp32 sums into its own shared memory, and adds up the blocks' sums, in rank
+// order, for its share of the tokens.
+template <typename TE, int NT>
+__global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant__ CUtensorMap mW,
+                                                           const __grid_constant__ CUtensorMap mX,
+                                                           const LinearArgs a, int early) {
+  using C = SplitCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ alignas(8) uint64_t full[C::kStages], empty[C::kStages], done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_err;
+  uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cs = gridDim.x, rank = blockIdx.x;   // the cluster spans the grid's x
+  const int n0 = blockIdx.y * kRows, t0 = blockIdx.z * NT;
+  const int nk = (a.H + 63) / 64, k0 = (int)((long long)nk * rank / cs), k1 = (int)((long long)nk * (rank + 1) / cs);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    s_err = MOE_OK;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)),
+                 "r"(C::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  // beside adapter_*_kernel (early) everything but u is there already: that
+  // kernel lets this one start only once the work before it has completed
+  if (!early) pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int k = k0; k < k1; ++k) {
+        const int i = k - k0, s = i % C::kStages;
+        if (i >= C::kStages && !mbar_wait_fast(&empty[s], (i / C::kStages - 1) & 1, &s_err)) break;
+        uint8_t* st = sm + s * C::kStage;
+        mbar_expect_tx(&full[s], C::kStage);
+        tma_2d(st, &mW, k * 64, n0, &full[s]);
+        tma_2d(st + kATile, &mX, k * 64, t0, &full[s]);
+      }
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f16(NT, std::is_same<TE, __nv_bfloat16>::value);
+    for (int k = k0; k < k1; ++k) {
+      const int i = k - k0, s = i % C::kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait_fast(&full[s], (i / C::kStages) & 1, &s_err))) break;
+      tc_fence_after();
+      uint8_t* st = sm + s * C::kStage;
+      mma_kstep(tmem, umma_desc_sw128(su32(st)), umma_desc_sw128(su32(st + kATile)), idesc, i != 0, &empty[s]);
+    }
+    mma_commit_elect(&done);
+  }
+  __syncwarp();
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(&done, 0, &s_err)) && *(volatile int*)&s_err == MOE_OK;
+  tc_fence_after();
+  // sums -> shared memory [NT][128]: a warp reads its quadrant's 32 rows, 16 tokens at a time
+  float* part = reinterpret_cast<float*>(sm);
+  const int q = warp & 3;
+#pragma unroll
+  for (int ch = warp >> 2; ch < NT / 16; ch += 2) {
+    uint32_t v[16];
+    tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ch * 16), v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      part[(ch * 16 + j) * kRows + q * 32 + lane] = ok ? __uint_as_float(v[j]) : NAN;
+  }
+  if (!ok) {   // a wait gave up: leave the copies in flight time to land
+    const uint64_t since = gtimer();
+    while (gtimer() - since < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (cs > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+  }
+  if (!ok && threadIdx.x == 0 && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
+  if (early) pdl_wait();   // u
+  const int share = NT / cs;
+  const uint32_t base = su32(part);
+  for (int i = threadIdx.x; i < share * (kRows / 4); i += 256) {
+    const int tt = rank * share + i / (kRows / 4), nn = (i % (kRows / 4)) * 4;
+    const long long t = t0 + tt;
+    if (t >= a.T || n0 + nn >= a.N) continue;
+    float v[4] = {};
+    for (int r = 0; r < cs; ++r) {
+      const uint32_t p = base + (uint32_t)(tt * kRows + nn) * 4;
+      const float4 f = cs > 1 ? ld_cluster4(p, r) : *reinterpret_cast<const float4*>(part + tt * kRows + nn);
+      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+    }
+    if (a.n) {
+      const int id = a.ids[t];
+      if (id >= 0 && id < a.n) add_adapter4<TE>(a, id, t, n0 + nn, v);
+    }
+    store4<TE>(a, t, n0 + nn, v);
+  }
+  __syncwarp();
+  if (cs > 1) cluster_sync();   // the others have read this block's sums
+}
+
+// --------------------------------------------------------------------- host --
+
+// rows x cols of 16-bit elements, `ld` apart: boxes of 64 columns x box_rows, 128-byte swizzle, zeros outside
+static moe_status map_rows(CUtensorMap* m, const void* base, int dtype, uint64_t cols, uint64_t rows, uint64_t ld,
+                           uint32_t box_rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(m, dtype == MOE_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (projection) failed: %d", (int)r);
+  return MOE_OK;
+}
+
+template <typename TE, int NT>
+static moe_status launch_split(const LinearArgs& a, int dtype, cudaStream_t s) {
+  using C = SplitCfg<NT>;
+  CUtensorMap mW, mX;
+  moe_status st = map_rows(&mW, a.W, dtype, a.H, a.N, a.ld_w, kRows);
+  if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.H, a.T, a.ld_x, NT);
+  if (st != MOE_OK) return st;
+  auto kernel = linear_split_kernel<TE, NT>;
+  static char allowed[64];
+  MOE_CUDA(allow_smem(kernel, C::kSmem, allowed));
+  const int tiles_n = (a.N + kRows - 1) / kRows, tiles_t = (a.T + NT - 1) / NT, nk = (a.H + 63) / 64;
+  MOE_ARG(tiles_n <= 65535 && tiles_t <= 65535, "T or N too large");
+  // split H while the blocks still fit the SMs at once and each keeps two steps
+  int cs = 1;
+  while (cs < 8 && (long long)tiles_n * tiles_t * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs, tiles_n, tiles_t);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mW, mX, a, a.n ? 1 : 0);
+  if (e != cudaSuccess) return cuda_fail(e, "linear_split_kernel");
+  return check_launch("linear_split_kernel");
+}
+
+template <typename TE, int RT>
+static moe_status launch_adapter_mma(const LinearArgs& a, cudaStream_t s) {
+  const size_t smem = (size_t)8 * 16 * a.R * sizeof(float);
+  auto kernel = adapter_mma_kernel<TE, RT>;
+  static char allowed[64];
+  MOE_CUDA(allow_smem(kernel, (size_t)8 * 16 * 8 * RT * sizeof(float), allowed));
+  cudaError_t e = launch_pdl(kernel, dim3((a.T + 15) / 16, 4), dim3(256), smem, s, a);
+  if (e != cudaSuccess) return cuda_fail(e, "adapter_mma_kernel");
+  return check_launch("adapter_mma_kernel");
+}
+
+template <typename TE>
+static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) {
   ProfScope ps(MOE_K_LINEAR, s);
+  moe_status st = MOE_OK;
   if (a.n) {
-    adapter_shrink_kernel<TE><<<(unsigned)((a.T + 3LL) / 4), 128, 0, s>>>(a);
-    const moe_status st = check_launch("adapter_shrink_kernel");
+    // one dot per token and rank re-reads A for every token: worth it up to this many bytes
+    if ((long long)a.T * a.R * a.H * 2 <= (64LL << 20)) {
+      const long long warps = (long long)a.T * (a.R / kDots);
+      cudaError_t e = launch_pdl(adapter_dot_kernel<TE>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, a);
+      if (e != cudaSuccess) return cuda_fail(e, "adapter_dot_kernel");
+      st = check_launch("adapter_dot_kernel");
+    } else if (a.R <= 32) {
+      st = launch_adapter_mma<TE, 4>(a, s);
+    } else if (a.R <= 64) {
+      st = launch_adapter_mma<TE, 8>(a, s);
+    } else {
+      st = launch_adapter_mma<TE, 16>(a, s);
+    }
     if (st != MOE_OK) return st;
   }
-  linear_kernel<TE><<<dim3((a.N + 63) / 64, (a.T + 63) / 64), 256, 0, s>>>(a);
-  return check_launch("linear_kernel");
+  if (a.T <= 16) return launch_split<TE, 16>(a, dtype, s);
+  if (a.T <= 32) return launch_split<TE, 32>(a, dtype, s);
+  if (a.T <= 64) return launch_split<TE, 64>(a, dtype, s);
+  if (a.T <= 128) return launch_split<TE, 128>(a, dtype, s);
+  // larger tiles re-read less of W, as long as they fill the SMs
+  const long long tiles_n = (a.N + kRows - 1) / kRows;
+  if (tiles_n * ((a.T + 255) / 256) < device_sms()) return launch_split<TE, 128>(a, dtype, s);
+  return launch_split<TE, 256>(a, dtype, s);
 }
 
 }  // namespace moe
@@ -130,5 +520,6 @@ extern "C" moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out
           "workspace missing, misaligned or too small (%zu bytes, %zu needed)", workspace_bytes, need);
   const LinearArgs a{T,    H,    N,      n_adapters, R,          out_dtype, x,  W, lora_a, lora_b, ld_x,
                      ld_w, ld_out, adapter_ids, lora_scale, out, (float*)workspace, d_error};
-  return dtype == MOE_DT_BF16 ? launch_linear<__nv_bfloat16>(a, stream) : launch_linear<__half>(a, stream);
+  return dtype == MOE_DT_BF16 ? launch_linear<__nv_bfloat16>(a, dtype, stream)
+                              : launch_linear<__half>(a, dtype, stream);
 }

@@ -333,15 +333,9 @@ static RowShape row_shape(int H, bool vec) {
   return H <= 1024 ? RowShape{1, 4, 256} : RowShape{1, 16, 1024};
 }
 
-static int norm_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
 // Blocks of the gradient kernel: what the workspace has lines for.
 static int bwd_blocks(long long T, int rows) {
-  const long long need = (T + rows - 1) / rows, most = norm_sms() * 2;
+  const long long need = (T + rows - 1) / rows, most = device_sms() * 2;
   return (int)(need < most ? need : most);
 }
 

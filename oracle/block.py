@@ -124,7 +124,8 @@ def block_norm_backward(x, y, du, dh, post=None, gate=None, alpha=1.0, nxt=None,
         A = dh * nxt
         D = D + ru * (A - u * ru ** 2 * (A * u).mean(1, keepdims=True))
         m = m + ru * (np.abs(A) + np.abs(u) * ru ** 2 * np.abs(A * u).mean(1, keepdims=True))
-        g["next"], mag["next"] = (dh * u * ru).sum(0), np.abs(dh * u * ru).sum(0)
+        g["next"] = (dh * u * ru).sum(0)
+        mag["next"] = (np.abs(dh) * ru * (np.abs(alpha * x) + np.abs(u - alpha * x))).sum(0)   # u can cancel too
     g["x"], mag["x"] = alpha * D, abs(alpha) * m
     if y is not None:
         ry = 1.0 if post is None else 1.0 / np.sqrt((y * y).mean(1, keepdims=True) + eps)

@@ -1,18 +1,24 @@
 // Norms before and after a block, fused with the block's gate and residual
-// scale, and their gradient:
-//   r_y = (mean y^2 + eps)^-1/2,  v = y r_y g_post,  u = a x + gate v,
-//   r_u = (mean u^2 + eps)^-1/2,  h = u r_u g_next.
-// Gradient, with du, dh coming in and A = dh g_next:
-//   D  = du + r_u (A - u r_u^2 mean(A u))           the gradient of u
-//   dx = a D,  dgate = sum v D,  dg_next = sum dh u r_u
-//   B  = gate D g_post,  dg_post = sum gate D y r_y
-//   dy = r_y (B - y r_y^2 mean(B y))
+// scale, and their gradient.  With w = gate * post_weight (per channel; for a
+// gate per token w = post_weight and g_t the token's gate, else g_t = 1):
+//   r_y = (mean y^2 + eps)^-1/2,  n = y r_y,  u = alpha x + g_t w n,
+//   r_u = (mean u^2 + eps)^-1/2,  h = u r_u next.
+// Gradient, with du, dh coming in, a = dh next and q = w n:
+//   m  = r_u^2 mean(a u),  D = du + r_u (a - u m)          the gradient of u
+//   dx = alpha D,  s = sum q D = sum q du + r_u (sum q a - m sum q u)
+//   dy = r_y (g_t w D - n g_t mean(q D)),  d gate_t = s
+//   E  = sum_t g_t D n:  d post = gate E,  d gate = post E;  d next = sum_t dh u r_u
+// so a row takes two sums over its columns (five values in the second), and
+// the three column gradients come from two column sums over the rows.
 //
-// A row is held in the registers of a group of NT threads (a warp, or the whole
-// block); thread i owns the same columns of every row, so the column sums of
-// the gradient stay in its registers until the block is done.  Their partial
-// sums go to the workspace, one row per block, and a second kernel adds them in
-// block order.
+// Bound by HBM: x, y read and x_out, h written (forward), x, y, du, dh read and
+// dx, dy written (gradient).  A row is held in the registers of a group of NT
+// threads (a warp, or the block), thread i owning the same columns of every
+// row: its weights and its column sums stay in registers while the block walks
+// over rows t, t + blocks, ...  Each thread copies its own columns of the next
+// rows to shared memory (cp.async, a ring of S rows) and reads back nothing
+// that another thread wrote, so the ring needs no barrier.  Partial column sums
+// go to the workspace, one line a block; a second kernel adds them in block order.
 #include <math.h>
 
 #include "dtype.cuh"
@@ -31,9 +37,11 @@ struct NormArgs {
   long long ld_dxo, ld_dh;
   void *d_x, *d_y;
   long long ld_dx, ld_dy;
-  float *d_gate_token, *part;   // part: [blocks][3][H], post, gate, next
-  int want_post, want_gate, want_next;
+  float *d_gate_token, *part;   // part: [blocks][2][line], E and d next
+  int sums;                     // whether a column sum is asked for
 };
+
+__host__ __device__ constexpr int column_line(int H) { return (H + 3) / 4 * 4; }
 
 // VEC elements at p as fp32 (VEC 8: 16-byte accesses, p aligned).
 template <int VEC, typename T>
@@ -62,314 +70,476 @@ __device__ __forceinline__ void store_vec(T* p, const float* f) {
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = q[i];
   }
 }
+template <int VEC>
+__device__ __forceinline__ void load_weight(const void* p, int dtype, int c, float* f) {
+  if (VEC == 8 && (uintptr_t)p % 16 == 0) {
+    if (dtype == MOE_DT_F32) load_vec<VEC>(reinterpret_cast<const float*>(p) + c, f);
+    else if (dtype == MOE_DT_BF16) load_vec<VEC>(reinterpret_cast<const __nv_bfloat16*>(p) + c, f);
+    else load_vec<VEC>(reinterpret_cast<const __half*>(p) + c, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = load_any(p, dtype, c + j);
+  }
+}
+
+// The weights of VEC columns: w = gate * post (1 where absent), next.
+template <int VEC>
+__device__ __forceinline__ void load_weights(const NormArgs& a, int c, float* w, float* nx) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) w[j] = 1.f;
+  if (a.post) load_weight<VEC>(a.post, a.w_dtype, c, w);
+  if (a.gate_mode == MOE_GATE_CHANNEL) {
+    float g[VEC];
+    load_weight<VEC>(a.gate, a.w_dtype, c, g);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[j] *= g[j];
+  }
+  if (a.next) load_weight<VEC>(a.next, a.w_dtype, c, nx);
+}
 
 // Sums of N values over the NT threads of a row, the same in all of them.
-template <int NT, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N]) {
+// Sums in turn use two buffers, so that one barrier a sum is enough: a warp that
+// writes a buffer again has passed the barrier after its last reads.
+template <int NT, int N, int M>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (&buf)[2][M], int& turn) {
+  float* red = buf[turn];
+  turn ^= 1;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
   if constexpr (NT > 32) {
-    const int wid = threadIdx.x >> 5;
-    __syncthreads();   // the sums before these have been read
+    constexpr int W = NT / 32;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-      for (int n = 0; n < N; ++n) red[wid][n] = v[n];
+      for (int n = 0; n < N; ++n) red[n * W + (threadIdx.x >> 5)] = v[n];
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      v[n] = 0.f;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < NT / 32; ++i) v[n] += red[i][n];
+      for (int i = 0; i < W / 4; ++i) {
+        const float4 f = reinterpret_cast<const float4*>(red + n * W)[i];
+        s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
+      }
+      v[n] = (s.x + s.y) + (s.z + s.w);
     }
   }
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int NT>
-constexpr int kRowThreads = NT < 128 ? 128 : NT;   // threads of a block
+constexpr int kBlock = NT < 128 ? 128 : NT;   // threads of a block
 
-template <typename TX, typename TY, int VEC, int NV, int NT>
-__global__ void __launch_bounds__(kRowThreads<NT>) block_norm_kernel(const NormArgs a) {
-  __shared__ float red[32][1];
-  constexpr int kRows = kRowThreads<NT> / NT;   // rows a block works on at once
-  const int tid = threadIdx.x % NT, H = a.H;
-  for (long long t = (long long)blockIdx.x * kRows + threadIdx.x / NT; t < a.T; t += (long long)gridDim.x * kRows) {
-    float u[NV][VEC];
-    const TX* x = reinterpret_cast<const TX*>(a.x) + t * a.ld_x;
-    float gt = 1.f;
-    if (a.gate_mode == MOE_GATE_TOKEN) gt = load_any(a.gate, a.w_dtype, t);
-    if (a.y) {
-      const TY* y = reinterpret_cast<const TY*>(a.y) + t * a.ld_y;
-      float ss[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + tid) * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) u[i][j] = 0.f;
-        if (c < H) load_vec<VEC>(y + c, u[i]);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
-      }
-      float r = 1.f;
-      if (a.post) {
-        row_sums<NT>(ss, red);
-        r = 1.f / sqrtf(ss[0] / (float)H + a.eps);
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + tid) * VEC;
-        if (c >= H) continue;
-        float xv[VEC];
-        load_vec<VEC>(x + c, xv);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          float v = u[i][j] * r;
-          if (a.post) v *= load_any(a.post, a.w_dtype, c + j);
-          const float g = a.gate_mode == MOE_GATE_CHANNEL ? load_any(a.gate, a.w_dtype, c + j) : gt;
-          u[i][j] = fmaf(g, v, a.alpha * xv[j]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + tid) * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) u[i][j] = 0.f;
-        if (c < H) load_vec<VEC>(x + c, u[i]);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) u[i][j] *= a.alpha;
-      }
-    }
-    if (a.x_out) {
-      TX* xo = reinterpret_cast<TX*>(a.x_out) + t * a.ld_xo;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + tid) * VEC;
-        if (c < H) store_vec<VEC>(xo + c, u[i]);
-      }
-    }
-    if (a.next) {
-      float ss[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
-      row_sums<NT>(ss, red);
-      const float r = 1.f / sqrtf(ss[0] / (float)H + a.eps);
-      TY* h = reinterpret_cast<TY*>(a.h) + t * a.ld_h;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + tid) * VEC;
-        if (c >= H) continue;
-        float hv[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) hv[j] = u[i][j] * r * load_any(a.next, a.w_dtype, c + j);
-        store_vec<VEC>(h + c, hv);
-      }
-    }
+// A thread's own slots of the ring: 16-byte pieces, [stage][piece][thread].
+template <int NT, int PIECES>
+struct Ring {
+  uint8_t* base;
+  __device__ __forceinline__ uint8_t* at(int stage, int piece) const {
+    return base + ((size_t)(stage * PIECES + piece) * kBlock<NT> + threadIdx.x) * 16;
   }
+};
+template <typename T>
+constexpr int kPieces = (int)sizeof(T) / 2;   // 16-byte pieces of eight elements
+
+template <typename T, typename R>
+__device__ __forceinline__ void ring_copy(const R& ring, int stage, int piece, const T* src) {
+#pragma unroll
+  for (int i = 0; i < kPieces<T>; ++i) cp_async16(ring.at(stage, piece + i), reinterpret_cast<const uint4*>(src) + i);
+}
+template <typename T, typename R>
+__device__ __forceinline__ void ring_load(const R& ring, int stage, int piece, float* f) {
+  uint4 q[kPieces<T>];
+#pragma unroll
+  for (int i = 0; i < kPieces<T>; ++i) q[i] = *reinterpret_cast<const uint4*>(ring.at(stage, piece + i));
+  const T* e = reinterpret_cast<const T*>(q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = to_f32(e[i]);
 }
 
-template <typename TX, typename TY, int VEC, int NV, int NT>
-__global__ void __launch_bounds__(kRowThreads<NT>) block_norm_bwd_kernel(const NormArgs a) {
-  __shared__ float red1[32][1], red2[32][2];
-  constexpr int kRows = kRowThreads<NT> / NT;
+// Threads an SM is to hold at once: 64 registers a thread are enough for eight
+// columns of the forward, 128 for the rest.
+template <int VEC, int NV, int NT, bool BWD>
+constexpr int kResident = BWD || NV * VEC > 8 ? (kBlock<NT> > 512 ? kBlock<NT> : 512) : 1024;
+
+// Rows of the ring: as many as the resident threads leave shared memory for, at
+// most 4; 0: rows are loaded straight to registers (single elements).
+template <typename TX, typename TY, int VEC, int NV, int NT, bool BWD>
+constexpr int ring_rows() {
+  if (VEC == 1) return 0;
+  const int bytes = NV * 8 * (int)(sizeof(TX) + sizeof(TY)) * (BWD ? 2 : 1);
+  const int most = 200 * 1024 / (kResident<VEC, NV, NT, BWD> * bytes);
+  return most < 4 ? most : 4;
+}
+
+template <typename TX, typename TY, int VEC, int NV, int NT, int S>
+__global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, false> / kBlock<NT>)
+    block_norm_kernel(const NormArgs a) {
+  extern __shared__ uint8_t ring_smem[];
+  __shared__ alignas(16) float red[2][32];
+  constexpr int kRows = kBlock<NT> / NT;   // rows a block works on at once
+  constexpr int kPX = kPieces<TX>, kP = kPieces<TX> + kPieces<TY>;
+  const Ring<NT, NV * kP> ring{ring_smem};
   const int tid = threadIdx.x % NT, H = a.H;
-  const float inv_h = 1.f / (float)H;
-  float acc_post[NV][VEC], acc_gate[NV][VEC], acc_next[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) acc_post[i][j] = acc_gate[i][j] = acc_next[i][j] = 0.f;
-  for (long long t = (long long)blockIdx.x * kRows + threadIdx.x / NT; t < a.T; t += (long long)gridDim.x * kRows) {
-    float y[NV][VEC], u[NV][VEC], d[NV][VEC];
-    float gt = 1.f, ry = 1.f;
-    if (a.gate_mode == MOE_GATE_TOKEN) gt = load_any(a.gate, a.w_dtype, t);
-    const TX* x = reinterpret_cast<const TX*>(a.x) + t * a.ld_x;
-    {
-      float ss[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + tid) * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) y[i][j] = u[i][j] = d[i][j] = 0.f;
-        if (c >= H) continue;
-        if (a.y) load_vec<VEC>(reinterpret_cast<const TY*>(a.y) + t * a.ld_y + c, y[i]);
-        if (a.d_xo) load_vec<VEC>(reinterpret_cast<const TX*>(a.d_xo) + t * a.ld_dxo + c, d[i]);
-        load_vec<VEC>(x + c, u[i]);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) ss[0] = fmaf(y[i][j], y[i][j], ss[0]);
-      }
-      if (a.post) {
-        row_sums<NT>(ss, red1);
-        ry = 1.f / sqrtf(ss[0] * inv_h + a.eps);
-      }
-    }
-    // from here y is n(y)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * NT + tid) * VEC;
-      if (c >= H) continue;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        y[i][j] *= ry;
-        u[i][j] *= a.alpha;
-        if (a.y) {
-          const float v = a.post ? y[i][j] * load_any(a.post, a.w_dtype, c + j) : y[i][j];
-          const float g = a.gate_mode == MOE_GATE_CHANNEL ? load_any(a.gate, a.w_dtype, c + j) : gt;
-          u[i][j] = fmaf(g, v, u[i][j]);
-        }
-      }
-    }
-    if (a.next) {
-      float dh[NV][VEC];
-      float s[2] = {0.f, 0.f};   // sum u^2, sum dh g_next u
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + tid) * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dh[i][j] = 0.f;
-        if (c >= H) continue;
-        load_vec<VEC>(reinterpret_cast<const TY*>(a.d_h) + t * a.ld_dh + c, dh[i]);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          s[0] = fmaf(u[i][j], u[i][j], s[0]);
-          s[1] = fmaf(dh[i][j] * load_any(a.next, a.w_dtype, c + j), u[i][j], s[1]);
-        }
-      }
-      row_sums<NT>(s, red2);
-      const float ru = 1.f / sqrtf(s[0] * inv_h + a.eps);
-      const float m = ru * ru * s[1] * inv_h;
+  const long long step = (long long)gridDim.x * kRows;
+  long long t = (long long)blockIdx.x * kRows + threadIdx.x / NT;
+  pdl_wait();
+  pdl_launch_dependents();
+  const TX* x = reinterpret_cast<const TX*>(a.x);
+  const TY* y = reinterpret_cast<const TY*>(a.y);
+  auto fetch = [&](long long r, int stage) {
+    if (r < a.T) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * NT + tid) * VEC;
         if (c >= H) continue;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          d[i][j] = fmaf(ru, dh[i][j] * load_any(a.next, a.w_dtype, c + j) - u[i][j] * m, d[i][j]);
-          acc_next[i][j] = fmaf(dh[i][j], u[i][j] * ru, acc_next[i][j]);
-        }
+        ring_copy<TX>(ring, stage, i * kP, x + r * a.ld_x + c);
+        if (y) ring_copy<TY>(ring, stage, i * kP + kPX, y + r * a.ld_y + c);
       }
     }
-    TX* dx = reinterpret_cast<TX*>(a.d_x) + t * a.ld_dx;
-    float s[2] = {0.f, 0.f};   // sum B n(y), sum D v
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * NT + tid) * VEC;
-      if (c >= H) continue;
-      float o[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = a.alpha * d[i][j];
-      store_vec<VEC>(dx + c, o);
-      if (!a.y) continue;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float p = a.post ? load_any(a.post, a.w_dtype, c + j) : 1.f;
-        const float g = a.gate_mode == MOE_GATE_CHANNEL ? load_any(a.gate, a.w_dtype, c + j) : gt;
-        const float dv = d[i][j] * y[i][j];
-        s[1] = fmaf(dv, p, s[1]);
-        acc_gate[i][j] = fmaf(dv, p, acc_gate[i][j]);
-        acc_post[i][j] = fmaf(dv, g, acc_post[i][j]);
-        s[0] = fmaf(dv, g * p, s[0]);
-        d[i][j] *= g * p;   // B
-      }
-    }
-    if (!a.y) continue;
-    if (a.post || a.d_gate_token) row_sums<NT>(s, red2);
-    if (a.d_gate_token && tid == 0) a.d_gate_token[t] = s[1];
-    TY* dy = reinterpret_cast<TY*>(a.d_y) + t * a.ld_dy;
-    const float m = a.post ? s[0] * inv_h : 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * NT + tid) * VEC;
-      if (c >= H) continue;
-      float o[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = ry * (d[i][j] - y[i][j] * m);
-      store_vec<VEC>(dy + c, o);
-    }
-  }
-  // the rows' partial column sums, one line of the workspace for each group of threads
-  float* part = a.part + ((long long)blockIdx.x * kRows + threadIdx.x / NT) * 3 * H;
+    cp_async_commit();
+  };
+  if constexpr (S > 0)
+    for (int s = 0; s < S - 1; ++s) fetch(t + s * step, s);
+  float w[NV][VEC], nx[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * NT + tid) * VEC;
-    if (c >= H) continue;
+    if (c < H) load_weights<VEC>(a, c, w[i], nx[i]);
+  }
+  int stage = 0, turn = 0;
+  for (; t < a.T; t += step) {
+    float u[NV][VEC], v[NV][VEC];
+    if constexpr (S > 0) {
+      fetch(t + (S - 1) * step, (stage + S - 1) % S);
+      cp_async_wait<S - 1>();
+    }
+    float ss[1] = {0.f};
+    const float gt = a.gate_mode == MOE_GATE_TOKEN ? load_any(a.gate, a.w_dtype, t) : 1.f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      if (a.want_post) part[c + j] = acc_post[i][j];
-      if (a.want_gate) part[H + c + j] = acc_gate[i][j];
-      if (a.want_next) part[2 * H + c + j] = acc_next[i][j];
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * NT + tid) * VEC;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) u[i][j] = v[i][j] = 0.f;
+      if (c >= H) continue;
+      if constexpr (S > 0) {
+        ring_load<TX>(ring, stage, i * kP, u[i]);
+        if (y) ring_load<TY>(ring, stage, i * kP + kPX, v[i]);
+      } else {
+        load_vec<VEC>(x + t * a.ld_x + c, u[i]);
+        if (y) load_vec<VEC>(y + t * a.ld_y + c, v[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+    }
+    if constexpr (S > 0) stage = (stage + 1) % S;
+    float r = gt;
+    if (a.post) {
+      row_sums<NT>(ss, red, turn);
+      r = gt / sqrtf(ss[0] / (float)H + a.eps);
+    }
+    ss[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * NT + tid) * VEC;
+      if (c >= H) continue;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        u[i][j] *= a.alpha;
+        if (y) u[i][j] = fmaf(v[i][j] * w[i][j], r, u[i][j]);
+        ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
+      }
+      if (a.x_out) store_vec<VEC>(reinterpret_cast<TX*>(a.x_out) + t * a.ld_xo + c, u[i]);
+    }
+    if (a.next) {
+      row_sums<NT>(ss, red, turn);
+      const float ru = 1.f / sqrtf(ss[0] / (float)H + a.eps);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * NT + tid) * VEC;
+        if (c >= H) continue;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) u[i][j] *= ru * nx[i][j];
+        store_vec<VEC>(reinterpret_cast<TY*>(a.h) + t * a.ld_h + c, u[i]);
+      }
     }
   }
 }
 
-// Adds the lines of the workspace, in their order: blockIdx.y is the array.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int lines, int H, float* post, float* gate,
-                                                         float* next) {
-  float* out = blockIdx.y == 0 ? post : blockIdx.y == 1 ? gate : next;
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (!out || c >= H) return;
-  float s = 0.f;
-  for (int i = 0; i < lines; ++i) s += part[((long long)i * 3 + blockIdx.y) * H + c];
-  out[c] = s;
-}
-
-// The (threads, vectors per thread) a row of H columns is held in.
-struct RowShape {
-  int vec, nv, nt;
-};
-static RowShape row_shape(int H, bool vec) {
-  if (vec) {
-    const int n = H / 8;
-    if (n <= 32) return {8, 1, 32};
-    if (n <= 128) return {8, 4, 32};
-    if (n <= 256) return {8, 2, 128};
-    if (n <= 512) return {8, 2, 256};
-    if (n <= 1024) return {8, 2, 512};
-    return {8, 2, 1024};
+template <typename TX, typename TY, int VEC, int NV, int NT, int S>
+__global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBlock<NT>)
+    block_norm_bwd_kernel(const NormArgs a) {
+  extern __shared__ uint8_t ring_smem[];
+  __shared__ alignas(16) float red[2][5 * 32];
+  constexpr int kRows = kBlock<NT> / NT;
+  constexpr int kPX = kPieces<TX>, kPY = kPieces<TY>, kP = 2 * kPX + 2 * kPY;
+  constexpr bool kKeep = NV * VEC <= 8;   // the weights stay in registers
+  const Ring<NT, NV * kP> ring{ring_smem};
+  const int tid = threadIdx.x % NT, H = a.H;
+  const float inv_h = 1.f / (float)H;
+  const long long step = (long long)gridDim.x * kRows;
+  long long t = (long long)blockIdx.x * kRows + threadIdx.x / NT;
+  pdl_wait();
+  pdl_launch_dependents();
+  const TX *x = reinterpret_cast<const TX*>(a.x), *du = reinterpret_cast<const TX*>(a.d_xo);
+  const TY *y = reinterpret_cast<const TY*>(a.y), *dh = reinterpret_cast<const TY*>(a.d_h);
+  auto fetch = [&](long long r, int stage) {
+    if (r < a.T) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * NT + tid) * VEC;
+        if (c >= H) continue;
+        ring_copy<TX>(ring, stage, i * kP, x + r * a.ld_x + c);
+        if (y) ring_copy<TY>(ring, stage, i * kP + kPX, y + r * a.ld_y + c);
+        if (du) ring_copy<TX>(ring, stage, i * kP + kPX + kPY, du + r * a.ld_dxo + c);
+        if (dh) ring_copy<TY>(ring, stage, i * kP + 2 * kPX + kPY, dh + r * a.ld_dh + c);
+      }
+    }
+    cp_async_commit();
+  };
+  if constexpr (S > 0)
+    for (int s = 0; s < S - 1; ++s) fetch(t + s * step, s);
+  float acc_e[NV][VEC], acc_n[NV][VEC], kw[NV][VEC], kn[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * NT + tid) * VEC;
+    if (kKeep && c < H) load_weights<VEC>(a, c, kw[i], kn[i]);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc_e[i][j] = acc_n[i][j] = 0.f;
   }
-  return H <= 1024 ? RowShape{1, 4, 256} : RowShape{1, 16, 1024};
+  int stage = 0, turn = 0;
+  for (; t < a.T; t += step) {
+    float n[NV][VEC], u[NV][VEC], d[NV][VEC], e[NV][VEC];   // n(y), u, du and then D, dh and then a
+    if constexpr (S > 0) {
+      fetch(t + (S - 1) * step, (stage + S - 1) % S);
+      cp_async_wait<S - 1>();
+    }
+    const float gt = a.gate_mode == MOE_GATE_TOKEN ? load_any(a.gate, a.w_dtype, t) : 1.f;
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * NT + tid) * VEC;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) n[i][j] = u[i][j] = d[i][j] = e[i][j] = 0.f;
+      if (c >= H) continue;
+      if constexpr (S > 0) {
+        ring_load<TX>(ring, stage, i * kP, u[i]);
+        if (y) ring_load<TY>(ring, stage, i * kP + kPX, n[i]);
+        if (du) ring_load<TX>(ring, stage, i * kP + kPX + kPY, d[i]);
+        if (dh) ring_load<TY>(ring, stage, i * kP + 2 * kPX + kPY, e[i]);
+      } else {
+        load_vec<VEC>(x + t * a.ld_x + c, u[i]);
+        if (y) load_vec<VEC>(y + t * a.ld_y + c, n[i]);
+        if (du) load_vec<VEC>(du + t * a.ld_dxo + c, d[i]);
+        if (dh) load_vec<VEC>(dh + t * a.ld_dh + c, e[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) ss[0] = fmaf(n[i][j], n[i][j], ss[0]);
+    }
+    if constexpr (S > 0) stage = (stage + 1) % S;
+    float ry = 1.f;
+    if (a.post) {
+      row_sums<NT>(ss, red, turn);
+      ry = 1.f / sqrtf(ss[0] * inv_h + a.eps);
+    }
+    float s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};   // of q du, u^2, a u, q a, q u
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * NT + tid) * VEC;
+      if (c >= H) continue;
+      float w[VEC], nx[VEC];
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) w[j] = kw[i][j], nx[j] = kn[i][j];
+      } else {
+        load_weights<VEC>(a, c, w, nx);
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        n[i][j] *= ry;
+        const float q = y ? w[j] * n[i][j] : 0.f;
+        u[i][j] = fmaf(gt, q, a.alpha * u[i][j]);
+        s[0] = fmaf(q, d[i][j], s[0]);
+        if (dh) {
+          const float av = e[i][j] * nx[j];
+          s[1] = fmaf(u[i][j], u[i][j], s[1]);
+          s[2] = fmaf(av, u[i][j], s[2]);
+          s[3] = fmaf(q, av, s[3]);
+          s[4] = fmaf(q, u[i][j], s[4]);
+        }
+      }
+    }
+    row_sums<NT>(s, red, turn);
+    const float ru = dh ? 1.f / sqrtf(s[1] * inv_h + a.eps) : 0.f;
+    const float m = ru * ru * s[2] * inv_h;
+    const float sd = fmaf(ru, s[3] - m * s[4], s[0]);
+    if (a.d_gate_token && tid == 0) a.d_gate_token[t] = sd;
+    const float my = a.post ? gt * sd * inv_h : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * NT + tid) * VEC;
+      if (c >= H) continue;
+      float w[VEC], nx[VEC];
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) w[j] = kw[i][j], nx[j] = kn[i][j];
+      } else {
+        load_weights<VEC>(a, c, w, nx);
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        if (dh) {
+          d[i][j] = fmaf(ru, e[i][j] * nx[j] - u[i][j] * m, d[i][j]);
+          acc_n[i][j] = fmaf(e[i][j], u[i][j] * ru, acc_n[i][j]);
+        }
+        const float g = gt * d[i][j];
+        acc_e[i][j] = fmaf(g, n[i][j], acc_e[i][j]);
+        n[i][j] = ry * fmaf(g, w[j], -n[i][j] * my);
+        d[i][j] *= a.alpha;
+      }
+      store_vec<VEC>(reinterpret_cast<TX*>(a.d_x) + t * a.ld_dx + c, d[i]);
+      if (y) store_vec<VEC>(reinterpret_cast<TY*>(a.d_y) + t * a.ld_dy + c, n[i]);
+    }
+  }
+  if (!a.sums) return;
+  // the block's column sums: one line of the workspace
+  const int line = column_line(H);
+  float* part = a.part + (long long)blockIdx.x * 2 * line;
+  if constexpr (kRows == 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * NT + tid) * VEC;
+      if (c >= H) continue;
+      if constexpr (VEC == 8) {
+        store_vec<8>(part + c, acc_e[i]);
+        store_vec<8>(part + line + c, acc_n[i]);
+      } else {
+        part[c] = acc_e[i][0];
+        part[line + c] = acc_n[i][0];
+      }
+    }
+  } else {   // rows of one warp each: added in shared memory first, in row order
+    __shared__ float sum[2][NT * NV * VEC];
+    for (int r = 0; r < kRows; ++r) {
+      if ((int)threadIdx.x / NT == r) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const int c = (i * NT + tid) * VEC + j;
+            sum[0][c] = (r ? sum[0][c] : 0.f) + acc_e[i][j];
+            sum[1][c] = (r ? sum[1][c] : 0.f) + acc_n[i][j];
+          }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < H; c += kBlock<NT>) part[c] = sum[0][c], part[line + c] = sum[1][c];
+  }
 }
 
-// Blocks of the gradient kernel: what the workspace has lines for.
-static int bwd_blocks(long long T, int rows) {
-  const long long need = (T + rows - 1) / rows, most = device_sms() * 2;
+// Adds the blocks' lines in their order, 32 columns a block, eight threads a
+// column of four each taking every eighth line: blockIdx.y 0: E, from which the
+// post weight's and the gate's gradients, 1: the next weight's.
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int lines, int H, const void* post,
+                                                         const void* gate, int w_dtype, float* d_post, float* d_gate,
+                                                         float* d_next) {
+  __shared__ float4 sum[32][8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int line = column_line(H), slice = threadIdx.x / 8, c = (blockIdx.x * 8 + threadIdx.x % 8) * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < H) {
+#pragma unroll 4
+    for (int i = slice; i < lines; i += 32) {
+      const float4 f = *reinterpret_cast<const float4*>(part + ((long long)i * 2 + blockIdx.y) * line + c);
+      s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
+    }
+  }
+  sum[slice][threadIdx.x % 8] = s;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int cc = blockIdx.x * 32 + threadIdx.x;
+  if (cc >= H) return;
+  float v = 0.f;
+  for (int i = 0; i < 32; ++i) v += reinterpret_cast<const float*>(&sum[i][threadIdx.x / 4])[threadIdx.x % 4];
+  if (blockIdx.y == 1) {
+    if (d_next) d_next[cc] = v;
+    return;
+  }
+  if (d_post) d_post[cc] = gate ? v * load_any(gate, w_dtype, cc) : v;
+  if (d_gate) d_gate[cc] = post ? v * load_any(post, w_dtype, cc) : v;
+}
+
+// Blocks of the gradient kernel, which the workspace has a line for each: what
+// fits the SMs at 512 threads each.
+static int bwd_blocks(long long T, int rows, int threads) {
+  const long long need = (T + rows - 1) / rows, most = (long long)device_sms() * (threads >= 512 ? 1 : 512 / threads);
   return (int)(need < most ? need : most);
 }
 
 template <typename TX, typename TY, int VEC, int NV, int NT>
-static moe_status launch_norm(const NormArgs& a, bool bwd, cudaStream_t s) {
-  constexpr int kRows = kRowThreads<NT> / NT;
+static moe_status launch_norm(const NormArgs& a, bool bwd, int* lines, cudaStream_t s) {
+  constexpr int kRows = kBlock<NT> / NT;
+  constexpr int SF = ring_rows<TX, TY, VEC, NV, NT, false>(), SB = ring_rows<TX, TY, VEC, NV, NT, true>();
   if (!bwd) {
-    const long long need = ((long long)a.T + kRows - 1) / kRows;
+    const long long need = ((long long)a.T + kRows - 1) / kRows, most = (long long)device_sms() * (kResident<VEC, NV, NT, false> / kBlock<NT>);
+    constexpr size_t smem = (size_t)SF * NV * 8 * (sizeof(TX) + sizeof(TY)) * kBlock<NT>;
+    auto kernel = block_norm_kernel<TX, TY, VEC, NV, NT, SF>;
+    static char allowed[64];
+    MOE_CUDA(allow_smem(kernel, smem, allowed));
     ProfScope ps(MOE_K_NORM, s);
-    block_norm_kernel<TX, TY, VEC, NV, NT><<<(unsigned)(need < (1 << 20) ? need : 1 << 20), kRowThreads<NT>, 0, s>>>(a);
+    cudaError_t e = launch_pdl(kernel, dim3((unsigned)(need < most ? need : most)), dim3(kBlock<NT>), smem, s, a);
+    if (e != cudaSuccess) return cuda_fail(e, "block_norm_kernel");
     return check_launch("block_norm_kernel");
   }
-  ProfScope ps(MOE_K_NORM_BWD, s);
-  block_norm_bwd_kernel<TX, TY, VEC, NV, NT><<<bwd_blocks(a.T, kRows), kRowThreads<NT>, 0, s>>>(a);
+  constexpr size_t smem = (size_t)SB * NV * 16 * (sizeof(TX) + sizeof(TY)) * kBlock<NT>;
+  auto kernel = block_norm_bwd_kernel<TX, TY, VEC, NV, NT, SB>;
+  static char allowed[64];
+  MOE_CUDA(allow_smem(kernel, smem, allowed));
+  *lines = bwd_blocks(a.T, kRows, kBlock<NT>);
+  cudaError_t e = launch_pdl(kernel, dim3(*lines), dim3(kBlock<NT>), smem, s, a);
+  if (e != cudaSuccess) return cuda_fail(e, "block_norm_bwd_kernel");
   return check_launch("block_norm_bwd_kernel");
 }
 
+// The shape a row is held in.  Rows of up to 512 columns take one warp (no
+// barriers at all); longer ones the fewest threads that hold 8 columns each, or
+// 16 where 8 would take more than 1024 threads (the gradient: 512, so that its
+// two sums of every column keep 128 registers); where rows cannot be read in
+// 16-byte vectors, single elements, 4 to 16 a thread.
 template <typename TX, typename TY>
-static moe_status norm_by_shape(const NormArgs& a, bool vec, bool bwd, cudaStream_t s) {
-  const RowShape r = row_shape(a.H, vec);
-  if (r.vec == 1) return r.nt == 256 ? launch_norm<TX, TY, 1, 4, 256>(a, bwd, s) : launch_norm<TX, TY, 1, 16, 1024>(a, bwd, s);
-  if (r.nt == 32) return r.nv == 1 ? launch_norm<TX, TY, 8, 1, 32>(a, bwd, s) : launch_norm<TX, TY, 8, 4, 32>(a, bwd, s);
-  if (r.nt == 128) return launch_norm<TX, TY, 8, 2, 128>(a, bwd, s);
-  if (r.nt == 256) return launch_norm<TX, TY, 8, 2, 256>(a, bwd, s);
-  if (r.nt == 512) return launch_norm<TX, TY, 8, 2, 512>(a, bwd, s);
-  return launch_norm<TX, TY, 8, 2, 1024>(a, bwd, s);
+static moe_status norm_by_shape(const NormArgs& a, bool vec, bool bwd, int* lines, cudaStream_t s) {
+  const int H = a.H;
+  if (!vec) {
+    if (H <= 512) return launch_norm<TX, TY, 1, 4, 128>(a, bwd, lines, s);
+    if (H <= 2048) return launch_norm<TX, TY, 1, 8, 256>(a, bwd, lines, s);
+    if (H <= 8192) return launch_norm<TX, TY, 1, 16, 512>(a, bwd, lines, s);
+    return launch_norm<TX, TY, 1, 16, 1024>(a, bwd, lines, s);
+  }
+  if (H <= 256) return launch_norm<TX, TY, 8, 1, 32>(a, bwd, lines, s);
+  if (H <= 512) return launch_norm<TX, TY, 8, 2, 32>(a, bwd, lines, s);
+  if (H <= 1024) return launch_norm<TX, TY, 8, 1, 128>(a, bwd, lines, s);
+  if (H <= 2048) return launch_norm<TX, TY, 8, 1, 256>(a, bwd, lines, s);
+  if (H <= 4096) return launch_norm<TX, TY, 8, 1, 512>(a, bwd, lines, s);
+  if (H <= 8192 && !bwd) return launch_norm<TX, TY, 8, 1, 1024>(a, bwd, lines, s);
+  if (H <= 8192) return launch_norm<TX, TY, 8, 2, 512>(a, bwd, lines, s);
+  return launch_norm<TX, TY, 8, 2, 1024>(a, bwd, lines, s);
 }
 
-static moe_status norm_by_type(const NormArgs& a, int xd, int yd, bool vec, bool bwd, cudaStream_t s) {
-  if (xd == MOE_DT_BF16) return norm_by_shape<__nv_bfloat16, __nv_bfloat16>(a, vec, bwd, s);
-  if (xd == MOE_DT_F16) return norm_by_shape<__half, __half>(a, vec, bwd, s);
-  if (yd == MOE_DT_BF16) return norm_by_shape<float, __nv_bfloat16>(a, vec, bwd, s);
-  if (yd == MOE_DT_F16) return norm_by_shape<float, __half>(a, vec, bwd, s);
-  return norm_by_shape<float, float>(a, vec, bwd, s);
+static moe_status norm_by_type(const NormArgs& a, int xd, int yd, bool vec, bool bwd, int* lines, cudaStream_t s) {
+  if (xd == MOE_DT_BF16) return norm_by_shape<__nv_bfloat16, __nv_bfloat16>(a, vec, bwd, lines, s);
+  if (xd == MOE_DT_F16) return norm_by_shape<__half, __half>(a, vec, bwd, lines, s);
+  if (yd == MOE_DT_BF16) return norm_by_shape<float, __nv_bfloat16>(a, vec, bwd, lines, s);
+  if (yd == MOE_DT_F16) return norm_by_shape<float, __half>(a, vec, bwd, lines, s);
+  return norm_by_shape<float, float>(a, vec, bwd, lines, s);
 }
 
 // Whether a tensor's rows can be read in 16-byte vectors.
@@ -413,13 +583,13 @@ extern "C" moe_status moe_block_norm(int T, int H, int x_dtype, int y_dtype, int
   a.ld_x = ld_x, a.ld_y = ld_y, a.x_out = x_out, a.h = h, a.ld_xo = ld_x_out, a.ld_h = ld_h;
   const bool vec = H % 8 == 0 && vec_ok(x, ld_x, x_dtype) && vec_ok(y, ld_y, y_dtype) &&
                    vec_ok(x_out, ld_x_out, x_dtype) && vec_ok(h, ld_h, y_dtype);
-  return norm_by_type(a, x_dtype, y_dtype, vec, false, stream);
+  return norm_by_type(a, x_dtype, y_dtype, vec, false, nullptr, stream);
 }
 
 extern "C" size_t moe_block_norm_backward_workspace(int T, int H) {
-  if (T <= 0 || H <= 0) return 0;
-  // the shapes of up to 4 rows a block have the most lines
-  return (size_t)bwd_blocks(T, 1) * 4 * 3 * H * sizeof(float);
+  if (T <= 0 || H <= 0 || H > 16384) return 0;
+  // one line of two sums a block; the narrowest blocks (128 threads, H <= 1024) are the most
+  return (size_t)bwd_blocks(T, 1, H <= 1024 ? 128 : H <= 2048 ? 256 : 512) * 2 * column_line(H) * sizeof(float);
 }
 
 extern "C" moe_status moe_block_norm_backward(int T, int H, int x_dtype, int y_dtype, int w_dtype, const void* x,
@@ -461,16 +631,18 @@ extern "C" moe_status moe_block_norm_backward(int T, int H, int x_dtype, int y_d
   a.d_x = d_x, a.d_y = d_y, a.ld_dx = ld_d_x, a.ld_dy = ld_d_y;
   a.d_gate_token = gate_mode == MOE_GATE_TOKEN ? d_gate : nullptr;
   a.part = (float*)workspace;
-  a.want_post = d_post_weight != nullptr, a.want_next = d_next_weight != nullptr;
-  a.want_gate = d_gate && gate_mode == MOE_GATE_CHANNEL;
+  a.sums = sums;
   const bool vec = H % 8 == 0 && vec_ok(x, ld_x, x_dtype) && vec_ok(y, ld_y, y_dtype) &&
                    vec_ok(d_x_out, ld_d_x_out, x_dtype) && vec_ok(d_h, ld_d_h, y_dtype) &&
                    vec_ok(d_x, ld_d_x, x_dtype) && vec_ok(d_y, ld_d_y, y_dtype);
-  st = norm_by_type(a, x_dtype, y_dtype, vec, true, stream);
+  int lines = 0;
+  ProfScope ps(MOE_K_NORM_BWD, stream);
+  st = norm_by_type(a, x_dtype, y_dtype, vec, true, &lines, stream);
   if (st != MOE_OK || !sums) return st;
-  const RowShape r = row_shape(H, vec);
-  const int rows = (r.nt < 128 ? 128 : r.nt) / r.nt;
-  column_sum_kernel<<<dim3((H + 255) / 256, 3), 256, 0, stream>>>(
-      a.part, bwd_blocks(T, rows) * rows, H, d_post_weight, a.want_gate ? d_gate : nullptr, d_next_weight);
+  const bool channel = gate_mode == MOE_GATE_CHANNEL;
+  cudaError_t e = launch_pdl(column_sum_kernel, dim3((H + 31) / 32, next_weight ? 2 : 1), dim3(256), 0, stream,
+                             (const float*)a.part, lines, H, post_weight, channel ? gate : nullptr, w_dtype,
+                             d_post_weight, channel ? d_gate : nullptr, d_next_weight);
+  if (e != cudaSuccess) return cuda_fail(e, "column_sum_kernel");
   return check_launch("column_sum_kernel");
 }

@@ -21,6 +21,8 @@
 // go to the workspace, one line a block; a second kernel adds them in block order.
 #include <math.h>
 
+#include <type_traits>
+
 #include "dtype.cuh"
 
 namespace moe {
@@ -43,88 +45,212 @@ struct NormArgs {
 
 __host__ __device__ constexpr int column_line(int H) { return (H + 3) / 4 * 4; }
 
-// VEC elements at p as fp32 (VEC 8: 16-byte accesses, p aligned).
-template <int VEC, typename T>
-__device__ __forceinline__ void load_vec(const T* p, float* f) {
-  if constexpr (VEC == 1) {
-    f[0] = to_f32(p[0]);
-  } else {
-    uint4 q[sizeof(T) / 2];
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
-    const T* e = reinterpret_cast<const T*>(q);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = to_f32(e[i]);
-  }
+// Two fp32 values in one 64-bit register: Blackwell's packed fp32 instructions
+// do both at once.  Columns are held as pairs (16-byte vectors of eight) or, in
+// the unaligned form, as single floats, with the same operations.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
 }
-template <int VEC, typename T>
-__device__ __forceinline__ void store_vec(T* p, const float* f) {
-  if constexpr (VEC == 1) {
-    p[0] = from_f32<T>(f[0]);
-  } else {
-    uint4 q[sizeof(T) / 2];
-    T* e = reinterpret_cast<T*>(q);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(f[i]);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = q[i];
-  }
+__device__ __forceinline__ float2 unpack2(F2 a) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(a.v));
+  return f;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float total(F2 a) {
+  const float2 f = unpack2(a);
+  return f.x + f.y;
+}
+__device__ __forceinline__ float total(float a) { return a; }
+template <typename E>
+__device__ __forceinline__ E splat(float f);
+template <>
+__device__ __forceinline__ F2 splat<F2>(float f) {
+  return pack2(f, f);
+}
+template <>
+__device__ __forceinline__ float splat<float>(float f) {
+  return f;
 }
 template <int VEC>
-__device__ __forceinline__ void load_weight(const void* p, int dtype, int c, float* f) {
-  if (VEC == 8 && (uintptr_t)p % 16 == 0) {
-    if (dtype == MOE_DT_F32) load_vec<VEC>(reinterpret_cast<const float*>(p) + c, f);
-    else if (dtype == MOE_DT_BF16) load_vec<VEC>(reinterpret_cast<const __nv_bfloat16*>(p) + c, f);
-    else load_vec<VEC>(reinterpret_cast<const __half*>(p) + c, f);
-  } else {
+using Elem = typename std::conditional<VEC == 8, F2, float>::type;
+template <int VEC>
+constexpr int kElems = VEC == 8 ? 4 : 1;
+
+__device__ __forceinline__ void widen(const uint4 (&q)[2], const float*, F2* e) {
+  e[0] = pack2(__uint_as_float(q[0].x), __uint_as_float(q[0].y));
+  e[1] = pack2(__uint_as_float(q[0].z), __uint_as_float(q[0].w));
+  e[2] = pack2(__uint_as_float(q[1].x), __uint_as_float(q[1].y));
+  e[3] = pack2(__uint_as_float(q[1].z), __uint_as_float(q[1].w));
+}
+__device__ __forceinline__ void widen(const uint4 (&q)[1], const __nv_bfloat16*, F2* e) {
+  const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] = load_any(p, dtype, c + j);
+  for (int i = 0; i < 4; ++i) e[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void widen(const uint4 (&q)[1], const __half*, F2* e) {
+  const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    e[i] = pack2(f.x, f.y);
   }
 }
+__device__ __forceinline__ uint32_t narrow(float2 f, const __nv_bfloat16*) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t narrow(float2 f, const __half*) {
+  const __half2 h = __floats2half2_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T>
+constexpr int kPieces = (int)sizeof(T) / 2;   // 16-byte pieces of eight elements
+
+// Eight elements (16-byte aligned) or one at p, as fp32.
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, F2* e) {
+  uint4 q[kPieces<T>];
+#pragma unroll
+  for (int i = 0; i < kPieces<T>; ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
+  widen(q, p, e);
+}
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, float* e) {
+  e[0] = to_f32(p[0]);
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const F2* e) {
+  if constexpr (sizeof(T) == 4) {
+    const float2 a = unpack2(e[0]), b = unpack2(e[1]), c = unpack2(e[2]), d = unpack2(e[3]);
+    reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(narrow(unpack2(e[0]), p), narrow(unpack2(e[1]), p),
+                                              narrow(unpack2(e[2]), p), narrow(unpack2(e[3]), p));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const float* e) {
+  p[0] = from_f32<T>(e[0]);
+}
+
+__device__ __forceinline__ void load_weight(const void* p, int dtype, int c, F2* e) {
+  if ((uintptr_t)p % 16 == 0) {
+    if (dtype == MOE_DT_F32) load_vec(reinterpret_cast<const float*>(p) + c, e);
+    else if (dtype == MOE_DT_BF16) load_vec(reinterpret_cast<const __nv_bfloat16*>(p) + c, e);
+    else load_vec(reinterpret_cast<const __half*>(p) + c, e);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      e[j] = pack2(load_any(p, dtype, c + 2 * j), load_any(p, dtype, c + 2 * j + 1));
+  }
+}
+__device__ __forceinline__ void load_weight(const void* p, int dtype, int c, float* e) { e[0] = load_any(p, dtype, c); }
 
 // The weights of VEC columns: w = gate * post (1 where absent), next.
-template <int VEC>
-__device__ __forceinline__ void load_weights(const NormArgs& a, int c, float* w, float* nx) {
+template <int VEC, typename E>
+__device__ __forceinline__ void load_weights(const NormArgs& a, int c, E* w, E* nx) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) w[j] = 1.f;
-  if (a.post) load_weight<VEC>(a.post, a.w_dtype, c, w);
+  for (int j = 0; j < kElems<VEC>; ++j) w[j] = nx[j] = splat<E>(1.f);
+  if (a.post) load_weight(a.post, a.w_dtype, c, w);
   if (a.gate_mode == MOE_GATE_CHANNEL) {
-    float g[VEC];
-    load_weight<VEC>(a.gate, a.w_dtype, c, g);
+    E g[kElems<VEC>];
+    load_weight(a.gate, a.w_dtype, c, g);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) w[j] *= g[j];
+    for (int j = 0; j < kElems<VEC>; ++j) w[j] = mul(w[j], g[j]);
   }
-  if (a.next) load_weight<VEC>(a.next, a.w_dtype, c, nx);
+  if (a.next) load_weight(a.next, a.w_dtype, c, nx);
 }
 
-// Sums of N values over the NT threads of a row, the same in all of them.
-// Sums in turn use two buffers, so that one barrier a sum is enough: a warp that
+// Sum of one value over the NT threads of a row, the same in all of them.  Sums
+// in turn use two buffers, so that one barrier a sum is enough: a warp that
 // writes a buffer again has passed the barrier after its last reads.
-template <int NT, int N, int M>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (&buf)[2][M], int& turn) {
-  float* red = buf[turn];
-  turn ^= 1;
+template <int NT, int M>
+__device__ __forceinline__ float row_sum(float v, float (&buf)[2][M], int& turn) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (NT > 32) {
     constexpr int W = NT / 32;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-      for (int n = 0; n < N; ++n) red[n * W + (threadIdx.x >> 5)] = v[n];
+    float* red = buf[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
+    F2 s = pack2(0.f, 0.f), r = s;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < W / 4; ++i) {
+      const float4 f = reinterpret_cast<const float4*>(red)[i];
+      s = add(s, pack2(f.x, f.y)), r = add(r, pack2(f.z, f.w));
+    }
+    v = total(add(s, r));
+  }
+  return v;
+}
+
+// Sums of five values.  The first four are halved on the way: at the first step
+// a lane keeps two of them and hands on the other two, at the second one and
+// one, so the butterfly moves 6 + 5 values instead of 20 + 5; lane l then holds
+// value l / 8 of the warp.  Across warps the same.
+__device__ __forceinline__ float halve4(const float (&v)[5], int lane) {
+  const bool hi = lane & 16, mid = lane & 8;
+  const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+  const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+  return (mid ? b : a) + __shfl_xor_sync(0xffffffffu, mid ? a : b, 8);
+}
+template <int NT, int M>
+__device__ __forceinline__ void row_sums5(float (&v)[5], float (&buf)[2][M], int& turn) {
+  const int lane = threadIdx.x & 31;
+  float q = halve4(v, lane), z = v[4];
 #pragma unroll
-      for (int i = 0; i < W / 4; ++i) {
-        const float4 f = reinterpret_cast<const float4*>(red + n * W)[i];
-        s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
-      }
-      v[n] = (s.x + s.y) + (s.z + s.w);
+  for (int o = 4; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  if constexpr (NT > 32) {
+    constexpr int W = NT / 32;   // 4, 8, 16 or 32
+    float* red = buf[turn];      // [5][W]
+    turn ^= 1;
+    if ((lane & 7) == 0) red[(lane >> 3) * W + (threadIdx.x >> 5)] = q;
+    if (lane == 1) red[4 * W + (threadIdx.x >> 5)] = z;
+    __syncthreads();
+    // eight lanes a value: lane l sums every eighth partial of value l / 8
+    q = z = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; i += 8) {
+      const bool in = W >= 8 || (lane & 7) < W;
+      if (in) q += red[(lane >> 3) * W + i + (lane & 7)], z += red[4 * W + i + (lane & 7)];
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+      z += __shfl_xor_sync(0xffffffffu, z, o);
     }
   }
+#pragma unroll
+  for (int n = 0; n < 4; ++n) v[n] = __shfl_sync(0xffffffffu, q, n * 8);
+  v[4] = z;
 }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -147,22 +273,17 @@ struct Ring {
     return base + ((size_t)(stage * PIECES + piece) * kBlock<NT> + threadIdx.x) * 16;
   }
 };
-template <typename T>
-constexpr int kPieces = (int)sizeof(T) / 2;   // 16-byte pieces of eight elements
-
 template <typename T, typename R>
 __device__ __forceinline__ void ring_copy(const R& ring, int stage, int piece, const T* src) {
 #pragma unroll
   for (int i = 0; i < kPieces<T>; ++i) cp_async16(ring.at(stage, piece + i), reinterpret_cast<const uint4*>(src) + i);
 }
 template <typename T, typename R>
-__device__ __forceinline__ void ring_load(const R& ring, int stage, int piece, float* f) {
+__device__ __forceinline__ void ring_load(const R& ring, int stage, int piece, F2* e) {
   uint4 q[kPieces<T>];
 #pragma unroll
   for (int i = 0; i < kPieces<T>; ++i) q[i] = *reinterpret_cast<const uint4*>(ring.at(stage, piece + i));
-  const T* e = reinterpret_cast<const T*>(q);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = to_f32(e[i]);
+  widen(q, (const T*)nullptr, e);
 }
 
 // Threads an SM is to hold at once: 64 registers a thread are enough for eight
@@ -185,6 +306,8 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, false> / kB
     block_norm_kernel(const NormArgs a) {
   extern __shared__ uint8_t ring_smem[];
   __shared__ alignas(16) float red[2][32];
+  using E = Elem<VEC>;
+  constexpr int P = kElems<VEC>;
   constexpr int kRows = kBlock<NT> / NT;   // rows a block works on at once
   constexpr int kPX = kPieces<TX>, kP = kPieces<TX> + kPieces<TY>;
   const Ring<NT, NV * kP> ring{ring_smem};
@@ -195,21 +318,24 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, false> / kB
   pdl_launch_dependents();
   const TX* x = reinterpret_cast<const TX*>(a.x);
   const TY* y = reinterpret_cast<const TY*>(a.y);
+  const float inv_h = 1.f / (float)H;
   auto fetch = [&](long long r, int stage) {
     if (r < a.T) {
+      const TX* xr = x + r * a.ld_x;
+      const TY* yr = y + r * a.ld_y;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * NT + tid) * VEC;
         if (c >= H) continue;
-        ring_copy<TX>(ring, stage, i * kP, x + r * a.ld_x + c);
-        if (y) ring_copy<TY>(ring, stage, i * kP + kPX, y + r * a.ld_y + c);
+        ring_copy<TX>(ring, stage, i * kP, xr + c);
+        if (y) ring_copy<TY>(ring, stage, i * kP + kPX, yr + c);
       }
     }
     cp_async_commit();
   };
   if constexpr (S > 0)
     for (int s = 0; s < S - 1; ++s) fetch(t + s * step, s);
-  float w[NV][VEC], nx[NV][VEC];
+  E w[NV][P], nx[NV][P];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * NT + tid) * VEC;
@@ -217,58 +343,54 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, false> / kB
   }
   int stage = 0, turn = 0;
   for (; t < a.T; t += step) {
-    float u[NV][VEC], v[NV][VEC];
+    E u[NV][P], v[NV][P];
     if constexpr (S > 0) {
       fetch(t + (S - 1) * step, (stage + S - 1) % S);
       cp_async_wait<S - 1>();
     }
-    float ss[1] = {0.f};
+    E ss = splat<E>(0.f);
     const float gt = a.gate_mode == MOE_GATE_TOKEN ? load_any(a.gate, a.w_dtype, t) : 1.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * NT + tid) * VEC;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) u[i][j] = v[i][j] = 0.f;
+      for (int j = 0; j < P; ++j) u[i][j] = v[i][j] = splat<E>(0.f);
       if (c >= H) continue;
       if constexpr (S > 0) {
         ring_load<TX>(ring, stage, i * kP, u[i]);
         if (y) ring_load<TY>(ring, stage, i * kP + kPX, v[i]);
       } else {
-        load_vec<VEC>(x + t * a.ld_x + c, u[i]);
-        if (y) load_vec<VEC>(y + t * a.ld_y + c, v[i]);
+        load_vec(x + t * a.ld_x + c, u[i]);
+        if (y) load_vec(y + t * a.ld_y + c, v[i]);
       }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+      for (int j = 0; j < P; ++j) ss = fma(v[i][j], v[i][j], ss);
     }
-    if constexpr (S > 0) stage = (stage + 1) % S;
-    float r = gt;
-    if (a.post) {
-      row_sums<NT>(ss, red, turn);
-      r = gt / sqrtf(ss[0] / (float)H + a.eps);
-    }
-    ss[0] = 0.f;
+    if constexpr (S > 0) stage = stage + 1 == S ? 0 : stage + 1;
+    const float r = a.post ? gt * rsqrtf(fmaf(row_sum<NT>(total(ss), red, turn), inv_h, a.eps)) : gt;
+    const E r2 = splat<E>(r), alpha = splat<E>(a.alpha);
+    ss = splat<E>(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * NT + tid) * VEC;
       if (c >= H) continue;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        u[i][j] *= a.alpha;
-        if (y) u[i][j] = fmaf(v[i][j] * w[i][j], r, u[i][j]);
-        ss[0] = fmaf(u[i][j], u[i][j], ss[0]);
+      for (int j = 0; j < P; ++j) {
+        u[i][j] = mul(u[i][j], alpha);
+        if (y) u[i][j] = fma(mul(v[i][j], w[i][j]), r2, u[i][j]);
+        ss = fma(u[i][j], u[i][j], ss);
       }
-      if (a.x_out) store_vec<VEC>(reinterpret_cast<TX*>(a.x_out) + t * a.ld_xo + c, u[i]);
+      if (a.x_out) store_vec(reinterpret_cast<TX*>(a.x_out) + t * a.ld_xo + c, u[i]);
     }
     if (a.next) {
-      row_sums<NT>(ss, red, turn);
-      const float ru = 1.f / sqrtf(ss[0] / (float)H + a.eps);
+      const E ru = splat<E>(rsqrtf(fmaf(row_sum<NT>(total(ss), red, turn), inv_h, a.eps)));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * NT + tid) * VEC;
         if (c >= H) continue;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) u[i][j] *= ru * nx[i][j];
-        store_vec<VEC>(reinterpret_cast<TY*>(a.h) + t * a.ld_h + c, u[i]);
+        for (int j = 0; j < P; ++j) u[i][j] = mul(mul(u[i][j], ru), nx[i][j]);
+        store_vec(reinterpret_cast<TY*>(a.h) + t * a.ld_h + c, u[i]);
       }
     }
   }
@@ -279,6 +401,8 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
     block_norm_bwd_kernel(const NormArgs a) {
   extern __shared__ uint8_t ring_smem[];
   __shared__ alignas(16) float red[2][5 * 32];
+  using E = Elem<VEC>;
+  constexpr int P = kElems<VEC>;
   constexpr int kRows = kBlock<NT> / NT;
   constexpr int kPX = kPieces<TX>, kPY = kPieces<TY>, kP = 2 * kPX + 2 * kPY;
   constexpr bool kKeep = NV * VEC <= 8;   // the weights stay in registers
@@ -307,28 +431,28 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
   };
   if constexpr (S > 0)
     for (int s = 0; s < S - 1; ++s) fetch(t + s * step, s);
-  float acc_e[NV][VEC], acc_n[NV][VEC], kw[NV][VEC], kn[NV][VEC];
+  E acc_e[NV][P], acc_n[NV][P], kw[NV][P], kn[NV][P];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * NT + tid) * VEC;
     if (kKeep && c < H) load_weights<VEC>(a, c, kw[i], kn[i]);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc_e[i][j] = acc_n[i][j] = 0.f;
+    for (int j = 0; j < P; ++j) acc_e[i][j] = acc_n[i][j] = splat<E>(0.f);
   }
   int stage = 0, turn = 0;
   for (; t < a.T; t += step) {
-    float n[NV][VEC], u[NV][VEC], d[NV][VEC], e[NV][VEC];   // n(y), u, du and then D, dh and then a
+    E n[NV][P], u[NV][P], d[NV][P], e[NV][P];   // n(y), u, du and then D, dh
     if constexpr (S > 0) {
       fetch(t + (S - 1) * step, (stage + S - 1) % S);
       cp_async_wait<S - 1>();
     }
     const float gt = a.gate_mode == MOE_GATE_TOKEN ? load_any(a.gate, a.w_dtype, t) : 1.f;
-    float ss[1] = {0.f};
+    E ss = splat<E>(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * NT + tid) * VEC;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) n[i][j] = u[i][j] = d[i][j] = e[i][j] = 0.f;
+      for (int j = 0; j < P; ++j) n[i][j] = u[i][j] = d[i][j] = e[i][j] = splat<E>(0.f);
       if (c >= H) continue;
       if constexpr (S > 0) {
         ring_load<TX>(ring, stage, i * kP, u[i]);
@@ -336,77 +460,77 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
         if (du) ring_load<TX>(ring, stage, i * kP + kPX + kPY, d[i]);
         if (dh) ring_load<TY>(ring, stage, i * kP + 2 * kPX + kPY, e[i]);
       } else {
-        load_vec<VEC>(x + t * a.ld_x + c, u[i]);
-        if (y) load_vec<VEC>(y + t * a.ld_y + c, n[i]);
-        if (du) load_vec<VEC>(du + t * a.ld_dxo + c, d[i]);
-        if (dh) load_vec<VEC>(dh + t * a.ld_dh + c, e[i]);
+        load_vec(x + t * a.ld_x + c, u[i]);
+        if (y) load_vec(y + t * a.ld_y + c, n[i]);
+        if (du) load_vec(du + t * a.ld_dxo + c, d[i]);
+        if (dh) load_vec(dh + t * a.ld_dh + c, e[i]);
       }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) ss[0] = fmaf(n[i][j], n[i][j], ss[0]);
+      for (int j = 0; j < P; ++j) ss = fma(n[i][j], n[i][j], ss);
     }
-    if constexpr (S > 0) stage = (stage + 1) % S;
-    float ry = 1.f;
-    if (a.post) {
-      row_sums<NT>(ss, red, turn);
-      ry = 1.f / sqrtf(ss[0] * inv_h + a.eps);
-    }
-    float s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};   // of q du, u^2, a u, q a, q u
+    if constexpr (S > 0) stage = stage + 1 == S ? 0 : stage + 1;
+    const float ry = a.post ? rsqrtf(fmaf(row_sum<NT>(total(ss), red, turn), inv_h, a.eps)) : 1.f;
+    E s2[5];   // of q du, u^2, a u, q a, q u
+#pragma unroll
+    for (int k = 0; k < 5; ++k) s2[k] = splat<E>(0.f);
+    const E ry2 = splat<E>(y ? ry : 0.f), gt2 = splat<E>(gt), alpha = splat<E>(a.alpha);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * NT + tid) * VEC;
       if (c >= H) continue;
-      float w[VEC], nx[VEC];
+      E w[P], nx[P];
       if constexpr (kKeep) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) w[j] = kw[i][j], nx[j] = kn[i][j];
+        for (int j = 0; j < P; ++j) w[j] = kw[i][j], nx[j] = kn[i][j];
       } else {
         load_weights<VEC>(a, c, w, nx);
       }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        n[i][j] *= ry;
-        const float q = y ? w[j] * n[i][j] : 0.f;
-        u[i][j] = fmaf(gt, q, a.alpha * u[i][j]);
-        s[0] = fmaf(q, d[i][j], s[0]);
-        if (dh) {
-          const float av = e[i][j] * nx[j];
-          s[1] = fmaf(u[i][j], u[i][j], s[1]);
-          s[2] = fmaf(av, u[i][j], s[2]);
-          s[3] = fmaf(q, av, s[3]);
-          s[4] = fmaf(q, u[i][j], s[4]);
-        }
+      for (int j = 0; j < P; ++j) {
+        n[i][j] = mul(n[i][j], ry2);
+        const E q = mul(w[j], n[i][j]);
+        u[i][j] = dh ? fma(gt2, q, mul(alpha, u[i][j])) : splat<E>(0.f);   // without h nothing hangs on u
+        s2[0] = fma(q, d[i][j], s2[0]);
+        const E av = mul(e[i][j], nx[j]);
+        s2[1] = fma(u[i][j], u[i][j], s2[1]);
+        s2[2] = fma(av, u[i][j], s2[2]);
+        s2[3] = fma(q, av, s2[3]);
+        s2[4] = fma(q, u[i][j], s2[4]);
       }
     }
-    row_sums<NT>(s, red, turn);
-    const float ru = dh ? 1.f / sqrtf(s[1] * inv_h + a.eps) : 0.f;
+    float s[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) s[k] = total(s2[k]);
+    row_sums5<NT>(s, red, turn);
+    const float ru = dh ? rsqrtf(fmaf(s[1], inv_h, a.eps)) : 0.f;
     const float m = ru * ru * s[2] * inv_h;
     const float sd = fmaf(ru, s[3] - m * s[4], s[0]);
     if (a.d_gate_token && tid == 0) a.d_gate_token[t] = sd;
     const float my = a.post ? gt * sd * inv_h : 0.f;
+    const E ru2 = splat<E>(ru), mm = splat<E>(-ru * m), mym = splat<E>(-my), ryo = splat<E>(ry);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * NT + tid) * VEC;
       if (c >= H) continue;
-      float w[VEC], nx[VEC];
+      E w[P], nx[P];
       if constexpr (kKeep) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) w[j] = kw[i][j], nx[j] = kn[i][j];
+        for (int j = 0; j < P; ++j) w[j] = kw[i][j], nx[j] = kn[i][j];
       } else {
         load_weights<VEC>(a, c, w, nx);
       }
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if (dh) {
-          d[i][j] = fmaf(ru, e[i][j] * nx[j] - u[i][j] * m, d[i][j]);
-          acc_n[i][j] = fmaf(e[i][j], u[i][j] * ru, acc_n[i][j]);
-        }
-        const float g = gt * d[i][j];
-        acc_e[i][j] = fmaf(g, n[i][j], acc_e[i][j]);
-        n[i][j] = ry * fmaf(g, w[j], -n[i][j] * my);
-        d[i][j] *= a.alpha;
+      for (int j = 0; j < P; ++j) {
+        const E er = mul(e[i][j], ru2);   // dh r_u
+        d[i][j] = fma(er, nx[j], fma(u[i][j], mm, d[i][j]));
+        acc_n[i][j] = fma(er, u[i][j], acc_n[i][j]);
+        const E g = mul(gt2, d[i][j]);
+        acc_e[i][j] = fma(g, n[i][j], acc_e[i][j]);
+        n[i][j] = a.post ? mul(ryo, fma(g, w[j], mul(n[i][j], mym))) : mul(g, w[j]);
+        d[i][j] = mul(d[i][j], alpha);
       }
-      store_vec<VEC>(reinterpret_cast<TX*>(a.d_x) + t * a.ld_dx + c, d[i]);
-      if (y) store_vec<VEC>(reinterpret_cast<TY*>(a.d_y) + t * a.ld_dy + c, n[i]);
+      store_vec(reinterpret_cast<TX*>(a.d_x) + t * a.ld_dx + c, d[i]);
+      if (y) store_vec(reinterpret_cast<TY*>(a.d_y) + t * a.ld_dy + c, n[i]);
     }
   }
   if (!a.sums) return;
@@ -418,30 +542,26 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
     for (int i = 0; i < NV; ++i) {
       const int c = (i * NT + tid) * VEC;
       if (c >= H) continue;
-      if constexpr (VEC == 8) {
-        store_vec<8>(part + c, acc_e[i]);
-        store_vec<8>(part + line + c, acc_n[i]);
-      } else {
-        part[c] = acc_e[i][0];
-        part[line + c] = acc_n[i][0];
-      }
+      store_vec(part + c, acc_e[i]);
+      store_vec(part + line + c, acc_n[i]);
     }
   } else {   // rows of one warp each: added in shared memory first, in row order
-    __shared__ float sum[2][NT * NV * VEC];
+    __shared__ alignas(16) E sum[2][NT * NV * P];
     for (int r = 0; r < kRows; ++r) {
       if ((int)threadIdx.x / NT == r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const int c = (i * NT + tid) * VEC + j;
-            sum[0][c] = (r ? sum[0][c] : 0.f) + acc_e[i][j];
-            sum[1][c] = (r ? sum[1][c] : 0.f) + acc_n[i][j];
+          for (int j = 0; j < P; ++j) {
+            const int c = (i * NT + tid) * P + j;
+            sum[0][c] = r ? add(sum[0][c], acc_e[i][j]) : acc_e[i][j];
+            sum[1][c] = r ? add(sum[1][c], acc_n[i][j]) : acc_n[i][j];
           }
       }
       __syncthreads();
     }
-    for (int c = threadIdx.x; c < H; c += kBlock<NT>) part[c] = sum[0][c], part[line + c] = sum[1][c];
+    const float *f0 = reinterpret_cast<const float*>(sum[0]), *f1 = reinterpret_cast<const float*>(sum[1]);
+    for (int c = threadIdx.x; c < H; c += kBlock<NT>) part[c] = f0[c], part[line + c] = f1[c];
   }
 }
 

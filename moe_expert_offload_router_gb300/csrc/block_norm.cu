@@ -316,20 +316,28 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, false> / kB
   long long t = (long long)blockIdx.x * kRows + threadIdx.x / NT;
   pdl_wait();
   pdl_launch_dependents();
-  const TX* x = reinterpret_cast<const TX*>(a.x);
-  const TY* y = reinterpret_cast<const TY*>(a.y);
   const float inv_h = 1.f / (float)H;
+  const bool has_y = a.y;
+  // this thread's first column in the row to be fetched next, and in the rows written
+  const int c0 = tid * VEC;
+  const TX* x = reinterpret_cast<const TX*>(a.x) + t * a.ld_x + c0;
+  const TY* y = reinterpret_cast<const TY*>(a.y) + (has_y ? t * a.ld_y + c0 : 0);
+  TX* xo = reinterpret_cast<TX*>(a.x_out) + (a.x_out ? t * a.ld_xo + c0 : 0);
+  TY* h = reinterpret_cast<TY*>(a.h) + (a.next ? t * a.ld_h + c0 : 0);
+  auto advance = [&] {
+    x += step * a.ld_x;
+    if (has_y) y += step * a.ld_y;
+  };
   auto fetch = [&](long long r, int stage) {
     if (r < a.T) {
-      const TX* xr = x + r * a.ld_x;
-      const TY* yr = y + r * a.ld_y;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + tid) * VEC;
-        if (c >= H) continue;
-        ring_copy<TX>(ring, stage, i * kP, xr + c);
-        if (y) ring_copy<TY>(ring, stage, i * kP + kPX, yr + c);
+        const int o = i * NT * VEC;
+        if (c0 + o >= H) continue;
+        ring_copy<TX>(ring, stage, i * kP, x + o);
+        if (has_y) ring_copy<TY>(ring, stage, i * kP + kPX, y + o);
       }
+      advance();
     }
     cp_async_commit();
   };
@@ -358,15 +366,16 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, false> / kB
       if (c >= H) continue;
       if constexpr (S > 0) {
         ring_load<TX>(ring, stage, i * kP, u[i]);
-        if (y) ring_load<TY>(ring, stage, i * kP + kPX, v[i]);
+        if (has_y) ring_load<TY>(ring, stage, i * kP + kPX, v[i]);
       } else {
-        load_vec(x + t * a.ld_x + c, u[i]);
-        if (y) load_vec(y + t * a.ld_y + c, v[i]);
+        load_vec(x + i * NT * VEC, u[i]);
+        if (has_y) load_vec(y + i * NT * VEC, v[i]);
       }
 #pragma unroll
       for (int j = 0; j < P; ++j) ss = fma(v[i][j], v[i][j], ss);
     }
     if constexpr (S > 0) stage = stage + 1 == S ? 0 : stage + 1;
+    else advance();
     const float r = a.post ? gt * rsqrtf(fmaf(row_sum<NT>(total(ss), red, turn), inv_h, a.eps)) : gt;
     const E r2 = splat<E>(r), alpha = splat<E>(a.alpha);
     ss = splat<E>(0.f);
@@ -377,11 +386,12 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, false> / kB
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         u[i][j] = mul(u[i][j], alpha);
-        if (y) u[i][j] = fma(mul(v[i][j], w[i][j]), r2, u[i][j]);
+        if (has_y) u[i][j] = fma(mul(v[i][j], w[i][j]), r2, u[i][j]);
         ss = fma(u[i][j], u[i][j], ss);
       }
-      if (a.x_out) store_vec(reinterpret_cast<TX*>(a.x_out) + t * a.ld_xo + c, u[i]);
+      if (a.x_out) store_vec(xo + i * NT * VEC, u[i]);
     }
+    if (a.x_out) xo += step * a.ld_xo;
     if (a.next) {
       const E ru = splat<E>(rsqrtf(fmaf(row_sum<NT>(total(ss), red, turn), inv_h, a.eps)));
 #pragma unroll
@@ -390,13 +400,16 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, false> / kB
         if (c >= H) continue;
 #pragma unroll
         for (int j = 0; j < P; ++j) u[i][j] = mul(mul(u[i][j], ru), nx[i][j]);
-        store_vec(reinterpret_cast<TY*>(a.h) + t * a.ld_h + c, u[i]);
+        store_vec(h + i * NT * VEC, u[i]);
       }
+      h += step * a.ld_h;
     }
   }
 }
 
-template <typename TX, typename TY, int VEC, int NV, int NT, int S>
+// FULL: a post norm, a next norm, d_x_out given and no gate per token (a
+// training step's usual call): nothing to ask for in the row loop.
+template <typename TX, typename TY, int VEC, int NV, int NT, int S, bool FULL>
 __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBlock<NT>)
     block_norm_bwd_kernel(const NormArgs a) {
   extern __shared__ uint8_t ring_smem[];
@@ -413,19 +426,34 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
   long long t = (long long)blockIdx.x * kRows + threadIdx.x / NT;
   pdl_wait();
   pdl_launch_dependents();
-  const TX *x = reinterpret_cast<const TX*>(a.x), *du = reinterpret_cast<const TX*>(a.d_xo);
-  const TY *y = reinterpret_cast<const TY*>(a.y), *dh = reinterpret_cast<const TY*>(a.d_h);
+  const bool has_y = FULL || a.y, has_du = FULL || a.d_xo, has_dh = FULL || a.d_h, post = FULL || a.post;
+  const bool token = !FULL && a.gate_mode == MOE_GATE_TOKEN;
+  // this thread's first column in the row to be fetched next, and in the rows written
+  const int c0 = tid * VEC;
+  const TX *x = reinterpret_cast<const TX*>(a.x) + t * a.ld_x + c0;
+  const TX *du = reinterpret_cast<const TX*>(a.d_xo) + (has_du ? t * a.ld_dxo + c0 : 0);
+  const TY *y = reinterpret_cast<const TY*>(a.y) + (has_y ? t * a.ld_y + c0 : 0);
+  const TY *dh = reinterpret_cast<const TY*>(a.d_h) + (has_dh ? t * a.ld_dh + c0 : 0);
+  TX* dx = reinterpret_cast<TX*>(a.d_x) + t * a.ld_dx + c0;
+  TY* dy = reinterpret_cast<TY*>(a.d_y) + (has_y ? t * a.ld_dy + c0 : 0);
+  auto advance = [&] {
+    x += step * a.ld_x;
+    if (has_y) y += step * a.ld_y;
+    if (has_du) du += step * a.ld_dxo;
+    if (has_dh) dh += step * a.ld_dh;
+  };
   auto fetch = [&](long long r, int stage) {
     if (r < a.T) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * NT + tid) * VEC;
-        if (c >= H) continue;
-        ring_copy<TX>(ring, stage, i * kP, x + r * a.ld_x + c);
-        if (y) ring_copy<TY>(ring, stage, i * kP + kPX, y + r * a.ld_y + c);
-        if (du) ring_copy<TX>(ring, stage, i * kP + kPX + kPY, du + r * a.ld_dxo + c);
-        if (dh) ring_copy<TY>(ring, stage, i * kP + 2 * kPX + kPY, dh + r * a.ld_dh + c);
+        const int o = i * NT * VEC;
+        if (c0 + o >= H) continue;
+        ring_copy<TX>(ring, stage, i * kP, x + o);
+        if (has_y) ring_copy<TY>(ring, stage, i * kP + kPX, y + o);
+        if (has_du) ring_copy<TX>(ring, stage, i * kP + kPX + kPY, du + o);
+        if (has_dh) ring_copy<TY>(ring, stage, i * kP + 2 * kPX + kPY, dh + o);
       }
+      advance();
     }
     cp_async_commit();
   };
@@ -446,34 +474,35 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
       fetch(t + (S - 1) * step, (stage + S - 1) % S);
       cp_async_wait<S - 1>();
     }
-    const float gt = a.gate_mode == MOE_GATE_TOKEN ? load_any(a.gate, a.w_dtype, t) : 1.f;
+    const float gt = token ? load_any(a.gate, a.w_dtype, t) : 1.f;
     E ss = splat<E>(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * NT + tid) * VEC;
+      const int o = i * NT * VEC;
 #pragma unroll
       for (int j = 0; j < P; ++j) n[i][j] = u[i][j] = d[i][j] = e[i][j] = splat<E>(0.f);
-      if (c >= H) continue;
+      if (c0 + o >= H) continue;
       if constexpr (S > 0) {
         ring_load<TX>(ring, stage, i * kP, u[i]);
-        if (y) ring_load<TY>(ring, stage, i * kP + kPX, n[i]);
-        if (du) ring_load<TX>(ring, stage, i * kP + kPX + kPY, d[i]);
-        if (dh) ring_load<TY>(ring, stage, i * kP + 2 * kPX + kPY, e[i]);
+        if (has_y) ring_load<TY>(ring, stage, i * kP + kPX, n[i]);
+        if (has_du) ring_load<TX>(ring, stage, i * kP + kPX + kPY, d[i]);
+        if (has_dh) ring_load<TY>(ring, stage, i * kP + 2 * kPX + kPY, e[i]);
       } else {
-        load_vec(x + t * a.ld_x + c, u[i]);
-        if (y) load_vec(y + t * a.ld_y + c, n[i]);
-        if (du) load_vec(du + t * a.ld_dxo + c, d[i]);
-        if (dh) load_vec(dh + t * a.ld_dh + c, e[i]);
+        load_vec(x + o, u[i]);
+        if (has_y) load_vec(y + o, n[i]);
+        if (has_du) load_vec(du + o, d[i]);
+        if (has_dh) load_vec(dh + o, e[i]);
       }
 #pragma unroll
       for (int j = 0; j < P; ++j) ss = fma(n[i][j], n[i][j], ss);
     }
     if constexpr (S > 0) stage = stage + 1 == S ? 0 : stage + 1;
-    const float ry = a.post ? rsqrtf(fmaf(row_sum<NT>(total(ss), red, turn), inv_h, a.eps)) : 1.f;
+    else advance();
+    const float ry = post ? rsqrtf(fmaf(row_sum<NT>(total(ss), red, turn), inv_h, a.eps)) : 1.f;
     E s2[5];   // of q du, u^2, a u, q a, q u
 #pragma unroll
     for (int k = 0; k < 5; ++k) s2[k] = splat<E>(0.f);
-    const E ry2 = splat<E>(y ? ry : 0.f), gt2 = splat<E>(gt), alpha = splat<E>(a.alpha);
+    const E ry2 = splat<E>(has_y ? ry : 0.f), gt2 = splat<E>(gt), alpha = splat<E>(a.alpha);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * NT + tid) * VEC;
@@ -489,7 +518,8 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
       for (int j = 0; j < P; ++j) {
         n[i][j] = mul(n[i][j], ry2);
         const E q = mul(w[j], n[i][j]);
-        u[i][j] = dh ? fma(gt2, q, mul(alpha, u[i][j])) : splat<E>(0.f);   // without h nothing hangs on u
+        u[i][j] = FULL ? fma(alpha, u[i][j], q) : fma(gt2, q, mul(alpha, u[i][j]));
+        if (!has_dh) u[i][j] = splat<E>(0.f);   // without h nothing hangs on u
         s2[0] = fma(q, d[i][j], s2[0]);
         const E av = mul(e[i][j], nx[j]);
         s2[1] = fma(u[i][j], u[i][j], s2[1]);
@@ -502,15 +532,14 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
 #pragma unroll
     for (int k = 0; k < 5; ++k) s[k] = total(s2[k]);
     row_sums5<NT>(s, red, turn);
-    const float ru = dh ? rsqrtf(fmaf(s[1], inv_h, a.eps)) : 0.f;
+    const float ru = has_dh ? rsqrtf(fmaf(s[1], inv_h, a.eps)) : 0.f;
     const float m = ru * ru * s[2] * inv_h;
     const float sd = fmaf(ru, s[3] - m * s[4], s[0]);
-    if (a.d_gate_token && tid == 0) a.d_gate_token[t] = sd;
-    const float my = a.post ? gt * sd * inv_h : 0.f;
-    const E ru2 = splat<E>(ru), mm = splat<E>(-ru * m), mym = splat<E>(-my), ryo = splat<E>(ry);
+    if (token && a.d_gate_token && tid == 0) a.d_gate_token[t] = sd;
+    const E ru2 = splat<E>(ru), mm = splat<E>(-ru * m), mym = splat<E>(-ry * gt * sd * inv_h), ryo = splat<E>(ry);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * NT + tid) * VEC;
+      const int c = (i * NT + tid) * VEC, o = i * NT * VEC;
       if (c >= H) continue;
       E w[P], nx[P];
       if constexpr (kKeep) {
@@ -524,14 +553,17 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
         const E er = mul(e[i][j], ru2);   // dh r_u
         d[i][j] = fma(er, nx[j], fma(u[i][j], mm, d[i][j]));
         acc_n[i][j] = fma(er, u[i][j], acc_n[i][j]);
-        const E g = mul(gt2, d[i][j]);
+        const E g = FULL ? d[i][j] : mul(gt2, d[i][j]);
         acc_e[i][j] = fma(g, n[i][j], acc_e[i][j]);
-        n[i][j] = a.post ? mul(ryo, fma(g, w[j], mul(n[i][j], mym))) : mul(g, w[j]);
+        const E b = mul(g, w[j]);
+        n[i][j] = post ? fma(b, ryo, mul(n[i][j], mym)) : b;
         d[i][j] = mul(d[i][j], alpha);
       }
-      store_vec(reinterpret_cast<TX*>(a.d_x) + t * a.ld_dx + c, d[i]);
-      if (y) store_vec(reinterpret_cast<TY*>(a.d_y) + t * a.ld_dy + c, n[i]);
+      store_vec(dx + o, d[i]);
+      if (has_y) store_vec(dy + o, n[i]);
     }
+    dx += step * a.ld_dx;
+    if (has_y) dy += step * a.ld_dy;
   }
   if (!a.sums) return;
   // the block's column sums: one line of the workspace
@@ -621,17 +653,19 @@ static moe_status launch_norm(const NormArgs& a, bool bwd, int* lines, cudaStrea
     return check_launch("block_norm_kernel");
   }
   constexpr size_t smem = (size_t)SB * NV * 16 * (sizeof(TX) + sizeof(TY)) * kBlock<NT>;
-  auto kernel = block_norm_bwd_kernel<TX, TY, VEC, NV, NT, SB>;
-  static char allowed[64];
-  MOE_CUDA(allow_smem(kernel, smem, allowed));
+  const bool full = VEC == 8 && a.post && a.d_h && a.d_xo && a.gate_mode != MOE_GATE_TOKEN;
+  auto kernel = full ? block_norm_bwd_kernel<TX, TY, VEC, NV, NT, SB, VEC == 8>
+                     : block_norm_bwd_kernel<TX, TY, VEC, NV, NT, SB, false>;
+  static char allowed[2][64];
+  MOE_CUDA(allow_smem(kernel, smem, allowed[full]));
   *lines = bwd_blocks(a.T, kRows, kBlock<NT>);
   cudaError_t e = launch_pdl(kernel, dim3(*lines), dim3(kBlock<NT>), smem, s, a);
   if (e != cudaSuccess) return cuda_fail(e, "block_norm_bwd_kernel");
   return check_launch("block_norm_bwd_kernel");
 }
 
-// The shape a row is held in.  Rows of up to 512 columns take one warp (no
-// barriers at all); longer ones the fewest threads that hold 8 columns each, or
+// The shape a row is held in.  Rows of up to 512 columns (the gradient: 256) take
+// one warp, with no barriers at all; longer ones the fewest threads that hold 8 columns each, or
 // 16 where 8 would take more than 1024 threads (the gradient: 512, so that its
 // two sums of every column keep 128 registers); where rows cannot be read in
 // 16-byte vectors, single elements, 4 to 16 a thread.
@@ -645,7 +679,7 @@ static moe_status norm_by_shape(const NormArgs& a, bool vec, bool bwd, int* line
     return launch_norm<TX, TY, 1, 16, 1024>(a, bwd, lines, s);
   }
   if (H <= 256) return launch_norm<TX, TY, 8, 1, 32>(a, bwd, lines, s);
-  if (H <= 512) return launch_norm<TX, TY, 8, 2, 32>(a, bwd, lines, s);
+  if (H <= 512 && !bwd) return launch_norm<TX, TY, 8, 2, 32>(a, bwd, lines, s);
   if (H <= 1024) return launch_norm<TX, TY, 8, 1, 128>(a, bwd, lines, s);
   if (H <= 2048) return launch_norm<TX, TY, 8, 1, 256>(a, bwd, lines, s);
   if (H <= 4096) return launch_norm<TX, TY, 8, 1, 512>(a, bwd, lines, s);

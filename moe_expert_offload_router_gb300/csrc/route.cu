@@ -3,8 +3,13 @@
 // the gradient of the weights with respect to the logits.
 //
 // One warp per token; lane l holds experts l * VPL .. l * VPL + VPL - 1, so
-// that the lowest lane among equals holds the lowest id.  Each of the k rounds
-// takes the warp-wide maximum key; the lane that holds it drops it.
+// that the lowest lane among equals holds the lowest id.  The k-th largest of
+// the 32 lanes' own maxima bounds the k-th largest key from below: k rounds of a
+// warp maximum find it, the keys that reach it (a few more than k) are packed
+// one to a lane in order of their ids, and k more rounds rank them.  Two rounds
+// of about six instructions a choice, against one that searches VPL registers.
+// Bound by instruction issue: with scores, about 500 instructions a token, a
+// third of them the 256 exponentials and reciprocals that the choice needs to the bit.
 #include <math.h>
 
 #include "dtype.cuh"
@@ -41,128 +46,269 @@ __device__ __forceinline__ float load_logit(const TL* row, int e) {
   return v == v ? v : -INFINITY;
 }
 
-__device__ __forceinline__ float sigmoid_f32(float z) { return __fdiv_rn(1.f, 1.f + expf(-z)); }
+__device__ __forceinline__ float sigmoid_f32(float z) { return __frcp_rn(1.f + expf(-z)); }
 // e^(z - top), also where both are +inf; 0 for z = -inf.
 __device__ __forceinline__ float exp_below(float z, float top) {
   return z == -INFINITY ? 0.f : (z == top ? 1.f : expf(z - top));
 }
 
+// The warp's maximum (no NaN among the values).
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Lane's VPL logits of a row; NaN and what lies past E count as -inf.  `vec`:
+// rows start where a lane's share can be read in one piece (up to 16 bytes).
 template <int VPL, typename TL>
-__global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
-  const int t = (int)((blockIdx.x * (size_t)blockDim.x + threadIdx.x) >> 5);
-  const int lane = threadIdx.x & 31;
-  if (t >= a.T) return;
+__device__ __forceinline__ void load_row(const TL* row, int lane, int E, bool vec, float (&z)[VPL]) {
+  constexpr int kBytes = VPL * (int)sizeof(TL), kPiece = kBytes < 16 ? kBytes : 16;
+  constexpr int kEach = kPiece / (int)sizeof(TL);
+  if (kPiece > 2 && vec && (lane + 1) * VPL <= E) {
+#pragma unroll
+    for (int i = 0; i < kBytes / kPiece; ++i) {
+      alignas(16) TL e[kEach];
+      const TL* p = row + lane * VPL + i * kEach;
+      if constexpr (kPiece == 16) *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
+      else if constexpr (kPiece == 8) *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+      else if constexpr (kPiece == 4) *reinterpret_cast<uint32_t*>(e) = *reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) z[i * kEach + j] = to_f32(e[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) z[i] = lane * VPL + i < E ? to_f32(row[lane * VPL + i]) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) z[i] = z[i] == z[i] ? z[i] : -INFINITY;
+}
+
+constexpr int kRouteWarps = 4;
+
+template <int VPL, typename TL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a, int vec) {
+  extern __shared__ int hist[];   // [E] with a load
+  __shared__ float c_key[kRouteWarps][32];
+  __shared__ int c_id[kRouteWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = a.k, E = a.E;
-  const TL* row = reinterpret_cast<const TL*>(a.logits) + (long long)t * a.ld;
-  int my_id = -1;
-  float top = -INFINITY, den = 0.f;
-  if (!a.mask || a.mask[t]) {
-    float key[VPL];
+  pdl_wait();
+  pdl_launch_dependents();
+  if (a.load) {
+    for (int e = threadIdx.x; e < E; e += kRouteWarps * 32) hist[e] = 0;
+    __syncthreads();
+  }
+  const bool grouped = a.topk_group < a.n_group;
+  const bool scored = a.bias || (grouped && a.group_score == MOE_GROUP_TOP2);
+  const bool whole = a.score == MOE_SCORE_SOFTMAX && (scored || !a.renorm);   // the softmax's denominator is needed
+  const int gs = E / a.n_group;
+  // lanes of a group, where every lane's experts belong to one group
+  const int lpg = gs % VPL == 0 && gs / VPL <= 32 && ((gs / VPL) & (gs / VPL - 1)) == 0 ? gs / VPL : 0;
+  float bias[VPL <= 16 ? VPL : 1];
+  if (VPL <= 16 && a.bias) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
-      key[i] = e < E ? load_logit(row, e) : -INFINITY;
-      top = fmaxf(top, key[i]);
-    }
-    top = warp_max(top);
-    const bool grouped = a.topk_group < a.n_group;
-    const bool scored = a.bias || (grouped && a.group_score == MOE_GROUP_TOP2);
-    if (a.score == MOE_SCORE_SOFTMAX && (scored || !a.renorm)) {
-      // the denominator, over neighbouring pairs: in the lane, then across lanes
-      float ex[VPL];
+    for (int i = 0; i < VPL; ++i) bias[i % (VPL <= 16 ? VPL : 1)] = lane * VPL + i < E ? a.bias[lane * VPL + i] : 0.f;
+  }
+  const long long step = (long long)gridDim.x * kRouteWarps;
+  for (long long t = (long long)blockIdx.x * kRouteWarps + warp; t < a.T; t += step) {
+    const TL* row = reinterpret_cast<const TL*>(a.logits) + t * a.ld;
+    int my_id = -1, my_rank = lane;   // lane holds the my_rank-th choice
+    float top = -INFINITY, den = 0.f;
+    if (!a.mask || a.mask[t]) {
+      float key[VPL];
+      load_row<VPL>(row, lane, E, vec, key);
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) ex[i] = exp_below(key[i], top);
+        for (int i = 0; i < VPL; ++i) top = fmaxf(top, key[i]);
+        top = redux_max(top);
+        // the denominator, over neighbouring pairs: in the lane, then across lanes
+        float ex[VPL];
 #pragma unroll
-      for (int n = VPL / 2; n > 0; n /= 2)
+        for (int i = 0; i < VPL; ++i) ex[i] = exp_below(key[i], top);
 #pragma unroll
-        for (int i = 0; i < n; ++i) ex[i] = ex[2 * i] + ex[2 * i + 1];
-      den = ex[0];
+        for (int n = VPL / 2; n > 0; n /= 2)
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    }
-    float val[VPL];   // what groups are valued by, and the key where there is a bias
+          for (int i = 0; i < n; ++i) ex[i] = ex[2 * i] + ex[2 * i + 1];
+        den = ex[0];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      val[i] = key[i];
-      if (scored && key[i] > -INFINITY) {
-        const float s = a.score == MOE_SCORE_SIGMOID ? sigmoid_f32(key[i]) : __fdiv_rn(exp_below(key[i], top), den);
-        val[i] = a.bias ? s + a.bias[lane * VPL + i] : s;
-        if (a.bias) key[i] = val[i];
+        for (int o = 1; o < 32; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
       }
-    }
-    if (grouped) {
-      const int gs = E / a.n_group;
-      float worth = -INFINITY;   // of group `lane`
-      for (int g = 0; g < a.n_group; ++g) {
-        float m1 = -INFINITY, m2 = -INFINITY;
+      float m1 = -INFINITY, m2 = -INFINITY;   // the lane's two largest group values
+      auto value = [&](int i) {               // what groups are valued by; the key, where there is a bias
+        float v = key[i];
+        if (scored && v > -INFINITY) {
+          v = a.score == MOE_SCORE_SIGMOID ? sigmoid_f32(v) : __fdiv_rn(exp_below(v, top), den);
+          if (a.bias) v += VPL <= 16 ? bias[i % (VPL <= 16 ? VPL : 1)] : a.bias[lane * VPL + i];
+        }
+        return v;
+      };
+      if (lpg) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-          const int e = lane * VPL + i;
-          if (e >= g * gs && e < (g + 1) * gs) {
-            m2 = fmaxf(m2, fminf(m1, val[i]));
-            m1 = fmaxf(m1, val[i]);
+          const float v = scored ? value(i) : key[i];
+          m2 = fmaxf(m2, fminf(m1, v));
+          m1 = fmaxf(m1, v);
+          if (a.bias) key[i] = v;
+        }
+      } else {
+        float val[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) val[i] = scored ? value(i) : key[i];
+        if (grouped) {   // groups that do not end with a lane: one after the other
+          float worth = -INFINITY;
+          for (int g = 0; g < a.n_group; ++g) {
+            float p1 = -INFINITY, p2 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+              const int e = lane * VPL + i;
+              if (e >= g * gs && e < (g + 1) * gs) {
+                p2 = fmaxf(p2, fminf(p1, val[i]));
+                p1 = fmaxf(p1, val[i]);
+              }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              const float o1 = __shfl_xor_sync(0xffffffffu, p1, o), o2 = __shfl_xor_sync(0xffffffffu, p2, o);
+              p2 = fmaxf(fminf(p1, o1), fmaxf(p2, o2));
+              p1 = fmaxf(p1, o1);
+            }
+            if (lane == g) worth = a.group_score == MOE_GROUP_MAX || p2 == -INFINITY ? p1 : p1 + p2;
+          }
+          m1 = worth;
+        }
+        if (a.bias) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) key[i] = val[i];
+        }
+      }
+      if (grouped) {
+        if (lpg) {
+          for (int o = 1; o < lpg; o <<= 1) {
+            const float o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
+            m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+            m1 = fmaxf(m1, o1);
+          }
+          if (a.group_score == MOE_GROUP_TOP2 && m2 > -INFINITY) m1 += m2;
+          m1 = __shfl_sync(0xffffffffu, m1, lane * lpg & 31);   // lane g: the worth of group g
+        }
+        // a group's place: how many are worth more, or as much with a lower index
+        uint32_t keep = 0;
+        float left = lane < a.n_group ? m1 : -INFINITY;
+        for (int j = 0; j < a.topk_group; ++j) {
+          const float m = redux_max(left);
+          if (!(m > -INFINITY)) break;
+          const int win = __ffs(__ballot_sync(0xffffffffu, left == m)) - 1;
+          keep |= 1u << win;
+          if (lane == win) left = -INFINITY;
+        }
+        if (lpg) {
+          const bool in = keep >> (lane / lpg) & 1;
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) key[i] = in ? key[i] : -INFINITY;
+        } else {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) {
+            const int e = lane * VPL + i;
+            if (e < E && !(keep >> (e / gs) & 1)) key[i] = -INFINITY;
           }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const float o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
-          m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
-          m1 = fmaxf(m1, o1);
-        }
-        if (lane == g) worth = a.group_score == MOE_GROUP_MAX || m2 == -INFINITY ? m1 : m1 + m2;
       }
-      int rank = 0;
-      for (int g = 0; g < a.n_group; ++g) {
-        const float o = __shfl_sync(0xffffffffu, worth, g);
-        rank += o > worth || (o == worth && g < lane);
-      }
-      const uint32_t keep = __ballot_sync(0xffffffffu, lane < a.n_group && rank < a.topk_group);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        if (e < E && !((keep >> (e / gs)) & 1)) key[i] = -INFINITY;
-      }
-    }
-    for (int j = 0; j < k; ++j) {
+      // the k-th largest of the lanes' maxima
       float best = key[0];
 #pragma unroll
       for (int i = 1; i < VPL; ++i) best = fmaxf(best, key[i]);
-      const float m = warp_max(best);
-      if (!(m > -INFINITY)) break;
-      const int win = __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
-      int id = 0;
-      if (lane == win) {
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (!found && key[i] == m) {
-            found = true;
-            id = lane * VPL + i;
-            key[i] = -INFINITY;
-          }
+      float least = -INFINITY;
+      for (int j = 0; j < k; ++j) {
+        least = redux_max(best);
+        if (!(least > -INFINITY)) break;
+        const int win = __ffs(__ballot_sync(0xffffffffu, best == least)) - 1;
+        if (lane == win) best = -INFINITY;
       }
-      id = __shfl_sync(0xffffffffu, id, win);
-      if (lane == j) my_id = id;
+      // the keys that reach it, packed in order of their ids
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) n += key[i] >= least && key[i] > -INFINITY;
+      int at = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+      }
+      const int all = __shfl_sync(0xffffffffu, at, 31);
+      at -= n;
+      if (all <= 32) {
+        if (n) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (key[i] >= least && key[i] > -INFINITY) {
+              c_key[warp][at] = key[i];
+              c_id[warp][at++] = lane * VPL + i;
+            }
+        }
+        __syncwarp();
+        float mine = lane < all ? c_key[warp][lane] : -INFINITY;
+        const int id = lane < all ? c_id[warp][lane] : -1;
+        __syncwarp();
+        const int most = all < k ? all : k;
+        int rank = -1;
+        for (int j = 0; j < most; ++j) {
+          const float m = redux_max(mine);
+          const int win = __ffs(__ballot_sync(0xffffffffu, mine == m)) - 1;
+          if (lane == win) rank = j, mine = -INFINITY;
+        }
+        // places past the last choice go to lanes without one, in order
+        const uint32_t free = __ballot_sync(0xffffffffu, rank < 0);
+        my_rank = rank >= 0 ? rank : most + __popc(free & ((1u << lane) - 1));
+        my_id = rank >= 0 ? id : -1;
+      } else {   // many equal keys, or a k near 32: round by round over all of them
+        for (int j = 0; j < k; ++j) {
+          float b = key[0];
+#pragma unroll
+          for (int i = 1; i < VPL; ++i) b = fmaxf(b, key[i]);
+          const float m = redux_max(b);
+          if (!(m > -INFINITY)) break;
+          const int win = __ffs(__ballot_sync(0xffffffffu, b == m)) - 1;
+          int id = 0;
+          if (lane == win) {
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+              if (!found && key[i] == m) {
+                found = true;
+                id = lane * VPL + i;
+                key[i] = -INFINITY;
+              }
+          }
+          id = __shfl_sync(0xffffffffu, id, win);
+          if (lane == j) my_id = id;
+        }
+      }
+    }
+    // weights, each lane its own choice's
+    const float z = my_id >= 0 ? load_logit(row, my_id) : -INFINITY;
+    float s;
+    if (a.score == MOE_SCORE_SIGMOID) {
+      s = my_id >= 0 ? sigmoid_f32(z) : 0.f;
+    } else if (a.renorm) {
+      s = exp_below(z, redux_max(z));
+    } else {
+      s = my_id >= 0 ? __fdiv_rn(exp_below(z, top), den) : 0.f;
+    }
+    if (a.renorm) {
+      const float sum = warp_sum(s);
+      s = sum > 0.f ? s / sum : 0.f;
+    }
+    if (my_rank < k) {
+      a.ids[t * k + my_rank] = my_id;
+      a.w[t * k + my_rank] = a.scale * s;
+      if (a.load && my_id >= 0) atomicAdd(hist + my_id, 1);
     }
   }
-  // weights: lane j holds the j-th choice
-  const float z = my_id >= 0 ? load_logit(row, my_id) : -INFINITY;
-  float s;
-  if (a.score == MOE_SCORE_SIGMOID) {
-    s = my_id >= 0 ? sigmoid_f32(z) : 0.f;
-  } else if (a.renorm) {
-    s = exp_below(z, warp_max(z));
-  } else {
-    s = my_id >= 0 ? __fdiv_rn(exp_below(z, top), den) : 0.f;
-  }
-  if (a.renorm) {
-    const float sum = warp_sum(s);
-    s = sum > 0.f ? s / sum : 0.f;
-  }
-  if (lane < k) {
-    a.ids[(long long)t * k + lane] = my_id;
-    a.w[(long long)t * k + lane] = a.scale * s;
-    if (a.load && my_id >= 0) atomicAdd(a.load + my_id, 1);
+  if (a.load) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kRouteWarps * 32)
+      if (hist[e]) atomicAdd(a.load + e, hist[e]);
   }
 }
 
@@ -178,60 +324,81 @@ struct RouteBwdArgs {
   long long ld_d;
 };
 
+// One warp per token: the row is written first (zeros, or the plain softmax's
+// own term), then the chosen experts' values over it.  Bound by the T * E
+// elements written.  `vec`: rows and their length allow 16-byte stores.
 template <typename TL>
-__global__ void __launch_bounds__(128) route_bwd_kernel(const RouteBwdArgs a) {
-  const int t = (int)((blockIdx.x * (size_t)blockDim.x + threadIdx.x) >> 5);
+__global__ void __launch_bounds__(128) route_bwd_kernel(const RouteBwdArgs a, int vec) {
   const int lane = threadIdx.x & 31;
-  if (t >= a.T) return;
-  const TL* row = reinterpret_cast<const TL*>(a.logits) + (long long)t * a.ld;
-  TL* d = reinterpret_cast<TL*>(a.d) + (long long)t * a.ld_d;
-  int id = -1;
-  float g = 0.f, z = -INFINITY;
-  if (lane < a.k && (!a.mask || a.mask[t])) {
-    id = a.ids[(long long)t * a.k + lane];
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long step = gridDim.x * 4LL;
+  for (long long t = blockIdx.x * 4LL + (threadIdx.x >> 5); t < a.T; t += step) {
+    const TL* row = reinterpret_cast<const TL*>(a.logits) + t * a.ld;
+    TL* d = reinterpret_cast<TL*>(a.d) + t * a.ld_d;
+    const bool on = !a.mask || a.mask[t];
+    int id = -1;
+    float g = 0.f, z = -INFINITY;
+    if (lane < a.k && on) {
+      id = a.ids[t * a.k + lane];
+      g = a.scale * a.dw[t * a.k + lane];
+    }
+    const bool dense = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
+    if (!dense) {   // while the ids are on their way
+      if (vec) {
+        constexpr int kEach = 16 / (int)sizeof(TL);
+        for (int e = lane * kEach; e < a.E; e += 32 * kEach)
+          *reinterpret_cast<uint4*>(d + e) = make_uint4(0, 0, 0, 0);
+      } else {
+        for (int e = lane; e < a.E; e += 32) d[e] = from_f32<TL>(0.f);
+      }
+    }
     if (id >= 0 && id < a.E) z = load_logit(row, id);
-    if (z > -INFINITY) g = a.scale * a.dw[(long long)t * a.k + lane];
-    else id = -1;
-  }
-  float dj;
-  if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) {
-    float top = -INFINITY, den = 0.f;
-    if (!a.mask || a.mask[t]) {
-      for (int e = lane; e < a.E; e += 32) top = fmaxf(top, load_logit(row, e));
-      top = warp_max(top);
-      for (int e = lane; e < a.E; e += 32) den += exp_below(load_logit(row, e), top);
-      den = warp_sum(den);
-    }
-    const float p = id >= 0 ? exp_below(z, top) / den : 0.f;
-    const float mean = warp_sum(g * p);
-    dj = p * (g - mean);
-    for (int e = lane; e < a.E; e += 32)
-      d[e] = from_f32<TL>(den > 0.f ? -mean * (exp_below(load_logit(row, e), top) / den) : 0.f);
-  } else {
-    float q, c = 1.f;
-    if (a.score == MOE_SCORE_SIGMOID) {
-      q = id >= 0 ? sigmoid_f32(z) : 0.f;
-      c = id >= 0 ? sigmoid_f32(-z) : 0.f;   // 1 - s without the cancellation
+    if (!(z > -INFINITY)) id = -1, g = 0.f;
+    float dj;
+    if (dense) {
+      float top = -INFINITY, den = 0.f;
+      if (on) {
+        for (int e = lane; e < a.E; e += 32) top = fmaxf(top, load_logit(row, e));
+        top = warp_max(top);
+        for (int e = lane; e < a.E; e += 32) den += exp_below(load_logit(row, e), top);
+        den = warp_sum(den);
+      }
+      const float p = id >= 0 ? exp_below(z, top) / den : 0.f;
+      const float mean = warp_sum(g * p);
+      dj = p * (g - mean);
+      for (int e = lane; e < a.E; e += 32)
+        d[e] = from_f32<TL>(den > 0.f ? -mean * (exp_below(load_logit(row, e), top) / den) : 0.f);
     } else {
-      q = exp_below(z, warp_max(z));
+      float q, c = 1.f;
+      if (a.score == MOE_SCORE_SIGMOID) {
+        q = id >= 0 ? sigmoid_f32(z) : 0.f;
+        c = id >= 0 ? sigmoid_f32(-z) : 0.f;   // 1 - s without the cancellation
+      } else {
+        q = exp_below(z, warp_max(z));
+      }
+      float mean = 0.f;
+      if (a.renorm) {
+        const float sum = warp_sum(q);
+        q = sum > 0.f ? q / sum : 0.f;
+        mean = warp_sum(q * g);
+      }
+      dj = q * c * (g - mean);
     }
-    float mean = 0.f;
-    if (a.renorm) {
-      const float sum = warp_sum(q);
-      q = sum > 0.f ? q / sum : 0.f;
-      mean = warp_sum(q * g);
-    }
-    dj = q * c * (g - mean);
-    for (int e = lane; e < a.E; e += 32) d[e] = from_f32<TL>(0.f);
+    __syncwarp();   // the row is written before the chosen experts' values
+    if (id >= 0) d[id] = from_f32<TL>(dj);
   }
-  __syncwarp();   // the row is written before the chosen experts' values
-  if (id >= 0) d[id] = from_f32<TL>(dj);
 }
 
 template <int VPL, typename TL>
 static moe_status launch_route(const RouteArgs& a, cudaStream_t s) {
+  constexpr int kBytes = VPL * (int)sizeof(TL), kPiece = kBytes < 16 ? kBytes : 16;
+  const int vec = (uintptr_t)a.logits % kPiece == 0 && a.ld * (long long)sizeof(TL) % kPiece == 0;
+  const long long need = ((long long)a.T + kRouteWarps - 1) / kRouteWarps, most = device_sms() * 8LL;
   ProfScope ps(MOE_K_ROUTE, s);
-  route_kernel<VPL, TL><<<(unsigned)((a.T + 3LL) / 4), 128, 0, s>>>(a);
+  cudaError_t e = launch_pdl(route_kernel<VPL, TL>, dim3((unsigned)(need < most ? need : most)),
+                             dim3(kRouteWarps * 32), a.load ? a.E * sizeof(int) : 0, s, a, vec);
+  if (e != cudaSuccess) return cuda_fail(e, "route_kernel");
   return check_launch("route_kernel");
 }
 
@@ -294,10 +461,14 @@ extern "C" moe_status moe_route_backward(const void* logits, int dtype, int64_t 
   MOE_ARG(d_logits != logits, "d_logits must not be the logits");
   const RouteBwdArgs a{logits, ld_logits, T, E, k, score, renorm, scale, token_mask, topk_ids, d_w, d_logits,
                        ld_d_logits};
-  const unsigned grid = (unsigned)((T + 3LL) / 4);
+  const long long need = (T + 3LL) / 4, most = device_sms() * 16LL;
+  const dim3 grid((unsigned)(need < most ? need : most)), block(128);
+  const int size = (int)dtype_size(dtype);
+  const int vec = (uintptr_t)d_logits % 16 == 0 && ld_d_logits * size % 16 == 0 && E * size % 16 == 0;
   ProfScope ps(MOE_K_ROUTE_BWD, stream);
-  if (dtype == MOE_DT_F32) route_bwd_kernel<float><<<grid, 128, 0, stream>>>(a);
-  else if (dtype == MOE_DT_BF16) route_bwd_kernel<__nv_bfloat16><<<grid, 128, 0, stream>>>(a);
-  else route_bwd_kernel<__half><<<grid, 128, 0, stream>>>(a);
+  cudaError_t e = dtype == MOE_DT_F32    ? launch_pdl(route_bwd_kernel<float>, grid, block, 0, stream, a, vec)
+                  : dtype == MOE_DT_BF16 ? launch_pdl(route_bwd_kernel<__nv_bfloat16>, grid, block, 0, stream, a, vec)
+                                         : launch_pdl(route_bwd_kernel<__half>, grid, block, 0, stream, a, vec);
+  if (e != cudaSuccess) return cuda_fail(e, "route_bwd_kernel");
   return check_launch("route_bwd_kernel");
 }

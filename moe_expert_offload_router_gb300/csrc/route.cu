@@ -4,12 +4,10 @@
 //
 // One warp per token; lane l holds experts l * VPL .. l * VPL + VPL - 1, so
 // that the lowest lane among equals holds the lowest id.  The k-th largest of
-// the 32 lanes' own maxima bounds the k-th largest key from below: k rounds of a
-// warp maximum find it, the keys that reach it (a few more than k) are packed
-// one to a lane in order of their ids, and k more rounds rank them.  Two rounds
-// of about six instructions a choice, against one that searches VPL registers.
-// Bound by instruction issue: with scores, about 500 instructions a token, a
-// third of them the 256 exponentials and reciprocals that the choice needs to the bit.
+// the 32 lanes' own maxima bounds the k-th largest key from below: k warp maxima
+// (redux) find it, the keys that reach it (a few more than k) are packed one to a
+// lane in order of their ids, and each counts those that go before it.
+#include <float.h>
 #include <math.h>
 
 #include "dtype.cuh"
@@ -81,15 +79,58 @@ __device__ __forceinline__ void load_row(const TL* row, int lane, int E, bool ve
     for (int i = 0; i < VPL; ++i) z[i] = lane * VPL + i < E ? to_f32(row[lane * VPL + i]) : -INFINITY;
   }
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) z[i] = z[i] == z[i] ? z[i] : -INFINITY;
+  for (int i = 0; i < VPL; ++i) z[i] = fmaxf(z[i], -INFINITY);   // NaN: the other operand
+}
+
+// Lane g: what group g (of n_group times gs experts) is worth.  `lpg`: the lanes
+// of a group, where a lane's experts belong to one group and a group's lanes are
+// a power of two; else 0, and the groups are taken one after the other.
+template <int VPL>
+__device__ __forceinline__ float group_worth(const float (&val)[VPL], int lane, int E, int gs, int n_group, int lpg,
+                                             int how) {
+  float m1 = -INFINITY, m2 = -INFINITY;   // the two largest
+  auto join = [&](int o) {
+    const float o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
+    m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+    m1 = fmaxf(m1, o1);
+  };
+  if (lpg) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      m2 = fmaxf(m2, fminf(m1, val[i]));
+      m1 = fmaxf(m1, val[i]);
+    }
+    for (int o = 1; o < lpg; o <<= 1) join(o);
+    if (how == MOE_GROUP_TOP2 && m2 > -INFINITY) m1 += m2;
+    return __shfl_sync(0xffffffffu, m1, lane * lpg & 31);
+  }
+  float worth = -INFINITY;
+  for (int g = 0; g < n_group; ++g) {
+    m1 = m2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane * VPL + i;
+      if (e >= g * gs && e < (g + 1) * gs) {
+        m2 = fmaxf(m2, fminf(m1, val[i]));
+        m1 = fmaxf(m1, val[i]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) join(o);
+    if (lane == g) worth = how == MOE_GROUP_TOP2 && m2 > -INFINITY ? m1 + m2 : m1;
+  }
+  return worth;
 }
 
 constexpr int kRouteWarps = 4;
+// Blocks an SM holds at once (64 to 168 registers a thread): the grid is that many times the SMs.
+template <int VPL>
+constexpr int kRouteBlocks = VPL <= 8 ? 8 : VPL == 16 ? 5 : 3;
 
 template <int VPL, typename TL>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a, int vec) {
+__global__ void __launch_bounds__(kRouteWarps * 32, kRouteBlocks<VPL>) route_kernel(const RouteArgs a, int vec) {
   extern __shared__ int hist[];   // [E] with a load
-  __shared__ float c_key[kRouteWarps][32];
+  __shared__ alignas(16) float c_key[kRouteWarps][32];
   __shared__ int c_id[kRouteWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = a.k, E = a.E;
@@ -134,70 +175,36 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
       }
-      float m1 = -INFINITY, m2 = -INFINITY;   // the lane's two largest group values
-      auto value = [&](int i) {               // what groups are valued by; the key, where there is a bias
-        float v = key[i];
-        if (scored && v > -INFINITY) {
-          v = a.score == MOE_SCORE_SIGMOID ? sigmoid_f32(v) : __fdiv_rn(exp_below(v, top), den);
-          if (a.bias) v += VPL <= 16 ? bias[i % (VPL <= 16 ? VPL : 1)] : a.bias[lane * VPL + i];
-        }
-        return v;
-      };
-      if (lpg) {
+      float m1 = -INFINITY;   // lane g: what group g is worth
+      if (scored) {
+        float val[VPL];   // what groups are valued by; the key, where there is a bias
+        if (a.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const float v = scored ? value(i) : key[i];
-          m2 = fmaxf(m2, fminf(m1, v));
-          m1 = fmaxf(m1, v);
-          if (a.bias) key[i] = v;
-        }
-      } else {
-        float val[VPL];
+          for (int i = 0; i < VPL; ++i) val[i] = sigmoid_f32(key[i]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) val[i] = scored ? value(i) : key[i];
-        if (grouped) {   // groups that do not end with a lane: one after the other
-          float worth = -INFINITY;
-          for (int g = 0; g < a.n_group; ++g) {
-            float p1 = -INFINITY, p2 = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-              const int e = lane * VPL + i;
-              if (e >= g * gs && e < (g + 1) * gs) {
-                p2 = fmaxf(p2, fminf(p1, val[i]));
-                p1 = fmaxf(p1, val[i]);
-              }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              const float o1 = __shfl_xor_sync(0xffffffffu, p1, o), o2 = __shfl_xor_sync(0xffffffffu, p2, o);
-              p2 = fmaxf(fminf(p1, o1), fmaxf(p2, o2));
-              p1 = fmaxf(p1, o1);
-            }
-            if (lane == g) worth = a.group_score == MOE_GROUP_MAX || p2 == -INFINITY ? p1 : p1 + p2;
-          }
-          m1 = worth;
+          for (int i = 0; i < VPL; ++i) val[i] = __fdiv_rn(exp_below(key[i], top), den);
         }
         if (a.bias) {
 #pragma unroll
-          for (int i = 0; i < VPL; ++i) key[i] = val[i];
+          for (int i = 0; i < VPL; ++i)
+            val[i] += VPL <= 16 ? bias[i % (VPL <= 16 ? VPL : 1)] : (lane * VPL + i < E ? a.bias[lane * VPL + i] : 0.f);
         }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          val[i] = key[i] > -INFINITY ? val[i] : -INFINITY;
+          if (a.bias) key[i] = val[i];
+        }
+        if (grouped) m1 = group_worth<VPL>(val, lane, E, gs, a.n_group, lpg, a.group_score);
+      } else if (grouped) {
+        m1 = group_worth<VPL>(key, lane, E, gs, a.n_group, lpg, a.group_score);
       }
       if (grouped) {
-        if (lpg) {
-          for (int o = 1; o < lpg; o <<= 1) {
-            const float o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
-            m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
-            m1 = fmaxf(m1, o1);
-          }
-          if (a.group_score == MOE_GROUP_TOP2 && m2 > -INFINITY) m1 += m2;
-          m1 = __shfl_sync(0xffffffffu, m1, lane * lpg & 31);   // lane g: the worth of group g
-        }
-        // a group's place: how many are worth more, or as much with a lower index
+        // the topk_group largest, ties to the lower group; an empty group among them holds no key
         uint32_t keep = 0;
         float left = lane < a.n_group ? m1 : -INFINITY;
         for (int j = 0; j < a.topk_group; ++j) {
           const float m = redux_max(left);
-          if (!(m > -INFINITY)) break;
           const int win = __ffs(__ballot_sync(0xffffffffu, left == m)) - 1;
           keep |= 1u << win;
           if (lane == win) left = -INFINITY;
@@ -214,21 +221,21 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
           }
         }
       }
-      // the k-th largest of the lanes' maxima
+      // a bound: the k-th largest of the lanes' maxima (lower yet where some are equal)
       float best = key[0];
 #pragma unroll
       for (int i = 1; i < VPL; ++i) best = fmaxf(best, key[i]);
       float least = -INFINITY;
+#pragma unroll 4
       for (int j = 0; j < k; ++j) {
         least = redux_max(best);
-        if (!(least > -INFINITY)) break;
-        const int win = __ffs(__ballot_sync(0xffffffffu, best == least)) - 1;
-        if (lane == win) best = -INFINITY;
+        best = best == least ? -INFINITY : best;
       }
+      least = fmaxf(least, -FLT_MAX);   // what is -inf is not eligible
       // the keys that reach it, packed in order of their ids
       int n = 0;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) n += key[i] >= least && key[i] > -INFINITY;
+      for (int i = 0; i < VPL; ++i) n += key[i] >= least;
       int at = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -238,29 +245,30 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
       const int all = __shfl_sync(0xffffffffu, at, 31);
       at -= n;
       if (all <= 32) {
+        c_key[warp][lane] = -INFINITY;
+        __syncwarp();
         if (n) {
 #pragma unroll
           for (int i = 0; i < VPL; ++i)
-            if (key[i] >= least && key[i] > -INFINITY) {
+            if (key[i] >= least) {
               c_key[warp][at] = key[i];
               c_id[warp][at++] = lane * VPL + i;
             }
         }
         __syncwarp();
-        float mine = lane < all ? c_key[warp][lane] : -INFINITY;
-        const int id = lane < all ? c_id[warp][lane] : -1;
-        __syncwarp();
-        const int most = all < k ? all : k;
-        int rank = -1;
-        for (int j = 0; j < most; ++j) {
-          const float m = redux_max(mine);
-          const int win = __ffs(__ballot_sync(0xffffffffu, mine == m)) - 1;
-          if (lane == win) rank = j, mine = -INFINITY;
+        // a candidate's place: how many are larger, or equal with a lower id
+        const float mine = c_key[warp][lane];
+        const int id = c_id[warp][lane];
+        int rank = 0;
+        for (int i = 0; i < all; i += 4) {
+          const float4 o = *reinterpret_cast<const float4*>(&c_key[warp][i]);
+          rank += (o.x > mine || (o.x == mine && i < lane)) + (o.y > mine || (o.y == mine && i + 1 < lane)) +
+                  (o.z > mine || (o.z == mine && i + 2 < lane)) + (o.w > mine || (o.w == mine && i + 3 < lane));
         }
-        // places past the last choice go to lanes without one, in order
-        const uint32_t free = __ballot_sync(0xffffffffu, rank < 0);
-        my_rank = rank >= 0 ? rank : most + __popc(free & ((1u << lane) - 1));
-        my_id = rank >= 0 ? id : -1;
+        __syncwarp();
+        // lanes without a candidate take the places after the last one, in order
+        my_rank = lane < all ? rank : lane;
+        my_id = lane < all && rank < k ? id : -1;
       } else {   // many equal keys, or a k near 32: round by round over all of them
         for (int j = 0; j < k; ++j) {
           float b = key[0];
@@ -394,7 +402,7 @@ template <int VPL, typename TL>
 static moe_status launch_route(const RouteArgs& a, cudaStream_t s) {
   constexpr int kBytes = VPL * (int)sizeof(TL), kPiece = kBytes < 16 ? kBytes : 16;
   const int vec = (uintptr_t)a.logits % kPiece == 0 && a.ld * (long long)sizeof(TL) % kPiece == 0;
-  const long long need = ((long long)a.T + kRouteWarps - 1) / kRouteWarps, most = device_sms() * 8LL;
+  const long long need = ((long long)a.T + kRouteWarps - 1) / kRouteWarps, most = device_sms() * (long long)kRouteBlocks<VPL>;
   ProfScope ps(MOE_K_ROUTE, s);
   cudaError_t e = launch_pdl(route_kernel<VPL, TL>, dim3((unsigned)(need < most ? need : most)),
                              dim3(kRouteWarps * 32), a.load ? a.E * sizeof(int) : 0, s, a, vec);

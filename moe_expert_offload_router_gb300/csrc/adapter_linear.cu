@@ -26,9 +26,13 @@ struct LinearArgs {
   const int32_t* ids;
   const float* scale;
   void* out;
-  float* u;
+  float* u;            // [T, R]
+  void *u_hi, *u_lo;   // [T, R] of x's type: u's leading bits and the next ones (large batches)
+  int32_t* group;      // [T / 16] (large batches): the adapter that 16 tokens share, -1: none, or kMixed
   int32_t* err;
 };
+
+constexpr int kMixed = -2;   // a group of 16 tokens whose adapters go token by token
 
 template <typename TE>
 struct Pair;   // two packed elements as fp32
@@ -139,6 +143,8 @@ __global__ void __launch_bounds__(256) adapter_mma_kernel(const LinearArgs a) {
   bool first = lane < 16 && mine >= 0;
   for (int i = 0; i < (lane & 15); ++i) first = first && s_id[i] != mine;
   uint32_t todo = __ballot_sync(0xffffffffu, first);   // the tokens that name an adapter first
+  const bool alone = todo && !(todo & (todo - 1));   // one adapter in the group: its block says how it is used
+  if (a.group && !alone && blockIdx.y == 0 && threadIdx.x == 0) a.group[blockIdx.x] = todo ? kMixed : -1;
   for (int i = 0; i < (int)blockIdx.y; ++i) todo &= todo - 1;
   const TE* x = reinterpret_cast<const TE*>(a.x);
   const int ta = t0 + g < a.T ? t0 + g : a.T - 1, tb = t0 + g + 8 < a.T ? t0 + g + 8 : a.T - 1;
@@ -172,13 +178,29 @@ __global__ void __launch_bounds__(256) adapter_mma_kernel(const LinearArgs a) {
     }
     __syncthreads();
     const float sc = a.scale ? a.scale[id] : 1.f;
+    bool fits = true;
     for (int i = threadIdx.x; i < 16 * a.R; i += 256) {
       const int t = i / a.R;
       if (s_id[t] != id) continue;
       float s = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) s += red[w * 16 * a.R + i];
-      a.u[(long long)t0 * a.R + i] = sc * s;
+      s *= sc;
+      const long long at = (long long)t0 * a.R + i;
+      a.u[at] = s;
+      if (a.group) {
+        const TE hi = from_f32<TE>(s);
+        reinterpret_cast<TE*>(a.u_hi)[at] = hi;
+        reinterpret_cast<TE*>(a.u_lo)[at] = from_f32<TE>(s - to_f32(hi));
+        fits = fits && (sizeof(TE) != 2 || std::is_same<TE, __nv_bfloat16>::value || fabsf(s) < 32768.f);
+      }
+    }
+    // shared by all 16 (a last group's missing tokens aside) and within the type's range
+    if (a.group && alone) {
+      const int last = a.T - t0 < 16 ? a.T - t0 : 16;
+      const bool same = lane >= last || s_id[lane & 15] == id;
+      const bool shared = __syncthreads_and(fits && same);
+      if (threadIdx.x == 0) a.group[blockIdx.x] = shared ? id : kMixed;
     }
     for (int i = 0; i < (int)gridDim.y && todo; ++i) todo &= todo - 1;
   }
@@ -228,7 +250,7 @@ constexpr int kATile = kRows * 128; // bytes of a 64-wide K step of W
 template <int NT>
 struct SplitCfg {
   static constexpr int kStage = kATile + NT * 128;
-  static constexpr int kStages = NT <= 64 ? 8 : NT == 128 ? 6 : 4;
+  static constexpr int kStages = NT <= 64 ? 8 : 6;
   static constexpr int kSmem = kStages * kStage + 1024;
   static constexpr int kCols = NT < 32 ? 32 : NT;
   static_assert(NT * kRows * 4 <= kStages * kStage, "the partial sums fit the stages");
@@ -256,6 +278,27 @@ __device__ __forceinline__ void add_adapter4(const LinearArgs& a, int id, long l
       acc[j] += s;
     }
   }
+}
+
+// B[a][n] . u[t] in fp32.
+template <typename TE>
+__device__ __noinline__ float adapter_dot(const LinearArgs& a, int id, long long t, int n) {
+  const float4* u = reinterpret_cast<const float4*>(a.u + t * a.R);
+  const TE* B = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + n) * a.R;
+  float s = 0.f;
+  for (int r = 0; r < a.R; r += 8) {
+    const float4 u0 = u[r / 4], u1 = u[r / 4 + 1];
+    const uint4 b = *reinterpret_cast<const uint4*>(B + r);
+    float2 p = Pair<TE>::f32(b.x);
+    s = fmaf(p.x, u0.x, fmaf(p.y, u0.y, s));
+    p = Pair<TE>::f32(b.y);
+    s = fmaf(p.x, u0.z, fmaf(p.y, u0.w, s));
+    p = Pair<TE>::f32(b.z);
+    s = fmaf(p.x, u1.x, fmaf(p.y, u1.y, s));
+    p = Pair<TE>::f32(b.w);
+    s = fmaf(p.x, u1.z, fmaf(p.y, u1.w, s));
+  }
+  return s;
 }
 
 template <typename TE>
@@ -394,6 +437,222 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
   if (cs > 1) cluster_sync();   // the others have read this block's sums
 }
 
+// Large batches: persistent blocks, one per SM, over tiles of 128 outputs x NT
+// tokens (NT <= 256, a multiple of 16).  Warp 0 brings 64-wide K steps of W and x
+// by TMA into a ring, warp 1 multiplies, eight warps empty the accumulators: two
+// of 256 columns, so a tile's epilogue runs under the next tile's steps.
+//
+// A tensor-core accumulator loses a little with every step (it truncates), so a
+// result kept in fp32 takes at most `chunk` steps in one accumulator; the epilogue
+// adds the chunks up in registers, in order.
+//
+// Adapters: tokens come in groups of 16.  A run of groups that share one adapter
+// gets more K steps at the end of its tile, over that run's columns alone: B[a]
+// times u's leading bits, and B[a] times the next ones (two terms of 16-bit type:
+// 16 significand bits of u with bf16, 22 with f16).  A group of several adapters
+// is done token by token in the epilogue with u in fp32.
+constexpr int kStreamStages = 4;
+constexpr int kStreamStage = kATile + 256 * 128;
+constexpr int kStreamSmem = kStreamStages * kStreamStage + 1024;
+constexpr int kStreamThreads = 320;   // TMA, MMA, eight epilogue warps
+constexpr int kF32Chunk = 8;          // K steps in one accumulator for fp32 results: 512 products a sum
+
+// One K = 16 step by one elected lane of a converged warp.
+__device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+struct StreamPlan {
+  int nt, tiles_n, tiles, nk, chunk;   // tokens of a tile, tiles of outputs, all tiles, K steps, K steps of an accumulator
+};
+
+template <typename TE>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    linear_stream_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
+                         const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mH,
+                         const __grid_constant__ CUtensorMap mL, const LinearArgs a, const StreamPlan pl) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ alignas(8) uint64_t full[kStreamStages], empty[kStreamStages], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_err;
+  uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStreamStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);
+    }
+    s_err = MOE_OK;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (!a.n) pdl_wait();   // as in linear_split_kernel
+  pdl_launch_dependents();
+  const int groups = pl.nt / 16;
+  const int rchunks = (a.R + 63) / 64;
+  bool ok = true;
+
+  // the runs of groups that share an adapter, of the tile at token t0: f(adapter, first group, groups)
+  auto runs = [&](int t0, auto f) {
+    for (int g = 0; g < groups && t0 + g * 16 < a.T;) {
+      const int id = a.group[t0 / 16 + g];
+      int len = 1;
+      while (g + len < groups && t0 + (g + len) * 16 < a.T && a.group[t0 / 16 + g + len] == id) ++len;
+      if (id >= 0 && !f(id, g, len)) return;
+      g += len;
+    }
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      const uint32_t bytes = kATile + pl.nt * 128;
+      auto stage = [&](const CUtensorMap* ma, const CUtensorMap* mb, int ka, int rowa, int rowb) {
+        const int s = it % kStreamStages;
+        if (it >= kStreamStages && !mbar_wait_fast(&empty[s], (it / kStreamStages - 1) & 1, &s_err)) return ok = false;
+        uint8_t* st = sm + s * kStreamStage;
+        mbar_expect_tx(&full[s], bytes);
+        tma_2d(st, ma, ka, rowa, &full[s]);
+        tma_2d(st + kATile, mb, ka, rowb, &full[s]);
+        ++it;
+        return true;
+      };
+      for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
+        const int n0 = tile % pl.tiles_n * kRows, t0 = tile / pl.tiles_n * pl.nt;
+        for (int k = 0; k < pl.nk && ok; ++k) stage(&mW, &mX, k * 64, n0, t0);
+        if (a.n && ok) {
+          pdl_wait();   // u and the groups (returns at once after the first tile)
+          runs(t0, [&](int id, int, int) {
+            for (int c = 0; c < rchunks; ++c)
+              if (!stage(&mB, &mH, c * 64, id * a.N + n0, t0) || !stage(&mB, &mL, c * 64, id * a.N + n0, t0))
+                return false;
+            return true;
+          });
+        }
+      }
+    }
+  } else if (warp == 1) {
+    int it = 0, acc = 0;   // K steps and accumulators so far
+    const bool bf16 = std::is_same<TE, __nv_bfloat16>::value;
+    const uint32_t idesc = idesc_f16(pl.nt, bf16);
+    auto wait_stage = [&] {
+      ok = __all_sync(0xffffffffu, mbar_wait_fast(&full[it % kStreamStages], (it / kStreamStages) & 1, &s_err));
+      tc_fence_after();
+      return ok;
+    };
+    for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
+      const int t0 = tile / pl.tiles_n * pl.nt;
+      for (int k = 0; k < pl.nk && ok; ++k) {
+        const int b = acc & 1;
+        const bool start = k % pl.chunk == 0;
+        if (start && acc >= 2)
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait_fast(&acc_empty[b], (acc / 2 - 1) & 1, &s_err)))) break;
+        if (!wait_stage()) break;
+        const uint8_t* st = sm + it % kStreamStages * kStreamStage;
+        mma_kstep(tmem + b * 256, umma_desc_sw128(su32(st)), umma_desc_sw128(su32(st + kATile)), idesc, !start,
+                  &empty[it % kStreamStages]);
+        ++it;
+        if (k + 1 == pl.nk) {
+          if (a.n) {
+            pdl_wait();
+            runs(t0, [&](int id, int g, int len) {
+              const uint32_t d = tmem + b * 256 + g * 16, id16 = idesc_f16(len * 16, bf16);
+              for (int c = 0; c < 2 * rchunks; ++c) {
+                if (!wait_stage()) return false;
+                const uint8_t* s2 = sm + it % kStreamStages * kStreamStage;
+                const uint64_t da = umma_desc_sw128(su32(s2)), db = umma_desc_sw128(su32(s2 + kATile + g * 2048));
+                const int left = a.R - (c / 2) * 64, steps = left >= 64 ? 4 : (left + 15) / 16;
+                for (int j = 0; j < steps; ++j) mma_one(d, da + 2 * j, db + 2 * j, id16, 1);
+                mma_commit_elect(&empty[it % kStreamStages]);
+                ++it;
+              }
+              return true;
+            });
+          }
+        }
+        if ((k + 1) % pl.chunk == 0 || k + 1 == pl.nk) {
+          mma_commit_elect(&acc_full[b]);
+          ++acc;
+        }
+      }
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;   // its 32 outputs, its 128 tokens of the tile
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    int acc = 0;
+    for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
+      const int n = tile % pl.tiles_n * kRows + q * 32 + lane, t0 = tile / pl.tiles_n * pl.nt + half * 128;
+      float v[128];
+      for (int k = 0; k < pl.nk; k += pl.chunk) {
+        const int b = acc & 1;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait_fast(&acc_full[b], (acc / 2) & 1, &s_err)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (half * 128 + c * 16 >= pl.nt) break;
+          uint32_t w[16];
+          tmem_ld16(tmem + lanes + b * 256 + half * 128 + c * 16, w);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[c * 16 + j] = k ? v[c * 16 + j] + __uint_as_float(w[j]) : __uint_as_float(w[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[b]);
+        ++acc;
+      }
+      if (a.n) pdl_wait();
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int t1 = t0 + c * 16;
+        if (half * 128 + c * 16 >= pl.nt || t1 >= a.T) break;
+        const bool mixed = a.n && a.group[t1 / 16] == kMixed;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const long long t = t1 + j;
+          if (t >= a.T || n >= a.N) break;
+          float s = ok ? v[c * 16 + j] : NAN;
+          if (mixed) {
+            const int id = a.ids[t];
+            if (id >= 0 && id < a.n) s += adapter_dot<TE>(a, id, t, n);
+          }
+          if (a.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(a.out)[t * a.ld_out + n] = s;
+          else reinterpret_cast<TE*>(a.out)[t * a.ld_out + n] = from_f32<TE>(s);
+        }
+      }
+    }
+  }
+  if (!ok) {   // a wait gave up: leave the copies in flight time to land
+    const uint64_t since = gtimer();
+    while (gtimer() - since < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+  if (threadIdx.x == 0 && s_err != MOE_OK && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
+  if (a.n) pdl_wait();
+}
+
 // --------------------------------------------------------------------- host --
 
 // rows x cols of 16-bit elements, `ld` apart: boxes of 64 columns x box_rows, 128-byte swizzle, zeros outside
@@ -455,13 +714,50 @@ static moe_status launch_adapter_mma(const LinearArgs& a, cudaStream_t s) {
   return check_launch("adapter_mma_kernel");
 }
 
+// Whether a call is large: with one block per SM, tiles of 128 x 128 fill them.
+static bool large_batch(int T, int N) {
+  return T > 128 && ((long long)N + kRows - 1) / kRows * ((T + 127) / 128) >= device_sms() * 3 / 4;
+}
+
+template <typename TE>
+static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) {
+  CUtensorMap mW, mX, mB = {}, mH = {}, mL = {};
+  StreamPlan pl;
+  pl.tiles_n = (a.N + kRows - 1) / kRows;
+  pl.nk = (a.H + 63) / 64;
+  pl.chunk = a.out_dtype == MOE_DT_F32 ? kF32Chunk : pl.nk;
+  // the tile that takes the fewest rounds of the SMs times its length (16: what a tile costs beside its tokens)
+  const int sms = device_sms();
+  long long best = -1;
+  for (int nt = 256; nt >= 64; nt -= 16) {
+    const long long tiles = (long long)pl.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + sms - 1) / sms * (nt + 16);
+    if (best < 0 || cost < best) best = cost, pl.nt = nt, pl.tiles = (int)tiles;
+  }
+  moe_status st = map_rows(&mW, a.W, dtype, a.H, a.N, a.ld_w, kRows);
+  if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.H, a.T, a.ld_x, pl.nt);
+  if (a.n) {
+    if (st == MOE_OK) st = map_rows(&mB, a.B, dtype, a.R, (uint64_t)a.n * a.N, a.R, kRows);
+    if (st == MOE_OK) st = map_rows(&mH, a.u_hi, dtype, a.R, a.T, a.R, pl.nt);
+    if (st == MOE_OK) st = map_rows(&mL, a.u_lo, dtype, a.R, a.T, a.R, pl.nt);
+  }
+  if (st != MOE_OK) return st;
+  auto kernel = linear_stream_kernel<TE>;
+  static char allowed[64];
+  MOE_CUDA(allow_smem(kernel, kStreamSmem, allowed));
+  cudaError_t e = launch_pdl(kernel, dim3(pl.tiles < sms ? pl.tiles : sms), dim3(kStreamThreads), kStreamSmem, s, mW,
+                             mX, mB, mH, mL, a, pl);
+  if (e != cudaSuccess) return cuda_fail(e, "linear_stream_kernel");
+  return check_launch("linear_stream_kernel");
+}
+
 template <typename TE>
 static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) {
   ProfScope ps(MOE_K_LINEAR, s);
   moe_status st = MOE_OK;
+  const bool large = large_batch(a.T, a.N);
   if (a.n) {
     // one dot per token and rank re-reads A for every token: worth it up to this many bytes
-    if ((long long)a.T * a.R * a.H * 2 <= (64LL << 20)) {
+    if (!large && (long long)a.T * a.R * a.H * 2 <= (64LL << 20)) {
       const long long warps = (long long)a.T * (a.R / kDots);
       cudaError_t e = launch_pdl(adapter_dot_kernel<TE>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, a);
       if (e != cudaSuccess) return cuda_fail(e, "adapter_dot_kernel");
@@ -475,14 +771,32 @@ static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) 
     }
     if (st != MOE_OK) return st;
   }
+  if (large) return launch_stream<TE>(a, dtype, s);
   if (a.T <= 16) return launch_split<TE, 16>(a, dtype, s);
   if (a.T <= 32) return launch_split<TE, 32>(a, dtype, s);
   if (a.T <= 64) return launch_split<TE, 64>(a, dtype, s);
-  if (a.T <= 128) return launch_split<TE, 128>(a, dtype, s);
-  // larger tiles re-read less of W, as long as they fill the SMs
-  const long long tiles_n = (a.N + kRows - 1) / kRows;
-  if (tiles_n * ((a.T + 255) / 256) < device_sms()) return launch_split<TE, 128>(a, dtype, s);
-  return launch_split<TE, 256>(a, dtype, s);
+  return launch_split<TE, 128>(a, dtype, s);
+}
+
+// The workspace's parts: u, and for large batches u's two 16-bit terms and the groups' table.
+struct LinearSpace {
+  size_t u, hi, lo, group, bytes;
+};
+static LinearSpace linear_space(int T, int N, int n, int R) {
+  LinearSpace w = {};
+  if (n <= 0) return w;
+  auto take = [&](size_t b) {
+    const size_t at = w.bytes;
+    w.bytes += (b + 127) / 128 * 128;
+    return at;
+  };
+  w.u = take((size_t)T * R * 4);
+  if (large_batch(T, N)) {
+    w.hi = take((size_t)T * R * 2);
+    w.lo = take((size_t)T * R * 2);
+    w.group = take(((size_t)T + 15) / 16 * 4);
+  }
+  return w;
 }
 
 }  // namespace moe
@@ -491,7 +805,7 @@ using namespace moe;
 
 extern "C" size_t moe_adapter_linear_workspace(int T, int H, int N, int n_adapters, int R) {
   if (T <= 0 || H <= 0 || N <= 0 || n_adapters <= 0 || R <= 0) return 0;
-  return ((size_t)T * R * sizeof(float) + 15) / 16 * 16;
+  return linear_space(T, N, n_adapters, R).bytes;
 }
 
 extern "C" moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out_dtype, const void* x, int64_t ld_x,
@@ -506,6 +820,7 @@ extern "C" moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out
   MOE_ARG(out_dtype == dtype || out_dtype == MOE_DT_F32, "out must be of x's type or fp32 (type %d)", out_dtype);
   MOE_ARG(n_adapters >= 0, "n_adapters must be >= 0 (got %d)", n_adapters);
   MOE_ARG(!n_adapters || (R >= 8 && R <= 128 && R % 8 == 0), "R must be a multiple of 8 up to 128 (got %d)", R);
+  MOE_ARG((long long)n_adapters * N + kRows <= 0x7fffffffLL, "n_adapters * N must be below 2^31");
   if (T == 0) return MOE_OK;
   MOE_ARG(x && W && out, "null pointer");
   MOE_ARG(ld_x >= H && ld_w >= H && ld_out >= N, "a row distance is below the row's length");
@@ -518,8 +833,16 @@ extern "C" moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out
   const size_t need = moe_adapter_linear_workspace(T, H, N, n_adapters, R);
   MOE_ARG(!need || (workspace && (uintptr_t)workspace % 16 == 0 && workspace_bytes >= need),
           "workspace missing, misaligned or too small (%zu bytes, %zu needed)", workspace_bytes, need);
-  const LinearArgs a{T,    H,    N,      n_adapters, R,          out_dtype, x,  W, lora_a, lora_b, ld_x,
-                     ld_w, ld_out, adapter_ids, lora_scale, out, (float*)workspace, d_error};
+  const LinearSpace w = linear_space(T, N, n_adapters, R);
+  char* ws = (char*)workspace;
+  LinearArgs a = {};
+  a.T = T, a.H = H, a.N = N, a.n = n_adapters, a.R = R, a.out_dtype = out_dtype;
+  a.x = x, a.W = W, a.A = lora_a, a.B = lora_b, a.ld_x = ld_x, a.ld_w = ld_w, a.ld_out = ld_out;
+  a.ids = adapter_ids, a.scale = lora_scale, a.out = out, a.err = d_error;
+  if (n_adapters) {
+    a.u = (float*)(ws + w.u);
+    if (w.group) a.u_hi = ws + w.hi, a.u_lo = ws + w.lo, a.group = (int32_t*)(ws + w.group);
+  }
   return dtype == MOE_DT_BF16 ? launch_linear<__nv_bfloat16>(a, dtype, stream)
                               : launch_linear<__half>(a, dtype, stream);
 }

@@ -208,22 +208,56 @@ __global__ void __launch_bounds__(256) adapter_mma_kernel(const LinearArgs a) {
 
 // -------------------------------------------------------------- projection --
 
-// D [128 x n] (fp32 in tensor memory) += A [128 x 64] B [n x 64]^T, four K = 16
-// MMAs by one elected lane of a converged warp, then a commit that arrives on
-// `bar` when they have completed.
-__device__ __forceinline__ void mma_kstep(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
-                                          uint64_t* bar) {
+// Waits for the phase of parity `parity`, at most 2^26 polls (some seconds); a
+// wait that gives up says so in *err (the block's own word), and ends the block's
+// other waits.
+__device__ __forceinline__ bool test_wait(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 aa, bb;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "add.s64 aa, %1, 2;\n\tadd.s64 bb, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], aa, bb, %3, t;\n\t"
-      "add.s64 aa, %1, 4;\n\tadd.s64 bb, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], aa, bb, %3, t;\n\t"
-      "add.s64 aa, %1, 6;\n\tadd.s64 bb, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], aa, bb, %3, t;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(su32(bar))
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __forceinline__ bool wait_bar(uint64_t* b, uint32_t parity, int* err) {
+  for (uint32_t i = 0; i < (1u << 26); ++i) {
+    if (test_wait(b, parity)) return true;
+    if ((i & 255) == 255 && *(volatile int*)err != MOE_OK) return false;
+  }
+  atomicExch(err, MOE_ERR_TIMEOUT);
+  return false;
+}
+
+// One thread of a warp issues all MMAs of a block.  Its loop has to stay short:
+// a K = 16 step of 128 x 128 takes 64 clocks and its issue alone about 54, so
+// stages and phases are counted, not divided out (with k % chunk in the loop a
+// 64-wide step of any width took 870 clocks; now 258 at n = 128, 514 at 256).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// D [128 x n] (fp32 in tensor memory) (+)= A [128 x 16] B [n x 16]^T.
+__device__ __forceinline__ void mma_k16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// Arrives on `bar` when the thread's MMAs so far have completed.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar)) : "memory");
+}
+// A place in a ring of N stages and the parity of its current pass.
+template <int N>
+struct RingPos {
+  int stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == N) stage = 0, parity ^= 1;
+  }
+};
 // kind::f16, D fp32, A and B of one 16-bit type, both K-major, M = 128.
 __device__ __forceinline__ uint32_t idesc_f16(int n, bool bf16) {
   const uint32_t t = bf16 ? 1u : 0u;
@@ -280,25 +314,37 @@ __device__ __forceinline__ void add_adapter4(const LinearArgs& a, int id, long l
   }
 }
 
-// B[a][n] . u[t] in fp32.
+// v[j] += B[a][n] . u[t1 + j] in fp32 for the tokens j of `who`: eight ranks at a
+// time, B's in registers for all of them.
 template <typename TE>
-__device__ __noinline__ float adapter_dot(const LinearArgs& a, int id, long long t, int n) {
-  const float4* u = reinterpret_cast<const float4*>(a.u + t * a.R);
+__device__ __forceinline__ void add_adapter16(const LinearArgs& a, int id, uint32_t who, int t1, int n, float* v) {
   const TE* B = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + n) * a.R;
-  float s = 0.f;
+  const float* u = a.u + (long long)t1 * a.R;
+#pragma unroll 2
   for (int r = 0; r < a.R; r += 8) {
-    const float4 u0 = u[r / 4], u1 = u[r / 4 + 1];
     const uint4 b = *reinterpret_cast<const uint4*>(B + r);
-    float2 p = Pair<TE>::f32(b.x);
-    s = fmaf(p.x, u0.x, fmaf(p.y, u0.y, s));
-    p = Pair<TE>::f32(b.y);
-    s = fmaf(p.x, u0.z, fmaf(p.y, u0.w, s));
-    p = Pair<TE>::f32(b.z);
-    s = fmaf(p.x, u1.x, fmaf(p.y, u1.y, s));
-    p = Pair<TE>::f32(b.w);
-    s = fmaf(p.x, u1.z, fmaf(p.y, u1.w, s));
+    const float2 b0 = Pair<TE>::f32(b.x), b1 = Pair<TE>::f32(b.y), b2 = Pair<TE>::f32(b.z), b3 = Pair<TE>::f32(b.w);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (!(who >> j & 1)) continue;
+      const float4 p = *reinterpret_cast<const float4*>(u + (long long)j * a.R + r);
+      const float4 q = *reinterpret_cast<const float4*>(u + (long long)j * a.R + r + 4);
+      v[j] += fmaf(b0.x, p.x, fmaf(b0.y, p.y, fmaf(b1.x, p.z, b1.y * p.w))) +
+              fmaf(b2.x, q.x, fmaf(b2.y, q.y, fmaf(b3.x, q.z, b3.y * q.w)));
+    }
   }
-  return s;
+}
+// One column of 16 tokens (those below `left`).
+template <typename T>
+__device__ __forceinline__ void store16(T* o, long long ld, int left, const float* v, bool ok) {
+  if (left >= 16 && ok) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j * ld] = from_f32<T>(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < left) o[j * ld] = from_f32<T>(ok ? v[j] : NAN);
+  }
 }
 
 template <typename TE>
@@ -365,29 +411,36 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
   pdl_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
+      RingPos<C::kStages> r;
       for (int k = k0; k < k1; ++k) {
-        const int i = k - k0, s = i % C::kStages;
-        if (i >= C::kStages && !mbar_wait_fast(&empty[s], (i / C::kStages - 1) & 1, &s_err)) break;
-        uint8_t* st = sm + s * C::kStage;
-        mbar_expect_tx(&full[s], C::kStage);
-        tma_2d(st, &mW, k * 64, n0, &full[s]);
-        tma_2d(st + kATile, &mX, k * 64, t0, &full[s]);
+        if (k - k0 >= C::kStages && !wait_bar(&empty[r.stage], r.parity ^ 1, &s_err)) break;
+        uint8_t* st = sm + r.stage * C::kStage;
+        mbar_expect_tx(&full[r.stage], C::kStage);
+        tma_2d(st, &mW, k * 64, n0, &full[r.stage]);
+        tma_2d(st + kATile, &mX, k * 64, t0, &full[r.stage]);
+        r.next();
       }
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_f16(NT, std::is_same<TE, __nv_bfloat16>::value);
-    for (int k = k0; k < k1; ++k) {
-      const int i = k - k0, s = i % C::kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait_fast(&full[s], (i / C::kStages) & 1, &s_err))) break;
-      tc_fence_after();
-      uint8_t* st = sm + s * C::kStage;
-      mma_kstep(tmem, umma_desc_sw128(su32(st)), umma_desc_sw128(su32(st + kATile)), idesc, i != 0, &empty[s]);
+    if (elect_one()) {
+      const uint32_t idesc = idesc_f16(NT, std::is_same<TE, __nv_bfloat16>::value);
+      const uint64_t d0 = umma_desc_sw128(su32(sm));
+      RingPos<C::kStages> r;
+      for (int k = k0; k < k1; ++k) {
+        if (!wait_bar(&full[r.stage], r.parity, &s_err)) break;
+        tc_fence_after();
+        const uint64_t da = d0 + (uint32_t)(r.stage * C::kStage / 16), db = da + kATile / 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_k16(tmem, da + 2 * j, db + 2 * j, idesc, k != k0 || j);
+        mma_commit(&empty[r.stage]);
+        r.next();
+      }
+      mma_commit(&done);
     }
-    mma_commit_elect(&done);
   }
   __syncwarp();
-  const bool ok = __all_sync(0xffffffffu, mbar_wait(&done, 0, &s_err)) && *(volatile int*)&s_err == MOE_OK;
+  const bool ok = __all_sync(0xffffffffu, wait_bar(&done, 0, &s_err)) && *(volatile int*)&s_err == MOE_OK;
   tc_fence_after();
   // sums -> shared memory [NT][128]: a warp reads its quadrant's 32 rows, 16 tokens at a time
   float* part = reinterpret_cast<float*>(sm);
@@ -444,7 +497,7 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
 //
 // A tensor-core accumulator loses a little with every step (it truncates), so a
 // result kept in fp32 takes at most `chunk` steps in one accumulator; the epilogue
-// adds the chunks up in registers, in order.
+// adds the chunks up in registers, in order (CHUNKS; tiles of at most 128 tokens).
 //
 // Adapters: tokens come in groups of 16.  A run of groups that share one adapter
 // gets more K steps at the end of its tile, over that run's columns alone: B[a]
@@ -457,20 +510,11 @@ constexpr int kStreamSmem = kStreamStages * kStreamStage + 1024;
 constexpr int kStreamThreads = 320;   // TMA, MMA, eight epilogue warps
 constexpr int kF32Chunk = 8;          // K steps in one accumulator for fp32 results: 512 products a sum
 
-// One K = 16 step by one elected lane of a converged warp.
-__device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
 struct StreamPlan {
   int nt, tiles_n, tiles, nk, chunk;   // tokens of a tile, tiles of outputs, all tiles, K steps, K steps of an accumulator
 };
 
-template <typename TE>
+template <typename TE, bool CHUNKS>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     linear_stream_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
                          const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mH,
@@ -508,133 +552,163 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const int rchunks = (a.R + 63) / 64;
   bool ok = true;
 
-  // the runs of groups that share an adapter, of the tile at token t0: f(adapter, first group, groups)
-  auto runs = [&](int t0, auto f) {
-    for (int g = 0; g < groups && t0 + g * 16 < a.T;) {
-      const int id = a.group[t0 / 16 + g];
-      int len = 1;
-      while (g + len < groups && t0 + (g + len) * 16 < a.T && a.group[t0 / 16 + g + len] == id) ++len;
-      if (id >= 0 && !f(id, g, len)) return;
-      g += len;
+  // the runs of groups that share an adapter among a tile's (lane g holds group
+  // g's entry, kMixed past T): f(adapter, first group, groups)
+  auto group_of = [&](int t0) {
+    return a.n && lane < groups && t0 + lane * 16 < a.T ? a.group[t0 / 16 + lane] : kMixed;
+  };
+  auto runs = [&](int mine, auto f) {
+    uint32_t left = __ballot_sync(0xffffffffu, mine >= 0);
+    while (left) {
+      const int g = __ffs(left) - 1, id = __shfl_sync(0xffffffffu, mine, g);
+      const uint32_t other = ~__ballot_sync(0xffffffffu, mine == id) & ~((1u << g) - 1);   // 16 groups at most
+      const int len = __ffs(other) - 1 - g;
+      if (!f(id, g, len)) return;
+      left &= ~(((1u << len) - 1) << g);
     }
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      const uint32_t bytes = kATile + pl.nt * 128;
-      auto stage = [&](const CUtensorMap* ma, const CUtensorMap* mb, int ka, int rowa, int rowb) {
-        const int s = it % kStreamStages;
-        if (it >= kStreamStages && !mbar_wait_fast(&empty[s], (it / kStreamStages - 1) & 1, &s_err)) return ok = false;
-        uint8_t* st = sm + s * kStreamStage;
-        mbar_expect_tx(&full[s], bytes);
-        tma_2d(st, ma, ka, rowa, &full[s]);
-        tma_2d(st + kATile, mb, ka, rowb, &full[s]);
-        ++it;
-        return true;
-      };
-      for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
-        const int n0 = tile % pl.tiles_n * kRows, t0 = tile / pl.tiles_n * pl.nt;
-        for (int k = 0; k < pl.nk && ok; ++k) stage(&mW, &mX, k * 64, n0, t0);
-        if (a.n && ok) {
-          pdl_wait();   // u and the groups (returns at once after the first tile)
-          runs(t0, [&](int id, int, int) {
-            for (int c = 0; c < rchunks; ++c)
-              if (!stage(&mB, &mH, c * 64, id * a.N + n0, t0) || !stage(&mB, &mL, c * 64, id * a.N + n0, t0))
-                return false;
-            return true;
-          });
-        }
-      }
-    }
-  } else if (warp == 1) {
-    int it = 0, acc = 0;   // K steps and accumulators so far
-    const bool bf16 = std::is_same<TE, __nv_bfloat16>::value;
-    const uint32_t idesc = idesc_f16(pl.nt, bf16);
-    auto wait_stage = [&] {
-      ok = __all_sync(0xffffffffu, mbar_wait_fast(&full[it % kStreamStages], (it / kStreamStages) & 1, &s_err));
-      tc_fence_after();
-      return ok;
+    RingPos<kStreamStages> r;
+    bool wrapped = false;
+    const uint32_t bytes = kATile + pl.nt * 128;
+    const bool lead = elect_one();
+    auto stage = [&](const CUtensorMap* ma, const CUtensorMap* mb, int ka, int rowa, int rowb) {
+      if (wrapped && !wait_bar(&empty[r.stage], r.parity ^ 1, &s_err)) return false;
+      uint8_t* st = sm + r.stage * kStreamStage;
+      mbar_expect_tx(&full[r.stage], bytes);
+      tma_2d(st, ma, ka, rowa, &full[r.stage]);
+      tma_2d(st + kATile, mb, ka, rowb, &full[r.stage]);
+      r.next();
+      wrapped |= r.stage == 0;
+      return true;
     };
     for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
+      const int n0 = tile % pl.tiles_n * kRows, t0 = tile / pl.tiles_n * pl.nt;
+      if (lead)
+        for (int k = 0; k < pl.nk && ok; ++k) ok = stage(&mW, &mX, k * 64, n0, t0);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!a.n || !ok) continue;
+      pdl_wait();   // u and the groups (returns at once after the first tile)
+      runs(group_of(t0), [&](int id, int, int) {
+        if (lead)
+          for (int c = 0; c < rchunks && ok; ++c)
+            ok = stage(&mB, &mH, c * 64, id * a.N + n0, t0) && stage(&mB, &mL, c * 64, id * a.N + n0, t0);
+        return ok = __all_sync(0xffffffffu, ok);
+      });
+    }
+  } else if (warp == 1) {
+    RingPos<kStreamStages> r;
+    RingPos<2> acc;
+    int used = 0;   // accumulators handed over so far (up to 2)
+    const bool bf16 = std::is_same<TE, __nv_bfloat16>::value, lead = elect_one();
+    const uint32_t idesc = idesc_f16(pl.nt, bf16);
+    const uint64_t d0 = umma_desc_sw128(su32(sm));
+    for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
       const int t0 = tile / pl.tiles_n * pl.nt;
-      for (int k = 0; k < pl.nk && ok; ++k) {
-        const int b = acc & 1;
-        const bool start = k % pl.chunk == 0;
-        if (start && acc >= 2)
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait_fast(&acc_empty[b], (acc / 2 - 1) & 1, &s_err)))) break;
-        if (!wait_stage()) break;
-        const uint8_t* st = sm + it % kStreamStages * kStreamStage;
-        mma_kstep(tmem + b * 256, umma_desc_sw128(su32(st)), umma_desc_sw128(su32(st + kATile)), idesc, !start,
-                  &empty[it % kStreamStages]);
-        ++it;
-        if (k + 1 == pl.nk) {
-          if (a.n) {
-            pdl_wait();
-            runs(t0, [&](int id, int g, int len) {
-              const uint32_t d = tmem + b * 256 + g * 16, id16 = idesc_f16(len * 16, bf16);
-              for (int c = 0; c < 2 * rchunks; ++c) {
-                if (!wait_stage()) return false;
-                const uint8_t* s2 = sm + it % kStreamStages * kStreamStage;
-                const uint64_t da = umma_desc_sw128(su32(s2)), db = umma_desc_sw128(su32(s2 + kATile + g * 2048));
-                const int left = a.R - (c / 2) * 64, steps = left >= 64 ? 4 : (left + 15) / 16;
-                for (int j = 0; j < steps; ++j) mma_one(d, da + 2 * j, db + 2 * j, id16, 1);
-                mma_commit_elect(&empty[it % kStreamStages]);
-                ++it;
-              }
-              return true;
-            });
+      for (int k = 0; k < pl.nk && ok; k += pl.chunk) {
+        const uint32_t d = tmem + acc.stage * 256;
+        const int end = k + pl.chunk < pl.nk ? k + pl.chunk : pl.nk;
+        if (lead) {
+          if (used >= 2) ok = wait_bar(&acc_empty[acc.stage], acc.parity ^ 1, &s_err);
+          tc_fence_after();
+          for (int i = k; i < end && ok; ++i) {
+            if (!(ok = wait_bar(&full[r.stage], r.parity, &s_err))) break;
+            tc_fence_after();
+            const uint64_t da = d0 + (uint32_t)(r.stage * (kStreamStage / 16)), db = da + kATile / 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma_k16(d, da + 2 * j, db + 2 * j, idesc, i != k || j);
+            mma_commit(&empty[r.stage]);
+            r.next();
           }
         }
-        if ((k + 1) % pl.chunk == 0 || k + 1 == pl.nk) {
-          mma_commit_elect(&acc_full[b]);
-          ++acc;
+        ok = __all_sync(0xffffffffu, ok);
+        if (a.n && end == pl.nk && ok) {
+          pdl_wait();
+          runs(group_of(t0), [&](int id, int g, int len) {
+            if (lead) {
+              const uint32_t id16 = idesc_f16(len * 16, bf16);
+              for (int c = 0; c < 2 * rchunks; ++c) {
+                if (!(ok = wait_bar(&full[r.stage], r.parity, &s_err))) break;
+                tc_fence_after();
+                const uint64_t da = d0 + (uint32_t)(r.stage * (kStreamStage / 16)), db = da + kATile / 16 + g * 128;
+                const int left = a.R - (c / 2) * 64, steps = left >= 64 ? 4 : (left + 15) / 16;
+                for (int j = 0; j < steps; ++j) mma_k16(d + g * 16, da + 2 * j, db + 2 * j, id16, 1);
+                mma_commit(&empty[r.stage]);
+                r.next();
+              }
+            }
+            return ok = __all_sync(0xffffffffu, ok);
+          });
         }
+        if (lead && ok) mma_commit(&acc_full[acc.stage]);
+        acc.next();
+        ++used;
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;   // its 32 outputs, its 128 tokens of the tile
+    constexpr int kHalf = CHUNKS ? 64 : 128;                  // tokens of the tile that a warp takes
+    const int q = warp & 3, c0 = ((warp - 2) >> 2) * kHalf;   // its 32 outputs, its first token
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    int acc = 0;
+    RingPos<2> acc;
     for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
-      const int n = tile % pl.tiles_n * kRows + q * 32 + lane, t0 = tile / pl.tiles_n * pl.nt + half * 128;
-      float v[128];
-      for (int k = 0; k < pl.nk; k += pl.chunk) {
-        const int b = acc & 1;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait_fast(&acc_full[b], (acc / 2) & 1, &s_err)))) break;
-        tc_fence_after();
+      const int n = tile % pl.tiles_n * kRows + q * 32 + lane, t0 = tile / pl.tiles_n * pl.nt;
+      float v[CHUNKS ? kHalf : 16];
+      auto columns = [&](int c, float* f, bool add) {   // 16 of the accumulator's columns
+        uint32_t w[16];
+        tmem_ld16(tmem + lanes + acc.stage * 256 + c0 + c * 16, w);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (half * 128 + c * 16 >= pl.nt) break;
-          uint32_t w[16];
-          tmem_ld16(tmem + lanes + b * 256 + half * 128 + c * 16, w);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[c * 16 + j] = k ? v[c * 16 + j] + __uint_as_float(w[j]) : __uint_as_float(w[j]);
-        }
+        for (int j = 0; j < 16; ++j) f[j] = add ? f[j] + __uint_as_float(w[j]) : __uint_as_float(w[j]);
+      };
+      auto release = [&] {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[b]);
-        ++acc;
+        if (lane == 0) mbar_arrive(&acc_empty[acc.stage]);
+        acc.next();
+      };
+      if (CHUNKS) {
+        for (int k = 0; k < pl.nk; k += pl.chunk) {
+          if (!(ok = __all_sync(0xffffffffu, wait_bar(&acc_full[acc.stage], acc.parity, &s_err)))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kHalf / 16; ++c)
+            if (c0 + c * 16 < pl.nt) columns(c, v + c * 16, k != 0);
+          release();
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, wait_bar(&acc_full[acc.stage], acc.parity, &s_err));
+        tc_fence_after();
       }
       if (a.n) pdl_wait();
+      const uint32_t mixed =
+          a.n ? __ballot_sync(0xffffffffu, lane < groups && group_of(t0) == kMixed) >> (c0 / 16) : 0;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int t1 = t0 + c * 16;
-        if (half * 128 + c * 16 >= pl.nt || t1 >= a.T) break;
-        const bool mixed = a.n && a.group[t1 / 16] == kMixed;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const long long t = t1 + j;
-          if (t >= a.T || n >= a.N) break;
-          float s = ok ? v[c * 16 + j] : NAN;
-          if (mixed) {
-            const int id = a.ids[t];
-            if (id >= 0 && id < a.n) s += adapter_dot<TE>(a, id, t, n);
+      for (int c = 0; c < kHalf / 16; ++c) {
+        const int t1 = t0 + c0 + c * 16;
+        if (c0 + c * 16 >= pl.nt || t1 >= a.T) break;
+        float* f = CHUNKS ? v + c * 16 : v;
+        if (!CHUNKS) columns(c, f, false);
+        if (mixed >> c & 1) {   // the adapters that the 16 tokens name, one after the other
+          const int mine = t1 + (lane & 15) < a.T ? a.ids[t1 + (lane & 15)] : -1;
+          uint32_t left = __ballot_sync(0xffffffffu, mine >= 0 && mine < a.n) & 0xffff;
+          while (left) {
+            const int id = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+            const uint32_t who = __ballot_sync(0xffffffffu, mine == id) & 0xffff;
+            left &= ~who;
+            if (n < a.N) add_adapter16<TE>(a, id, who, t1, n, f);
+            __syncwarp();
           }
-          if (a.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(a.out)[t * a.ld_out + n] = s;
-          else reinterpret_cast<TE*>(a.out)[t * a.ld_out + n] = from_f32<TE>(s);
         }
+        if (n < a.N) {
+          const long long o = (long long)t1 * a.ld_out + n;
+          if (CHUNKS || a.out_dtype == MOE_DT_F32)
+            store16(reinterpret_cast<float*>(a.out) + o, a.ld_out, a.T - t1, f, ok);
+          else
+            store16(reinterpret_cast<TE*>(a.out) + o, a.ld_out, a.T - t1, f, ok);
+        }
+        __syncwarp();
       }
+      if (!CHUNKS) release();
     }
   }
   if (!ok) {   // a wait gave up: leave the copies in flight time to land
@@ -725,11 +799,12 @@ static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) 
   StreamPlan pl;
   pl.tiles_n = (a.N + kRows - 1) / kRows;
   pl.nk = (a.H + 63) / 64;
-  pl.chunk = a.out_dtype == MOE_DT_F32 ? kF32Chunk : pl.nk;
+  const bool chunks = a.out_dtype == MOE_DT_F32 && pl.nk > kF32Chunk;
+  pl.chunk = chunks ? kF32Chunk : pl.nk;
   // the tile that takes the fewest rounds of the SMs times its length (16: what a tile costs beside its tokens)
   const int sms = device_sms();
   long long best = -1;
-  for (int nt = 256; nt >= 64; nt -= 16) {
+  for (int nt = chunks ? 128 : 256; nt >= 64; nt -= 16) {
     const long long tiles = (long long)pl.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + sms - 1) / sms * (nt + 16);
     if (best < 0 || cost < best) best = cost, pl.nt = nt, pl.tiles = (int)tiles;
   }
@@ -741,9 +816,9 @@ static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) 
     if (st == MOE_OK) st = map_rows(&mL, a.u_lo, dtype, a.R, a.T, a.R, pl.nt);
   }
   if (st != MOE_OK) return st;
-  auto kernel = linear_stream_kernel<TE>;
-  static char allowed[64];
-  MOE_CUDA(allow_smem(kernel, kStreamSmem, allowed));
+  auto kernel = chunks ? linear_stream_kernel<TE, true> : linear_stream_kernel<TE, false>;
+  static char allowed[2][64];
+  MOE_CUDA(allow_smem(kernel, kStreamSmem, allowed[chunks]));
   cudaError_t e = launch_pdl(kernel, dim3(pl.tiles < sms ? pl.tiles : sms), dim3(kStreamThreads), kStreamSmem, s, mW,
                              mX, mB, mH, mL, a, pl);
   if (e != cudaSuccess) return cuda_fail(e, "linear_stream_kernel");

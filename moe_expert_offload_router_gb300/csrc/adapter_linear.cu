@@ -102,110 +102,6 @@ __global__ void __launch_bounds__(128) adapter_dot_kernel(const LinearArgs a) {
   }
 }
 
-template <typename TE>
-__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  if constexpr (sizeof(TE) == 2 && std::is_same<TE, __nv_bfloat16>::value)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Many tokens: a block takes 16 tokens and goes through the adapters that they
-// name (one, mostly: a prompt's tokens share theirs), its eight warps splitting
-// H.  x and A rows go straight to MMA fragments: lane (g, c) loads 16 bytes at
-// k = 32 i + 8 c of rows g and g + 8 and uses them as the k16 steps 2 i and
-// 2 i + 1; both operands take k in that same order.
-template <typename TE, int RT>
-__global__ void __launch_bounds__(256) adapter_mma_kernel(const LinearArgs a) {
-  extern __shared__ float red[];   // [8 warps][16 tokens][R]
-  __shared__ int s_id[16];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int t0 = blockIdx.x * 16, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, c = lane & 3;
-  if (threadIdx.x < 16) {
-    int id = t0 + (int)threadIdx.x < a.T ? a.ids[t0 + threadIdx.x] : -1;
-    if (id >= a.n) {
-      if (a.err && blockIdx.y == 0) atomicCAS(a.err, MOE_OK, MOE_ERR_INVALID);
-      id = -1;
-    }
-    s_id[threadIdx.x] = id;
-  }
-  __syncthreads();
-  const int mine = s_id[lane & 15];
-  bool first = lane < 16 && mine >= 0;
-  for (int i = 0; i < (lane & 15); ++i) first = first && s_id[i] != mine;
-  uint32_t todo = __ballot_sync(0xffffffffu, first);   // the tokens that name an adapter first
-  const bool alone = todo && !(todo & (todo - 1));   // one adapter in the group: its block says how it is used
-  if (a.group && !alone && blockIdx.y == 0 && threadIdx.x == 0) a.group[blockIdx.x] = todo ? kMixed : -1;
-  for (int i = 0; i < (int)blockIdx.y; ++i) todo &= todo - 1;
-  const TE* x = reinterpret_cast<const TE*>(a.x);
-  const int ta = t0 + g < a.T ? t0 + g : a.T - 1, tb = t0 + g + 8 < a.T ? t0 + g + 8 : a.T - 1;
-  const uint4* xa = reinterpret_cast<const uint4*>(x + ta * a.ld_x);
-  const uint4* xb = reinterpret_cast<const uint4*>(x + tb * a.ld_x);
-  const int nc = a.H / 8;
-  while (todo) {
-    const int id = s_id[__ffs(todo) - 1];
-    const TE* A = reinterpret_cast<const TE*>(a.A) + (long long)id * a.R * a.H;
-    float acc[RT][4] = {};
-#pragma unroll 2
-    for (int i = warp; 4 * i < nc; i += 8) {
-      const int ch = 4 * i + c;
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      const uint4 p = ch < nc ? xa[ch] : z, q = ch < nc ? xb[ch] : z;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (8 * r >= a.R) break;
-        const uint4 b = ch < nc ? reinterpret_cast<const uint4*>(A + (long long)(8 * r + g) * a.H)[ch] : z;
-        mma16816<TE>(acc[r], p.x, q.x, p.y, q.y, b.x, b.y);
-        mma16816<TE>(acc[r], p.z, q.z, p.w, q.w, b.z, b.w);
-      }
-    }
-    __syncthreads();   // the sums before these have been read
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      if (8 * r >= a.R) break;
-      float* d = red + (warp * 16 + g) * a.R + 8 * r + 2 * c;
-      d[0] = acc[r][0], d[1] = acc[r][1];
-      d[8 * a.R] = acc[r][2], d[8 * a.R + 1] = acc[r][3];
-    }
-    __syncthreads();
-    const float sc = a.scale ? a.scale[id] : 1.f;
-    bool fits = true;
-    for (int i = threadIdx.x; i < 16 * a.R; i += 256) {
-      const int t = i / a.R;
-      if (s_id[t] != id) continue;
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) s += red[w * 16 * a.R + i];
-      s *= sc;
-      const long long at = (long long)t0 * a.R + i;
-      a.u[at] = s;
-      if (a.group) {
-        const TE hi = from_f32<TE>(s);
-        reinterpret_cast<TE*>(a.u_hi)[at] = hi;
-        reinterpret_cast<TE*>(a.u_lo)[at] = from_f32<TE>(s - to_f32(hi));
-        fits = fits && (sizeof(TE) != 2 || std::is_same<TE, __nv_bfloat16>::value || fabsf(s) < 32768.f);
-      }
-    }
-    // shared by all 16 (a last group's missing tokens aside) and within the type's range
-    if (a.group && alone) {
-      const int last = a.T - t0 < 16 ? a.T - t0 : 16;
-      const bool same = lane >= last || s_id[lane & 15] == id;
-      const bool shared = __syncthreads_and(fits && same);
-      if (threadIdx.x == 0) a.group[blockIdx.x] = shared ? id : kMixed;
-    }
-    for (int i = 0; i < (int)gridDim.y && todo; ++i) todo &= todo - 1;
-  }
-}
-
 // -------------------------------------------------------------- projection --
 
 // Waits for the phase of parity `parity`, at most 2^26 polls (some seconds); a
@@ -490,6 +386,194 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
   if (cs > 1) cluster_sync();   // the others have read this block's sums
 }
 
+// u of a large batch: a cluster takes 128 tokens and splits H like
+// linear_split_kernel, the MMA's 128 rows being A rows: those of as many of the
+// adapters that the tokens name as fit (128 / R; a prompt's tokens name one or
+// two, more take another pass).  Every row meets every token; a token takes the
+// rows of its own adapter, so nothing else's values reach it.
+constexpr int kShrinkTokens = 128;
+constexpr int kShrinkStage = kATile + kShrinkTokens * 128;
+constexpr int kShrinkStages = 6;
+constexpr int kShrinkSmem = kShrinkStages * kShrinkStage + 1024;
+
+template <typename TE>
+__global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_constant__ CUtensorMap mA,
+                                                             const __grid_constant__ CUtensorMap mX,
+                                                             const LinearArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ alignas(8) uint64_t full[kShrinkStages], empty[kShrinkStages], done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_err, s_id[kShrinkTokens], s_slot[kShrinkTokens], s_list[kShrinkTokens], s_big[kShrinkTokens / 16];
+  __shared__ int s_first[kShrinkTokens], s_count[kShrinkTokens / 32];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cs = gridDim.x, rank = blockIdx.x, t0 = blockIdx.y * kShrinkTokens;
+  const int nk = (a.H + 63) / 64, k0 = (int)((long long)nk * rank / cs), k1 = (int)((long long)nk * (rank + 1) / cs);
+  if (tid == 0) {
+    for (int s = 0; s < kShrinkStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    s_err = MOE_OK;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)),
+                 "r"(kShrinkTokens));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  pdl_launch_dependents();   // after the wait: the projection may read x from its start
+  // the adapters that the tokens name, in order of their first token: first of a warp's tokens ...
+  int mine = -1;
+  bool first = false;
+  if (tid < kShrinkTokens) {
+    mine = t0 + tid < a.T ? a.ids[t0 + tid] : -1;
+    if (mine >= a.n) {
+      if (a.err && rank == 0) atomicCAS(a.err, MOE_OK, MOE_ERR_INVALID);
+      mine = -1;
+    }
+    s_id[tid] = mine;
+    const uint32_t same = __match_any_sync(0xffffffffu, mine);
+    first = mine >= 0 && (same & ((1u << lane) - 1)) == 0;
+    const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+    if (first) s_first[warp * 32 + __popc(firsts & ((1u << lane) - 1))] = mine;
+    if (lane == 0) s_count[warp] = __popc(firsts);
+    if (tid < kShrinkTokens / 16) s_big[tid] = 0;
+  }
+  __syncthreads();
+  // ... and of the warps before it
+  if (tid < kShrinkTokens) {
+    for (int w = 0; w < warp; ++w)
+      for (int i = 0; i < s_count[w]; ++i) first = first && s_first[w * 32 + i] != mine;
+  }
+  const int total = __syncthreads_count(first);
+  const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+  if (tid < kShrinkTokens && lane == 0) s_count[warp] = __popc(firsts);
+  __syncthreads();
+  if (first) {
+    int at = __popc(firsts & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) at += s_count[w];
+    s_list[at] = mine;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid < kShrinkTokens) {
+    int slot = -1;
+    for (int i = 0; i < total; ++i) slot = s_list[i] == mine ? i : slot;
+    s_slot[tid] = slot;
+  }
+  const uint32_t tmem = tmem_slot;
+  const int per = kRows / a.R;
+  bool ok = true;
+  RingPos<kShrinkStages> r;
+  bool wrapped = false;
+  uint32_t turn = 0;
+  float* part = reinterpret_cast<float*>(sm);   // [tokens][128]
+  const int share = kShrinkTokens / cs;
+  for (int p = 0; p < total; p += per) {
+    const int cnt = total - p < per ? total - p : per;
+    if (warp == 0) {
+      if (elect_one()) {
+        for (int k = k0; k < k1; ++k) {
+          if (wrapped && !wait_bar(&empty[r.stage], r.parity ^ 1, &s_err)) break;
+          uint8_t* st = sm + r.stage * kShrinkStage;
+          mbar_expect_tx(&full[r.stage], cnt * a.R * 128 + kShrinkTokens * 128);
+          for (int i = 0; i < cnt; ++i) tma_2d(st + i * a.R * 128, &mA, k * 64, s_list[p + i] * a.R, &full[r.stage]);
+          tma_2d(st + kATile, &mX, k * 64, t0, &full[r.stage]);
+          r.next();
+          wrapped |= r.stage == 0;
+        }
+      }
+    } else if (warp == 1) {
+      if (elect_one()) {
+        const uint32_t idesc = idesc_f16(kShrinkTokens, std::is_same<TE, __nv_bfloat16>::value);
+        const uint64_t d0 = umma_desc_sw128(su32(sm));
+        for (int k = k0; k < k1; ++k) {
+          if (!wait_bar(&full[r.stage], r.parity, &s_err)) break;
+          tc_fence_after();
+          const uint64_t da = d0 + (uint32_t)(r.stage * (kShrinkStage / 16)), db = da + kATile / 16;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_k16(tmem, da + 2 * j, db + 2 * j, idesc, k != k0 || j);
+          mma_commit(&empty[r.stage]);
+          r.next();
+        }
+        mma_commit(&done);
+      }
+    }
+    __syncwarp();
+    ok = __all_sync(0xffffffffu, wait_bar(&done, turn, &s_err)) && *(volatile int*)&s_err == MOE_OK;
+    turn ^= 1;
+    tc_fence_after();
+#pragma unroll
+    for (int ch = warp >> 2; ch < kShrinkTokens / 16; ch += 2) {
+      uint32_t v[16];
+      tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(ch * 16), v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        part[(ch * 16 + j) * kRows + (warp & 3) * 32 + lane] = ok ? __uint_as_float(v[j]) : NAN;
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    const int rq = a.R / 4;
+    for (int i = tid; i < share * rq; i += 256) {
+      const int tt = rank * share + i / rq, c = i % rq, slot = s_slot[tt] - p;
+      if (slot < 0 || slot >= cnt) continue;
+      const uint32_t at = su32(part) + (uint32_t)(tt * kRows + slot * a.R + c * 4) * 4;
+      float v[4] = {};
+      for (int k = 0; k < cs; ++k) {
+        const float4 f = ld_cluster4(at, k);
+        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+      }
+      const float sc = a.scale ? a.scale[s_id[tt]] : 1.f;
+      const long long o = (long long)(t0 + tt) * a.R + c * 4;
+      TE hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] *= sc;
+        hi[j] = from_f32<TE>(v[j]);
+        lo[j] = from_f32<TE>(v[j] - to_f32(hi[j]));
+        if (!std::is_same<TE, __nv_bfloat16>::value && !(fabsf(v[j]) < 32768.f)) s_big[tt / 16] = 1;
+      }
+      *reinterpret_cast<float4*>(a.u + o) = make_float4(v[0], v[1], v[2], v[3]);
+      if (a.group) {
+        *reinterpret_cast<uint2*>(reinterpret_cast<TE*>(a.u_hi) + o) = *reinterpret_cast<const uint2*>(hi);
+        *reinterpret_cast<uint2*>(reinterpret_cast<TE*>(a.u_lo) + o) = *reinterpret_cast<const uint2*>(lo);
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the sums' place goes back to the copies
+    __syncwarp();
+    cluster_sync();   // the others have read this block's sums
+  }
+  __syncthreads();
+  // how the projection takes a group: together where all 16 (a last group's missing tokens
+  // aside) share an adapter and u is within the 16-bit type's range
+  if (a.group && tid < share / 16) {
+    const int g = rank * (share / 16) + tid, base = g * 16;
+    if (t0 + base < a.T) {
+      int id = s_id[base];
+      for (int i = 1; i < 16 && t0 + base + i < a.T; ++i) id = s_id[base + i] == s_id[base] ? id : kMixed;
+      a.group[t0 / 16 + g] = id >= 0 && s_big[g] ? kMixed : id;
+    }
+  }
+  if (!ok) {   // a wait gave up: leave the copies in flight time to land
+    const uint64_t since = gtimer();
+    while (gtimer() - since < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kShrinkTokens));
+  }
+  if (!ok && tid == 0 && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
+}
+
 // Large batches: persistent blocks, one per SM, over tiles of 128 outputs x NT
 // tokens (NT <= 256, a multiple of 16).  Warp 0 brings 64-wide K steps of W and x
 // by TMA into a ring, warp 1 multiplies, eight warps empty the accumulators: two
@@ -745,6 +829,27 @@ static moe_status map_rows(CUtensorMap* m, const void* base, int dtype, uint64_t
   return MOE_OK;
 }
 
+// 256 threads a block, clusters of cs along x, started early (programmatic dependent launch).
+template <typename... KArgs, typename... Args>
+static moe_status launch_cluster(void (*kernel)(KArgs...), dim3 grid, int cs, size_t smem, cudaStream_t s,
+                                 const char* name, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return check_launch(name);
+}
+
 template <typename TE, int NT>
 static moe_status launch_split(const LinearArgs& a, int dtype, cudaStream_t s) {
   using C = SplitCfg<NT>;
@@ -760,32 +865,23 @@ static moe_status launch_split(const LinearArgs& a, int dtype, cudaStream_t s) {
   // split H while the blocks still fit the SMs at once and each keeps two steps
   int cs = 1;
   while (cs < 8 && (long long)tiles_n * tiles_t * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cs, tiles_n, tiles_t);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cs, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mW, mX, a, a.n ? 1 : 0);
-  if (e != cudaSuccess) return cuda_fail(e, "linear_split_kernel");
-  return check_launch("linear_split_kernel");
+  return launch_cluster(kernel, dim3(cs, tiles_n, tiles_t), cs, C::kSmem, s, "linear_split_kernel", mW, mX, a,
+                        a.n ? 1 : 0);
 }
 
-template <typename TE, int RT>
-static moe_status launch_adapter_mma(const LinearArgs& a, cudaStream_t s) {
-  const size_t smem = (size_t)8 * 16 * a.R * sizeof(float);
-  auto kernel = adapter_mma_kernel<TE, RT>;
+template <typename TE>
+static moe_status launch_shrink(const LinearArgs& a, int dtype, cudaStream_t s) {
+  CUtensorMap mA, mX;
+  moe_status st = map_rows(&mA, a.A, dtype, a.H, (uint64_t)a.n * a.R, a.H, a.R);
+  if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.H, a.T, a.ld_x, kShrinkTokens);
+  if (st != MOE_OK) return st;
+  auto kernel = adapter_shrink_kernel<TE>;
   static char allowed[64];
-  MOE_CUDA(allow_smem(kernel, (size_t)8 * 16 * 8 * RT * sizeof(float), allowed));
-  cudaError_t e = launch_pdl(kernel, dim3((a.T + 15) / 16, 4), dim3(256), smem, s, a);
-  if (e != cudaSuccess) return cuda_fail(e, "adapter_mma_kernel");
-  return check_launch("adapter_mma_kernel");
+  MOE_CUDA(allow_smem(kernel, kShrinkSmem, allowed));
+  const int tiles = (a.T + kShrinkTokens - 1) / kShrinkTokens, nk = (a.H + 63) / 64;
+  int cs = 1;
+  while (cs < 8 && (long long)tiles * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
+  return launch_cluster(kernel, dim3(cs, tiles), cs, kShrinkSmem, s, "adapter_shrink_kernel", mA, mX, a);
 }
 
 // Whether a call is large: with one block per SM, tiles of 128 x 128 fill them.
@@ -837,12 +933,8 @@ static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) 
       cudaError_t e = launch_pdl(adapter_dot_kernel<TE>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, a);
       if (e != cudaSuccess) return cuda_fail(e, "adapter_dot_kernel");
       st = check_launch("adapter_dot_kernel");
-    } else if (a.R <= 32) {
-      st = launch_adapter_mma<TE, 4>(a, s);
-    } else if (a.R <= 64) {
-      st = launch_adapter_mma<TE, 8>(a, s);
     } else {
-      st = launch_adapter_mma<TE, 16>(a, s);
+      st = launch_shrink<TE>(a, dtype, s);
     }
     if (st != MOE_OK) return st;
   }

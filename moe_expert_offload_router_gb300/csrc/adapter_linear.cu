@@ -145,13 +145,13 @@ __device__ __forceinline__ void mma_k16(uint32_t d, uint64_t a, uint64_t b, uint
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar)) : "memory");
 }
-// A place in a ring of N stages and the parity of its current pass.
-template <int N>
+// A place in a ring of stages and the parity of its current pass.
 struct RingPos {
-  int stage = 0;
+  int stages, stage = 0;
   uint32_t parity = 0;
+  __device__ __forceinline__ explicit RingPos(int n) : stages(n) {}
   __device__ __forceinline__ void next() {
-    if (++stage == N) stage = 0, parity ^= 1;
+    if (++stage == stages) stage = 0, parity ^= 1;
   }
 };
 // kind::f16, D fp32, A and B of one 16-bit type, both K-major, M = 128.
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
 
   if (warp == 0) {
     if (elect_one()) {
-      RingPos<C::kStages> r;
+      RingPos r(C::kStages);
       for (int k = k0; k < k1; ++k) {
         if (k - k0 >= C::kStages && !wait_bar(&empty[r.stage], r.parity ^ 1, &s_err)) break;
         uint8_t* st = sm + r.stage * C::kStage;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
     if (elect_one()) {
       const uint32_t idesc = idesc_f16(NT, std::is_same<TE, __nv_bfloat16>::value);
       const uint64_t d0 = umma_desc_sw128(su32(sm));
-      RingPos<C::kStages> r;
+      RingPos r(C::kStages);
       for (int k = k0; k < k1; ++k) {
         if (!wait_bar(&full[r.stage], r.parity, &s_err)) break;
         tc_fence_after();
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
   const uint32_t tmem = tmem_slot;
   const int per = kRows / a.R;
   bool ok = true;
-  RingPos<kShrinkStages> r;
+  RingPos r(kShrinkStages);
   bool wrapped = false;
   uint32_t turn = 0;
   float* part = reinterpret_cast<float*>(sm);   // [tokens][128]
@@ -588,14 +588,14 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
 // times u's leading bits, and B[a] times the next ones (two terms of 16-bit type:
 // 16 significand bits of u with bf16, 22 with f16).  A group of several adapters
 // is done token by token in the epilogue with u in fp32.
-constexpr int kStreamStages = 4;
-constexpr int kStreamStage = kATile + 256 * 128;
-constexpr int kStreamSmem = kStreamStages * kStreamStage + 1024;
+constexpr int kStreamStages = 8;   // at most: as many as fit 208 KB
+constexpr int kStreamBytes = 208 * 1024;
 constexpr int kStreamThreads = 320;   // TMA, MMA, eight epilogue warps
 constexpr int kF32Chunk = 8;          // K steps in one accumulator for fp32 results: 512 products a sum
 
 struct StreamPlan {
-  int nt, tiles_n, tiles, nk, chunk;   // tokens of a tile, tiles of outputs, all tiles, K steps, K steps of an accumulator
+  int nt, stages, tiles_n, tiles;   // tokens of a tile, stages of the ring, tiles of outputs, all tiles
+  int nk, chunk;                    // K steps, K steps of an accumulator
 };
 
 template <typename TE, bool CHUNKS>
@@ -633,6 +633,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   if (!a.n) pdl_wait();   // as in linear_split_kernel
   pdl_launch_dependents();
   const int groups = pl.nt / 16;
+  const uint32_t bytes = kATile + pl.nt * 128;   // of a stage
   const int rchunks = (a.R + 63) / 64;
   bool ok = true;
 
@@ -653,13 +654,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   };
 
   if (warp == 0) {
-    RingPos<kStreamStages> r;
+    RingPos r(pl.stages);
     bool wrapped = false;
-    const uint32_t bytes = kATile + pl.nt * 128;
     const bool lead = elect_one();
     auto stage = [&](const CUtensorMap* ma, const CUtensorMap* mb, int ka, int rowa, int rowb) {
       if (wrapped && !wait_bar(&empty[r.stage], r.parity ^ 1, &s_err)) return false;
-      uint8_t* st = sm + r.stage * kStreamStage;
+      uint8_t* st = sm + r.stage * bytes;
       mbar_expect_tx(&full[r.stage], bytes);
       tma_2d(st, ma, ka, rowa, &full[r.stage]);
       tma_2d(st + kATile, mb, ka, rowb, &full[r.stage]);
@@ -682,8 +682,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       });
     }
   } else if (warp == 1) {
-    RingPos<kStreamStages> r;
-    RingPos<2> acc;
+    RingPos r(pl.stages);
+    RingPos acc(2);
     int used = 0;   // accumulators handed over so far (up to 2)
     const bool bf16 = std::is_same<TE, __nv_bfloat16>::value, lead = elect_one();
     const uint32_t idesc = idesc_f16(pl.nt, bf16);
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           for (int i = k; i < end && ok; ++i) {
             if (!(ok = wait_bar(&full[r.stage], r.parity, &s_err))) break;
             tc_fence_after();
-            const uint64_t da = d0 + (uint32_t)(r.stage * (kStreamStage / 16)), db = da + kATile / 16;
+            const uint64_t da = d0 + r.stage * (bytes / 16), db = da + kATile / 16;
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma_k16(d, da + 2 * j, db + 2 * j, idesc, i != k || j);
             mma_commit(&empty[r.stage]);
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
               for (int c = 0; c < 2 * rchunks; ++c) {
                 if (!(ok = wait_bar(&full[r.stage], r.parity, &s_err))) break;
                 tc_fence_after();
-                const uint64_t da = d0 + (uint32_t)(r.stage * (kStreamStage / 16)), db = da + kATile / 16 + g * 128;
+                const uint64_t da = d0 + r.stage * (bytes / 16), db = da + kATile / 16 + g * 128;
                 const int left = a.R - (c / 2) * 64, steps = left >= 64 ? 4 : (left + 15) / 16;
                 for (int j = 0; j < steps; ++j) mma_k16(d + g * 16, da + 2 * j, db + 2 * j, id16, 1);
                 mma_commit(&empty[r.stage]);
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     constexpr int kHalf = CHUNKS ? 64 : 128;                  // tokens of the tile that a warp takes
     const int q = warp & 3, c0 = ((warp - 2) >> 2) * kHalf;   // its 32 outputs, its first token
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    RingPos<2> acc;
+    RingPos acc(2);
     for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
       const int n = tile % pl.tiles_n * kRows + q * 32 + lane, t0 = tile / pl.tiles_n * pl.nt;
       float v[CHUNKS ? kHalf : 16];
@@ -864,7 +864,7 @@ static moe_status launch_split(const LinearArgs& a, int dtype, cudaStream_t s) {
   MOE_ARG(tiles_n <= 65535 && tiles_t <= 65535, "T or N too large");
   // split H while the blocks still fit the SMs at once and each keeps two steps
   int cs = 1;
-  while (cs < 8 && (long long)tiles_n * tiles_t * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
+  while (cs < (tiles_n * tiles_t <= 8 ? 8 : 4) && (long long)tiles_n * tiles_t * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
   return launch_cluster(kernel, dim3(cs, tiles_n, tiles_t), cs, C::kSmem, s, "linear_split_kernel", mW, mX, a,
                         a.n ? 1 : 0);
 }
@@ -912,10 +912,12 @@ static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) 
     if (st == MOE_OK) st = map_rows(&mL, a.u_lo, dtype, a.R, a.T, a.R, pl.nt);
   }
   if (st != MOE_OK) return st;
+  const int fit = kStreamBytes / (kATile + pl.nt * 128);
+  pl.stages = fit < kStreamStages ? fit : kStreamStages;
   auto kernel = chunks ? linear_stream_kernel<TE, true> : linear_stream_kernel<TE, false>;
   static char allowed[2][64];
-  MOE_CUDA(allow_smem(kernel, kStreamSmem, allowed[chunks]));
-  cudaError_t e = launch_pdl(kernel, dim3(pl.tiles < sms ? pl.tiles : sms), dim3(kStreamThreads), kStreamSmem, s, mW,
+  MOE_CUDA(allow_smem(kernel, kStreamBytes + 1024, allowed[chunks]));
+  cudaError_t e = launch_pdl(kernel, dim3(pl.tiles < sms ? pl.tiles : sms), dim3(kStreamThreads), kStreamBytes + 1024, s, mW,
                              mX, mB, mH, mL, a, pl);
   if (e != cudaSuccess) return cuda_fail(e, "linear_stream_kernel");
   return check_launch("linear_stream_kernel");

@@ -8,14 +8,16 @@ there is no fallback path.
 """
 import importlib
 
-_SUBMODULES = ("build", "layer", "_lib")
+_SUBMODULES = ("build", "layer", "block", "_lib")
+_HOST = {"DecodeLayerRunner": "layer", "PrefillStreamer": "layer", "Routing": "layer", "BlockWeights": "block",
+         "RoutedBlocks": "block"}
 
 
 def __getattr__(name):
     if name in _SUBMODULES or name.startswith("__"):
         raise AttributeError(name)   # the import system then loads the submodule
-    if name in ("DecodeLayerRunner", "PrefillStreamer"):
-        found = getattr(importlib.import_module(__name__ + ".layer"), name)
+    if name in _HOST:
+        found = getattr(importlib.import_module(__name__ + "." + _HOST[name]), name)
     else:
         lib = importlib.import_module(__name__ + "._lib")
         try:

@@ -45,9 +45,42 @@ from __future__ import annotations
 
 from typing import Optional
 
+from dataclasses import dataclass
+
 import torch
 
 from . import _lib as L
+
+
+@dataclass(frozen=True)
+class Routing:
+    """How a layer's logits become experts and weights (``moe_route``), beyond the
+    runners' default (softmax, top-k, renormalised: ``moe_router_topk``).
+
+    ``bias``: one device fp32 [E] balance bias for every layer, or a sequence with
+    one (or None) per layer.  ``load``: device int32 [layers, E], counts added per
+    call (cleared by the caller); what a bias is moved by."""
+    score: int = L.MOE_SCORE_SIGMOID
+    bias: object = None
+    n_group: int = 1
+    topk_group: int = 1
+    group_score: int = L.MOE_GROUP_TOP2
+    renorm: bool = True
+    scale: float = 1.0
+    load: object = None
+
+    def __call__(self, layer: int, logits, k: int, ids, w, stream):
+        bias = self.bias[layer] if isinstance(self.bias, (list, tuple)) else self.bias
+        L.moe_route(logits, k, self.score, bias, self.n_group, self.topk_group, self.group_score, self.renorm,
+                    self.scale, topk_ids=ids, topk_w=w, load=None if self.load is None else self.load[layer],
+                    stream=stream)
+
+
+def _route(routing, layer, logits, k, ids, w, stream):
+    if routing is None:
+        L.moe_router_topk(logits, k, True, ids, w, stream)
+    else:
+        routing(layer, logits, k, ids, w, stream)
 
 
 class DecodeLayerRunner:
@@ -71,6 +104,7 @@ class DecodeLayerRunner:
     * ``assume_resident``: every key has its slot (a cache of L * E slots);
       no copies, no host waits.
     * ``int2_cache`` and ``ladder`` = (a, b): the precision ladder.
+    * ``routing``: a :class:`Routing`; None for softmax, top-k, renormalised.
     """
 
     # overlap="auto" overlaps copies and compute from this many pairs per call:
@@ -81,7 +115,8 @@ class DecodeLayerRunner:
                  T_max: int, device=None, int2_cache: Optional[L.moe_cache] = None,
                  ladder=None, assume_resident: bool = False, copy: str = "engine",
                  overlap=False, copy_ctas: int = 32, graph: bool = False, copy_parts: int = 1,
-                 down_parts: int = 1):
+                 down_parts: int = 1, routing: Optional[Routing] = None):
+        self.routing = routing
         self.cache, self.views, self.E, self.k, self.T_max = cache, views, E, k, T_max
         self.dev = torch.device(device or "cuda")
         self.c2, self.ladder = int2_cache, ladder
@@ -342,7 +377,7 @@ class DecodeLayerRunner:
             with torch.cuda.graph(g):
                 s = torch.cuda.current_stream(self.dev)
                 ids, w, slots = self.ids[:T], self.w[:T], self.slots[:T]
-                L.moe_router_topk(lg, self.k, True, ids, w, s)
+                _route(self.routing, layer_id, lg, self.k, ids, w, s)
                 self._run_device(layer_id, T, ids, w, slots, xb, yb, s)
         finally:
             self._capturing = False
@@ -380,7 +415,7 @@ class DecodeLayerRunner:
         else:
             capture_after = False
         ids, w, slots = self.ids[:T], self.w[:T], self.slots[:T]
-        L.moe_router_topk(logits, k, True, ids, w, stream)
+        _route(self.routing, layer_id, logits, k, ids, w, stream)
         if self.copy == "device" and not self.assume_resident:
             if self.ladder is None:
                 self.stats["calls"] += 1
@@ -460,7 +495,9 @@ class PrefillStreamer:
     prefill; the buffer is then refilled with layer l + 2.
     """
 
-    def __init__(self, h_bank, num_layers: int, E: int, H: int, I: int, k: int, T_max: int, device=None):
+    def __init__(self, h_bank, num_layers: int, E: int, H: int, I: int, k: int, T_max: int, device=None,
+                 routing: Optional[Routing] = None):
+        self.routing = routing
         self.bank, self.L, self.E, self.H, self.I, self.k = h_bank, num_layers, E, H, I, k
         self.dev = torch.device(device or "cuda")
         self.B = L.moe_fp4_expert_bytes(H, I)
@@ -508,7 +545,7 @@ class PrefillStreamer:
             self._load(layer, stream)
         T = logits.shape[0]
         ids, w = self.ids[:T], self.w[:T]
-        L.moe_router_topk(logits, self.k, True, ids, w, stream)
+        _route(self.routing, layer, logits, self.k, ids, w, stream)
         stream.wait_event(self.loaded[b])
         L.moe_expert_prefill(self.views[b], x, ids, w, y, self.ws, self.err, stream)
         if layer + 2 < self.L:

@@ -639,8 +639,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
   // the runs of groups that share an adapter among a tile's (lane g holds group
   // g's entry, kMixed past T): f(adapter, first group, groups)
-  auto group_of = [&](int t0) {
-    return a.n && lane < groups && t0 + lane * 16 < a.T ? a.group[t0 / 16 + lane] : kMixed;
+  auto group_of = [&](int t0) { return lane < groups && t0 + lane * 16 < a.T ? a.group[t0 / 16 + lane] : kMixed; };
+  // u and the groups are waited for once, as late as the first tile allows; later tiles load their
+  // groups before their K steps
+  bool there = false;
+  int mine = kMixed;
+  auto groups_early = [&](int t0) {
+    if (there) mine = group_of(t0);
+  };
+  auto groups_now = [&](int t0) {
+    if (there) return;
+    pdl_wait();
+    there = true;
+    mine = group_of(t0);
   };
   auto runs = [&](int mine, auto f) {
     uint32_t left = __ballot_sync(0xffffffffu, mine >= 0);
@@ -669,12 +680,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     };
     for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
       const int n0 = tile % pl.tiles_n * kRows, t0 = tile / pl.tiles_n * pl.nt;
+      groups_early(t0);
       if (lead)
         for (int k = 0; k < pl.nk && ok; ++k) ok = stage(&mW, &mX, k * 64, n0, t0);
       ok = __all_sync(0xffffffffu, ok);
       if (!a.n || !ok) continue;
-      pdl_wait();   // u and the groups (returns at once after the first tile)
-      runs(group_of(t0), [&](int id, int, int) {
+      groups_now(t0);
+      runs(mine, [&](int id, int, int) {
         if (lead)
           for (int c = 0; c < rchunks && ok; ++c)
             ok = stage(&mB, &mH, c * 64, id * a.N + n0, t0) && stage(&mB, &mL, c * 64, id * a.N + n0, t0);
@@ -690,6 +702,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     const uint64_t d0 = umma_desc_sw128(su32(sm));
     for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
       const int t0 = tile / pl.tiles_n * pl.nt;
+      groups_early(t0);
       for (int k = 0; k < pl.nk && ok; k += pl.chunk) {
         const uint32_t d = tmem + acc.stage * 256;
         const int end = k + pl.chunk < pl.nk ? k + pl.chunk : pl.nk;
@@ -708,8 +721,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         }
         ok = __all_sync(0xffffffffu, ok);
         if (a.n && end == pl.nk && ok) {
-          pdl_wait();
-          runs(group_of(t0), [&](int id, int g, int len) {
+          groups_now(t0);
+          runs(mine, [&](int id, int g, int len) {
             if (lead) {
               const uint32_t id16 = idesc_f16(len * 16, bf16);
               for (int c = 0; c < 2 * rchunks; ++c) {
@@ -738,6 +751,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
       const int n = tile % pl.tiles_n * kRows + q * 32 + lane, t0 = tile / pl.tiles_n * pl.nt;
       float v[CHUNKS ? kHalf : 16];
+      groups_early(t0);
       auto columns = [&](int c, float* f, bool add) {   // 16 of the accumulator's columns
         uint32_t w[16];
         tmem_ld16(tmem + lanes + acc.stage * 256 + c0 + c * 16, w);
@@ -763,9 +777,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         ok = __all_sync(0xffffffffu, wait_bar(&acc_full[acc.stage], acc.parity, &s_err));
         tc_fence_after();
       }
-      if (a.n) pdl_wait();
+      if (a.n) groups_now(t0);
       const uint32_t mixed =
-          a.n ? __ballot_sync(0xffffffffu, lane < groups && group_of(t0) == kMixed) >> (c0 / 16) : 0;
+          a.n ? __ballot_sync(0xffffffffu, lane < groups && t0 + lane * 16 < a.T && mine == kMixed) >> (c0 / 16) : 0;
 #pragma unroll
       for (int c = 0; c < kHalf / 16; ++c) {
         const int t1 = t0 + c0 + c * 16;

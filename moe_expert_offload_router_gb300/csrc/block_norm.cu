@@ -286,19 +286,27 @@ __device__ __forceinline__ void ring_load(const R& ring, int stage, int piece, F
   widen(q, (const T*)nullptr, e);
 }
 
+template <typename R>
+__device__ __forceinline__ void put_slot(const R& slots, int piece, const F2* e) {
+  const float2 a = unpack2(e[0]), b = unpack2(e[1]), c = unpack2(e[2]), d = unpack2(e[3]);
+  *reinterpret_cast<float4*>(slots.at(0, piece)) = make_float4(a.x, a.y, b.x, b.y);
+  *reinterpret_cast<float4*>(slots.at(0, piece + 1)) = make_float4(c.x, c.y, d.x, d.y);
+}
+
 // Threads an SM is to hold at once: 64 registers a thread are enough for eight
 // columns of the forward, 128 for the rest.
 template <int VEC, int NV, int NT, bool BWD>
 constexpr int kResident = BWD || NV * VEC > 8 ? (kBlock<NT> > 512 ? kBlock<NT> : 512) : 1024;
 
 // Rows of the ring: as many as the resident threads leave shared memory for, at
-// most 4; 0: rows are loaded straight to registers (single elements).
+// most 4; 0: rows are loaded straight to registers (single elements, and the
+// gradient's longest rows).
 template <typename TX, typename TY, int VEC, int NV, int NT, bool BWD>
 constexpr int ring_rows() {
   if (VEC == 1) return 0;
-  const int bytes = NV * 8 * (int)(sizeof(TX) + sizeof(TY)) * (BWD ? 2 : 1);
-  const int most = 200 * 1024 / (kResident<VEC, NV, NT, BWD> * bytes);
-  return most < 4 ? most : 4;
+  const int bytes = NV * 8 * (int)(sizeof(TX) + sizeof(TY)) * (BWD ? 2 : 1), weights = BWD && NV > 1 ? NV * 64 : 0;
+  const int most = (208 * 1024 / kResident<VEC, NV, NT, BWD> - weights) / bytes;
+  return most < 0 ? 0 : most < 4 ? most : 4;
 }
 
 template <typename TX, typename TY, int VEC, int NV, int NT, int S>
@@ -418,8 +426,10 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
   constexpr int P = kElems<VEC>;
   constexpr int kRows = kBlock<NT> / NT;
   constexpr int kPX = kPieces<TX>, kPY = kPieces<TY>, kP = 2 * kPX + 2 * kPY;
-  constexpr bool kKeep = NV * VEC <= 8;   // the weights stay in registers
+  constexpr bool kKeep = NV == 1;               // the weights stay in registers,
+  constexpr bool kSlots = VEC == 8 && NV > 1;   // or as fp32 in slots of the thread's own in shared memory
   const Ring<NT, NV * kP> ring{ring_smem};
+  const Ring<NT, NV * 4> slots{ring_smem + (size_t)S * NV * kP * 16 * kBlock<NT>};
   const int tid = threadIdx.x % NT, H = a.H;
   const float inv_h = 1.f / (float)H;
   const long long step = (long long)gridDim.x * kRows;
@@ -464,6 +474,14 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
   for (int i = 0; i < NV; ++i) {
     const int c = (i * NT + tid) * VEC;
     if (kKeep && c < H) load_weights<VEC>(a, c, kw[i], kn[i]);
+    if constexpr (kSlots) {
+      if (c < H) {
+        E w[P], nx[P];
+        load_weights<VEC>(a, c, w, nx);
+        put_slot(slots, i * 4, w);
+        put_slot(slots, i * 4 + 2, nx);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < P; ++j) acc_e[i][j] = acc_n[i][j] = splat<E>(0.f);
   }
@@ -511,6 +529,9 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
       if constexpr (kKeep) {
 #pragma unroll
         for (int j = 0; j < P; ++j) w[j] = kw[i][j], nx[j] = kn[i][j];
+      } else if constexpr (kSlots) {
+        ring_load<float>(slots, 0, i * 4, w);
+        ring_load<float>(slots, 0, i * 4 + 2, nx);
       } else {
         load_weights<VEC>(a, c, w, nx);
       }
@@ -545,6 +566,9 @@ __global__ void __launch_bounds__(kBlock<NT>, kResident<VEC, NV, NT, true> / kBl
       if constexpr (kKeep) {
 #pragma unroll
         for (int j = 0; j < P; ++j) w[j] = kw[i][j], nx[j] = kn[i][j];
+      } else if constexpr (kSlots) {
+        ring_load<float>(slots, 0, i * 4, w);
+        ring_load<float>(slots, 0, i * 4 + 2, nx);
       } else {
         load_weights<VEC>(a, c, w, nx);
       }
@@ -637,63 +661,76 @@ static int bwd_blocks(long long T, int rows, int threads) {
   return (int)(need < most ? need : most);
 }
 
-template <typename TX, typename TY, int VEC, int NV, int NT>
-static moe_status launch_norm(const NormArgs& a, bool bwd, int* lines, cudaStream_t s) {
-  constexpr int kRows = kBlock<NT> / NT;
-  constexpr int SF = ring_rows<TX, TY, VEC, NV, NT, false>(), SB = ring_rows<TX, TY, VEC, NV, NT, true>();
-  if (!bwd) {
+template <bool BWD, typename TX, typename TY, int VEC, int NV, int NT>
+static moe_status launch_norm(const NormArgs& a, int* lines, cudaStream_t s) {
+  constexpr int kRows = kBlock<NT> / NT, S = ring_rows<TX, TY, VEC, NV, NT, BWD>();
+  if constexpr (!BWD) {
     const long long need = ((long long)a.T + kRows - 1) / kRows, most = (long long)device_sms() * (kResident<VEC, NV, NT, false> / kBlock<NT>);
-    constexpr size_t smem = (size_t)SF * NV * 8 * (sizeof(TX) + sizeof(TY)) * kBlock<NT>;
-    auto kernel = block_norm_kernel<TX, TY, VEC, NV, NT, SF>;
+    constexpr size_t smem = (size_t)S * NV * 8 * (sizeof(TX) + sizeof(TY)) * kBlock<NT>;
+    auto kernel = block_norm_kernel<TX, TY, VEC, NV, NT, S>;
     static char allowed[64];
     MOE_CUDA(allow_smem(kernel, smem, allowed));
     ProfScope ps(MOE_K_NORM, s);
     cudaError_t e = launch_pdl(kernel, dim3((unsigned)(need < most ? need : most)), dim3(kBlock<NT>), smem, s, a);
     if (e != cudaSuccess) return cuda_fail(e, "block_norm_kernel");
     return check_launch("block_norm_kernel");
+  } else {
+    constexpr size_t smem = ((size_t)S * NV * 16 * (sizeof(TX) + sizeof(TY)) + (VEC == 8 && NV > 1 ? NV * 64 : 0)) * kBlock<NT>;
+    const bool full = VEC == 8 && a.post && a.d_h && a.d_xo && a.gate_mode != MOE_GATE_TOKEN;
+    auto kernel = full ? block_norm_bwd_kernel<TX, TY, VEC, NV, NT, S, VEC == 8>
+                       : block_norm_bwd_kernel<TX, TY, VEC, NV, NT, S, false>;
+    static char allowed[2][64];
+    MOE_CUDA(allow_smem(kernel, smem, allowed[full]));
+    *lines = bwd_blocks(a.T, kRows, kBlock<NT>);
+    cudaError_t e = launch_pdl(kernel, dim3(*lines), dim3(kBlock<NT>), smem, s, a);
+    if (e != cudaSuccess) return cuda_fail(e, "block_norm_bwd_kernel");
+    return check_launch("block_norm_bwd_kernel");
   }
-  constexpr size_t smem = (size_t)SB * NV * 16 * (sizeof(TX) + sizeof(TY)) * kBlock<NT>;
-  const bool full = VEC == 8 && a.post && a.d_h && a.d_xo && a.gate_mode != MOE_GATE_TOKEN;
-  auto kernel = full ? block_norm_bwd_kernel<TX, TY, VEC, NV, NT, SB, VEC == 8>
-                     : block_norm_bwd_kernel<TX, TY, VEC, NV, NT, SB, false>;
-  static char allowed[2][64];
-  MOE_CUDA(allow_smem(kernel, smem, allowed[full]));
-  *lines = bwd_blocks(a.T, kRows, kBlock<NT>);
-  cudaError_t e = launch_pdl(kernel, dim3(*lines), dim3(kBlock<NT>), smem, s, a);
-  if (e != cudaSuccess) return cuda_fail(e, "block_norm_bwd_kernel");
-  return check_launch("block_norm_bwd_kernel");
 }
 
 // The shape a row is held in.  Rows of up to 512 columns (the gradient: 256) take
-// one warp, with no barriers at all; longer ones the fewest threads that hold 8 columns each, or
-// 16 where 8 would take more than 1024 threads (the gradient: 512, so that its
-// two sums of every column keep 128 registers); where rows cannot be read in
-// 16-byte vectors, single elements, 4 to 16 a thread.
-template <typename TX, typename TY>
-static moe_status norm_by_shape(const NormArgs& a, bool vec, bool bwd, int* lines, cudaStream_t s) {
+// one warp, with no barriers at all; longer ones the fewest threads that hold 8
+// columns each.  The gradient of 16-bit rows takes 16 a thread from 1025 columns
+// on: half the warps to add up, and two blocks an SM whose sums wait in turn (at
+// T = 8192, H = 4096: 81.8 us with 8 columns a thread, 74.6 with 16).  Rows of fp32 leave no room for that ring; past 4096
+// columns they take 16 as well, past 1024 threads the forward does.  Where rows
+// cannot be read in 16-byte vectors: single elements, 4 to 16 a thread.
+template <bool BWD, typename TX, typename TY>
+static moe_status norm_by_shape(const NormArgs& a, bool vec, int* lines, cudaStream_t s) {
   const int H = a.H;
+  constexpr bool kNarrow = sizeof(TX) + sizeof(TY) == 4;
   if (!vec) {
-    if (H <= 512) return launch_norm<TX, TY, 1, 4, 128>(a, bwd, lines, s);
-    if (H <= 2048) return launch_norm<TX, TY, 1, 8, 256>(a, bwd, lines, s);
-    if (H <= 8192) return launch_norm<TX, TY, 1, 16, 512>(a, bwd, lines, s);
-    return launch_norm<TX, TY, 1, 16, 1024>(a, bwd, lines, s);
+    if (H <= 512) return launch_norm<BWD, TX, TY, 1, 4, 128>(a, lines, s);
+    if (H <= 2048) return launch_norm<BWD, TX, TY, 1, 8, 256>(a, lines, s);
+    if (H <= 8192) return launch_norm<BWD, TX, TY, 1, 16, 512>(a, lines, s);
+    return launch_norm<BWD, TX, TY, 1, 16, 1024>(a, lines, s);
   }
-  if (H <= 256) return launch_norm<TX, TY, 8, 1, 32>(a, bwd, lines, s);
-  if (H <= 512 && !bwd) return launch_norm<TX, TY, 8, 2, 32>(a, bwd, lines, s);
-  if (H <= 1024) return launch_norm<TX, TY, 8, 1, 128>(a, bwd, lines, s);
-  if (H <= 2048) return launch_norm<TX, TY, 8, 1, 256>(a, bwd, lines, s);
-  if (H <= 4096) return launch_norm<TX, TY, 8, 1, 512>(a, bwd, lines, s);
-  if (H <= 8192 && !bwd) return launch_norm<TX, TY, 8, 1, 1024>(a, bwd, lines, s);
-  if (H <= 8192) return launch_norm<TX, TY, 8, 2, 512>(a, bwd, lines, s);
-  return launch_norm<TX, TY, 8, 2, 1024>(a, bwd, lines, s);
+  if (H <= 256) return launch_norm<BWD, TX, TY, 8, 1, 32>(a, lines, s);
+  if constexpr (!BWD)
+    if (H <= 512) return launch_norm<BWD, TX, TY, 8, 2, 32>(a, lines, s);
+  if (H <= 1024) return launch_norm<BWD, TX, TY, 8, 1, 128>(a, lines, s);
+  if constexpr (BWD && kNarrow) {
+    if (H <= 2048) return launch_norm<BWD, TX, TY, 8, 2, 128>(a, lines, s);
+    if (H <= 4096) return launch_norm<BWD, TX, TY, 8, 2, 256>(a, lines, s);
+  } else {
+    if (H <= 2048) return launch_norm<BWD, TX, TY, 8, 1, 256>(a, lines, s);
+    if (H <= 4096) return launch_norm<BWD, TX, TY, 8, 1, 512>(a, lines, s);
+  }
+  if constexpr (BWD) {
+    if (H <= 8192) return launch_norm<BWD, TX, TY, 8, 2, 512>(a, lines, s);
+  } else {
+    if (H <= 8192) return launch_norm<BWD, TX, TY, 8, 1, 1024>(a, lines, s);
+  }
+  return launch_norm<BWD, TX, TY, 8, 2, 1024>(a, lines, s);
 }
 
-static moe_status norm_by_type(const NormArgs& a, int xd, int yd, bool vec, bool bwd, int* lines, cudaStream_t s) {
-  if (xd == MOE_DT_BF16) return norm_by_shape<__nv_bfloat16, __nv_bfloat16>(a, vec, bwd, lines, s);
-  if (xd == MOE_DT_F16) return norm_by_shape<__half, __half>(a, vec, bwd, lines, s);
-  if (yd == MOE_DT_BF16) return norm_by_shape<float, __nv_bfloat16>(a, vec, bwd, lines, s);
-  if (yd == MOE_DT_F16) return norm_by_shape<float, __half>(a, vec, bwd, lines, s);
-  return norm_by_shape<float, float>(a, vec, bwd, lines, s);
+template <bool BWD>
+static moe_status norm_by_type(const NormArgs& a, int xd, int yd, bool vec, int* lines, cudaStream_t s) {
+  if (xd == MOE_DT_BF16) return norm_by_shape<BWD, __nv_bfloat16, __nv_bfloat16>(a, vec, lines, s);
+  if (xd == MOE_DT_F16) return norm_by_shape<BWD, __half, __half>(a, vec, lines, s);
+  if (yd == MOE_DT_BF16) return norm_by_shape<BWD, float, __nv_bfloat16>(a, vec, lines, s);
+  if (yd == MOE_DT_F16) return norm_by_shape<BWD, float, __half>(a, vec, lines, s);
+  return norm_by_shape<BWD, float, float>(a, vec, lines, s);
 }
 
 // Whether a tensor's rows can be read in 16-byte vectors.
@@ -737,13 +774,13 @@ extern "C" moe_status moe_block_norm(int T, int H, int x_dtype, int y_dtype, int
   a.ld_x = ld_x, a.ld_y = ld_y, a.x_out = x_out, a.h = h, a.ld_xo = ld_x_out, a.ld_h = ld_h;
   const bool vec = H % 8 == 0 && vec_ok(x, ld_x, x_dtype) && vec_ok(y, ld_y, y_dtype) &&
                    vec_ok(x_out, ld_x_out, x_dtype) && vec_ok(h, ld_h, y_dtype);
-  return norm_by_type(a, x_dtype, y_dtype, vec, false, nullptr, stream);
+  return norm_by_type<false>(a, x_dtype, y_dtype, vec, nullptr, stream);
 }
 
 extern "C" size_t moe_block_norm_backward_workspace(int T, int H) {
   if (T <= 0 || H <= 0 || H > 16384) return 0;
-  // one line of two sums a block; the narrowest blocks (128 threads, H <= 1024) are the most
-  return (size_t)bwd_blocks(T, 1, H <= 1024 ? 128 : H <= 2048 ? 256 : 512) * 2 * column_line(H) * sizeof(float);
+  // one line of two sums a block; the narrowest blocks that norm_by_shape may take are the most
+  return (size_t)bwd_blocks(T, 1, H <= 2048 ? 128 : H <= 4096 ? 256 : 512) * 2 * column_line(H) * sizeof(float);
 }
 
 extern "C" moe_status moe_block_norm_backward(int T, int H, int x_dtype, int y_dtype, int w_dtype, const void* x,
@@ -791,7 +828,7 @@ extern "C" moe_status moe_block_norm_backward(int T, int H, int x_dtype, int y_d
                    vec_ok(d_x, ld_d_x, x_dtype) && vec_ok(d_y, ld_d_y, y_dtype);
   int lines = 0;
   ProfScope ps(MOE_K_NORM_BWD, stream);
-  st = norm_by_type(a, x_dtype, y_dtype, vec, true, &lines, stream);
+  st = norm_by_type<true>(a, x_dtype, y_dtype, vec, &lines, stream);
   if (st != MOE_OK || !sums) return st;
   const bool channel = gate_mode == MOE_GATE_CHANNEL;
   cudaError_t e = launch_pdl(column_sum_kernel, dim3((H + 31) / 32, next_weight ? 2 : 1), dim3(256), 0, stream,

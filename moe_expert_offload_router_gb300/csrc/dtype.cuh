@@ -54,6 +54,7 @@ inline cudaError_t allow_smem(K kernel, size_t bytes, char (&done)[64]) {
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && __atomic_load_n(&done[dev], __ATOMIC_RELAXED)) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) cudaGetLastError();   // reported here, not by the next launch's check
   if (e == cudaSuccess && dev >= 0 && dev < 64) __atomic_store_n(&done[dev], (char)1, __ATOMIC_RELAXED);
   return e;
 }

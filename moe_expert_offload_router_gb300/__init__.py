@@ -8,7 +8,7 @@ there is no fallback path.
 """
 import importlib
 
-_SUBMODULES = ("build", "layer", "block", "_lib")
+_SUBMODULES = ("build", "layer", "block", "_lib", "_binding")
 _HOST = {"DecodeLayerRunner": "layer", "PrefillStreamer": "layer", "Routing": "layer", "BlockWeights": "block",
          "RoutedBlocks": "block"}
 

@@ -5,7 +5,6 @@ if the library is not built this module raises on import."""
 from __future__ import annotations
 
 import ctypes as C
-import functools
 import os
 
 import torch
@@ -499,247 +498,24 @@ def moe_rms_carry(y, eps: float, x_next, stream=None):
     _check(_lib.moe_rms_carry(_p(y), T, H, eps, _p(x_next), _s(stream)))
 
 
-_DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16,
-       torch.int16: MOE_DT_BF16}   # int16: bf16 bits, as the expert calls take them
+# Routing, block norms and the adapter projection: calls of microseconds, whose
+# argument checks are compiled (csrc/binding.cpp) into functions of these names.
+from . import _binding  # noqa: E402  (needs torch's libraries and the library above loaded)
 
-
-def _dt(t) -> int:
-    d = _DT.get(t.dtype)
-    if d is None:
-        raise ValueError(f"unsupported tensor type {t.dtype}")
-    return d
-
-
-# The checks below run in every call of microseconds: plain comparisons, no loops.
-
-
-def _rows(t, shape, what: str):
-    """(pointer, row distance) of a [T, n] tensor whose rows may be strided."""
-    if t.shape != shape:
-        raise ValueError(f"{what} must be {list(shape)}, got {tuple(t.shape)}")
-    sr, sc = t.stride()
-    n = shape[1]
-    if sc != 1 and n > 1:
-        raise ValueError(f"{what}: the elements of a row must be adjacent (strides {t.stride()})")
-    if sr < n:
-        if shape[0] > 1:
-            raise ValueError(f"{what}: rows overlap (strides {t.stride()})")
-        sr = n
-    return t.data_ptr(), sr
-
-
-def _vec(t, shape, dtype, what: str):
-    """Pointer of a dense tensor of the given shape and type."""
-    if t.shape != shape or t.dtype is not dtype:
-        raise ValueError(f"{what} must be {list(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
-    return t.data_ptr()
-
-
-def _mask(t, T: int):
-    return None if t is None else _vec(t, (T,), torch.bool if t.dtype is torch.bool else torch.uint8, "token_mask")
-
-
-def _scratch(nbytes: int, dev, stream):
-    """A workspace for one call on `stream`: freed for that stream's later use."""
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    return ws
-
-
-_I32, _F32 = torch.int32, torch.float32
-
-
-def moe_route(logits, k: int, score: int = MOE_SCORE_SOFTMAX, bias=None, n_group: int = 1, topk_group: int = 1,
-              group_score: int = MOE_GROUP_TOP2, renorm: bool = True, scale: float = 1.0, token_mask=None,
-              topk_ids=None, topk_w=None, load=None, stream=None):
-    """(topk_ids, topk_w) of logits [T, E] (fp32, bf16 or f16; rows may be strided)."""
-    shape = T, E = logits.shape
-    if topk_ids is None:
-        topk_ids = torch.empty((T, k), dtype=_I32, device=logits.device)
-    if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=_F32, device=logits.device)
-    p, ld = _rows(logits, shape, "logits")
-    _check(_lib.moe_route(p, _dt(logits), ld, T, E, k, score, None if bias is None else _vec(bias, (E,), _F32, "bias"),
-                          n_group, topk_group, group_score, 1 if renorm else 0, scale, _mask(token_mask, T),
-                          _vec(topk_ids, (T, k), _I32, "topk_ids"), _vec(topk_w, (T, k), _F32, "topk_w"),
-                          None if load is None else _vec(load, (E,), _I32, "load"), _s(stream)))
-    return topk_ids, topk_w
-
-
-def moe_route_backward(logits, topk_ids, d_w, score: int = MOE_SCORE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
-                       token_mask=None, d_logits=None, stream=None):
-    """d_logits [T, E] (the logits' type) from d_w [T, k], the choice topk_ids held fixed."""
-    shape = T, E = logits.shape
-    k = topk_ids.shape[1]
-    if d_logits is None:
-        d_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    if d_logits.dtype is not logits.dtype:
-        raise ValueError(f"d_logits must be of the logits' type {logits.dtype}, got {d_logits.dtype}")
-    p, ld = _rows(logits, shape, "logits")
-    pd, ldd = _rows(d_logits, shape, "d_logits")
-    _check(_lib.moe_route_backward(p, _dt(logits), ld, T, E, k, score, 1 if renorm else 0, scale,
-                                   _mask(token_mask, T), _vec(topk_ids, (T, k), _I32, "topk_ids"),
-                                   _vec(d_w, (T, k), _F32, "d_w"), pd, ldd, _s(stream)))
-    return d_logits
-
-
-def _norm_weights(T, H, post_weight, gate, next_weight):
-    """(w_dtype, post pointer, gate pointer, gate mode, next pointer): all of one type."""
-    one = post_weight if post_weight is not None else gate if gate is not None else next_weight
-    if one is None:
-        return MOE_DT_F32, None, None, MOE_GATE_NONE, None
-    d, pp, pg, pn, mode, ch = one.dtype, None, None, None, MOE_GATE_NONE, (H,)
-    if post_weight is not None:
-        pp = _vec(post_weight, ch, d, "post_weight")
-    if gate is not None:   # [H]: for each channel; [T, 1]: for each token
-        mode = MOE_GATE_CHANNEL if gate.dim() == 1 else MOE_GATE_TOKEN
-        pg = _vec(gate, ch if mode == MOE_GATE_CHANNEL else (T, 1), d, "gate (of the weights' one type)")
-    if next_weight is not None:
-        pn = _vec(next_weight, ch, d, "next_weight (of the weights' one type)")
-    return _dt(one), pp, pg, mode, pn
-
-
-def _same_type(t, dtype, what: str):
-    if t is not None and t.dtype is not dtype:
-        raise ValueError(f"{what} must be of type {dtype}, got {t.dtype}")
-
-
-def moe_block_norm(x, y=None, post_weight=None, gate=None, residual_scale: float = 1.0, next_weight=None,
-                   eps: float = 1e-6, x_out=None, h=None, stream=None):
-    """(x_out, h) = (residual_scale x + gate n(y) post_weight, n(x_out) next_weight).
-
-    x [T, H] is the residual stream, y [T, H] a block's output (None: the norm
-    before a first block alone, no x_out unless one is given); gate [H] (each
-    channel) or [T, 1] (each token).  Without next_weight h is None."""
-    shape = T, H = x.shape
-    w_dtype, pp, pg, mode, pn = _norm_weights(T, H, post_weight, gate, next_weight)
-    like = y if y is not None else h if h is not None else x
-    if x_out is None and y is not None:
-        x_out = torch.empty(shape, dtype=x.dtype, device=x.device)
-    if h is None and next_weight is not None:
-        h = torch.empty(shape, dtype=like.dtype, device=x.device)
-    px, ldx = _rows(x, shape, "x")
-    py = po = ph = None
-    ldy = ldo = ldh = 0
-    if y is not None:
-        py, ldy = _rows(y, shape, "y")
-    if x_out is not None:
-        _same_type(x_out, x.dtype, "x_out")
-        po, ldo = _rows(x_out, shape, "x_out")
-    if h is not None:
-        _same_type(h, like.dtype, "h")
-        ph, ldh = _rows(h, shape, "h")
-    _check(_lib.moe_block_norm(T, H, _dt(x), _dt(like), w_dtype, px, ldx, py, ldy, pp, pg, mode, residual_scale, pn,
-                               eps, po, ldo, ph, ldh, _s(stream)))
-    return x_out, h
-
-
-@functools.lru_cache(maxsize=1024)
-def _norm_backward_bytes(T: int, H: int, device: int) -> int:
-    return _lib.moe_block_norm_backward_workspace(T, H)
+_binding.set_check(_check)
+moe_route = _binding.moe_route
+moe_route_backward = _binding.moe_route_backward
+moe_block_norm = _binding.moe_block_norm
+moe_block_norm_backward = _binding.moe_block_norm_backward
+moe_adapter_linear = _binding.moe_adapter_linear
 
 
 def moe_block_norm_backward_workspace(T: int, H: int) -> int:
-    return _norm_backward_bytes(T, H, torch.cuda.current_device() if torch.cuda.is_available() else -1)
-
-
-def moe_block_norm_backward(x, y, d_x_out, d_h, post_weight=None, gate=None, residual_scale: float = 1.0,
-                            next_weight=None, eps: float = 1e-6, d_x=None, d_y=None, d_post_weight=None, d_gate=None,
-                            d_next_weight=None, workspace=None, stream=None):
-    """(d_x, d_y, d_post_weight, d_gate, d_next_weight) of moe_block_norm; the weights'
-    gradients are fp32, and None where the weight is not given."""
-    shape = T, H = x.shape
-    dev = x.device
-    w_dtype, pp, pg, mode, pn = _norm_weights(T, H, post_weight, gate, next_weight)
-    like = y if y is not None else d_h if d_h is not None else x
-    if d_x is None:
-        d_x = torch.empty(shape, dtype=x.dtype, device=dev)
-    if d_y is None and y is not None:
-        d_y = torch.empty(shape, dtype=y.dtype, device=dev)
-    px, ldx = _rows(x, shape, "x")
-    py = pu = ph = pdy = pdp = pdg = pdn = None
-    ldy = ldu = ldh = lddy = 0
-    if y is not None:
-        py, ldy = _rows(y, shape, "y")
-    if d_x_out is not None:
-        _same_type(d_x_out, x.dtype, "d_x_out")
-        pu, ldu = _rows(d_x_out, shape, "d_x_out")
-    if d_h is not None:
-        _same_type(d_h, like.dtype, "d_h")
-        ph, ldh = _rows(d_h, shape, "d_h")
-    _same_type(d_x, x.dtype, "d_x")
-    pdx, lddx = _rows(d_x, shape, "d_x")
-    if d_y is not None:
-        _same_type(d_y, like.dtype, "d_y")
-        pdy, lddy = _rows(d_y, shape, "d_y")
-    if post_weight is not None:
-        if d_post_weight is None:
-            d_post_weight = torch.empty(H, dtype=_F32, device=dev)
-        pdp = _vec(d_post_weight, (H,), _F32, "d_post_weight")
-    if gate is not None:
-        if d_gate is None:
-            d_gate = torch.empty(gate.shape, dtype=_F32, device=dev)
-        pdg = _vec(d_gate, gate.shape, _F32, "d_gate")
-    if next_weight is not None:
-        if d_next_weight is None:
-            d_next_weight = torch.empty(H, dtype=_F32, device=dev)
-        pdn = _vec(d_next_weight, (H,), _F32, "d_next_weight")
-    if workspace is None:
-        workspace = _scratch(moe_block_norm_backward_workspace(T, H), dev, stream)
-    _check(_lib.moe_block_norm_backward(
-        T, H, _dt(x), _dt(like), w_dtype, px, ldx, py, ldy, pu, ldu, ph, ldh, pp, pg, mode, residual_scale, pn, eps,
-        pdx, lddx, pdy, lddy, pdp, pdg, pdn, _p(workspace), workspace.numel() * workspace.element_size(), _s(stream)))
-    return d_x, d_y, d_post_weight, d_gate, d_next_weight
-
-
-@functools.lru_cache(maxsize=1024)
-def _linear_bytes(T: int, H: int, N: int, n_adapters: int, R: int, device: int) -> int:
-    return _lib.moe_adapter_linear_workspace(T, H, N, n_adapters, R)
+    return _lib.moe_block_norm_backward_workspace(T, H)
 
 
 def moe_adapter_linear_workspace(T: int, H: int, N: int, n_adapters: int, R: int) -> int:
-    return _linear_bytes(T, H, N, n_adapters, R, torch.cuda.current_device() if torch.cuda.is_available() else -1)
-
-
-def moe_adapter_linear(x, weight, lora_a=None, lora_b=None, adapter_ids=None, lora_scale=None, out=None,
-                       out_dtype=None, workspace=None, d_error=None, stream=None):
-    """out [T, N] = x weight^T + lora_scale[a] (x lora_a[a]^T) lora_b[a]^T, a = adapter_ids[t] (< 0: none).
-
-    x [T, H] and weight [N, H] (rows may be strided), lora_a [n, R, H], lora_b
-    [n, N, R], all bf16 or all f16; out of x's type or fp32.  Without lora_a the
-    projection alone."""
-    shape = T, H = x.shape
-    N = weight.shape[0]
-    d = x.dtype
-    px, ldx = _rows(x, shape, "x")
-    pw, ldw = _rows(weight, (N, H), "weight")
-    _same_type(weight, d, "weight (as x)")
-    n = R = nb = 0
-    pa = pb = pi = ps = pws = None
-    if lora_a is not None:
-        if lora_b is None or adapter_ids is None:
-            raise ValueError("lora_a needs lora_b and adapter_ids")
-        n, R, _ = lora_a.shape
-        pa = _vec(lora_a, (n, R, H), d, "lora_a")
-        pb = _vec(lora_b, (n, N, R), d, "lora_b")
-        pi = _vec(adapter_ids, (T,), _I32, "adapter_ids")
-        if lora_scale is not None:
-            ps = _vec(lora_scale, (n,), _F32, "lora_scale")
-        if workspace is None:
-            nb = _linear_bytes(T, H, N, n, R, x.get_device())
-            workspace = _scratch(nb, x.device, stream)
-            pws = workspace.data_ptr()
-        else:
-            pws, nb = _p(workspace), workspace.numel() * workspace.element_size()
-    if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or d, device=x.device)
-    po, ldo = _rows(out, (T, N), "out")
-    _check(_lib.moe_adapter_linear(T, H, N, _dt(x), _dt(out), px, ldx, pw, ldw, n, R, pa, pb, pi, ps, po, ldo, pws, nb,
-                                   None if d_error is None else _p(d_error), _s(stream)))
-    return out
+    return _lib.moe_adapter_linear_workspace(T, H, N, n_adapters, R)
 
 
 def moe_debug_timeout_probe(limit_ns: int, d_status, stream=None):

@@ -1,5 +1,7 @@
 """Builds libmoe_gb300.so in-tree for sm_103a with nvcc (one translation unit per
-.cu file, compiled in parallel, then linked with the static CUDA runtime)."""
+.cu file, compiled in parallel, then linked with the static CUDA runtime), and
+beside it _binding.so, the compiled Python entry points of the short calls (g++,
+against the installed torch's headers)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -14,6 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,24 +45,57 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    """binding.cpp -> object, with the flags of the torch that will load it."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           "-isystem", sysconfig.get_path("include"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB, "-L", lib, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every kernel source and link the shared library; returns its path."""
+    """Compile every source and link the shared libraries; returns the C library's path."""
     srcs = sources()
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     hdrs.append(os.path.join(INCLUDE, "moe_gb300.h"))
-    if not force and os.path.exists(LIB):
-        newest = max(os.path.getmtime(p) for p in srcs + hdrs + [__file__])
-        if os.path.getmtime(LIB) >= newest:
+    if not force and os.path.exists(LIB) and os.path.exists(BINDING):
+        newest = max(os.path.getmtime(p) for p in srcs + hdrs + [os.path.join(CSRC, "binding.cpp"), __file__])
+        if min(os.path.getmtime(LIB), os.path.getmtime(BINDING)) >= newest:
             return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
+        bound = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        binding = bound.result()
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libmoe_gb300.so", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

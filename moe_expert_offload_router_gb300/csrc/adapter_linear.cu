@@ -51,37 +51,30 @@ struct Pair<__half> {
 
 // ------------------------------------------------------------ u = scale A x --
 
-// Few tokens: a warp takes kDots ranks of one token, each lane 16-byte chunks
-// of x and of the A rows.  Every token reads its own R x H of A (from L2 where
-// tokens share an adapter).
-constexpr int kDots = 2;
+// Few tokens: a block takes kDots ranks of one token, its four warps splitting H,
+// so that every load of a row of 4096 is under way at once.  Every token reads its
+// own R x H of A (from L2 where tokens share an adapter).
+constexpr int kDots = 4;
 template <typename TE>
 __global__ void __launch_bounds__(128) adapter_dot_kernel(const LinearArgs a) {
+  __shared__ float part[4][kDots];
   pdl_wait();
   pdl_launch_dependents();   // after the wait: the projection may read x from its start
-  const int per = a.R / kDots;
-  const long long w = (blockIdx.x * 128LL + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const long long t = w / per;
-  if (t >= a.T) return;
-  const int r0 = (int)(w % per) * kDots;
+  const int t = blockIdx.x, r0 = blockIdx.y * kDots, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int id = a.ids[t];
-  if (id >= a.n && a.err && lane == 0) atomicCAS(a.err, MOE_OK, MOE_ERR_INVALID);
+  if (id >= a.n && a.err && blockIdx.y == 0 && threadIdx.x == 0) atomicCAS(a.err, MOE_OK, MOE_ERR_INVALID);
   if (id < 0 || id >= a.n) return;
   const uint4* x = reinterpret_cast<const uint4*>(reinterpret_cast<const TE*>(a.x) + t * a.ld_x);
-  const int nc = a.H / 8;
-  const uint4* A[kDots];
-#pragma unroll
-  for (int r = 0; r < kDots; ++r)
-    A[r] = reinterpret_cast<const uint4*>(reinterpret_cast<const TE*>(a.A) + ((long long)id * a.R + r0 + r) * a.H);
+  const uint4* A = reinterpret_cast<const uint4*>(reinterpret_cast<const TE*>(a.A) + ((long long)id * a.R + r0) * a.H);
+  const int nc = a.H / 8;   // 16-byte chunks of a row
   float s[kDots] = {};
 #pragma unroll 4
-  for (int c = lane; c < nc; c += 32) {
+  for (int c = threadIdx.x; c < nc; c += 128) {
     const uint4 xv = x[c];
     const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
     for (int r = 0; r < kDots; ++r) {
-      const uint4 av = A[r][c];
+      const uint4 av = A[r * (long long)nc + c];
       const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -94,12 +87,14 @@ __global__ void __launch_bounds__(128) adapter_dot_kernel(const LinearArgs a) {
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int r = 0; r < kDots; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
-  if (lane < kDots) {
-    float v = s[0];
+  if (lane == 0)
 #pragma unroll
-    for (int r = 1; r < kDots; ++r) v = lane == r ? s[r] : v;
-    a.u[t * a.R + r0 + lane] = (a.scale ? a.scale[id] : 1.f) * v;
-  }
+    for (int r = 0; r < kDots; ++r) part[warp][r] = s[r];
+  __syncthreads();
+  if (threadIdx.x < kDots)
+    a.u[(long long)t * a.R + r0 + threadIdx.x] =
+        (a.scale ? a.scale[id] : 1.f) *
+        ((part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]));
 }
 
 // -------------------------------------------------------------- projection --
@@ -186,47 +181,25 @@ struct SplitCfg {
   static_assert(NT * kRows * 4 <= kStages * kStage, "the partial sums fit the stages");
 };
 
-// acc += B[a][n..n+3] . u[t] in fp32.
+// v[j] += B[a][n] . u[t1 + j] in fp32 for the tokens j of `who` (below `left`):
+// eight ranks at a time, B's in registers for all of them.  u is read for every
+// token and dropped where it is not asked for, so that no load waits for a branch.
 template <typename TE>
-__device__ __forceinline__ void add_adapter4(const LinearArgs& a, int id, long long t, int n, float* acc) {
-  const float4* u = reinterpret_cast<const float4*>(a.u + t * a.R);
-  const TE* B = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + n) * a.R;
-  for (int r = 0; r < a.R; r += 8) {
-    const float4 u0 = u[r / 4], u1 = u[r / 4 + 1];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (n + j >= a.N) break;
-      const uint4 b = *reinterpret_cast<const uint4*>(B + (long long)j * a.R + r);
-      float2 p = Pair<TE>::f32(b.x);
-      float s = fmaf(p.x, u0.x, p.y * u0.y);
-      p = Pair<TE>::f32(b.y);
-      s = fmaf(p.x, u0.z, fmaf(p.y, u0.w, s));
-      p = Pair<TE>::f32(b.z);
-      s = fmaf(p.x, u1.x, fmaf(p.y, u1.y, s));
-      p = Pair<TE>::f32(b.w);
-      s = fmaf(p.x, u1.z, fmaf(p.y, u1.w, s));
-      acc[j] += s;
-    }
-  }
-}
-
-// v[j] += B[a][n] . u[t1 + j] in fp32 for the tokens j of `who`: eight ranks at a
-// time, B's in registers for all of them.
-template <typename TE>
-__device__ __forceinline__ void add_adapter16(const LinearArgs& a, int id, uint32_t who, int t1, int n, float* v) {
+__device__ __forceinline__ void add_adapter16(const LinearArgs& a, int id, uint32_t who, int t1, int left, int n,
+                                              float* v) {
   const TE* B = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + n) * a.R;
   const float* u = a.u + (long long)t1 * a.R;
-#pragma unroll 2
+  uint4 b = *reinterpret_cast<const uint4*>(B);
   for (int r = 0; r < a.R; r += 8) {
-    const uint4 b = *reinterpret_cast<const uint4*>(B + r);
     const float2 b0 = Pair<TE>::f32(b.x), b1 = Pair<TE>::f32(b.y), b2 = Pair<TE>::f32(b.z), b3 = Pair<TE>::f32(b.w);
+    if (r + 8 < a.R) b = *reinterpret_cast<const uint4*>(B + r + 8);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      if (!(who >> j & 1)) continue;
-      const float4 p = *reinterpret_cast<const float4*>(u + (long long)j * a.R + r);
-      const float4 q = *reinterpret_cast<const float4*>(u + (long long)j * a.R + r + 4);
-      v[j] += fmaf(b0.x, p.x, fmaf(b0.y, p.y, fmaf(b1.x, p.z, b1.y * p.w))) +
-              fmaf(b2.x, q.x, fmaf(b2.y, q.y, fmaf(b3.x, q.z, b3.y * q.w)));
+      const float* w = u + (j < left ? j : 0) * a.R + r;
+      const float4 p = *reinterpret_cast<const float4*>(w), q = *reinterpret_cast<const float4*>(w + 4);
+      const float s = fmaf(b0.x, p.x, fmaf(b0.y, p.y, fmaf(b1.x, p.z, b1.y * p.w))) +
+                      fmaf(b2.x, q.x, fmaf(b2.y, q.y, fmaf(b3.x, q.z, b3.y * q.w)));
+      v[j] = who >> j & 1 ? v[j] + s : v[j];
     }
   }
 }
@@ -364,23 +337,67 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
   }
   if (!ok && threadIdx.x == 0 && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
   if (early) pdl_wait();   // u
-  const int share = NT / cs;
+  // four outputs of two tokens at a time: the loads of both are under way together
+  const int share = NT / cs, items = share * (kRows / 4);
   const uint32_t base = su32(part);
-  for (int i = threadIdx.x; i < share * (kRows / 4); i += 256) {
-    const int tt = rank * share + i / (kRows / 4), nn = (i % (kRows / 4)) * 4;
-    const long long t = t0 + tt;
-    if (t >= a.T || n0 + nn >= a.N) continue;
-    float v[4] = {};
+  for (int i = threadIdx.x; i < items; i += 512) {
+    float v[2][4] = {};
+    int id[2], tt[2], nn[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int it = i + m * 256;
+      tt[m] = it < items ? rank * share + it / (kRows / 4) : NT;
+      nn[m] = n0 + it % (kRows / 4) * 4;
+      const bool in = tt[m] < NT && t0 + tt[m] < a.T && nn[m] < a.N;
+      if (!in) tt[m] = -1;
+      id[m] = in && a.n ? a.ids[t0 + tt[m]] : -1;
+      if (id[m] >= a.n) id[m] = -1;
+    }
     for (int r = 0; r < cs; ++r) {
-      const uint32_t p = base + (uint32_t)(tt * kRows + nn) * 4;
-      const float4 f = cs > 1 ? ld_cluster4(p, r) : *reinterpret_cast<const float4*>(part + tt * kRows + nn);
-      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (tt[m] < 0) continue;
+        const uint32_t at = (uint32_t)(tt[m] * kRows + nn[m] - n0) * 4;
+        const float4 f = cs > 1 ? ld_cluster4(base + at, r) : *reinterpret_cast<const float4*>(sm + at);
+        v[m][0] += f.x, v[m][1] += f.y, v[m][2] += f.z, v[m][3] += f.w;
+      }
     }
-    if (a.n) {
-      const int id = a.ids[t];
-      if (id >= 0 && id < a.n) add_adapter4<TE>(a, id, t, n0 + nn, v);
+    if (id[0] >= 0 || id[1] >= 0) {
+      const TE* B[2];
+      const float* u[2];
+      int row[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {   // where there is no adapter or no output: another's, dropped below
+        const bool own = id[m] >= 0;
+        const int of = own ? id[m] : id[1 - m], n1 = own ? nn[m] : nn[1 - m], t1 = own ? tt[m] : tt[1 - m];
+        B[m] = reinterpret_cast<const TE*>(a.B) + ((long long)of * a.N + n1) * a.R;
+        u[m] = a.u + (long long)(t0 + t1) * a.R;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) row[m][j] = n1 + j < a.N ? j * a.R : 0;
+      }
+      float d[2][4] = {};
+      for (int r = 0; r < a.R; r += 8) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float4 p = *reinterpret_cast<const float4*>(u[m] + r), q = *reinterpret_cast<const float4*>(u[m] + r + 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 b = *reinterpret_cast<const uint4*>(B[m] + row[m][j] + r);
+            const float2 b0 = Pair<TE>::f32(b.x), b1 = Pair<TE>::f32(b.y), b2 = Pair<TE>::f32(b.z),
+                         b3 = Pair<TE>::f32(b.w);
+            d[m][j] += fmaf(b0.x, p.x, fmaf(b0.y, p.y, fmaf(b1.x, p.z, b1.y * p.w))) +
+                       fmaf(b2.x, q.x, fmaf(b2.y, q.y, fmaf(b3.x, q.z, b3.y * q.w)));
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[m][j] = id[m] < 0 ? v[m][j] : v[m][j] + d[m][j];
     }
-    store4<TE>(a, t, n0 + nn, v);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      if (tt[m] >= 0) store4<TE>(a, t0 + tt[m], nn[m], v[m]);
   }
   __syncwarp();
   if (cs > 1) cluster_sync();   // the others have read this block's sums
@@ -793,7 +810,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             const int id = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
             const uint32_t who = __ballot_sync(0xffffffffu, mine == id) & 0xffff;
             left &= ~who;
-            if (n < a.N) add_adapter16<TE>(a, id, who, t1, n, f);
+            if (n < a.N) add_adapter16<TE>(a, id, who, t1, a.T - t1, n, f);
             __syncwarp();
           }
         }
@@ -945,8 +962,7 @@ static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) 
   if (a.n) {
     // one dot per token and rank re-reads A for every token: worth it up to this many bytes
     if (!large && (long long)a.T * a.R * a.H * 2 <= (64LL << 20)) {
-      const long long warps = (long long)a.T * (a.R / kDots);
-      cudaError_t e = launch_pdl(adapter_dot_kernel<TE>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, a);
+      cudaError_t e = launch_pdl(adapter_dot_kernel<TE>, dim3(a.T, a.R / kDots), dim3(128), 0, s, a);
       if (e != cudaSuccess) return cuda_fail(e, "adapter_dot_kernel");
       st = check_launch("adapter_dot_kernel");
     } else {

@@ -140,6 +140,10 @@ __device__ __forceinline__ void mma_k16(uint32_t d, uint64_t a, uint64_t b, uint
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar)) : "memory");
 }
+// Bytes to come on `bar`, without an arrival.
+__device__ __forceinline__ void mbar_expect_only(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(su32(bar)), "r"(bytes) : "memory");
+}
 // A place in a ring of stages and the parity of its current pass.
 struct RingPos {
   int stages, stage = 0;
@@ -168,6 +172,11 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t saddr, uint32_t rank) {
                : "memory");
   return v;
 }
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 constexpr int kRows = 128;          // outputs (W rows) of a tile
 constexpr int kATile = kRows * 128; // bytes of a 64-wide K step of W
@@ -257,6 +266,8 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
   const int nk = (a.H + 63) / 64, k0 = (int)((long long)nk * rank / cs), k1 = (int)((long long)nk * (rank + 1) / cs);
 
   if (threadIdx.x == 0) {
+    prefetch_map(&mW);
+    prefetch_map(&mX);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -306,6 +317,14 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
         r.next();
       }
       mma_commit(&done);
+    }
+  } else if (early) {   // the adapters' rows of this block's outputs, on their way to L2 meanwhile
+    const int share = NT / cs;
+    for (int i = threadIdx.x - 64; i < share * kRows; i += 192) {
+      const int t = t0 + rank * share + i / kRows, n = n0 + i % kRows;
+      const int id = t < a.T && n < a.N ? a.ids[t] : -1;
+      const char* row = reinterpret_cast<const char*>(a.B) + ((long long)id * a.N + n) * a.R * 2;
+      if (id >= 0 && id < a.n && ((uintptr_t)row % 128 < (unsigned)a.R * 2)) prefetch_l2(row);
     }
   }
   __syncwarp();
@@ -427,6 +446,8 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
   const int cs = gridDim.x, rank = blockIdx.x, t0 = blockIdx.y * kShrinkTokens;
   const int nk = (a.H + 63) / 64, k0 = (int)((long long)nk * rank / cs), k1 = (int)((long long)nk * (rank + 1) / cs);
   if (tid == 0) {
+    prefetch_map(&mA);
+    prefetch_map(&mX);
     for (int s = 0; s < kShrinkStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -440,8 +461,18 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
                  "r"(kShrinkTokens));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();   // after the wait: the projection may read x from its start
+  // x's first stages are on their way while the list of adapters is made
+  const int early = k1 - k0 < kShrinkStages ? k1 - k0 : kShrinkStages;
+  if (tid == 0) {
+    for (int i = 0; i < early; ++i) {
+      mbar_expect_only(&full[i], kShrinkTokens * 128);
+      tma_2d(sm + i * kShrinkStage + kATile, &mX, (k0 + i) * 64, t0, &full[i]);
+    }
+  }
+  __syncwarp();
   // the adapters that the tokens name, in order of their first token: first of a warp's tokens ...
   int mine = -1;
   bool first = false;
@@ -497,9 +528,10 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
         for (int k = k0; k < k1; ++k) {
           if (wrapped && !wait_bar(&empty[r.stage], r.parity ^ 1, &s_err)) break;
           uint8_t* st = sm + r.stage * kShrinkStage;
-          mbar_expect_tx(&full[r.stage], cnt * a.R * 128 + kShrinkTokens * 128);
+          const bool have = p == 0 && k - k0 < early;
+          mbar_expect_tx(&full[r.stage], cnt * a.R * 128 + (have ? 0 : kShrinkTokens * 128));
           for (int i = 0; i < cnt; ++i) tma_2d(st + i * a.R * 128, &mA, k * 64, s_list[p + i] * a.R, &full[r.stage]);
-          tma_2d(st + kATile, &mX, k * 64, t0, &full[r.stage]);
+          if (!have) tma_2d(st + kATile, &mX, k * 64, t0, &full[r.stage]);
           r.next();
           wrapped |= r.stage == 0;
         }
@@ -566,6 +598,10 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
     __syncwarp();
     cluster_sync();   // the others have read this block's sums
   }
+  if (total == 0 && tid == 0) {   // nothing to multiply: x's first stages still have to land
+    for (int i = 0; i < early; ++i) mbar_arrive(&full[i]);
+    for (int i = 0; i < early && ok; ++i) ok = wait_bar(&full[i], 0, &s_err);
+  }
   __syncthreads();
   // how the projection takes a group: together where all 16 (a last group's missing tokens
   // aside) share an adapter and u is within the 16-bit type's range
@@ -588,7 +624,7 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kShrinkTokens));
   }
-  if (!ok && tid == 0 && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
+  if (tid == 0 && s_err != MOE_OK && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
 }
 
 // Large batches: persistent blocks, one per SM, over tiles of 128 outputs x NT
@@ -627,6 +663,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    prefetch_map(&mW);
+    prefetch_map(&mX);
     for (int s = 0; s < kStreamStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -910,6 +948,7 @@ static moe_status launch_shrink(const LinearArgs& a, int dtype, cudaStream_t s) 
   static char allowed[64];
   MOE_CUDA(allow_smem(kernel, kShrinkSmem, allowed));
   const int tiles = (a.T + kShrinkTokens - 1) / kShrinkTokens, nk = (a.H + 63) / 64;
+  MOE_ARG(tiles <= 65535, "T too large");
   int cs = 1;
   while (cs < 8 && (long long)tiles * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
   return launch_cluster(kernel, dim3(cs, tiles), cs, kShrinkSmem, s, "adapter_shrink_kernel", mA, mX, a);

@@ -26,11 +26,6 @@ struct RouteArgs {
   int32_t* load;
 };
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -332,33 +327,50 @@ struct RouteBwdArgs {
   long long ld_d;
 };
 
-// One warp per token: the row is written first (zeros, or the plain softmax's
-// own term), then the chosen experts' values over it.  Bound by the T * E
-// elements written.  `vec`: rows and their length allow 16-byte stores.
-template <typename TL>
+// GROUP lanes per token (k <= GROUP; 32 for the plain softmax, whose gradient is
+// dense): the rows are written first (zeros, or the plain softmax's own term),
+// then the chosen experts' values over them.  Bound by the T * E elements
+// written.  `vec`: rows and their length allow 16-byte stores.
+__device__ __forceinline__ float group_sum(float v, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float group_max(float v, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+template <typename TL, int GROUP>
 __global__ void __launch_bounds__(128) route_bwd_kernel(const RouteBwdArgs a, int vec) {
-  const int lane = threadIdx.x & 31;
+  constexpr int kTokens = 32 / GROUP;   // of a warp
+  const int lane = threadIdx.x & 31, sub = lane / GROUP, gl = lane % GROUP;
   pdl_wait();
   pdl_launch_dependents();
-  const long long step = gridDim.x * 4LL;
-  for (long long t = blockIdx.x * 4LL + (threadIdx.x >> 5); t < a.T; t += step) {
+  const long long step = gridDim.x * 4LL * kTokens;
+  for (long long t0 = (blockIdx.x * 4LL + (threadIdx.x >> 5)) * kTokens; t0 < a.T; t0 += step) {
+    const long long t = t0 + sub;
     const TL* row = reinterpret_cast<const TL*>(a.logits) + t * a.ld;
     TL* d = reinterpret_cast<TL*>(a.d) + t * a.ld_d;
-    const bool on = !a.mask || a.mask[t];
+    const bool on = t < a.T && (!a.mask || a.mask[t]);
     int id = -1;
     float g = 0.f, z = -INFINITY;
-    if (lane < a.k && on) {
-      id = a.ids[t * a.k + lane];
-      g = a.scale * a.dw[t * a.k + lane];
+    if (gl < a.k && on) {
+      id = a.ids[t * a.k + gl];
+      g = a.scale * a.dw[t * a.k + gl];
     }
-    const bool dense = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
+    const bool dense = GROUP == 32 && a.score == MOE_SCORE_SOFTMAX && !a.renorm;
     if (!dense) {   // while the ids are on their way
-      if (vec) {
-        constexpr int kEach = 16 / (int)sizeof(TL);
-        for (int e = lane * kEach; e < a.E; e += 32 * kEach)
-          *reinterpret_cast<uint4*>(d + e) = make_uint4(0, 0, 0, 0);
-      } else {
-        for (int e = lane; e < a.E; e += 32) d[e] = from_f32<TL>(0.f);
+#pragma unroll
+      for (int q = 0; q < kTokens; ++q) {
+        if (t0 + q >= a.T) break;
+        TL* dq = reinterpret_cast<TL*>(a.d) + (t0 + q) * a.ld_d;
+        if (vec) {
+          constexpr int kEach = 16 / (int)sizeof(TL);
+          for (int e = lane * kEach; e < a.E; e += 32 * kEach)
+            *reinterpret_cast<uint4*>(dq + e) = make_uint4(0, 0, 0, 0);
+        } else {
+          for (int e = lane; e < a.E; e += 32) dq[e] = from_f32<TL>(0.f);
+        }
       }
     }
     if (id >= 0 && id < a.E) z = load_logit(row, id);
@@ -368,12 +380,12 @@ __global__ void __launch_bounds__(128) route_bwd_kernel(const RouteBwdArgs a, in
       float top = -INFINITY, den = 0.f;
       if (on) {
         for (int e = lane; e < a.E; e += 32) top = fmaxf(top, load_logit(row, e));
-        top = warp_max(top);
+        top = group_max(top, 32);
         for (int e = lane; e < a.E; e += 32) den += exp_below(load_logit(row, e), top);
-        den = warp_sum(den);
+        den = group_sum(den, 32);
       }
       const float p = id >= 0 ? exp_below(z, top) / den : 0.f;
-      const float mean = warp_sum(g * p);
+      const float mean = group_sum(g * p, 32);
       dj = p * (g - mean);
       for (int e = lane; e < a.E; e += 32)
         d[e] = from_f32<TL>(den > 0.f ? -mean * (exp_below(load_logit(row, e), top) / den) : 0.f);
@@ -383,19 +395,30 @@ __global__ void __launch_bounds__(128) route_bwd_kernel(const RouteBwdArgs a, in
         q = id >= 0 ? sigmoid_f32(z) : 0.f;
         c = id >= 0 ? sigmoid_f32(-z) : 0.f;   // 1 - s without the cancellation
       } else {
-        q = exp_below(z, warp_max(z));
+        q = exp_below(z, group_max(z, GROUP));
       }
       float mean = 0.f;
       if (a.renorm) {
-        const float sum = warp_sum(q);
+        const float sum = group_sum(q, GROUP);
         q = sum > 0.f ? q / sum : 0.f;
-        mean = warp_sum(q * g);
+        mean = group_sum(q * g, GROUP);
       }
       dj = q * c * (g - mean);
     }
-    __syncwarp();   // the row is written before the chosen experts' values
+    __syncwarp();   // the rows are written before the chosen experts' values
     if (id >= 0) d[id] = from_f32<TL>(dj);
   }
+}
+
+template <typename TL>
+static cudaError_t launch_route_bwd(const RouteBwdArgs& a, int vec, cudaStream_t s) {
+  const bool dense = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
+  const int group = dense || a.k > 16 ? 32 : a.k > 8 ? 16 : 8;
+  const long long warps = (a.T + 32LL / group - 1) / (32 / group), need = (warps + 3) / 4, most = device_sms() * 16LL;
+  const dim3 grid((unsigned)(need < most ? need : most)), block(128);
+  if (group == 32) return launch_pdl(route_bwd_kernel<TL, 32>, grid, block, 0, s, a, vec);
+  if (group == 16) return launch_pdl(route_bwd_kernel<TL, 16>, grid, block, 0, s, a, vec);
+  return launch_pdl(route_bwd_kernel<TL, 8>, grid, block, 0, s, a, vec);
 }
 
 template <int VPL, typename TL>
@@ -469,14 +492,12 @@ extern "C" moe_status moe_route_backward(const void* logits, int dtype, int64_t 
   MOE_ARG(d_logits != logits, "d_logits must not be the logits");
   const RouteBwdArgs a{logits, ld_logits, T, E, k, score, renorm, scale, token_mask, topk_ids, d_w, d_logits,
                        ld_d_logits};
-  const long long need = (T + 3LL) / 4, most = device_sms() * 16LL;
-  const dim3 grid((unsigned)(need < most ? need : most)), block(128);
   const int size = (int)dtype_size(dtype);
   const int vec = (uintptr_t)d_logits % 16 == 0 && ld_d_logits * size % 16 == 0 && E * size % 16 == 0;
   ProfScope ps(MOE_K_ROUTE_BWD, stream);
-  cudaError_t e = dtype == MOE_DT_F32    ? launch_pdl(route_bwd_kernel<float>, grid, block, 0, stream, a, vec)
-                  : dtype == MOE_DT_BF16 ? launch_pdl(route_bwd_kernel<__nv_bfloat16>, grid, block, 0, stream, a, vec)
-                                         : launch_pdl(route_bwd_kernel<__half>, grid, block, 0, stream, a, vec);
+  const cudaError_t e = dtype == MOE_DT_F32    ? launch_route_bwd<float>(a, vec, stream)
+                        : dtype == MOE_DT_BF16 ? launch_route_bwd<__nv_bfloat16>(a, vec, stream)
+                                               : launch_route_bwd<__half>(a, vec, stream);
   if (e != cudaSuccess) return cuda_fail(e, "route_bwd_kernel");
   return check_launch("route_bwd_kernel");
 }

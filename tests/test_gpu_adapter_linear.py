@@ -92,6 +92,38 @@ def test_adapter_linear_prompts(T, N):
     assert torch.equal(a, b)
 
 
+# more than 16 x 7 tiles of 128 x 128: the persistent kernel, with ragged H, N and T, ranks past one
+# and two 64-wide steps, fp32 results in one sum (H <= 512) and in several
+LARGE = [(1300, 1032, 2048, 40, 5), (1030, 136, 2304, 128, 2), (1100, 200, 2200, 72, 3), (16400, 64, 100, 8, 9),
+         (1999, 520, 2049, 16, 30), (1024, 4096, 2048, 64, 1)]
+
+
+@pytest.mark.parametrize("T,H,N,R,n", LARGE)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+@pytest.mark.parametrize("ids", ["mixed", "runs", 0])
+def test_adapter_linear_large_batches(T, H, N, R, n, dtype, out, ids):
+    M = load_lib()
+    _check(M, _data(T + N, T, H, N, R, n, dtype, ids), dtype, out, rows=200)
+
+
+def test_adapter_linear_without_adapters_large():
+    M = load_lib()
+    for T, H, N in ((1300, 1032, 2048), (16400, 64, 100), (1999, 520, 2049)):
+        d = _data(T, T, H, N, 8, 0, "bf16", "none")
+        for out in ("bf16", "f32"):
+            _check(M, d, "bf16", out, rows=100)
+
+
+@pytest.mark.parametrize("T", [40, 1300])
+def test_adapter_linear_f16_past_its_range(T):
+    # A x past fp16's largest value, brought back by B: nothing may be carried in fp16 then
+    M = load_lib()
+    d = _data(11, T, 256, 2048, 16, 3, "f16", "runs")
+    d["A"] = (d["A"].float() * 3e4).to(torch.float16)
+    d["B"] = (d["B"].float() * 1e-4).to(torch.float16)
+    _check(M, d, "f16", "f32", rows=150)
+
+
 @pytest.mark.parametrize("T", [5, 700])
 @pytest.mark.parametrize("ids", ["none", 0, 2, "mixed"])
 def test_adapter_linear_uses_of_adapters(T, ids):

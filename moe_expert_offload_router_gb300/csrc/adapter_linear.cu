@@ -190,25 +190,37 @@ struct SplitCfg {
   static_assert(NT * kRows * 4 <= kStages * kStage, "the partial sums fit the stages");
 };
 
-// v[j] += B[a][n] . u[t1 + j] in fp32 for the tokens j of `who` (below `left`):
-// eight ranks at a time, B's in registers for all of them.  u is read for every
-// token and dropped where it is not asked for, so that no load waits for a branch.
+// v[j] += B[a][n] . u[t1 + j] in fp32 for the tokens j of `who` (below `left`), by
+// a whole warp, lane -> n.  Eight ranks at a time: a lane loads a quarter row of
+// one token's u, which shuffles hand to all, and B's eight for its own n; both a
+// step ahead.
 template <typename TE>
 __device__ __forceinline__ void add_adapter16(const LinearArgs& a, int id, uint32_t who, int t1, int left, int n,
                                               float* v) {
-  const TE* B = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + n) * a.R;
-  const float* u = a.u + (long long)t1 * a.R;
+  const int lane = threadIdx.x & 31;
+  const TE* B = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + (n < a.N ? n : a.N - 1)) * a.R;
+  const float* u = a.u + (long long)(t1 + ((lane & 15) < left ? lane & 15 : 0)) * a.R + (lane >> 4) * 4;
   uint4 b = *reinterpret_cast<const uint4*>(B);
+  float4 w = *reinterpret_cast<const float4*>(u);
   for (int r = 0; r < a.R; r += 8) {
     const float2 b0 = Pair<TE>::f32(b.x), b1 = Pair<TE>::f32(b.y), b2 = Pair<TE>::f32(b.z), b3 = Pair<TE>::f32(b.w);
-    if (r + 8 < a.R) b = *reinterpret_cast<const uint4*>(B + r + 8);
+    const float4 c = w;
+    if (r + 8 < a.R) {
+      b = *reinterpret_cast<const uint4*>(B + r + 8);
+      w = *reinterpret_cast<const float4*>(u + r + 8);
+    }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const float* w = u + (j < left ? j : 0) * a.R + r;
-      const float4 p = *reinterpret_cast<const float4*>(w), q = *reinterpret_cast<const float4*>(w + 4);
-      const float s = fmaf(b0.x, p.x, fmaf(b0.y, p.y, fmaf(b1.x, p.z, b1.y * p.w))) +
-                      fmaf(b2.x, q.x, fmaf(b2.y, q.y, fmaf(b3.x, q.z, b3.y * q.w)));
-      v[j] = who >> j & 1 ? v[j] + s : v[j];
+      if (!(who >> j & 1)) continue;
+      float s = b0.x * __shfl_sync(0xffffffffu, c.x, j);
+      s = fmaf(b0.y, __shfl_sync(0xffffffffu, c.y, j), s);
+      s = fmaf(b1.x, __shfl_sync(0xffffffffu, c.z, j), s);
+      s = fmaf(b1.y, __shfl_sync(0xffffffffu, c.w, j), s);
+      s = fmaf(b2.x, __shfl_sync(0xffffffffu, c.x, j + 16), s);
+      s = fmaf(b2.y, __shfl_sync(0xffffffffu, c.y, j + 16), s);
+      s = fmaf(b3.x, __shfl_sync(0xffffffffu, c.z, j + 16), s);
+      s = fmaf(b3.y, __shfl_sync(0xffffffffu, c.w, j + 16), s);
+      v[j] += s;
     }
   }
 }
@@ -627,10 +639,18 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
   if (tid == 0 && s_err != MOE_OK && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
 }
 
-// Large batches: persistent blocks, one per SM, over tiles of 128 outputs x NT
-// tokens (NT <= 256, a multiple of 16).  Warp 0 brings 64-wide K steps of W and x
-// by TMA into a ring, warp 1 multiplies, eight warps empty the accumulators: two
-// of 256 columns, so a tile's epilogue runs under the next tile's steps.
+// Large batches: persistent pairs of blocks (clusters of two, one block per SM)
+// over tiles of 256 outputs x NT tokens (NT <= 256, a multiple of 16).  An SM takes
+// in about 64 bytes a clock, and a block of its own needs (128 + NT) rows of a K
+// step for 128 x NT of output: it waits for its operands (0.33 us a step at NT =
+// 224 where the MMAs take 0.23).  A pair's MMA (cta_group::2) reads half of the
+// tokens' rows from each block, so each brings 128 rows of W and NT / 2 of x.
+//
+// In each block warp 0 brings its rows by TMA into a ring, and eight warps empty
+// its 128 rows of the accumulators: two of 256 columns, so a tile's epilogue runs
+// under the next tile's steps.  Warp 1 of the first block (the leader) multiplies
+// for both; its barriers take both blocks' copies and both epilogues' releases,
+// and its commits arrive in both.
 //
 // A tensor-core accumulator loses a little with every step (it truncates), so a
 // result kept in fp32 takes at most `chunk` steps in one accumulator; the epilogue
@@ -647,10 +667,43 @@ constexpr int kStreamThreads = 320;   // TMA, MMA, eight epilogue warps
 constexpr int kF32Chunk = 8;          // K steps in one accumulator for fp32 results: 512 products a sum
 
 struct StreamPlan {
-  int nt, stages, tiles_n, tiles;   // tokens of a tile, stages of the ring, tiles of outputs, all tiles
+  int nt, stages, tiles_n, tiles;   // tokens of a tile, stages of the ring, tiles of 256 outputs, all tiles
   int nk, chunk;                    // K steps, K steps of an accumulator
 };
 
+// The pair's forms: a copy into this block that completes on a barrier of the leader (a cluster
+// address), an MMA over both blocks' rows, its commit (arrives at the same barrier of both).
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(su32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(su32(dst)),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_k16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          su32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t idesc_pair(int n, bool bf16) {   // M = 256
+  return (idesc_f16(n, bf16) & ~(31u << 24)) | (16u << 24);
+}
 template <typename TE, bool CHUNKS>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     linear_stream_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
@@ -661,7 +714,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int s_err;
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;   // clusters of two along x
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
     prefetch_map(&mW);
     prefetch_map(&mX);
@@ -671,24 +725,25 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);
+      mbar_init(&acc_empty[b], 16);   // the leader's: eight warps of each block
     }
     s_err = MOE_OK;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)),
                  "r"(512));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();   // the barriers of both are there
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   if (!a.n) pdl_wait();   // as in linear_split_kernel
   pdl_launch_dependents();
   const int groups = pl.nt / 16;
-  const uint32_t bytes = kATile + pl.nt * 128;   // of a stage
+  const uint32_t bytes = kATile + pl.nt * 64;   // of a stage in each block
   const int rchunks = (a.R + 63) / 64;
   bool ok = true;
 
@@ -726,36 +781,38 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     auto stage = [&](const CUtensorMap* ma, const CUtensorMap* mb, int ka, int rowa, int rowb) {
       if (wrapped && !wait_bar(&empty[r.stage], r.parity ^ 1, &s_err)) return false;
       uint8_t* st = sm + r.stage * bytes;
-      mbar_expect_tx(&full[r.stage], bytes);
-      tma_2d(st, ma, ka, rowa, &full[r.stage]);
-      tma_2d(st + kATile, mb, ka, rowb, &full[r.stage]);
+      if (rank == 0) mbar_expect_tx(&full[r.stage], 2 * bytes);
+      const uint32_t bar = cluster_addr(&full[r.stage], 0);
+      tma_2d_pair(st, ma, ka, rowa, bar);
+      tma_2d_pair(st + kATile, mb, ka, rowb, bar);
       r.next();
       wrapped |= r.stage == 0;
       return true;
     };
-    for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
-      const int n0 = tile % pl.tiles_n * kRows, t0 = tile / pl.tiles_n * pl.nt;
+    for (int tile = pair; tile < pl.tiles && ok; tile += pairs) {
+      const int n0 = (tile % pl.tiles_n * 2 + rank) * kRows, t0 = tile / pl.tiles_n * pl.nt;
       groups_early(t0);
       if (lead)
-        for (int k = 0; k < pl.nk && ok; ++k) ok = stage(&mW, &mX, k * 64, n0, t0);
+        for (int k = 0; k < pl.nk && ok; ++k) ok = stage(&mW, &mX, k * 64, n0, t0 + rank * (pl.nt / 2));
       ok = __all_sync(0xffffffffu, ok);
       if (!a.n || !ok) continue;
       groups_now(t0);
-      runs(mine, [&](int id, int, int) {
+      runs(mine, [&](int id, int g, int len) {   // the run's first half here, its second in the other block
+        const int t1 = t0 + g * 16 + rank * len * 8;
         if (lead)
           for (int c = 0; c < rchunks && ok; ++c)
-            ok = stage(&mB, &mH, c * 64, id * a.N + n0, t0) && stage(&mB, &mL, c * 64, id * a.N + n0, t0);
+            ok = stage(&mB, &mH, c * 64, id * a.N + n0, t1) && stage(&mB, &mL, c * 64, id * a.N + n0, t1);
         return ok = __all_sync(0xffffffffu, ok);
       });
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     RingPos r(pl.stages);
     RingPos acc(2);
     int used = 0;   // accumulators handed over so far (up to 2)
     const bool bf16 = std::is_same<TE, __nv_bfloat16>::value, lead = elect_one();
-    const uint32_t idesc = idesc_f16(pl.nt, bf16);
+    const uint32_t idesc = idesc_pair(pl.nt, bf16);
     const uint64_t d0 = umma_desc_sw128(su32(sm));
-    for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
+    for (int tile = pair; tile < pl.tiles && ok; tile += pairs) {
       const int t0 = tile / pl.tiles_n * pl.nt;
       groups_early(t0);
       for (int k = 0; k < pl.nk && ok; k += pl.chunk) {
@@ -769,8 +826,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             tc_fence_after();
             const uint64_t da = d0 + r.stage * (bytes / 16), db = da + kATile / 16;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_k16(d, da + 2 * j, db + 2 * j, idesc, i != k || j);
-            mma_commit(&empty[r.stage]);
+            for (int j = 0; j < 4; ++j) mma_k16_pair(d, da + 2 * j, db + 2 * j, idesc, i != k || j);
+            mma_commit_pair(&empty[r.stage]);
             r.next();
           }
         }
@@ -779,32 +836,32 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           groups_now(t0);
           runs(mine, [&](int id, int g, int len) {
             if (lead) {
-              const uint32_t id16 = idesc_f16(len * 16, bf16);
+              const uint32_t id16 = idesc_pair(len * 16, bf16);
               for (int c = 0; c < 2 * rchunks; ++c) {
                 if (!(ok = wait_bar(&full[r.stage], r.parity, &s_err))) break;
                 tc_fence_after();
-                const uint64_t da = d0 + r.stage * (bytes / 16), db = da + kATile / 16 + g * 128;
+                const uint64_t da = d0 + r.stage * (bytes / 16), db = da + kATile / 16;
                 const int left = a.R - (c / 2) * 64, steps = left >= 64 ? 4 : (left + 15) / 16;
-                for (int j = 0; j < steps; ++j) mma_k16(d + g * 16, da + 2 * j, db + 2 * j, id16, 1);
-                mma_commit(&empty[r.stage]);
+                for (int j = 0; j < steps; ++j) mma_k16_pair(d + g * 16, da + 2 * j, db + 2 * j, id16, 1);
+                mma_commit_pair(&empty[r.stage]);
                 r.next();
               }
             }
             return ok = __all_sync(0xffffffffu, ok);
           });
         }
-        if (lead && ok) mma_commit(&acc_full[acc.stage]);
+        if (lead && ok) mma_commit_pair(&acc_full[acc.stage]);
         acc.next();
         ++used;
       }
     }
-  } else {
+  } else if (warp >= 2) {
     constexpr int kHalf = CHUNKS ? 64 : 128;                  // tokens of the tile that a warp takes
     const int q = warp & 3, c0 = ((warp - 2) >> 2) * kHalf;   // its 32 outputs, its first token
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     RingPos acc(2);
-    for (int tile = blockIdx.x; tile < pl.tiles && ok; tile += gridDim.x) {
-      const int n = tile % pl.tiles_n * kRows + q * 32 + lane, t0 = tile / pl.tiles_n * pl.nt;
+    for (int tile = pair; tile < pl.tiles && ok; tile += pairs) {
+      const int n = (tile % pl.tiles_n * 2 + rank) * kRows + q * 32 + lane, t0 = tile / pl.tiles_n * pl.nt;
       float v[CHUNKS ? kHalf : 16];
       groups_early(t0);
       auto columns = [&](int c, float* f, bool add) {   // 16 of the accumulator's columns
@@ -816,7 +873,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[acc.stage]);
+        if (lane == 0) arrive_cluster(cluster_addr(&acc_empty[acc.stage], 0));
         acc.next();
       };
       if (CHUNKS) {
@@ -848,8 +905,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             const int id = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
             const uint32_t who = __ballot_sync(0xffffffffu, mine == id) & 0xffff;
             left &= ~who;
-            if (n < a.N) add_adapter16<TE>(a, id, who, t1, a.T - t1, n, f);
-            __syncwarp();
+            add_adapter16<TE>(a, id, who, t1, a.T - t1, n, f);
           }
         }
         if (n < a.N) {
@@ -871,10 +927,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
   tc_fence_before();
   __syncwarp();
-  __syncthreads();
+  cluster_sync();   // nothing of this block is used by the other any more
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
   if (threadIdx.x == 0 && s_err != MOE_OK && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
   if (a.n) pdl_wait();
@@ -898,13 +954,13 @@ static moe_status map_rows(CUtensorMap* m, const void* base, int dtype, uint64_t
   return MOE_OK;
 }
 
-// 256 threads a block, clusters of cs along x, started early (programmatic dependent launch).
+// Clusters of cs blocks along x, started early (programmatic dependent launch).
 template <typename... KArgs, typename... Args>
-static moe_status launch_cluster(void (*kernel)(KArgs...), dim3 grid, int cs, size_t smem, cudaStream_t s,
+static moe_status launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int cs, size_t smem, cudaStream_t s,
                                  const char* name, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -934,7 +990,7 @@ static moe_status launch_split(const LinearArgs& a, int dtype, cudaStream_t s) {
   // split H while the blocks still fit the SMs at once and each keeps two steps
   int cs = 1;
   while (cs < (tiles_n * tiles_t <= 8 ? 8 : 4) && (long long)tiles_n * tiles_t * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
-  return launch_cluster(kernel, dim3(cs, tiles_n, tiles_t), cs, C::kSmem, s, "linear_split_kernel", mW, mX, a,
+  return launch_cluster(kernel, dim3(cs, tiles_n, tiles_t), 256, cs, C::kSmem, s, "linear_split_kernel", mW, mX, a,
                         a.n ? 1 : 0);
 }
 
@@ -951,7 +1007,7 @@ static moe_status launch_shrink(const LinearArgs& a, int dtype, cudaStream_t s) 
   MOE_ARG(tiles <= 65535, "T too large");
   int cs = 1;
   while (cs < 8 && (long long)tiles * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
-  return launch_cluster(kernel, dim3(cs, tiles), cs, kShrinkSmem, s, "adapter_shrink_kernel", mA, mX, a);
+  return launch_cluster(kernel, dim3(cs, tiles), 256, cs, kShrinkSmem, s, "adapter_shrink_kernel", mA, mX, a);
 }
 
 // Whether a call is large: with one block per SM, tiles of 128 x 128 fill them.
@@ -963,34 +1019,33 @@ template <typename TE>
 static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) {
   CUtensorMap mW, mX, mB = {}, mH = {}, mL = {};
   StreamPlan pl;
-  pl.tiles_n = (a.N + kRows - 1) / kRows;
+  pl.tiles_n = (a.N + 2 * kRows - 1) / (2 * kRows);
   pl.nk = (a.H + 63) / 64;
   const bool chunks = a.out_dtype == MOE_DT_F32 && pl.nk > kF32Chunk;
   pl.chunk = chunks ? kF32Chunk : pl.nk;
-  // the tile that takes the fewest rounds of the SMs times its length (16: what a tile costs beside its tokens)
-  const int sms = device_sms();
+  // the tile that takes the fewest rounds of the pairs times its length; 16: what a tile costs beside its
+  // tokens, 240: a step takes no less (0.27 us at NT = 112 as at 224: the copies' and the commits' own time)
+  const int pairs = device_sms() / 2;
   long long best = -1;
   for (int nt = chunks ? 128 : 256; nt >= 64; nt -= 16) {
-    const long long tiles = (long long)pl.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + sms - 1) / sms * (nt + 16);
+    const long long tiles = (long long)pl.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + pairs - 1) / pairs * (nt > 224 ? nt + 16 : 240);
     if (best < 0 || cost < best) best = cost, pl.nt = nt, pl.tiles = (int)tiles;
   }
   moe_status st = map_rows(&mW, a.W, dtype, a.H, a.N, a.ld_w, kRows);
-  if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.H, a.T, a.ld_x, pl.nt);
+  if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.H, a.T, a.ld_x, pl.nt / 2);
   if (a.n) {
     if (st == MOE_OK) st = map_rows(&mB, a.B, dtype, a.R, (uint64_t)a.n * a.N, a.R, kRows);
-    if (st == MOE_OK) st = map_rows(&mH, a.u_hi, dtype, a.R, a.T, a.R, pl.nt);
-    if (st == MOE_OK) st = map_rows(&mL, a.u_lo, dtype, a.R, a.T, a.R, pl.nt);
+    if (st == MOE_OK) st = map_rows(&mH, a.u_hi, dtype, a.R, a.T, a.R, pl.nt / 2);
+    if (st == MOE_OK) st = map_rows(&mL, a.u_lo, dtype, a.R, a.T, a.R, pl.nt / 2);
   }
   if (st != MOE_OK) return st;
-  const int fit = kStreamBytes / (kATile + pl.nt * 128);
+  const int fit = kStreamBytes / (kATile + pl.nt * 64);
   pl.stages = fit < kStreamStages ? fit : kStreamStages;
   auto kernel = chunks ? linear_stream_kernel<TE, true> : linear_stream_kernel<TE, false>;
   static char allowed[2][64];
   MOE_CUDA(allow_smem(kernel, kStreamBytes + 1024, allowed[chunks]));
-  cudaError_t e = launch_pdl(kernel, dim3(pl.tiles < sms ? pl.tiles : sms), dim3(kStreamThreads), kStreamBytes + 1024, s, mW,
-                             mX, mB, mH, mL, a, pl);
-  if (e != cudaSuccess) return cuda_fail(e, "linear_stream_kernel");
-  return check_launch("linear_stream_kernel");
+  return launch_cluster(kernel, dim3(2 * (pl.tiles < pairs ? pl.tiles : pairs)), kStreamThreads, 2, kStreamBytes + 1024,
+                        s, "linear_stream_kernel", mW, mX, mB, mH, mL, a, pl);
 }
 
 template <typename TE>

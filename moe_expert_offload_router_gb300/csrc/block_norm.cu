@@ -11,8 +11,10 @@
 // so a row takes two sums over its columns (five values in the second), and
 // the three column gradients come from two column sums over the rows.
 //
-// Bound by HBM: x, y read and x_out, h written (forward), x, y, du, dh read and
-// dx, dy written (gradient).  A row is held in the registers of a group of NT
+// Bound by HBM: x, y read and x_out, h written (forward: T = 8192, H = 4096 bf16,
+// 268 MB in 43.9 us, 6.1 TB/s), x, y, du, dh read and dx, dy written (gradient: 403
+// MB in 74.4 us with the column sums, 5.4 TB/s; its row kernel is as near to the
+// issue slots as to HBM, hence the packed fp32 instructions).  A row is held in the registers of a group of NT
 // threads (a warp, or the block), thread i owning the same columns of every
 // row: its weights and its column sums stay in registers while the block walks
 // over rows t, t + blocks, ...  Each thread copies its own columns of the next

@@ -6,7 +6,13 @@
 // that the lowest lane among equals holds the lowest id.  The k-th largest of
 // the 32 lanes' own maxima bounds the k-th largest key from below: k warp maxima
 // (redux) find it, the keys that reach it (a few more than k) are packed one to a
-// lane in order of their ids, and each counts those that go before it.
+// lane in order of their ids, and each counts those that go before it.  Against
+// k rounds that each search a lane's VPL keys: 40 us for 92 at 32768 tokens of
+// 256 experts, top-8, with bias and groups (37 without the host).  That is bound
+// by instruction issue (about 880 a token, 71 % of the slots), not by the 19 MB
+// it moves (2.8 us): 256 exponentials and reciprocals have to be exact to the bit
+// for the choice to be that of the definition.  Softmax without a bias needs none
+// of them for the choice: 20 us.
 #include <float.h>
 #include <math.h>
 
@@ -329,8 +335,9 @@ struct RouteBwdArgs {
 
 // GROUP lanes per token (k <= GROUP; 32 for the plain softmax, whose gradient is
 // dense): the rows are written first (zeros, or the plain softmax's own term),
-// then the chosen experts' values over them.  Bound by the T * E elements
-// written.  `vec`: rows and their length allow 16-byte stores.
+// then the chosen experts' values over them.  16384 tokens of 256 experts, top-6,
+// fp32: 6.2 us (17.9 MB: 2.65 us at the copy rate), the rest two dependent reads,
+// ids and then their logits, and a launch.  `vec`: rows and their length allow 16-byte stores.
 __device__ __forceinline__ float group_sum(float v, int width) {
   for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;

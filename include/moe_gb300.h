@@ -677,8 +677,11 @@ moe_status moe_block_norm_backward(int T, int H, int x_dtype, int y_dtype, int w
  *   lora_scale  device fp32 [n] or NULL (all 1)
  *   out         device [T, N] of out_dtype (`dtype` or MOE_DT_F32)
  * n_adapters == 0: the projection alone (the adapter pointers are not read).
- * Products of the projection and of A x are exact in fp32 and summed in fp32;
- * A x stays fp32 for the second product.
+ * Products of the projection and of A x are exact in fp32 and summed in fp32.
+ * A x enters the second product in fp32, or, where 16 neighbouring tokens share
+ * an adapter in a large batch, as terms of `dtype` that carry 16 of its
+ * significand bits (bf16; 24 for fp32 results) or 22 (f16).  An adapter's values,
+ * NaN included, reach the tokens that name it and no others.
  * H a multiple of 8, R a multiple of 8 up to 128, x, W, lora_a and lora_b
  * 16-byte aligned, ld_x and ld_w multiples of 8; T >= 0, N >= 1.
  * workspace: device memory of moe_adapter_linear_workspace bytes (16-byte

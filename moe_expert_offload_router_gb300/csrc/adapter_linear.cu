@@ -27,7 +27,8 @@ struct LinearArgs {
   const float* scale;
   void* out;
   float* u;            // [T, R]
-  void *u_hi, *u_lo;   // [T, R] of x's type: u's leading bits and the next ones (large batches)
+  void* u_terms;       // [terms][T, R] of x's type: u's leading bits, the next ones, ... (large batches)
+  int terms;
   int32_t* group;      // [T / 16] (large batches): the adapter that 16 tokens share, -1: none, or kMixed
   int32_t* err;
 };
@@ -179,6 +180,10 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+// A tensor-core accumulator loses a little with every step (it truncates: 4.2e-6
+// of the result over 4096 products, 0.5e-6 over 512), so a result kept in fp32
+// takes at most this many 64-wide steps in one accumulator where there is room.
+constexpr int kF32Chunk = 8;
 constexpr int kRows = 128;          // outputs (W rows) of a tile
 constexpr int kATile = kRows * 128; // bytes of a 64-wide K step of W
 
@@ -187,7 +192,8 @@ struct SplitCfg {
   static constexpr int kStage = kATile + NT * 128;
   static constexpr int kStages = NT <= 64 ? 8 : 6;
   static constexpr int kSmem = kStages * kStage + 1024;
-  static constexpr int kCols = NT < 32 ? 32 : NT;
+  static constexpr int kAcc = NT <= 64 ? 8 : 512 / NT;   // accumulators for fp32 results
+  static constexpr int kCols = kAcc * NT;
   static_assert(NT * kRows * 4 <= kStages * kStage, "the partial sums fit the stages");
 };
 
@@ -268,7 +274,7 @@ __device__ __forceinline__ void store4(const LinearArgs& a, long long t, int n, 
 template <typename TE, int NT>
 __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant__ CUtensorMap mW,
                                                            const __grid_constant__ CUtensorMap mX,
-                                                           const LinearArgs a, int early) {
+                                                           const LinearArgs a, int early, int chunk) {
   using C = SplitCfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ alignas(8) uint64_t full[C::kStages], empty[C::kStages], done;
@@ -322,14 +328,17 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
       const uint32_t idesc = idesc_f16(NT, std::is_same<TE, __nv_bfloat16>::value);
       const uint64_t d0 = umma_desc_sw128(su32(sm));
       RingPos r(C::kStages);
+      uint32_t d = tmem;
+      int in = 0;   // K steps in the accumulator
       for (int k = k0; k < k1; ++k) {
         if (!wait_bar(&full[r.stage], r.parity, &s_err)) break;
         tc_fence_after();
         const uint64_t da = d0 + (uint32_t)(r.stage * C::kStage / 16), db = da + kATile / 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_k16(tmem, da + 2 * j, db + 2 * j, idesc, k != k0 || j);
+        for (int j = 0; j < 4; ++j) mma_k16(d, da + 2 * j, db + 2 * j, idesc, in || j);
         mma_commit(&empty[r.stage]);
         r.next();
+        if (++in == chunk) in = 0, d += NT;
       }
       mma_commit(&done);
     }
@@ -350,11 +359,15 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
   const int q = warp & 3;
 #pragma unroll
   for (int ch = warp >> 2; ch < NT / 16; ch += 2) {
-    uint32_t v[16];
-    tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ch * 16), v);
+    float f[16];
+    for (int b = 0; b * chunk < k1 - k0; ++b) {   // the accumulators in order
+      uint32_t v[16];
+      tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + ch * 16), v);
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      part[(ch * 16 + j) * kRows + q * 32 + lane] = ok ? __uint_as_float(v[j]) : NAN;
+      for (int j = 0; j < 16; ++j) f[j] = b ? f[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) part[(ch * 16 + j) * kRows + q * 32 + lane] = ok ? f[j] : NAN;
   }
   if (!ok) {   // a wait gave up: leave the copies in flight time to land
     const uint64_t since = gtimer();
@@ -596,18 +609,18 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
       }
       const float sc = a.scale ? a.scale[s_id[tt]] : 1.f;
       const long long o = (long long)(t0 + tt) * a.R + c * 4;
-      TE hi[4], lo[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] *= sc;
-        hi[j] = from_f32<TE>(v[j]);
-        lo[j] = from_f32<TE>(v[j] - to_f32(hi[j]));
         if (!std::is_same<TE, __nv_bfloat16>::value && !(fabsf(v[j]) < 32768.f)) s_big[tt / 16] = 1;
       }
       *reinterpret_cast<float4*>(a.u + o) = make_float4(v[0], v[1], v[2], v[3]);
-      if (a.group) {
-        *reinterpret_cast<uint2*>(reinterpret_cast<TE*>(a.u_hi) + o) = *reinterpret_cast<const uint2*>(hi);
-        *reinterpret_cast<uint2*>(reinterpret_cast<TE*>(a.u_lo) + o) = *reinterpret_cast<const uint2*>(lo);
+      for (int k = 0; a.group && k < a.terms; ++k) {
+        TE e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = from_f32<TE>(v[j]), v[j] -= to_f32(e[j]);
+        *reinterpret_cast<uint2*>(reinterpret_cast<TE*>(a.u_terms) + (long long)k * a.T * a.R + o) =
+            *reinterpret_cast<const uint2*>(e);
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the sums' place goes back to the copies
@@ -658,19 +671,18 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
 // (1.89 PFLOP/s, 0.99 of the library's product), 80 at 4001 x 4096 x 4096, whose
 // tiles fill 3.79 of four rounds.
 //
-// A tensor-core accumulator loses a little with every step (it truncates), so a
-// result kept in fp32 takes at most `chunk` steps in one accumulator; the epilogue
-// adds the chunks up in registers, in order (CHUNKS; tiles of at most 128 tokens).
+// An fp32 result of more than kF32Chunk steps: the epilogue adds the chunks up in
+// registers, in order (CHUNKS; tiles of at most 128 tokens).
 //
 // Adapters: tokens come in groups of 16.  A run of groups that share one adapter
 // gets more K steps at the end of its tile, over that run's columns alone: B[a]
-// times u's leading bits, and B[a] times the next ones (two terms of 16-bit type:
-// 16 significand bits of u with bf16, 22 with f16).  A group of several adapters
+// times u's leading bits, B[a] times the next ones (terms of 16-bit type: two carry
+// 16 significand bits of u with bf16, 22 with f16; an fp32 result takes three of
+// bf16, 24 bits).  A group of several adapters
 // is done token by token in the epilogue with u in fp32.
 constexpr int kStreamStages = 8;   // at most: as many as fit 208 KB
 constexpr int kStreamBytes = 208 * 1024;
 constexpr int kStreamThreads = 320;   // TMA, MMA, eight epilogue warps
-constexpr int kF32Chunk = 8;          // K steps in one accumulator for fp32 results: 512 products a sum
 
 struct StreamPlan {
   int nt, stages, tiles_n, tiles;   // tokens of a tile, stages of the ring, tiles of 256 outputs, all tiles
@@ -713,8 +725,8 @@ __device__ __forceinline__ uint32_t idesc_pair(int n, bool bf16) {   // M = 256
 template <typename TE, bool CHUNKS>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     linear_stream_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
-                         const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mH,
-                         const __grid_constant__ CUtensorMap mL, const LinearArgs a, const StreamPlan pl) {
+                         const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mU,
+                         const LinearArgs a, const StreamPlan pl) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ alignas(8) uint64_t full[kStreamStages], empty[kStreamStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
@@ -807,7 +819,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const int t1 = t0 + g * 16 + rank * len * 8;
         if (lead)
           for (int c = 0; c < rchunks && ok; ++c)
-            ok = stage(&mB, &mH, c * 64, id * a.N + n0, t1) && stage(&mB, &mL, c * 64, id * a.N + n0, t1);
+            for (int k = 0; k < a.terms && ok; ++k) ok = stage(&mB, &mU, c * 64, id * a.N + n0, k * a.T + t1);
         return ok = __all_sync(0xffffffffu, ok);
       });
     }
@@ -843,11 +855,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           runs(mine, [&](int id, int g, int len) {
             if (lead) {
               const uint32_t id16 = idesc_pair(len * 16, bf16);
-              for (int c = 0; c < 2 * rchunks; ++c) {
+              for (int c = 0; c < a.terms * rchunks; ++c) {
                 if (!(ok = wait_bar(&full[r.stage], r.parity, &s_err))) break;
                 tc_fence_after();
                 const uint64_t da = d0 + r.stage * (bytes / 16), db = da + kATile / 16;
-                const int left = a.R - (c / 2) * 64, steps = left >= 64 ? 4 : (left + 15) / 16;
+                const int left = a.R - (c / a.terms) * 64, steps = left >= 64 ? 4 : (left + 15) / 16;
                 for (int j = 0; j < steps; ++j) mma_k16_pair(d + g * 16, da + 2 * j, db + 2 * j, id16, 1);
                 mma_commit_pair(&empty[r.stage]);
                 r.next();
@@ -997,8 +1009,11 @@ static moe_status launch_split(const LinearArgs& a, int dtype, cudaStream_t s) {
   // where one of the eight GPCs takes each (16 of them: 13.4 us for 64 tokens to 2048 outputs, of four 8.9)
   int cs = 1;
   while (cs < (tiles_n * tiles_t <= 8 ? 8 : 4) && (long long)tiles_n * tiles_t * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
+  // K steps of an accumulator: all of a block's for 16-bit results, else 8 or what its accumulators ask for
+  const int most = (nk + cs - 1) / cs, each = (most + C::kAcc - 1) / C::kAcc;
+  const int chunk = a.out_dtype != MOE_DT_F32 ? most : each > kF32Chunk ? each : kF32Chunk;
   return launch_cluster(kernel, dim3(cs, tiles_n, tiles_t), 256, cs, C::kSmem, s, "linear_split_kernel", mW, mX, a,
-                        a.n ? 1 : 0);
+                        a.n ? 1 : 0, chunk);
 }
 
 template <typename TE>
@@ -1017,33 +1032,37 @@ static moe_status launch_shrink(const LinearArgs& a, int dtype, cudaStream_t s) 
   return launch_cluster(kernel, dim3(cs, tiles), 256, cs, kShrinkSmem, s, "adapter_shrink_kernel", mA, mX, a);
 }
 
-// Whether a call is large: with one block per SM, tiles of 128 x 128 fill them.
-static bool large_batch(int T, int N) {
-  return T > 128 && ((long long)N + kRows - 1) / kRows * ((T + 127) / 128) >= device_sms() * 3 / 4;
+// Whether a call goes to the persistent pairs: once its tiles of 128 x 128 are
+// more than the SMs (H = 4096, 192 tiles: 34.5 us split, 22.8 streamed; 128 tiles:
+// 17.9 and 22.5).  With adapters or fp32 results from three quarters of the SMs
+// on: the split kernel takes adapters token by token on the CUDA cores, and has
+// accumulators for 512 products each only up to H = 2048 a block.
+static bool large_batch(int T, int N, bool early) {
+  const long long tiles = ((long long)N + kRows - 1) / kRows * ((T + 127) / 128);
+  return T > 128 && tiles * (early ? 4 : 3) >= device_sms() * 3LL + (early ? 0 : 1);
 }
 
 template <typename TE>
 static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) {
-  CUtensorMap mW, mX, mB = {}, mH = {}, mL = {};
+  CUtensorMap mW, mX, mB = {}, mU = {};
   StreamPlan pl;
   pl.tiles_n = (a.N + 2 * kRows - 1) / (2 * kRows);
   pl.nk = (a.H + 63) / 64;
   const bool chunks = a.out_dtype == MOE_DT_F32 && pl.nk > kF32Chunk;
   pl.chunk = chunks ? kF32Chunk : pl.nk;
-  // the tile that takes the fewest rounds of the pairs times its length; 16: what a tile costs beside its
-  // tokens, 240: a step takes no less (0.27 us at NT = 112 as at 224: the copies' and the commits' own time)
+  // the tile that takes the least time: rounds of the pairs times a step's rows into an SM (128 of W and
+  // NT / 2 of x, in units of half a row); among equals the one that leaves fewest pairs idle
   const int pairs = device_sms() / 2;
   long long best = -1;
   for (int nt = chunks ? 128 : 256; nt >= 64; nt -= 16) {
-    const long long tiles = (long long)pl.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + pairs - 1) / pairs * (nt > 224 ? nt + 16 : 240);
+    const long long tiles = (long long)pl.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + pairs - 1) / pairs * (nt + 256);
     if (best < 0 || cost < best) best = cost, pl.nt = nt, pl.tiles = (int)tiles;
   }
   moe_status st = map_rows(&mW, a.W, dtype, a.H, a.N, a.ld_w, kRows);
   if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.H, a.T, a.ld_x, pl.nt / 2);
   if (a.n) {
     if (st == MOE_OK) st = map_rows(&mB, a.B, dtype, a.R, (uint64_t)a.n * a.N, a.R, kRows);
-    if (st == MOE_OK) st = map_rows(&mH, a.u_hi, dtype, a.R, a.T, a.R, pl.nt / 2);
-    if (st == MOE_OK) st = map_rows(&mL, a.u_lo, dtype, a.R, a.T, a.R, pl.nt / 2);
+    if (st == MOE_OK) st = map_rows(&mU, a.u_terms, dtype, a.R, (uint64_t)a.terms * a.T, a.R, pl.nt / 2);
   }
   if (st != MOE_OK) return st;
   const int fit = kStreamBytes / (kATile + pl.nt * 64);
@@ -1052,14 +1071,14 @@ static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) 
   static char allowed[2][64];
   MOE_CUDA(allow_smem(kernel, kStreamBytes + 1024, allowed[chunks]));
   return launch_cluster(kernel, dim3(2 * (pl.tiles < pairs ? pl.tiles : pairs)), kStreamThreads, 2, kStreamBytes + 1024,
-                        s, "linear_stream_kernel", mW, mX, mB, mH, mL, a, pl);
+                        s, "linear_stream_kernel", mW, mX, mB, mU, a, pl);
 }
 
 template <typename TE>
 static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) {
   ProfScope ps(MOE_K_LINEAR, s);
   moe_status st = MOE_OK;
-  const bool large = large_batch(a.T, a.N);
+  const bool large = large_batch(a.T, a.N, a.n || a.out_dtype == MOE_DT_F32);
   if (a.n) {
     // one dot per token and rank re-reads A for every token: worth it up to this many bytes
     if (!large && (long long)a.T * a.R * a.H * 2 <= (64LL << 20)) {
@@ -1078,9 +1097,9 @@ static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) 
   return launch_split<TE, 128>(a, dtype, s);
 }
 
-// The workspace's parts: u, and for large batches u's two 16-bit terms and the groups' table.
+// The workspace's parts: u, and for large batches u's 16-bit terms (room for three) and the groups' table.
 struct LinearSpace {
-  size_t u, hi, lo, group, bytes;
+  size_t u, terms, group, bytes;
 };
 static LinearSpace linear_space(int T, int N, int n, int R) {
   LinearSpace w = {};
@@ -1091,9 +1110,8 @@ static LinearSpace linear_space(int T, int N, int n, int R) {
     return at;
   };
   w.u = take((size_t)T * R * 4);
-  if (large_batch(T, N)) {
-    w.hi = take((size_t)T * R * 2);
-    w.lo = take((size_t)T * R * 2);
+  if (large_batch(T, N, true)) {
+    w.terms = take((size_t)T * R * 2 * 3);
     w.group = take(((size_t)T + 15) / 16 * 4);
   }
   return w;
@@ -1120,7 +1138,9 @@ extern "C" moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out
   MOE_ARG(out_dtype == dtype || out_dtype == MOE_DT_F32, "out must be of x's type or fp32 (type %d)", out_dtype);
   MOE_ARG(n_adapters >= 0, "n_adapters must be >= 0 (got %d)", n_adapters);
   MOE_ARG(!n_adapters || (R >= 8 && R <= 128 && R % 8 == 0), "R must be a multiple of 8 up to 128 (got %d)", R);
-  MOE_ARG((long long)n_adapters * N + kRows <= 0x7fffffffLL, "n_adapters * N must be below 2^31");
+  MOE_ARG((long long)n_adapters * N + 2 * kRows <= 0x7fffffffLL && (long long)n_adapters * R <= 0x7fffffffLL,
+          "n_adapters * N and n_adapters * R must be below 2^31");
+  MOE_ARG(T <= 1 << 29, "T must be at most 2^29 (got %d)", T);
   if (T == 0) return MOE_OK;
   MOE_ARG(x && W && out, "null pointer");
   MOE_ARG(ld_x >= H && ld_w >= H && ld_out >= N, "a row distance is below the row's length");
@@ -1141,7 +1161,8 @@ extern "C" moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out
   a.ids = adapter_ids, a.scale = lora_scale, a.out = out, a.err = d_error;
   if (n_adapters) {
     a.u = (float*)(ws + w.u);
-    if (w.group) a.u_hi = ws + w.hi, a.u_lo = ws + w.lo, a.group = (int32_t*)(ws + w.group);
+    if (w.group) a.u_terms = ws + w.terms, a.group = (int32_t*)(ws + w.group);
+    a.terms = dtype == MOE_DT_BF16 && out_dtype == MOE_DT_F32 ? 3 : 2;
   }
   return dtype == MOE_DT_BF16 ? launch_linear<__nv_bfloat16>(a, dtype, stream)
                               : launch_linear<__half>(a, dtype, stream);

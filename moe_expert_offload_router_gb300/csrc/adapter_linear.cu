@@ -197,38 +197,127 @@ struct SplitCfg {
   static_assert(NT * kRows * 4 <= kStages * kStage, "the partial sums fit the stages");
 };
 
-// v[j] += B[a][n] . u[t1 + j] in fp32 for the tokens j of `who` (below `left`), by
-// a whole warp, lane -> n.  Eight ranks at a time: a lane loads a quarter row of
-// one token's u, which shuffles hand to all, and B's eight for its own n; both a
-// step ahead.
 template <typename TE>
-__device__ __forceinline__ void add_adapter16(const LinearArgs& a, int id, uint32_t who, int t1, int left, int n,
-                                              float* v) {
-  const int lane = threadIdx.x & 31;
-  const TE* B = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + (n < a.N ? n : a.N - 1)) * a.R;
-  const float* u = a.u + (long long)(t1 + ((lane & 15) < left ? lane & 15 : 0)) * a.R + (lane >> 4) * 4;
-  uint4 b = *reinterpret_cast<const uint4*>(B);
-  float4 w = *reinterpret_cast<const float4*>(u);
-  for (int r = 0; r < a.R; r += 8) {
-    const float2 b0 = Pair<TE>::f32(b.x), b1 = Pair<TE>::f32(b.y), b2 = Pair<TE>::f32(b.z), b3 = Pair<TE>::f32(b.w);
-    const float4 c = w;
-    if (r + 8 < a.R) {
-      b = *reinterpret_cast<const uint4*>(B + r + 8);
-      w = *reinterpret_cast<const float4*>(u + r + 8);
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack_pair<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack_pair<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename TE>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (std::is_same<TE, __nv_bfloat16>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The adapters' part of 32 outputs (from n0) x 16 tokens (from t0, `cols` of them
+// there) by a warp; lane l holds the id of token l & 15 in `mine` (negative: none).
+// Whatever the mixture: B[a] u is taken for every adapter that the tokens name,
+// over all 16 columns, and a token keeps the column of its own; no value of
+// another adapter is added to it, not even times 0.  u enters as terms of x's type
+// (fp16: scaled by a power of two to below 2^14 first, so that it neither
+// overflows nor loses its low bits).  Fragments come straight from memory: lane
+// (g, c) loads 16 bytes of B at k = 32 i + 8 c of rows g and g + 8 and takes them
+// as the k16 steps 2 i and 2 i + 1, u's eight values in the same order.
+// sel[m][j]: rows 16 m + g (+ 8), columns 8 j + 2 c (+ 1), as m16n8 accumulators.
+template <typename TE>
+__device__ __forceinline__ void adapter_block(const LinearArgs& a, int mine, long long t0, int cols, int n0,
+                                              float (&sel)[2][2][4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  constexpr bool kScaled = !std::is_same<TE, __nv_bfloat16>::value;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) (&sel[0][0][0])[i] = 0.f;
+  uint32_t left = __ballot_sync(0xffffffffu, mine >= 0) & 0xffff;
+  const float* u[2];
+  float up[2] = {1.f, 1.f}, down[2][2];   // of column g; of columns 2 c and 2 c + 1
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int col = j * 8 + g;
+    u[j] = a.u + (t0 + (col < cols ? col : 0)) * a.R + c * 8;
+    if (kScaled) {
+      float top = 0.f;
+      for (int k = 0; k + c * 8 < a.R; k += 32) {
+        const float4 p = *reinterpret_cast<const float4*>(u[j] + k), q = *reinterpret_cast<const float4*>(u[j] + k + 4);
+        top = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))),
+                    fmaxf(fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w))), top));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      int e = (int)(__float_as_uint(top) >> 23 & 255) - 127 - 13;   // top in [2^13, 2^14) after the scale
+      e = top == 0.f || e > 114 ? 0 : e < -100 ? -100 : e;
+      up[j] = __uint_as_float((uint32_t)(127 - e) << 23);
+      const float dn = __uint_as_float((uint32_t)(127 + e) << 23);
+      down[j][0] = __shfl_sync(0xffffffffu, dn, c * 8);
+      down[j][1] = __shfl_sync(0xffffffffu, dn, c * 8 + 4);
+    }
+  }
+  while (left) {
+    const int id = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+    const uint32_t who = __ballot_sync(0xffffffffu, mine == id) & 0xffff;
+    left &= ~who;
+    const TE* rows[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int n = n0 + m * 8 + g;
+      rows[m] = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + (n < a.N ? n : a.N - 1)) * a.R + c * 8;
+    }
+    float d[2][2][4] = {};
+#pragma unroll 2
+    for (int k = 0; k < a.R; k += 32) {
+      const bool in = k + c * 8 < a.R;
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      uint4 A[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) A[m] = in ? *reinterpret_cast<const uint4*>(rows[m] + k) : z;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4 z4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 p = in ? *reinterpret_cast<const float4*>(u[j] + k) : z4;
+        const float4 q = in ? *reinterpret_cast<const float4*>(u[j] + k + 4) : z4;
+        float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+        if (kScaled)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= up[j];
+        for (int term = 0; term < a.terms; ++term) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = pack_pair<TE>(f[2 * i], f[2 * i + 1]);
+            const float2 t = Pair<TE>::f32(w[i]);
+            f[2 * i] -= t.x, f[2 * i + 1] -= t.y;
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            mma16816<TE>(d[m][j], A[2 * m].x, A[2 * m + 1].x, A[2 * m].y, A[2 * m + 1].y, w[0], w[1]);
+            mma16816<TE>(d[m][j], A[2 * m].z, A[2 * m + 1].z, A[2 * m].w, A[2 * m + 1].w, w[2], w[3]);
+          }
+        }
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (!(who >> j & 1)) continue;
-      float s = b0.x * __shfl_sync(0xffffffffu, c.x, j);
-      s = fmaf(b0.y, __shfl_sync(0xffffffffu, c.y, j), s);
-      s = fmaf(b1.x, __shfl_sync(0xffffffffu, c.z, j), s);
-      s = fmaf(b1.y, __shfl_sync(0xffffffffu, c.w, j), s);
-      s = fmaf(b2.x, __shfl_sync(0xffffffffu, c.x, j + 16), s);
-      s = fmaf(b2.y, __shfl_sync(0xffffffffu, c.y, j + 16), s);
-      s = fmaf(b3.x, __shfl_sync(0xffffffffu, c.z, j + 16), s);
-      s = fmaf(b3.y, __shfl_sync(0xffffffffu, c.w, j + 16), s);
-      v[j] += s;
-    }
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (who >> (j * 8 + 2 * c + i) & 1)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            sel[m][j][i] += kScaled ? d[m][j][i] * down[j][i] : d[m][j][i];
+            sel[m][j][i + 2] += kScaled ? d[m][j][i + 2] * down[j][i] : d[m][j][i + 2];
+          }
   }
 }
 // One column of 16 tokens (those below `left`).
@@ -384,67 +473,52 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
   }
   if (!ok && threadIdx.x == 0 && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
   if (early) pdl_wait();   // u
-  // four outputs of two tokens at a time: the loads of both are under way together
-  const int share = NT / cs, items = share * (kRows / 4);
+  // the blocks' sums of this block's share of the tokens, four outputs at a time; with adapters they
+  // go back to their place in this block's own sums (which no other block reads) for the adapters' part
+  const int share = NT / cs;
   const uint32_t base = su32(part);
-  for (int i = threadIdx.x; i < items; i += 512) {
-    float v[2][4] = {};
-    int id[2], tt[2], nn[2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int it = i + m * 256;
-      tt[m] = it < items ? rank * share + it / (kRows / 4) : NT;
-      nn[m] = n0 + it % (kRows / 4) * 4;
-      const bool in = tt[m] < NT && t0 + tt[m] < a.T && nn[m] < a.N;
-      if (!in) tt[m] = -1;
-      id[m] = in && a.n ? a.ids[t0 + tt[m]] : -1;
-      if (id[m] >= a.n) id[m] = -1;
-    }
+  for (int i = threadIdx.x; i < share * (kRows / 4); i += 256) {
+    const int tt = rank * share + i / (kRows / 4), nn = i % (kRows / 4) * 4;
+    if (t0 + tt >= a.T || n0 + nn >= a.N) continue;
+    float* own = part + tt * kRows + nn;
+    float v[4] = {};
     for (int r = 0; r < cs; ++r) {
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (tt[m] < 0) continue;
-        const uint32_t at = (uint32_t)(tt[m] * kRows + nn[m] - n0) * 4;
-        const float4 f = cs > 1 ? ld_cluster4(base + at, r) : *reinterpret_cast<const float4*>(sm + at);
-        v[m][0] += f.x, v[m][1] += f.y, v[m][2] += f.z, v[m][3] += f.w;
-      }
+      const float4 f = cs > 1 ? ld_cluster4(base + (uint32_t)(tt * kRows + nn) * 4, r) : *reinterpret_cast<const float4*>(own);
+      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
     }
-    if (id[0] >= 0 || id[1] >= 0) {
-      const TE* B[2];
-      const float* u[2];
-      int row[2][4];
+    if (a.n) *reinterpret_cast<float4*>(own) = make_float4(v[0], v[1], v[2], v[3]);
+    else store4<TE>(a, t0 + tt, n0 + nn, v);
+  }
+  if (a.n) {
+    __syncthreads();
+    // a warp takes 32 outputs of 16 tokens
+    for (int i = (warp >> 2) * 16; i < share && t0 + rank * share + i < a.T; i += 32) {
+      const long long tb = t0 + rank * share + i;
+      const int room = share - i < 16 ? share - i : 16, cols = a.T - tb < room ? (int)(a.T - tb) : room;
+      int mine = (lane & 15) < cols ? a.ids[tb + (lane & 15)] : -1;
+      if (mine >= a.n) mine = -1;
+      if (!__any_sync(0xffffffffu, mine >= 0)) continue;
+      float sel[2][2][4];
+      adapter_block<TE>(a, mine, tb, cols, n0 + q * 32, sel);
+      float* at = part + (rank * share + i) * kRows + q * 32;
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {   // where there is no adapter or no output: another's, dropped below
-        const bool own = id[m] >= 0;
-        const int of = own ? id[m] : id[1 - m], n1 = own ? nn[m] : nn[1 - m], t1 = own ? tt[m] : tt[1 - m];
-        B[m] = reinterpret_cast<const TE*>(a.B) + ((long long)of * a.N + n1) * a.R;
-        u[m] = a.u + (long long)(t0 + t1) * a.R;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) row[m][j] = n1 + j < a.N ? j * a.R : 0;
-      }
-      float d[2][4] = {};
-      for (int r = 0; r < a.R; r += 8) {
+        for (int k = 0; k < 2; ++k) {
+          const int col = j * 8 + 2 * (lane & 3) + k;
+          if (col >= cols) continue;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const float4 p = *reinterpret_cast<const float4*>(u[m] + r), q = *reinterpret_cast<const float4*>(u[m] + r + 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 b = *reinterpret_cast<const uint4*>(B[m] + row[m][j] + r);
-            const float2 b0 = Pair<TE>::f32(b.x), b1 = Pair<TE>::f32(b.y), b2 = Pair<TE>::f32(b.z),
-                         b3 = Pair<TE>::f32(b.w);
-            d[m][j] += fmaf(b0.x, p.x, fmaf(b0.y, p.y, fmaf(b1.x, p.z, b1.y * p.w))) +
-                       fmaf(b2.x, q.x, fmaf(b2.y, q.y, fmaf(b3.x, q.z, b3.y * q.w)));
+          for (int m = 0; m < 2; ++m) {
+            at[col * kRows + m * 16 + (lane >> 2)] += sel[m][j][k];
+            at[col * kRows + m * 16 + (lane >> 2) + 8] += sel[m][j][k + 2];
           }
         }
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[m][j] = id[m] < 0 ? v[m][j] : v[m][j] + d[m][j];
     }
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-      if (tt[m] >= 0) store4<TE>(a, t0 + tt[m], nn[m], v[m]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < share * (kRows / 4); i += 256) {
+      const int tt = rank * share + i / (kRows / 4), nn = i % (kRows / 4) * 4;
+      if (t0 + tt < a.T && n0 + nn < a.N) store4<TE>(a, t0 + tt, n0 + nn, part + tt * kRows + nn);
+    }
   }
   __syncwarp();
   if (cs > 1) cluster_sync();   // the others have read this block's sums
@@ -679,9 +753,11 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
 // times u's leading bits, B[a] times the next ones (terms of 16-bit type: two carry
 // 16 significand bits of u with bf16, 22 with f16; an fp32 result takes three of
 // bf16, 24 bits).  A group of several adapters
-// is done token by token in the epilogue with u in fp32.
+// is done in the epilogue (adapter_block).
 constexpr int kStreamStages = 8;   // at most: as many as fit 208 KB
 constexpr int kStreamBytes = 208 * 1024;
+constexpr int kStreamSmem = kStreamBytes + 8 * 2048 + 1024;
+static_assert(kStreamSmem + 512 <= 232448, "shared memory per block");
 constexpr int kStreamThreads = 320;   // TMA, MMA, eight epilogue warps
 
 struct StreamPlan {
@@ -732,6 +808,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int s_err;
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  float* turn = reinterpret_cast<float*>(sm + kStreamBytes);   // the epilogue's, 2 KB a warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;   // clusters of two along x
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
@@ -916,15 +993,25 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (c0 + c * 16 >= pl.nt || t1 >= a.T) break;
         float* f = CHUNKS ? v + c * 16 : v;
         if (!CHUNKS) columns(c, f, false);
-        if (mixed >> c & 1) {   // the adapters that the 16 tokens name, one after the other
-          const int mine = t1 + (lane & 15) < a.T ? a.ids[t1 + (lane & 15)] : -1;
-          uint32_t left = __ballot_sync(0xffffffffu, mine >= 0 && mine < a.n) & 0xffff;
-          while (left) {
-            const int id = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
-            const uint32_t who = __ballot_sync(0xffffffffu, mine == id) & 0xffff;
-            left &= ~who;
-            add_adapter16<TE>(a, id, who, t1, a.T - t1, n, f);
-          }
+        if (mixed >> c & 1) {
+          const int cols = a.T - t1 < 16 ? a.T - t1 : 16;
+          int id = (lane & 15) < cols ? a.ids[t1 + (lane & 15)] : -1;
+          if (id >= a.n) id = -1;
+          float sel[2][2][4];
+          adapter_block<TE>(a, id, t1, cols, n - lane, sel);
+          // fragments -> lane l the output n, through the warp's own [16][32] of shared memory
+          float* own = turn + (warp - 2) * 512;
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+                own[(j * 8 + 2 * (lane & 3) + (k & 1)) * 32 + m * 16 + (lane >> 2) + (k & 2) * 4] = sel[m][j][k];
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] += own[j * 32 + lane];
         }
         if (n < a.N) {
           const long long o = (long long)t1 * a.ld_out + n;
@@ -1069,8 +1156,8 @@ static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) 
   pl.stages = fit < kStreamStages ? fit : kStreamStages;
   auto kernel = chunks ? linear_stream_kernel<TE, true> : linear_stream_kernel<TE, false>;
   static char allowed[2][64];
-  MOE_CUDA(allow_smem(kernel, kStreamBytes + 1024, allowed[chunks]));
-  return launch_cluster(kernel, dim3(2 * (pl.tiles < pairs ? pl.tiles : pairs)), kStreamThreads, 2, kStreamBytes + 1024,
+  MOE_CUDA(allow_smem(kernel, kStreamSmem, allowed[chunks]));
+  return launch_cluster(kernel, dim3(2 * (pl.tiles < pairs ? pl.tiles : pairs)), kStreamThreads, 2, kStreamSmem,
                         s, "linear_stream_kernel", mW, mX, mB, mU, a, pl);
 }
 

@@ -3,7 +3,7 @@
 //
 // u (fp32 [T, R]) comes from a first kernel; the projection's kernel starts
 // beside it (programmatic dependent launch) and waits for it only before its
-// epilogue, where B[a] u is added in fp32 token by token: an adapter touches
+// epilogue, where B[a] u is added in fp32 to the tokens that name a: an adapter touches
 // the tokens that name it and no others, whoever shares their tile.
 //
 // The projection runs on tcgen05 (kind::f16, fp32 accumulators in tensor
@@ -33,7 +33,7 @@ struct LinearArgs {
   int32_t* err;
 };
 
-constexpr int kMixed = -2;   // a group of 16 tokens whose adapters go token by token
+constexpr int kMixed = -2;   // a group of 16 tokens that do not share one adapter (adapter_block)
 
 template <typename TE>
 struct Pair;   // two packed elements as fp32
@@ -224,6 +224,38 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Eight values of u (fp32, times `up`; zeros where not `in`) as three terms of x's type.
+template <typename TE>
+__device__ __forceinline__ void split_terms(const float* u, bool in, float up, uint32_t (&w)[3][4]) {
+  float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
+  if (in) p = *reinterpret_cast<const float4*>(u), q = *reinterpret_cast<const float4*>(u + 4);
+  float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+  if (!std::is_same<TE, __nv_bfloat16>::value)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= up;
+#pragma unroll
+  for (int t = 0; t < 3; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[t][i] = pack_pair<TE>(f[2 * i], f[2 * i + 1]);
+      const float2 r = Pair<TE>::f32(w[t][i]);
+      f[2 * i] -= r.x, f[2 * i + 1] -= r.y;
+    }
+}
+// Both m16 tiles of B's rows (A: rows g, g + 8, g + 16, g + 24) times u's first `terms` terms.
+template <typename TE>
+__device__ __forceinline__ void mma_terms(float (&d0)[4], float (&d1)[4], const uint4 (&A)[4],
+                                          const uint32_t (&w)[3][4], int terms) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    if (t == 2 && terms < 3) break;
+    mma16816<TE>(d0, A[0].x, A[1].x, A[0].y, A[1].y, w[t][0], w[t][1]);
+    mma16816<TE>(d1, A[2].x, A[3].x, A[2].y, A[3].y, w[t][0], w[t][1]);
+    mma16816<TE>(d0, A[0].z, A[1].z, A[0].w, A[1].w, w[t][2], w[t][3]);
+    mma16816<TE>(d1, A[2].z, A[3].z, A[2].w, A[3].w, w[t][2], w[t][3]);
+  }
+}
+
 // The adapters' part of 32 outputs (from n0) x 16 tokens (from t0, `cols` of them
 // there) by a warp; lane l holds the id of token l & 15 in `mine` (negative: none).
 // Whatever the mixture: B[a] u is taken for every adapter that the tokens name,
@@ -265,47 +297,42 @@ __device__ __forceinline__ void adapter_block(const LinearArgs& a, int mine, lon
       down[j][1] = __shfl_sync(0xffffffffu, dn, c * 8 + 4);
     }
   }
+  // u's terms of the first 32 ranks, for all adapters; B's rows one adapter ahead
+  uint32_t w0[2][3][4];
+  const bool in0 = c * 8 < a.R;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) split_terms<TE>(u[j], in0, up[j], w0[j]);
+  auto row_of = [&](int id, int m) {
+    const int n = n0 + m * 8 + g;
+    return reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + (n < a.N ? n : a.N - 1)) * a.R + c * 8;
+  };
+  auto rows_at = [&](int id, int k, uint4 (&A)[4]) {
+    const bool in = k + c * 8 < a.R;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      A[m] = in ? *reinterpret_cast<const uint4*>(row_of(id, m) + k) : make_uint4(0, 0, 0, 0);
+  };
+  int id = left ? __shfl_sync(0xffffffffu, mine, __ffs(left) - 1) : 0;
+  uint4 A[4];
+  if (left) rows_at(id, 0, A);
   while (left) {
-    const int id = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
     const uint32_t who = __ballot_sync(0xffffffffu, mine == id) & 0xffff;
     left &= ~who;
-    const TE* rows[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int n = n0 + m * 8 + g;
-      rows[m] = reinterpret_cast<const TE*>(a.B) + ((long long)id * a.N + (n < a.N ? n : a.N - 1)) * a.R + c * 8;
-    }
+    const int next = left ? __shfl_sync(0xffffffffu, mine, __ffs(left) - 1) : id;
+    uint4 N[4];
+    if (left) rows_at(next, 0, N);
     float d[2][2][4] = {};
-#pragma unroll 2
-    for (int k = 0; k < a.R; k += 32) {
-      const bool in = k + c * 8 < a.R;
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      uint4 A[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) A[m] = in ? *reinterpret_cast<const uint4*>(rows[m] + k) : z;
+    for (int j = 0; j < 2; ++j)
+      if (who >> (j * 8) & 0xff) mma_terms<TE>(d[0][j], d[1][j], A, w0[j], a.terms);
+    for (int k = 32; k < a.R; k += 32) {
+      rows_at(id, k, A);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float4 z4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 p = in ? *reinterpret_cast<const float4*>(u[j] + k) : z4;
-        const float4 q = in ? *reinterpret_cast<const float4*>(u[j] + k + 4) : z4;
-        float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-        if (kScaled)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= up[j];
-        for (int term = 0; term < a.terms; ++term) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w[i] = pack_pair<TE>(f[2 * i], f[2 * i + 1]);
-            const float2 t = Pair<TE>::f32(w[i]);
-            f[2 * i] -= t.x, f[2 * i + 1] -= t.y;
-          }
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            mma16816<TE>(d[m][j], A[2 * m].x, A[2 * m + 1].x, A[2 * m].y, A[2 * m + 1].y, w[0], w[1]);
-            mma16816<TE>(d[m][j], A[2 * m].z, A[2 * m + 1].z, A[2 * m].w, A[2 * m + 1].w, w[2], w[3]);
-          }
-        }
+        if (!(who >> (j * 8) & 0xff)) continue;
+        uint32_t w[3][4];
+        split_terms<TE>(u[j] + k, k + c * 8 < a.R, up[j], w);
+        mma_terms<TE>(d[0][j], d[1][j], A, w, a.terms);
       }
     }
 #pragma unroll
@@ -318,7 +345,28 @@ __device__ __forceinline__ void adapter_block(const LinearArgs& a, int mine, lon
             sel[m][j][i] += kScaled ? d[m][j][i] * down[j][i] : d[m][j][i];
             sel[m][j][i + 2] += kScaled ? d[m][j][i + 2] * down[j][i] : d[m][j][i + 2];
           }
+    id = next;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) A[m] = N[m];
   }
+}
+// The same into a warp's own [16][32] of shared memory, from where lane l takes output n0 + l.
+template <typename TE>
+__device__ __forceinline__ void adapter_turn(const LinearArgs& a, int t1, int n0, float* own) {
+  const int lane = threadIdx.x & 31, cols = a.T - t1 < 16 ? a.T - t1 : 16;
+  int mine = (lane & 15) < cols ? a.ids[t1 + (lane & 15)] : -1;
+  if (mine >= a.n) mine = -1;
+  float sel[2][2][4];
+  adapter_block<TE>(a, mine, t1, cols, n0, sel);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        own[(j * 8 + 2 * (lane & 3) + (k & 1)) * 32 + m * 16 + (lane >> 2) + (k & 2) * 4] = sel[m][j][k];
+  __syncwarp();
 }
 // One column of 16 tokens (those below `left`).
 template <typename T>
@@ -473,11 +521,11 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
   }
   if (!ok && threadIdx.x == 0 && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
   if (early) pdl_wait();   // u
-  // the blocks' sums of this block's share of the tokens, four outputs at a time; with adapters they
-  // go back to their place in this block's own sums (which no other block reads) for the adapters' part
-  const int share = NT / cs;
+  // the blocks' sums of this block's share of the tokens, four outputs at a time; with adapters they go
+  // back to their place in this block's own sums (which no other block reads)
+  const int share = NT / cs, items = share * (kRows / 4);
   const uint32_t base = su32(part);
-  for (int i = threadIdx.x; i < share * (kRows / 4); i += 256) {
+  for (int i = threadIdx.x; i < items; i += 256) {
     const int tt = rank * share + i / (kRows / 4), nn = i % (kRows / 4) * 4;
     if (t0 + tt >= a.T || n0 + nn >= a.N) continue;
     float* own = part + tt * kRows + nn;
@@ -489,8 +537,64 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
     if (a.n) *reinterpret_cast<float4*>(own) = make_float4(v[0], v[1], v[2], v[3]);
     else store4<TE>(a, t0 + tt, n0 + nn, v);
   }
-  if (a.n) {
-    __syncthreads();
+  // the adapters' part.  Few ranks and tokens: each token reads its own B rows, two tokens at a time
+  // (64 tokens of 32 adapters, rank 16: 11.5 us, by MMAs 14.8); else by MMAs (128 tokens of 16 adapters,
+  // rank 128: 59 us and 51; of one adapter 56 and 25)
+  const bool few = (items + 511) / 512 * a.R <= 32;
+  if (a.n) __syncthreads();
+  for (int i = threadIdx.x; a.n && few && i < items; i += 512) {
+    int id[2], tt[2], nn[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int it = i + m * 256;
+      tt[m] = it < items ? rank * share + it / (kRows / 4) : NT;
+      nn[m] = n0 + it % (kRows / 4) * 4;
+      const bool in = tt[m] < NT && t0 + tt[m] < a.T && nn[m] < a.N;
+      if (!in) tt[m] = -1;
+      id[m] = in ? a.ids[t0 + tt[m]] : -1;
+      if (id[m] >= a.n) id[m] = -1;
+    }
+    float d[2][4] = {};
+    if (id[0] >= 0 || id[1] >= 0) {
+      const TE* B[2];
+      const float* u[2];
+      int row[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {   // where there is no adapter or no output: the other's, dropped below
+        const bool own = id[m] >= 0;
+        const int of = own ? id[m] : id[1 - m], n1 = own ? nn[m] : nn[1 - m], t1 = own ? tt[m] : tt[1 - m];
+        B[m] = reinterpret_cast<const TE*>(a.B) + ((long long)of * a.N + n1) * a.R;
+        u[m] = a.u + (long long)(t0 + t1) * a.R;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) row[m][j] = n1 + j < a.N ? j * a.R : 0;
+      }
+#pragma unroll 2
+      for (int r = 0; r < a.R; r += 8) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float4 p = *reinterpret_cast<const float4*>(u[m] + r), q = *reinterpret_cast<const float4*>(u[m] + r + 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 b = *reinterpret_cast<const uint4*>(B[m] + row[m][j] + r);
+            const float2 b0 = Pair<TE>::f32(b.x), b1 = Pair<TE>::f32(b.y), b2 = Pair<TE>::f32(b.z),
+                         b3 = Pair<TE>::f32(b.w);
+            d[m][j] += fmaf(b0.x, p.x, fmaf(b0.y, p.y, fmaf(b1.x, p.z, b1.y * p.w))) +
+                       fmaf(b2.x, q.x, fmaf(b2.y, q.y, fmaf(b3.x, q.z, b3.y * q.w)));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (tt[m] < 0) continue;
+      const float* own = part + tt[m] * kRows + nn[m] - n0;
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = id[m] < 0 ? own[j] : own[j] + d[m][j];
+      store4<TE>(a, t0 + tt[m], nn[m], v);
+    }
+  }
+  if (a.n && !few) {
     // a warp takes 32 outputs of 16 tokens
     for (int i = (warp >> 2) * 16; i < share && t0 + rank * share + i < a.T; i += 32) {
       const long long tb = t0 + rank * share + i;
@@ -753,7 +857,9 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
 // times u's leading bits, B[a] times the next ones (terms of 16-bit type: two carry
 // 16 significand bits of u with bf16, 22 with f16; an fp32 result takes three of
 // bf16, 24 bits).  A group of several adapters
-// is done in the epilogue (adapter_block).
+// is done in the epilogue (adapter_block), but with
+// CHUNKS, whose accumulators leave it no registers: adapter_mixed_kernel then adds
+// to the fp32 results.
 constexpr int kStreamStages = 8;   // at most: as many as fit 208 KB
 constexpr int kStreamBytes = 208 * 1024;
 constexpr int kStreamSmem = kStreamBytes + 8 * 2048 + 1024;
@@ -802,7 +908,7 @@ template <typename TE, bool CHUNKS>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     linear_stream_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
                          const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mU,
-                         const LinearArgs a, const StreamPlan pl) {
+                         const __grid_constant__ LinearArgs a, const StreamPlan pl) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ alignas(8) uint64_t full[kStreamStages], empty[kStreamStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
@@ -984,32 +1090,18 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         ok = __all_sync(0xffffffffu, wait_bar(&acc_full[acc.stage], acc.parity, &s_err));
         tc_fence_after();
       }
-      if (a.n) groups_now(t0);
+      if (a.n && !CHUNKS) groups_now(t0);
       const uint32_t mixed =
-          a.n ? __ballot_sync(0xffffffffu, lane < groups && t0 + lane * 16 < a.T && mine == kMixed) >> (c0 / 16) : 0;
+          a.n && !CHUNKS ? __ballot_sync(0xffffffffu, lane < groups && t0 + lane * 16 < a.T && mine == kMixed) >> (c0 / 16) : 0;
 #pragma unroll
       for (int c = 0; c < kHalf / 16; ++c) {
         const int t1 = t0 + c0 + c * 16;
         if (c0 + c * 16 >= pl.nt || t1 >= a.T) break;
         float* f = CHUNKS ? v + c * 16 : v;
         if (!CHUNKS) columns(c, f, false);
-        if (mixed >> c & 1) {
-          const int cols = a.T - t1 < 16 ? a.T - t1 : 16;
-          int id = (lane & 15) < cols ? a.ids[t1 + (lane & 15)] : -1;
-          if (id >= a.n) id = -1;
-          float sel[2][2][4];
-          adapter_block<TE>(a, id, t1, cols, n - lane, sel);
-          // fragments -> lane l the output n, through the warp's own [16][32] of shared memory
+        if (!CHUNKS && (mixed >> c & 1)) {
           float* own = turn + (warp - 2) * 512;
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int m = 0; m < 2; ++m)
-                own[(j * 8 + 2 * (lane & 3) + (k & 1)) * 32 + m * 16 + (lane >> 2) + (k & 2) * 4] = sel[m][j][k];
-          __syncwarp();
+          adapter_turn<TE>(a, t1, n - lane, own);
 #pragma unroll
           for (int j = 0; j < 16; ++j) f[j] += own[j * 32 + lane];
         }
@@ -1039,6 +1131,25 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
   if (threadIdx.x == 0 && s_err != MOE_OK && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
   if (a.n) pdl_wait();
+}
+
+// The mixed groups' adapters, added to fp32 results: a block per 16 tokens and 256
+// outputs, which ends at once where the group is not a mixed one.
+template <typename TE>
+__global__ void __launch_bounds__(256) adapter_mixed_kernel(const LinearArgs a) {
+  __shared__ float turn[8][512];
+  pdl_wait();
+  pdl_launch_dependents();
+  if (a.group[blockIdx.x] != kMixed) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = blockIdx.x * 16;
+  const int n0 = blockIdx.y * 256 + warp * 32, n = n0 + lane;
+  if (n0 >= a.N) return;
+  adapter_turn<TE>(a, t0, n0, turn[warp]);
+  if (n >= a.N) return;
+  float* o = reinterpret_cast<float*>(a.out) + (long long)t0 * a.ld_out + n;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (t0 + j < a.T) o[j * a.ld_out] += turn[warp][j * 32 + lane];
 }
 
 // --------------------------------------------------------------------- host --
@@ -1122,8 +1233,8 @@ static moe_status launch_shrink(const LinearArgs& a, int dtype, cudaStream_t s) 
 // Whether a call goes to the persistent pairs: once its tiles of 128 x 128 are
 // more than the SMs (H = 4096, 192 tiles: 34.5 us split, 22.8 streamed; 128 tiles:
 // 17.9 and 22.5).  With adapters or fp32 results from three quarters of the SMs
-// on: the split kernel takes adapters token by token on the CUDA cores, and has
-// accumulators for 512 products each only up to H = 2048 a block.
+// on: the split kernel takes all adapters in its epilogue, and has accumulators
+// for 512 products each only up to H = 2048 a block.
 static bool large_batch(int T, int N, bool early) {
   const long long tiles = ((long long)N + kRows - 1) / kRows * ((T + 127) / 128);
   return T > 128 && tiles * (early ? 4 : 3) >= device_sms() * 3LL + (early ? 0 : 1);
@@ -1157,8 +1268,13 @@ static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) 
   auto kernel = chunks ? linear_stream_kernel<TE, true> : linear_stream_kernel<TE, false>;
   static char allowed[2][64];
   MOE_CUDA(allow_smem(kernel, kStreamSmem, allowed[chunks]));
-  return launch_cluster(kernel, dim3(2 * (pl.tiles < pairs ? pl.tiles : pairs)), kStreamThreads, 2, kStreamSmem,
-                        s, "linear_stream_kernel", mW, mX, mB, mU, a, pl);
+  st = launch_cluster(kernel, dim3(2 * (pl.tiles < pairs ? pl.tiles : pairs)), kStreamThreads, 2, kStreamSmem, s,
+                      "linear_stream_kernel", mW, mX, mB, mU, a, pl);
+  if (st != MOE_OK || !chunks || !a.n) return st;
+  MOE_ARG((a.N + 255) / 256 <= 65535, "N too large");
+  cudaError_t e = launch_pdl(adapter_mixed_kernel<TE>, dim3((a.T + 15) / 16, (a.N + 255) / 256), dim3(256), 0, s, a);
+  if (e != cudaSuccess) return cuda_fail(e, "adapter_mixed_kernel");
+  return check_launch("adapter_mixed_kernel");
 }
 
 template <typename TE>
@@ -1167,8 +1283,9 @@ static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) 
   moe_status st = MOE_OK;
   const bool large = large_batch(a.T, a.N, a.n || a.out_dtype == MOE_DT_F32);
   if (a.n) {
-    // one dot per token and rank re-reads A for every token: worth it up to this many bytes
-    if (!large && (long long)a.T * a.R * a.H * 2 <= (64LL << 20)) {
+    // a dot per token and rank reads A again for every token, the tcgen05 kernel x again for every 128 / R
+    // adapters among 128 tokens (which only the device knows): dots for a batch that may name many
+    if (!large && (a.T <= 256 || (long long)a.T * a.R * a.H * 2 <= (64LL << 20))) {
       cudaError_t e = launch_pdl(adapter_dot_kernel<TE>, dim3(a.T, a.R / kDots), dim3(128), 0, s, a);
       if (e != cudaSuccess) return cuda_fail(e, "adapter_dot_kernel");
       st = check_launch("adapter_dot_kernel");

@@ -405,8 +405,8 @@ __device__ __forceinline__ void store4(const LinearArgs& a, long long t, int n, 
 // brings its share of W and x by TMA (as many 64-wide steps in flight as the
 // stages hold: with H / cluster <= 512 the whole share), multiplies it, puts its
 // fp32 sums into its own shared memory, and adds up the blocks' sums, in rank
-// order, for its share of the tokens.  64 tokens to 2048 outputs, H = 4096: 7.6 us
-// alone (19.5 MB), 11.4 with adapters; bound by what an SM takes in (W's 128 rows
+// order, for its share of the tokens.  64 tokens to 2048 outputs, H = 4096: 7.2 us
+// alone (19.5 MB), 11.9 with adapters; bound by what an SM takes in (W's 128 rows
 // and x's 64 of 1024 columns: 390 KB) and the way there and back.
 template <typename TE, int NT>
 __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant__ CUtensorMap mW,

@@ -194,7 +194,9 @@ struct SplitCfg {
   static constexpr int kSmem = kStages * kStage + 1024;
   static constexpr int kAcc = NT <= 64 ? 8 : 512 / NT;   // accumulators for fp32 results
   static constexpr int kCols = kAcc * NT;
-  static_assert(NT * kRows * 4 <= kStages * kStage, "the partial sums fit the stages");
+  // u's three terms of all ranks, a row for each token (adapter_tiles)
+  static constexpr int kTerms = 3 * NT * (128 * 2 + 16);
+  static_assert(NT * kRows * 4 + kTerms <= kStages * kStage, "the partial sums and u's terms fit the stages");
 };
 
 template <typename TE>
@@ -401,6 +403,150 @@ __device__ __forceinline__ void store4(const LinearArgs& a, long long t, int n, 
   }
 }
 
+// The adapters' part of a block of the split kernel.  Its tokens are put in order of
+// their adapters, and a tile is up to eight of them that share one: a tile is
+// multiplied by its own adapter's rows alone, so nothing of another one can reach a
+// token, and B is read once for eight tokens of an adapter and not for each.
+template <int NT>
+struct AdapterTiles {
+  int id[NT], start[NT];      // a token's adapter; the place of its tile, if it is the first of one
+  int token[NT];              // in order of adapters
+  int2 tile[NT];              // its first place and tokens (shifted by 8), its adapter
+  float down[NT];             // fp16: what a place's product is multiplied by
+  int tokens, tiles;
+
+  // By threads 0 to 191: tokens t0 to t0 + share.
+  __device__ __forceinline__ void fill(const LinearArgs& a, int i, int t0, int share) {
+    int mine = 0x7fffffff, before = 0, less = 0, same = 0;
+    if (i < share) {
+      if (t0 + i < a.T) mine = a.ids[t0 + i];
+      if (mine < 0 || mine >= a.n) mine = 0x7fffffff;
+      id[i] = mine;
+    }
+    asm volatile("bar.sync 1, 192;" ::: "memory");
+    int all = 0;
+#pragma unroll 4
+    for (int j = 0; i < share && j < share; ++j) {
+      const int o = id[j];
+      all += o != 0x7fffffff;
+      less += o < mine;
+      same += o == mine;
+      before += o == mine && j < i;
+    }
+    const int place = less + before;
+    const bool there = i < share && mine != 0x7fffffff, head = there && before % 8 == 0;
+    if (there) token[place] = i;
+    if (i < share) start[i] = head ? place : -1;
+    asm volatile("bar.sync 1, 192;" ::: "memory");
+    int at = 0, heads = 0;
+#pragma unroll 4
+    for (int j = 0; i < share && j < share; ++j) {
+      at += start[j] >= 0 && start[j] < place;
+      heads += start[j] >= 0;
+    }
+    if (head) tile[at] = make_int2(place | (same - before < 8 ? same - before : 8) << 8, mine);
+    if (i == 0) tokens = all, tiles = heads;
+  }
+};
+// u (fp32) enters as terms of x's type, which all threads first lay into shared
+// memory (`room`) in the tiles' order; fp16 scaled by a power of two to below 2^14, so
+// that it neither overflows nor loses its low bits.  A warp then takes 32 of the 128
+// outputs and every other tile.  B comes straight from memory, kAhead steps of 32
+// ranks ahead: lane (g, c) loads 16 bytes at k = 32 i + 8 c of rows g, g + 8, g + 16
+// and g + 24 and takes them as the k16 steps 2 i and 2 i + 1, u's eight values in the
+// same order.  `sums`: [share][128], made by fill_sums, to which the products are added.  FIG
+template <typename TE, int NT, typename F>
+__device__ __forceinline__ void adapter_tiles(const LinearArgs& a, AdapterTiles<NT>& s, int t0, int n0, float* sums,
+                                              uint8_t* room, F fill_sums) {
+  constexpr bool kScaled = !std::is_same<TE, __nv_bfloat16>::value;
+  constexpr int kAhead = 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, half = warp >> 2;
+  const int ld = a.R * 2 + 16, term = NT * ld;   // bytes of a token's row, of a term
+  const int n1 = n0 + (warp & 3) * 32 + g, tiles = s.tiles;
+  int row[4];   // of B, within an adapter's
+#pragma unroll
+  for (int m = 0; m < 4; ++m) row[m] = (n1 + m * 8 < a.N ? n1 + m * 8 : a.N - 1) * a.R + c * 8;
+  uint4 A[kAhead][4];
+  int lt = half, lk = 0;
+  auto fetch = [&](uint4 (&X)[4]) {
+    if (lt >= tiles) return;
+    const TE* B = reinterpret_cast<const TE*>(a.B) + (long long)s.tile[lt].y * a.N * a.R + lk;
+    const bool in = lk + c * 8 < a.R;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) X[m] = in ? *reinterpret_cast<const uint4*>(B + row[m]) : make_uint4(0, 0, 0, 0);
+    if ((lk += 32) >= a.R) lk = 0, lt += 2;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(A[i]);
+  pdl_wait();   // u
+  const int width = a.R <= 16 ? 4 : a.R <= 32 ? 8 : a.R <= 64 ? 16 : 32;   // lanes of a token, four ranks each
+  const int wl = lane & (width - 1), each = 32 / width;
+#pragma unroll 4
+  for (int p0 = warp * each; p0 < s.tokens; p0 += 8 * each) {
+    const int p = p0 + lane / width;
+    const bool in = p < s.tokens && wl * 4 < a.R;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) v = *reinterpret_cast<const float4*>(a.u + (long long)(t0 + s.token[p]) * a.R + wl * 4);
+    float f[4] = {v.x, v.y, v.z, v.w};
+    if (kScaled) {
+      float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+      for (int o = 1; o < width; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      int e = (int)(__float_as_uint(top) >> 23 & 255) - 127 - 13;   // top in [2^13, 2^14) after the scale
+      e = top == 0.f || e > 114 ? 0 : e < -100 ? -100 : e;
+      const float up = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] *= up;
+      if (in && wl == 0) s.down[p] = __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      if (t == 2 && a.terms < 3) break;
+      const uint2 w = make_uint2(pack_pair<TE>(f[0], f[1]), pack_pair<TE>(f[2], f[3]));
+      if (in) *reinterpret_cast<uint2*>(room + t * term + p * ld + wl * 8) = w;
+      const float2 q = Pair<TE>::f32(w.x), r = Pair<TE>::f32(w.y);
+      f[0] -= q.x, f[1] -= q.y, f[2] -= r.x, f[3] -= r.y;
+    }
+  }
+  fill_sums();   // B's rows are on their way
+  __syncthreads();
+  int ct = half, ck = 0;
+  float d[2][2][4] = {};   // by rows, by k16 step: four chains of MMAs
+  while (ct < tiles) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (ct >= tiles) break;
+      const int span = s.tile[ct].x, p = span & 255, len = span >> 8;
+      const uint8_t* u = room + (p + (g < len ? g : 0)) * ld + (ck + c * 8) * 2;
+      const bool in = ck + c * 8 < a.R;
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        if (t == 2 && a.terms < 3) break;
+        const uint4 w = in ? *reinterpret_cast<const uint4*>(u + t * term) : make_uint4(0, 0, 0, 0);
+        mma16816<TE>(d[0][0], A[i][0].x, A[i][1].x, A[i][0].y, A[i][1].y, w.x, w.y);
+        mma16816<TE>(d[1][0], A[i][2].x, A[i][3].x, A[i][2].y, A[i][3].y, w.x, w.y);
+        mma16816<TE>(d[0][1], A[i][0].z, A[i][1].z, A[i][0].w, A[i][1].w, w.z, w.w);
+        mma16816<TE>(d[1][1], A[i][2].z, A[i][3].z, A[i][2].w, A[i][3].w, w.z, w.w);
+      }
+      fetch(A[i]);
+      if ((ck += 32) < a.R) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (2 * c + j >= len) continue;
+        float* at = sums + s.token[p + 2 * c + j] * kRows + (warp & 3) * 32 + g;
+        const float by = kScaled ? s.down[p + 2 * c + j] : 1.f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float v = d[m >> 1][0][(m & 1) * 2 + j] + d[m >> 1][1][(m & 1) * 2 + j];
+          at[m * 8] += kScaled ? v * by : v;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 16; ++m) (&d[0][0][0])[m] = 0.f;
+      ck = 0, ct += 2;
+    }
+  }
+}
+
 // One tile of 128 outputs x NT tokens per cluster, whose blocks split H: each
 // brings its share of W and x by TMA (as many 64-wide steps in flight as the
 // stages hold: with H / cluster <= 512 the whole share), multiplies it, puts its
@@ -417,6 +563,7 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
   __shared__ alignas(8) uint64_t full[C::kStages], empty[C::kStages], done;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_err;
+  __shared__ AdapterTiles<NT> s_tiles;
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cs = gridDim.x, rank = blockIdx.x;   // the cluster spans the grid's x
@@ -480,12 +627,12 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
       mma_commit(&done);
     }
   } else if (early) {   // the adapters' rows of this block's outputs, on their way to L2 meanwhile
-    const int share = NT / cs;
-    for (int i = threadIdx.x - 64; i < share * kRows; i += 192) {
-      const int t = t0 + rank * share + i / kRows, n = n0 + i % kRows;
-      const int id = t < a.T && n < a.N ? a.ids[t] : -1;
-      const char* row = reinterpret_cast<const char*>(a.B) + ((long long)id * a.N + n) * a.R * 2;
-      if (id >= 0 && id < a.n && ((uintptr_t)row % 128 < (unsigned)a.R * 2)) prefetch_l2(row);
+    s_tiles.fill(a, threadIdx.x - 64, t0 + rank * (NT / cs), NT / cs);
+    asm volatile("bar.sync 1, 192;" ::: "memory");
+    for (int i = threadIdx.x - 64; i < s_tiles.tiles * kRows; i += 192) {
+      const int j = i / kRows, n = n0 + i % kRows;
+      const char* row = reinterpret_cast<const char*>(a.B) + ((long long)s_tiles.tile[j].y * a.N + n) * a.R * 2;
+      if (n < a.N && (j == 0 || s_tiles.tile[j].y != s_tiles.tile[j - 1].y) && (uintptr_t)row % 128 < (unsigned)a.R * 2) prefetch_l2(row);
     }
   }
   __syncwarp();
@@ -520,104 +667,29 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
   }
   if (!ok && threadIdx.x == 0 && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
-  if (early) pdl_wait();   // u
   // the blocks' sums of this block's share of the tokens, four outputs at a time; with adapters they go
   // back to their place in this block's own sums (which no other block reads)
-  const int share = NT / cs, items = share * (kRows / 4);
+  const int share = NT / cs;
   const uint32_t base = su32(part);
-  for (int i = threadIdx.x; i < items; i += 256) {
-    const int tt = rank * share + i / (kRows / 4), nn = i % (kRows / 4) * 4;
-    if (t0 + tt >= a.T || n0 + nn >= a.N) continue;
-    float* own = part + tt * kRows + nn;
-    float v[4] = {};
-    for (int r = 0; r < cs; ++r) {
-      const float4 f = cs > 1 ? ld_cluster4(base + (uint32_t)(tt * kRows + nn) * 4, r) : *reinterpret_cast<const float4*>(own);
-      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-    }
-    if (a.n) *reinterpret_cast<float4*>(own) = make_float4(v[0], v[1], v[2], v[3]);
-    else store4<TE>(a, t0 + tt, n0 + nn, v);
-  }
-  // the adapters' part.  Few ranks and tokens: each token reads its own B rows, two tokens at a time
-  // (64 tokens of 32 adapters, rank 16: 11.5 us, by MMAs 14.8); else by MMAs (128 tokens of 16 adapters,
-  // rank 128: 59 us and 51; of one adapter 56 and 25)
-  const bool few = (items + 511) / 512 * a.R <= 32;
-  if (a.n) __syncthreads();
-  for (int i = threadIdx.x; a.n && few && i < items; i += 512) {
-    int id[2], tt[2], nn[2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int it = i + m * 256;
-      tt[m] = it < items ? rank * share + it / (kRows / 4) : NT;
-      nn[m] = n0 + it % (kRows / 4) * 4;
-      const bool in = tt[m] < NT && t0 + tt[m] < a.T && nn[m] < a.N;
-      if (!in) tt[m] = -1;
-      id[m] = in ? a.ids[t0 + tt[m]] : -1;
-      if (id[m] >= a.n) id[m] = -1;
-    }
-    float d[2][4] = {};
-    if (id[0] >= 0 || id[1] >= 0) {
-      const TE* B[2];
-      const float* u[2];
-      int row[2][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {   // where there is no adapter or no output: the other's, dropped below
-        const bool own = id[m] >= 0;
-        const int of = own ? id[m] : id[1 - m], n1 = own ? nn[m] : nn[1 - m], t1 = own ? tt[m] : tt[1 - m];
-        B[m] = reinterpret_cast<const TE*>(a.B) + ((long long)of * a.N + n1) * a.R;
-        u[m] = a.u + (long long)(t0 + t1) * a.R;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) row[m][j] = n1 + j < a.N ? j * a.R : 0;
+  auto sum = [&] {
+    for (int i = threadIdx.x; i < share * (kRows / 4); i += 256) {
+      const int tt = rank * share + i / (kRows / 4), nn = i % (kRows / 4) * 4;
+      if (t0 + tt >= a.T || n0 + nn >= a.N) continue;
+      float* own = part + tt * kRows + nn;
+      float v[4] = {};
+      for (int r = 0; r < cs; ++r) {
+        const float4 f = cs > 1 ? ld_cluster4(base + (uint32_t)(tt * kRows + nn) * 4, r) : *reinterpret_cast<const float4*>(own);
+        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
       }
-#pragma unroll 2
-      for (int r = 0; r < a.R; r += 8) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const float4 p = *reinterpret_cast<const float4*>(u[m] + r), q = *reinterpret_cast<const float4*>(u[m] + r + 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 b = *reinterpret_cast<const uint4*>(B[m] + row[m][j] + r);
-            const float2 b0 = Pair<TE>::f32(b.x), b1 = Pair<TE>::f32(b.y), b2 = Pair<TE>::f32(b.z),
-                         b3 = Pair<TE>::f32(b.w);
-            d[m][j] += fmaf(b0.x, p.x, fmaf(b0.y, p.y, fmaf(b1.x, p.z, b1.y * p.w))) +
-                       fmaf(b2.x, q.x, fmaf(b2.y, q.y, fmaf(b3.x, q.z, b3.y * q.w)));
-          }
-        }
-      }
+      if (a.n) *reinterpret_cast<float4*>(own) = make_float4(v[0], v[1], v[2], v[3]);
+      else store4<TE>(a, t0 + tt, n0 + nn, v);
     }
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      if (tt[m] < 0) continue;
-      const float* own = part + tt[m] * kRows + nn[m] - n0;
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = id[m] < 0 ? own[j] : own[j] + d[m][j];
-      store4<TE>(a, t0 + tt[m], nn[m], v);
-    }
-  }
-  if (a.n && !few) {
-    // a warp takes 32 outputs of 16 tokens
-    for (int i = (warp >> 2) * 16; i < share && t0 + rank * share + i < a.T; i += 32) {
-      const long long tb = t0 + rank * share + i;
-      const int room = share - i < 16 ? share - i : 16, cols = a.T - tb < room ? (int)(a.T - tb) : room;
-      int mine = (lane & 15) < cols ? a.ids[tb + (lane & 15)] : -1;
-      if (mine >= a.n) mine = -1;
-      if (!__any_sync(0xffffffffu, mine >= 0)) continue;
-      float sel[2][2][4];
-      adapter_block<TE>(a, mine, tb, cols, n0 + q * 32, sel);
-      float* at = part + (rank * share + i) * kRows + q * 32;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int col = j * 8 + 2 * (lane & 3) + k;
-          if (col >= cols) continue;
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            at[col * kRows + m * 16 + (lane >> 2)] += sel[m][j][k];
-            at[col * kRows + m * 16 + (lane >> 2) + 8] += sel[m][j][k + 2];
-          }
-        }
-    }
+  };
+  if (!a.n) sum();
+  else {
+    adapter_tiles<TE, NT>(a, s_tiles, t0 + rank * share, n0, part + rank * share * kRows, sm + NT * kRows * 4, [&] {
+      if (cs > 1) sum();
+    });
     __syncthreads();
     for (int i = threadIdx.x; i < share * (kRows / 4); i += 256) {
       const int tt = rank * share + i / (kRows / 4), nn = i % (kRows / 4) * 4;

@@ -33,7 +33,7 @@ struct LinearArgs {
   int32_t* err;
 };
 
-constexpr int kMixed = -2;   // a group of 16 tokens that do not share one adapter (adapter_block)
+constexpr int kMixed = -2;   // a group of 16 tokens that do not share one adapter
 
 template <typename TE>
 struct Pair;   // two packed elements as fp32
@@ -454,7 +454,9 @@ struct AdapterTiles {
 // outputs and every other tile.  B comes straight from memory, kAhead steps of 32
 // ranks ahead: lane (g, c) loads 16 bytes at k = 32 i + 8 c of rows g, g + 8, g + 16
 // and g + 24 and takes them as the k16 steps 2 i and 2 i + 1, u's eight values in the
-// same order.  `sums`: [share][128], made by fill_sums, to which the products are added.  FIG
+// same order.  `sums`: [share][128], made by fill_sums, to which the products are added.  The MMAs'
+// latency bounds a tile: in four chains 57 tokens of 20 adapters of rank 40 to 2035
+// outputs take 15.0 us, in two 17.0; two steps ahead 16.2, eight (more code) 16.9.
 template <typename TE, int NT, typename F>
 __device__ __forceinline__ void adapter_tiles(const LinearArgs& a, AdapterTiles<NT>& s, int t0, int n0, float* sums,
                                               uint8_t* room, F fill_sums) {
@@ -941,6 +943,7 @@ constexpr int kStreamThreads = 320;   // TMA, MMA, eight epilogue warps
 struct StreamPlan {
   int nt, stages, tiles_n, tiles;   // tokens of a tile, stages of the ring, tiles of 256 outputs, all tiles
   int nk, chunk;                    // K steps, K steps of an accumulator
+  int blocks;
 };
 
 // The pair's forms: a copy into this block that completes on a barrier of the leader (a cluster
@@ -1205,25 +1208,29 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   if (a.n) pdl_wait();
 }
 
-// The mixed groups' adapters, added to fp32 results: a block per 16 tokens and 256
+// The mixed groups' adapters, added to fp32 results: a block per 16 tokens and 128
 // outputs, which ends at once where the group is not a mixed one.  About 3 us for
 // 8192 tokens in 16 requests; in the projection's epilogue this code took the
 // registers that it adds its chunks up in (25.9 us for 20.9 even without adapters).
 template <typename TE>
 __global__ void __launch_bounds__(256) adapter_mixed_kernel(const LinearArgs a) {
-  __shared__ float turn[8][512];
+  __shared__ alignas(16) uint8_t room[SplitCfg<16>::kTerms];
+  __shared__ alignas(16) float sums[16 * kRows];
+  __shared__ AdapterTiles<16> s_tiles;
   pdl_wait();
   pdl_launch_dependents();
   if (a.group[blockIdx.x] != kMixed) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = blockIdx.x * 16;
-  const int n0 = blockIdx.y * 256 + warp * 32, n = n0 + lane;
-  if (n0 >= a.N) return;
-  adapter_turn<TE>(a, t0, n0, turn[warp]);
-  if (n >= a.N) return;
-  float* o = reinterpret_cast<float*>(a.out) + (long long)t0 * a.ld_out + n;
+  const int t0 = blockIdx.x * 16, n0 = blockIdx.y * kRows;
+  if (threadIdx.x < 192) s_tiles.fill(a, threadIdx.x, t0, 16);
+  for (int i = threadIdx.x; i < 16 * kRows; i += 256) sums[i] = 0.f;
+  __syncthreads();
+  adapter_tiles<TE, 16>(a, s_tiles, t0, n0, sums, room, [] {});
+  __syncthreads();
+  const int n = threadIdx.x % kRows;
+  float* o = reinterpret_cast<float*>(a.out) + (long long)t0 * a.ld_out + n0 + n;
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (t0 + j < a.T) o[j * a.ld_out] += turn[warp][j * 32 + lane];
+  for (int j = threadIdx.x / kRows; j < 16; j += 2)
+    if (t0 + j < a.T && n0 + n < a.N) o[j * a.ld_out] += sums[j * kRows + n];
 }
 
 // --------------------------------------------------------------------- host --
@@ -1265,6 +1272,15 @@ static moe_status launch_cluster(void (*kernel)(KArgs...), dim3 grid, int thread
   return check_launch(name);
 }
 
+// Blocks that split H, of a call of so many tiles: while the blocks still fit the SMs at once and each
+// keeps two steps; clusters of eight only where one of the eight GPCs takes each (16 of them: 13.4 us for
+// 64 tokens to 2048 outputs, of four 8.9).
+static int split_cluster(long long tiles, int nk) {
+  int cs = 1;
+  while (cs < (tiles <= 8 ? 8 : 4) && tiles * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
+  return cs;
+}
+
 template <typename TE, int NT>
 static moe_status launch_split(const LinearArgs& a, int dtype, cudaStream_t s) {
   using C = SplitCfg<NT>;
@@ -1277,10 +1293,7 @@ static moe_status launch_split(const LinearArgs& a, int dtype, cudaStream_t s) {
   MOE_CUDA(allow_smem(kernel, C::kSmem, allowed));
   const int tiles_n = (a.N + kRows - 1) / kRows, tiles_t = (a.T + NT - 1) / NT, nk = (a.H + 63) / 64;
   MOE_ARG(tiles_n <= 65535 && tiles_t <= 65535, "T or N too large");
-  // split H while the blocks still fit the SMs at once and each keeps two steps; clusters of eight only
-  // where one of the eight GPCs takes each (16 of them: 13.4 us for 64 tokens to 2048 outputs, of four 8.9)
-  int cs = 1;
-  while (cs < (tiles_n * tiles_t <= 8 ? 8 : 4) && (long long)tiles_n * tiles_t * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
+  const int cs = split_cluster((long long)tiles_n * tiles_t, nk);
   // K steps of an accumulator: all of a block's for 16-bit results, else 8 or what its accumulators ask for
   const int most = (nk + cs - 1) / cs, each = (most + C::kAcc - 1) / C::kAcc;
   const int chunk = a.out_dtype != MOE_DT_F32 ? most : each > kF32Chunk ? each : kF32Chunk;
@@ -1288,8 +1301,9 @@ static moe_status launch_split(const LinearArgs& a, int dtype, cudaStream_t s) {
                         a.n ? 1 : 0, chunk);
 }
 
+// `beside`: the projection's blocks, which take an SM each as this kernel's do.
 template <typename TE>
-static moe_status launch_shrink(const LinearArgs& a, int dtype, cudaStream_t s) {
+static moe_status launch_shrink(const LinearArgs& a, int dtype, long long beside, cudaStream_t s) {
   CUtensorMap mA, mX;
   moe_status st = map_rows(&mA, a.A, dtype, a.H, (uint64_t)a.n * a.R, a.H, a.R);
   if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.H, a.T, a.ld_x, kShrinkTokens);
@@ -1299,24 +1313,31 @@ static moe_status launch_shrink(const LinearArgs& a, int dtype, cudaStream_t s) 
   MOE_CUDA(allow_smem(kernel, kShrinkSmem, allowed));
   const int tiles = (a.T + kShrinkTokens - 1) / kShrinkTokens, nk = (a.H + 63) / 64;
   MOE_ARG(tiles <= 65535, "T too large");
-  int cs = 1;
-  while (cs < 8 && (long long)tiles * cs * 2 <= device_sms() && nk >= 4 * cs) cs *= 2;
+  // as many blocks as leave the projection's room to run at the same time (1599 tokens to 378 outputs, H = 4744:
+  // 25.4 us, one after the other 31.7), else, or with more than 24 steps a block (1786 to 256, H = 4096: 24.7 us
+  // beside it, 21.8 after it), as many as there are SMs
+  auto cluster = [&](long long room) {
+    int cs = 1;
+    while (cs < 8 && (long long)tiles * cs * 2 <= room && nk >= 4 * cs) cs *= 2;
+    return cs;
+  };
+  const long long free = device_sms() - beside;
+  int cs = cluster(free);
+  if (tiles > free || nk > 24 * cs) cs = cluster(device_sms());
   return launch_cluster(kernel, dim3(cs, tiles), 256, cs, kShrinkSmem, s, "adapter_shrink_kernel", mA, mX, a);
 }
 
 // Whether a call goes to the persistent pairs: once its tiles of 128 x 128 are
 // more than the SMs (H = 4096, 192 tiles: 34.5 us split, 22.8 streamed; 128 tiles:
-// 17.9 and 22.5).  With adapters or fp32 results from three quarters of the SMs
-// on: the split kernel takes all adapters in its epilogue, and has accumulators
-// for 512 products each only up to H = 2048 a block.
-static bool large_batch(int T, int N, bool early) {
+// 17.9 and 22.5, with adapters of rank 16 27.6 and 37.1, of mixed ones 27.5 and
+// 50.7).  fp32 results from three quarters of the SMs on: the split kernel has
+// accumulators for 512 products each only up to H = 2048 a block.
+static bool large_batch(int T, int N, bool f32) {
   const long long tiles = ((long long)N + kRows - 1) / kRows * ((T + 127) / 128);
-  return T > 128 && tiles * (early ? 4 : 3) >= device_sms() * 3LL + (early ? 0 : 1);
+  return T > 128 && tiles * (f32 ? 4 : 3) >= device_sms() * 3LL + (f32 ? 0 : 1);
 }
 
-template <typename TE>
-static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) {
-  CUtensorMap mW, mX, mB = {}, mU = {};
+static StreamPlan stream_plan(const LinearArgs& a) {
   StreamPlan pl;
   pl.tiles_n = (a.N + 2 * kRows - 1) / (2 * kRows);
   pl.nk = (a.H + 63) / 64;
@@ -1330,6 +1351,16 @@ static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) 
     const long long tiles = (long long)pl.tiles_n * ((a.T + nt - 1) / nt), cost = (tiles + pairs - 1) / pairs * (nt + 256);
     if (best < 0 || cost < best) best = cost, pl.nt = nt, pl.tiles = (int)tiles;
   }
+  const int fit = kStreamBytes / (kATile + pl.nt * 64);
+  pl.stages = fit < kStreamStages ? fit : kStreamStages;
+  pl.blocks = 2 * (pl.tiles < pairs ? pl.tiles : pairs);
+  return pl;
+}
+
+template <typename TE>
+static moe_status launch_stream(const LinearArgs& a, const StreamPlan& pl, int dtype, cudaStream_t s) {
+  CUtensorMap mW, mX, mB = {}, mU = {};
+  const bool chunks = pl.chunk < pl.nk;
   moe_status st = map_rows(&mW, a.W, dtype, a.H, a.N, a.ld_w, kRows);
   if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.H, a.T, a.ld_x, pl.nt / 2);
   if (a.n) {
@@ -1337,16 +1368,14 @@ static moe_status launch_stream(const LinearArgs& a, int dtype, cudaStream_t s) 
     if (st == MOE_OK) st = map_rows(&mU, a.u_terms, dtype, a.R, (uint64_t)a.terms * a.T, a.R, pl.nt / 2);
   }
   if (st != MOE_OK) return st;
-  const int fit = kStreamBytes / (kATile + pl.nt * 64);
-  pl.stages = fit < kStreamStages ? fit : kStreamStages;
   auto kernel = chunks ? linear_stream_kernel<TE, true> : linear_stream_kernel<TE, false>;
   static char allowed[2][64];
   MOE_CUDA(allow_smem(kernel, kStreamSmem, allowed[chunks]));
-  st = launch_cluster(kernel, dim3(2 * (pl.tiles < pairs ? pl.tiles : pairs)), kStreamThreads, 2, kStreamSmem, s,
+  st = launch_cluster(kernel, dim3(pl.blocks), kStreamThreads, 2, kStreamSmem, s,
                       "linear_stream_kernel", mW, mX, mB, mU, a, pl);
   if (st != MOE_OK || !chunks || !a.n) return st;
-  MOE_ARG((a.N + 255) / 256 <= 65535, "N too large");
-  cudaError_t e = launch_pdl(adapter_mixed_kernel<TE>, dim3((a.T + 15) / 16, (a.N + 255) / 256), dim3(256), 0, s, a);
+  MOE_ARG((a.N + kRows - 1) / kRows <= 65535, "N too large");
+  cudaError_t e = launch_pdl(adapter_mixed_kernel<TE>, dim3((a.T + 15) / 16, (a.N + kRows - 1) / kRows), dim3(256), 0, s, a);
   if (e != cudaSuccess) return cuda_fail(e, "adapter_mixed_kernel");
   return check_launch("adapter_mixed_kernel");
 }
@@ -1355,7 +1384,9 @@ template <typename TE>
 static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) {
   ProfScope ps(MOE_K_LINEAR, s);
   moe_status st = MOE_OK;
-  const bool large = large_batch(a.T, a.N, a.n || a.out_dtype == MOE_DT_F32);
+  const bool large = large_batch(a.T, a.N, a.out_dtype == MOE_DT_F32);
+  StreamPlan pl = {};
+  if (large) pl = stream_plan(a);
   if (a.n) {
     // a dot per token and rank reads A again for every token, the tcgen05 kernel x again for every 128 / R
     // adapters among 128 tokens (which only the device knows): dots for a batch that may name many
@@ -1364,11 +1395,12 @@ static moe_status launch_linear(const LinearArgs& a, int dtype, cudaStream_t s) 
       if (e != cudaSuccess) return cuda_fail(e, "adapter_dot_kernel");
       st = check_launch("adapter_dot_kernel");
     } else {
-      st = launch_shrink<TE>(a, dtype, s);
+      const long long tiles = (a.N + kRows - 1LL) / kRows * ((a.T + 127LL) / 128);
+      st = launch_shrink<TE>(a, dtype, large ? pl.blocks : tiles * split_cluster(tiles, (a.H + 63) / 64), s);
     }
     if (st != MOE_OK) return st;
   }
-  if (large) return launch_stream<TE>(a, dtype, s);
+  if (large) return launch_stream<TE>(a, pl, dtype, s);
   if (a.T <= 16) return launch_split<TE, 16>(a, dtype, s);
   if (a.T <= 32) return launch_split<TE, 32>(a, dtype, s);
   if (a.T <= 64) return launch_split<TE, 64>(a, dtype, s);
@@ -1439,7 +1471,7 @@ extern "C" moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out
   a.ids = adapter_ids, a.scale = lora_scale, a.out = out, a.err = d_error;
   if (n_adapters) {
     a.u = (float*)(ws + w.u);
-    if (w.group) a.u_terms = ws + w.terms, a.group = (int32_t*)(ws + w.group);
+    if (large_batch(T, N, out_dtype == MOE_DT_F32)) a.u_terms = ws + w.terms, a.group = (int32_t*)(ws + w.group);
     a.terms = dtype == MOE_DT_BF16 && out_dtype == MOE_DT_F32 ? 3 : 2;
   }
   return dtype == MOE_DT_BF16 ? launch_linear<__nv_bfloat16>(a, dtype, stream)

@@ -16,6 +16,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "dtype.cuh"
 
 namespace moe {
@@ -333,9 +335,8 @@ struct RouteBwdArgs {
   long long ld_d;
 };
 
-// GROUP lanes per token (k <= GROUP; 32 for the plain softmax, whose gradient is
-// dense): the rows are written first (zeros, or the plain softmax's own term),
-// then the chosen experts' values over them.  16384 tokens of 256 experts, top-6,
+// GROUP lanes per token (k <= GROUP): the rows are written first (zeros), then the
+// chosen experts' values over them.  16384 tokens of 256 experts, top-6,
 // fp32: 6.2 us (17.9 MB: 2.65 us at the copy rate), the rest two dependent reads,
 // ids and then their logits, and a launch.  `vec`: rows and their length allow 16-byte stores.
 __device__ __forceinline__ float group_sum(float v, int width) {
@@ -365,64 +366,143 @@ __global__ void __launch_bounds__(128) route_bwd_kernel(const RouteBwdArgs a, in
       id = a.ids[t * a.k + gl];
       g = a.scale * a.dw[t * a.k + gl];
     }
-    const bool dense = GROUP == 32 && a.score == MOE_SCORE_SOFTMAX && !a.renorm;
-    if (!dense) {   // while the ids are on their way
+    // while the ids are on their way
 #pragma unroll
-      for (int q = 0; q < kTokens; ++q) {
-        if (t0 + q >= a.T) break;
-        TL* dq = reinterpret_cast<TL*>(a.d) + (t0 + q) * a.ld_d;
-        if (vec) {
-          constexpr int kEach = 16 / (int)sizeof(TL);
-          for (int e = lane * kEach; e < a.E; e += 32 * kEach)
-            *reinterpret_cast<uint4*>(dq + e) = make_uint4(0, 0, 0, 0);
-        } else {
-          for (int e = lane; e < a.E; e += 32) dq[e] = from_f32<TL>(0.f);
-        }
+    for (int q = 0; q < kTokens; ++q) {
+      if (t0 + q >= a.T) break;
+      TL* dq = reinterpret_cast<TL*>(a.d) + (t0 + q) * a.ld_d;
+      if (vec) {
+        constexpr int kEach = 16 / (int)sizeof(TL);
+        for (int e = lane * kEach; e < a.E; e += 32 * kEach)
+          *reinterpret_cast<uint4*>(dq + e) = make_uint4(0, 0, 0, 0);
+      } else {
+        for (int e = lane; e < a.E; e += 32) dq[e] = from_f32<TL>(0.f);
       }
     }
     if (id >= 0 && id < a.E) z = load_logit(row, id);
     if (!(z > -INFINITY)) id = -1, g = 0.f;
-    float dj;
-    if (dense) {
-      float top = -INFINITY, den = 0.f;
-      if (on) {
-        for (int e = lane; e < a.E; e += 32) top = fmaxf(top, load_logit(row, e));
-        top = group_max(top, 32);
-        for (int e = lane; e < a.E; e += 32) den += exp_below(load_logit(row, e), top);
-        den = group_sum(den, 32);
-      }
-      const float p = id >= 0 ? exp_below(z, top) / den : 0.f;
-      const float mean = group_sum(g * p, 32);
-      dj = p * (g - mean);
-      for (int e = lane; e < a.E; e += 32)
-        d[e] = from_f32<TL>(den > 0.f ? -mean * (exp_below(load_logit(row, e), top) / den) : 0.f);
+    float q, c = 1.f;
+    if (a.score == MOE_SCORE_SIGMOID) {
+      q = id >= 0 ? sigmoid_f32(z) : 0.f;
+      c = id >= 0 ? sigmoid_f32(-z) : 0.f;   // 1 - s without the cancellation
     } else {
-      float q, c = 1.f;
-      if (a.score == MOE_SCORE_SIGMOID) {
-        q = id >= 0 ? sigmoid_f32(z) : 0.f;
-        c = id >= 0 ? sigmoid_f32(-z) : 0.f;   // 1 - s without the cancellation
-      } else {
-        q = exp_below(z, group_max(z, GROUP));
-      }
-      float mean = 0.f;
-      if (a.renorm) {
-        const float sum = group_sum(q, GROUP);
-        q = sum > 0.f ? q / sum : 0.f;
-        mean = group_sum(q * g, GROUP);
-      }
-      dj = q * c * (g - mean);
+      q = exp_below(z, group_max(z, GROUP));
     }
+    float mean = 0.f;
+    if (a.renorm) {
+      const float sum = group_sum(q, GROUP);
+      q = sum > 0.f ? q / sum : 0.f;
+      mean = group_sum(q * g, GROUP);
+    }
+    const float dj = q * c * (g - mean);
     __syncwarp();   // the rows are written before the chosen experts' values
     if (id >= 0) d[id] = from_f32<TL>(dj);
   }
 }
 
+// Softmax weights that are not renormalised: every logit of a token has a gradient,
+//   d z_e = p_e (g_e - sum_j g_j p_j),  g_e = 0 for experts not chosen.
+// One warp per token, its row kept in registers between the softmax's sums and the
+// gradient, a lane's share in pieces of 16 bytes or, where rows do not start for
+// that, every 32nd element.  16384 tokens of 256 experts, fp32: 6.9 us (33.6 MB: 5.0
+// at the copy rate; 14.8 with the row read again for each of its three uses).
+template <int VPL, typename TL>
+__global__ void __launch_bounds__(128) route_bwd_dense_kernel(const RouteBwdArgs a, int vec) {
+  constexpr int kBytes = VPL * (int)sizeof(TL), kPiece = kBytes < 16 ? kBytes : 16;
+  constexpr int kEach = kPiece / (int)sizeof(TL);
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long step = gridDim.x * 4LL;
+  for (long long t = blockIdx.x * 4LL + (threadIdx.x >> 5); t < a.T; t += step) {
+    const TL* row = reinterpret_cast<const TL*>(a.logits) + t * a.ld;
+    TL* d = reinterpret_cast<TL*>(a.d) + t * a.ld_d;
+    const bool on = !a.mask || a.mask[t];
+    int id = -1;
+    float g = 0.f, z = -INFINITY, v[VPL];
+    if (lane < a.k && on) {
+      id = a.ids[t * a.k + lane];
+      g = a.scale * a.dw[t * a.k + lane];
+    }
+    if (vec) {
+      load_row<VPL>(row, lane, a.E, true, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) v[i] = i * 32 + lane < a.E ? load_logit(row, i * 32 + lane) : -INFINITY;
+    }
+    if (id >= 0 && id < a.E) z = load_logit(row, id);
+    if (!(z > -INFINITY)) id = -1, g = 0.f;
+    float top = -INFINITY, den = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) top = fmaxf(top, v[i]);
+    top = redux_max(top);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) den += v[i] = exp_below(v[i], top);
+    den = warp_sum(den);
+    const float p = id >= 0 ? exp_below(z, top) / den : 0.f, mean = warp_sum(g * p), dj = p * (g - mean);
+    const bool some = on && den > 0.f;
+    const float by = some ? -mean / den : 0.f;
+    TL o[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) o[i] = from_f32<TL>(some ? v[i] * by : 0.f);
+    if (!vec) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i * 32 + lane < a.E) d[i * 32 + lane] = o[i];
+    } else if (kPiece > 2 && (lane + 1) * VPL <= a.E) {
+#pragma unroll
+      for (int i = 0; i < kBytes / kPiece; ++i) {
+        alignas(16) TL q[kEach];
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) q[j] = o[i * kEach + j];
+        TL* at = d + lane * VPL + i * kEach;
+        if constexpr (kPiece == 16) *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(q);
+        else if constexpr (kPiece == 8) *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(q);
+        else if constexpr (kPiece == 4) *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(q);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (lane * VPL + i < a.E) d[lane * VPL + i] = o[i];
+    }
+    __syncwarp();   // the row is written before the chosen experts' values
+    if (id >= 0) d[id] = from_f32<TL>(dj);
+  }
+}
+
+// f(constant VPL): experts of a lane, a power of two.
+template <typename F>
+static auto by_lane_share(int E, F f) {
+  const int vpl = (E + 31) / 32;
+  if (vpl <= 1) return f(std::integral_constant<int, 1>());
+  if (vpl <= 2) return f(std::integral_constant<int, 2>());
+  if (vpl <= 4) return f(std::integral_constant<int, 4>());
+  if (vpl <= 8) return f(std::integral_constant<int, 8>());
+  if (vpl <= 16) return f(std::integral_constant<int, 16>());
+  if (vpl <= 32) return f(std::integral_constant<int, 32>());
+  return f(std::integral_constant<int, 64>());
+}
+// Whether a lane's share of a row can be moved in pieces of up to 16 bytes.
+template <int VPL, typename TL>
+static int whole_pieces(const void* base, long long ld) {
+  constexpr int kBytes = VPL * (int)sizeof(TL), kPiece = kBytes < 16 ? kBytes : 16;
+  return (uintptr_t)base % kPiece == 0 && ld * (long long)sizeof(TL) % kPiece == 0;
+}
+
 template <typename TL>
-static cudaError_t launch_route_bwd(const RouteBwdArgs& a, int vec, cudaStream_t s) {
+static cudaError_t launch_route_bwd(const RouteBwdArgs& a, cudaStream_t s) {
   const bool dense = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
   const int group = dense || a.k > 16 ? 32 : a.k > 8 ? 16 : 8;
   const long long warps = (a.T + 32LL / group - 1) / (32 / group), need = (warps + 3) / 4, most = device_sms() * 16LL;
   const dim3 grid((unsigned)(need < most ? need : most)), block(128);
+  if (dense)
+    return by_lane_share(a.E, [&](auto n) {
+      constexpr int VPL = decltype(n)::value;
+      return launch_pdl(route_bwd_dense_kernel<VPL, TL>, grid, block, 0, s, a,
+                        (int)(whole_pieces<VPL, TL>(a.logits, a.ld) && whole_pieces<VPL, TL>(a.d, a.ld_d)));
+    });
+  const long long size = sizeof(TL);
+  const int vec = (uintptr_t)a.d % 16 == 0 && a.ld_d * size % 16 == 0 && a.E * size % 16 == 0;
   if (group == 32) return launch_pdl(route_bwd_kernel<TL, 32>, grid, block, 0, s, a, vec);
   if (group == 16) return launch_pdl(route_bwd_kernel<TL, 16>, grid, block, 0, s, a, vec);
   return launch_pdl(route_bwd_kernel<TL, 8>, grid, block, 0, s, a, vec);
@@ -430,8 +510,7 @@ static cudaError_t launch_route_bwd(const RouteBwdArgs& a, int vec, cudaStream_t
 
 template <int VPL, typename TL>
 static moe_status launch_route(const RouteArgs& a, cudaStream_t s) {
-  constexpr int kBytes = VPL * (int)sizeof(TL), kPiece = kBytes < 16 ? kBytes : 16;
-  const int vec = (uintptr_t)a.logits % kPiece == 0 && a.ld * (long long)sizeof(TL) % kPiece == 0;
+  const int vec = whole_pieces<VPL, TL>(a.logits, a.ld);
   const long long need = ((long long)a.T + kRouteWarps - 1) / kRouteWarps, most = device_sms() * (long long)kRouteBlocks<VPL>;
   ProfScope ps(MOE_K_ROUTE, s);
   cudaError_t e = launch_pdl(route_kernel<VPL, TL>, dim3((unsigned)(need < most ? need : most)),
@@ -442,14 +521,7 @@ static moe_status launch_route(const RouteArgs& a, cudaStream_t s) {
 
 template <typename TL>
 static moe_status route_by_size(const RouteArgs& a, cudaStream_t s) {
-  const int vpl = (a.E + 31) / 32;
-  if (vpl <= 1) return launch_route<1, TL>(a, s);
-  if (vpl <= 2) return launch_route<2, TL>(a, s);
-  if (vpl <= 4) return launch_route<4, TL>(a, s);
-  if (vpl <= 8) return launch_route<8, TL>(a, s);
-  if (vpl <= 16) return launch_route<16, TL>(a, s);
-  if (vpl <= 32) return launch_route<32, TL>(a, s);
-  return launch_route<64, TL>(a, s);
+  return by_lane_share(a.E, [&](auto n) { return launch_route<decltype(n)::value, TL>(a, s); });
 }
 
 }  // namespace moe
@@ -499,12 +571,10 @@ extern "C" moe_status moe_route_backward(const void* logits, int dtype, int64_t 
   MOE_ARG(d_logits != logits, "d_logits must not be the logits");
   const RouteBwdArgs a{logits, ld_logits, T, E, k, score, renorm, scale, token_mask, topk_ids, d_w, d_logits,
                        ld_d_logits};
-  const int size = (int)dtype_size(dtype);
-  const int vec = (uintptr_t)d_logits % 16 == 0 && ld_d_logits * size % 16 == 0 && E * size % 16 == 0;
   ProfScope ps(MOE_K_ROUTE_BWD, stream);
-  const cudaError_t e = dtype == MOE_DT_F32    ? launch_route_bwd<float>(a, vec, stream)
-                        : dtype == MOE_DT_BF16 ? launch_route_bwd<__nv_bfloat16>(a, vec, stream)
-                                               : launch_route_bwd<__half>(a, vec, stream);
+  const cudaError_t e = dtype == MOE_DT_F32    ? launch_route_bwd<float>(a, stream)
+                        : dtype == MOE_DT_BF16 ? launch_route_bwd<__nv_bfloat16>(a, stream)
+                                               : launch_route_bwd<__half>(a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "route_bwd_kernel");
   return check_launch("route_bwd_kernel");
 }

@@ -130,29 +130,40 @@ constexpr int kRouteWarps = 4;
 template <int VPL>
 constexpr int kRouteBlocks = VPL <= 8 ? 8 : VPL == 16 ? 5 : 3;
 
+// With more than 16 experts a lane its biases wait in shared memory, read from global
+// memory in their order and laid out so that the lanes' reads meet no common bank:
+// lane l's i-th at l * (VPL + 1) + i (4096 tokens of
+// 1024 experts, softmax: 37.5 us read in place by every token, 25.2 so).
+template <int VPL>
+constexpr int kLaid = 32 * (VPL + 1);
+template <int VPL>
+constexpr bool kBiasLaid = VPL > 16;
+
 template <int VPL, typename TL>
 __global__ void __launch_bounds__(kRouteWarps * 32, kRouteBlocks<VPL>) route_kernel(const RouteArgs a, int vec) {
-  extern __shared__ int hist[];   // [E] with a load
+  extern __shared__ float laid_bias[];   // [kLaid], with kBiasLaid and a bias; then hist
+  int* hist = reinterpret_cast<int*>(laid_bias + (kBiasLaid<VPL> && a.bias ? kLaid<VPL> : 0));   // [E] with a load
   __shared__ alignas(16) float c_key[kRouteWarps][32];
   __shared__ int c_id[kRouteWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = a.k, E = a.E;
   pdl_wait();
   pdl_launch_dependents();
-  if (a.load) {
+  if (a.load)
     for (int e = threadIdx.x; e < E; e += kRouteWarps * 32) hist[e] = 0;
-    __syncthreads();
-  }
+  if (kBiasLaid<VPL> && a.bias)
+    for (int e = threadIdx.x; e < 32 * VPL; e += kRouteWarps * 32) laid_bias[e + e / VPL] = e < E ? a.bias[e] : 0.f;
+  if (a.load || (kBiasLaid<VPL> && a.bias)) __syncthreads();
   const bool grouped = a.topk_group < a.n_group;
   const bool scored = a.bias || (grouped && a.group_score == MOE_GROUP_TOP2);
   const bool whole = a.score == MOE_SCORE_SOFTMAX && (scored || !a.renorm);   // the softmax's denominator is needed
   const int gs = E / a.n_group;
   // lanes of a group, where every lane's experts belong to one group
   const int lpg = gs % VPL == 0 && gs / VPL <= 32 && ((gs / VPL) & (gs / VPL - 1)) == 0 ? gs / VPL : 0;
-  float bias[VPL <= 16 ? VPL : 1];
-  if (VPL <= 16 && a.bias) {
+  float bias[kBiasLaid<VPL> ? 1 : VPL];
+  if (!kBiasLaid<VPL> && a.bias) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) bias[i % (VPL <= 16 ? VPL : 1)] = lane * VPL + i < E ? a.bias[lane * VPL + i] : 0.f;
+    for (int i = 0; i < VPL; ++i) bias[i % (kBiasLaid<VPL> ? 1 : VPL)] = lane * VPL + i < E ? a.bias[lane * VPL + i] : 0.f;
   }
   const long long step = (long long)gridDim.x * kRouteWarps;
   for (long long t = (long long)blockIdx.x * kRouteWarps + warp; t < a.T; t += step) {
@@ -181,17 +192,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32, kRouteBlocks<VPL>) route_ker
       float m1 = -INFINITY;   // lane g: what group g is worth
       if (scored) {
         float val[VPL];   // what groups are valued by; the key, where there is a bias
+        // what is -inf gets its value below: an ordinary operand here, since a reciprocal of inf or a
+        // quotient of 0 takes a slower way, and the whole warp with it (one token of 768 experts: 13.0 us, 9.2 so)
         if (a.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-          for (int i = 0; i < VPL; ++i) val[i] = sigmoid_f32(key[i]);
+          for (int i = 0; i < VPL; ++i) val[i] = sigmoid_f32(key[i] > -INFINITY ? key[i] : 0.f);
         } else {
 #pragma unroll
-          for (int i = 0; i < VPL; ++i) val[i] = __fdiv_rn(exp_below(key[i], top), den);
+          for (int i = 0; i < VPL; ++i) val[i] = __fdiv_rn(key[i] > -INFINITY ? exp_below(key[i], top) : 1.f, den);
         }
         if (a.bias) {
 #pragma unroll
           for (int i = 0; i < VPL; ++i)
-            val[i] += VPL <= 16 ? bias[i % (VPL <= 16 ? VPL : 1)] : (lane * VPL + i < E ? a.bias[lane * VPL + i] : 0.f);
+            val[i] += kBiasLaid<VPL> ? laid_bias[lane * (VPL + 1) + i] : bias[i % (kBiasLaid<VPL> ? 1 : VPL)];
         }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -404,7 +417,7 @@ __global__ void __launch_bounds__(128) route_bwd_kernel(const RouteBwdArgs a, in
 //   d z_e = p_e (g_e - sum_j g_j p_j),  g_e = 0 for experts not chosen.
 // One warp per token, its row kept in registers between the softmax's sums and the
 // gradient, a lane's share in pieces of 16 bytes or, where rows do not start for
-// that, every 32nd element.  16384 tokens of 256 experts, fp32: 6.9 us (33.6 MB: 5.0
+// that, every 32nd element.  16384 tokens of 256 experts, fp32: 7.7 us (33.6 MB: 5.0
 // at the copy rate; 14.8 with the row read again for each of its three uses).
 template <int VPL, typename TL>
 __global__ void __launch_bounds__(128) route_bwd_dense_kernel(const RouteBwdArgs a, int vec) {
@@ -514,7 +527,7 @@ static moe_status launch_route(const RouteArgs& a, cudaStream_t s) {
   const long long need = ((long long)a.T + kRouteWarps - 1) / kRouteWarps, most = device_sms() * (long long)kRouteBlocks<VPL>;
   ProfScope ps(MOE_K_ROUTE, s);
   cudaError_t e = launch_pdl(route_kernel<VPL, TL>, dim3((unsigned)(need < most ? need : most)),
-                             dim3(kRouteWarps * 32), a.load ? a.E * sizeof(int) : 0, s, a, vec);
+                             dim3(kRouteWarps * 32), (kBiasLaid<VPL> && a.bias ? kLaid<VPL> * 4 : 0) + (a.load ? a.E * 4 : 0), s, a, vec);
   if (e != cudaSuccess) return cuda_fail(e, "route_kernel");
   return check_launch("route_kernel");
 }

@@ -235,3 +235,24 @@ def test_adapter_linear_empty_batch():
     M = load_lib()
     d = _data(9, 2, 64, 48, 8, 2, "bf16", "mixed")
     assert M.moe_adapter_linear(d["x"][:0], d["W"], d["A"], d["B"], d["ids"][:0], d["c"]).shape == (0, 48)
+
+
+# small batches' tiles of tokens that share an adapter: an adapter a token, a few tokens of each, all of
+# one; ranks of one and four 32-wide steps; H small enough that no cluster splits it, and in a cluster
+@pytest.mark.parametrize("T,H,N,R,n", [(128, 64, 130, 128, 200), (128, 2048, 256, 104, 16), (97, 128, 1000, 8, 13),
+                                       (24, 1024, 96, 32, 2), (520, 256, 1100, 56, 5)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("ids", ["mixed", "runs", 0])
+def test_adapter_linear_tiles_of_an_adapter(T, H, N, R, n, dtype, out, ids):
+    M = load_lib()
+    _check(M, _data(T + R, T, H, N, R, n, dtype, ids), dtype, out, rows=130)
+
+
+def test_adapter_linear_results_do_not_depend_on_the_neighbours():
+    # a token's result is that of its own adapter, in whatever order the batch names them
+    M = load_lib()
+    d = _data(9, 100, 512, 300, 24, 6, "bf16", "mixed")
+    a = M.moe_adapter_linear(d["x"], d["W"], d["A"], d["B"], d["ids"], d["c"])
+    order = torch.randperm(100, device="cuda")
+    b = M.moe_adapter_linear(d["x"][order].contiguous(), d["W"], d["A"], d["B"], d["ids"][order].contiguous(), d["c"])
+    assert torch.equal(b, a[order])

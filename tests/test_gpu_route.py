@@ -227,3 +227,40 @@ def test_route_empty_batch():
     ids, w = M.moe_route(lg, 4)
     assert ids.shape == (0, 4) and w.shape == (0, 4)
     assert M.moe_route_backward(lg, ids, w).shape == (0, 16)
+
+
+@pytest.mark.parametrize("E", [33, 700, 1003, 2047])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_route_gradient_of_plain_softmax_whatever_the_rows_start(E, dtype):
+    # rows that start anywhere take another order of the experts than those on 16-byte boundaries
+    M = load_lib()
+    rng = np.random.default_rng(E)
+    T, k = 21, 5
+    wide = torch.from_numpy((rng.standard_normal((T, E + 4)) * 1.5).astype(np.float32)).cuda().to(DT[dtype])
+    lg = wide[:, 3:E + 3]
+    lg[4, 1:] = -np.inf
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ids[4] = [0, -1, -1, -1, -1]
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    out = torch.full((T, E + 6), 7.0, dtype=DT[dtype], device="cuda")
+    M.moe_route_backward(lg, torch.from_numpy(ids).cuda(), torch.from_numpy(dw).cuda(), M.MOE_SCORE_SOFTMAX, False, 2.5,
+                         d_logits=out[:, 5:E + 5])
+    assert (out[:, :5] == 7).all() and (out[:, E + 5:] == 7).all()
+    ref = O.route_backward(lg.double().cpu().numpy(), ids, dw, "softmax", False, 2.5)
+    tol = 8 * REL * 2.5 * np.abs(dw).max(1, keepdims=True) + ULP[dtype] * np.abs(ref)
+    if dtype == "f16":
+        tol = tol + 2.0 ** -25
+    assert np.all(np.abs(out[:, 5:E + 5].double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.parametrize("E,G,tg", [(764, 1, 1), (1003, 1, 1), (2046, 6, 2), (700, 7, 3)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_many_experts_with_bias(E, G, tg, score):
+    M = load_lib()
+    rng = np.random.default_rng(E)
+    wide = torch.from_numpy((rng.standard_normal((23, E + 1)) * 1.5).astype(np.float32)).cuda()
+    bias = np.round(rng.standard_normal(E) * 40) * 1e-3
+    for lg in (wide[:, :E], wide[:, 1:], wide[:, :E].contiguous()):
+        lg = lg.clone() if lg.is_contiguous() else lg
+        for load in (True, False):
+            _check(M, lg, 9, score, bias, G, tg, load=load)

@@ -678,9 +678,10 @@ moe_status moe_block_norm_backward(int T, int H, int x_dtype, int y_dtype, int w
  *   out         device [T, N] of out_dtype (`dtype` or MOE_DT_F32)
  * n_adapters == 0: the projection alone (the adapter pointers are not read).
  * Products of the projection and of A x are exact in fp32 and summed in fp32.
- * A x enters the second product in fp32, or, where 16 neighbouring tokens share
- * an adapter in a large batch, as terms of `dtype` that carry 16 of its
- * significand bits (bf16; 24 for fp32 results) or 22 (f16).  An adapter's values,
+ * A x enters the second product as terms of `dtype`: with bf16 two, which carry
+ * 16 bits of each value's significand, or for fp32 results three (24 bits);
+ * with f16 two, which carry 22 bits of a token's largest |A x| (times scale) or
+ * more, whatever its size and whoever shares its batch.  An adapter's values,
  * NaN included, reach the tokens that name it and no others.
  * H a multiple of 8, R a multiple of 8 up to 128, x, W, lora_a and lora_b
  * 16-byte aligned, ld_x and ld_w multiples of 8; T >= 0, N >= 1.

@@ -720,7 +720,8 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   __shared__ alignas(8) uint64_t full[kShrinkStages], empty[kShrinkStages], done;
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_err, s_id[kShrinkTokens], s_slot[kShrinkTokens], s_list[kShrinkTokens], s_big[kShrinkTokens / 16];
+  __shared__ int s_err, s_id[kShrinkTokens], s_slot[kShrinkTokens], s_list[kShrinkTokens];
+  __shared__ uint32_t s_top[kShrinkTokens];   // fp16: the largest |u| of a token, as bits
   __shared__ int s_first[kShrinkTokens], s_count[kShrinkTokens / 32];
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -769,7 +770,7 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
     const uint32_t firsts = __ballot_sync(0xffffffffu, first);
     if (first) s_first[warp * 32 + __popc(firsts & ((1u << lane) - 1))] = mine;
     if (lane == 0) s_count[warp] = __popc(firsts);
-    if (tid < kShrinkTokens / 16) s_big[tid] = 0;
+    s_top[tid] = 0;
   }
   __syncthreads();
   // ... and of the warps before it
@@ -861,11 +862,14 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
       }
       const float sc = a.scale ? a.scale[s_id[tt]] : 1.f;
       const long long o = (long long)(t0 + tt) * a.R + c * 4;
+      uint32_t top = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] *= sc;
-        if (!std::is_same<TE, __nv_bfloat16>::value && !(fabsf(v[j]) < 32768.f)) s_big[tt / 16] = 1;
+        const uint32_t bits = __float_as_uint(fabsf(v[j]));   // in the numbers' order, inf and NaN last
+        top = top > bits ? top : bits;
       }
+      if (!std::is_same<TE, __nv_bfloat16>::value && a.group) atomicMax(&s_top[tt], top);
       *reinterpret_cast<float4*>(a.u + o) = make_float4(v[0], v[1], v[2], v[3]);
       for (int k = 0; a.group && k < a.terms; ++k) {
         TE e[4];
@@ -885,13 +889,21 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
   }
   __syncthreads();
   // how the projection takes a group: together where all 16 (a last group's missing tokens
-  // aside) share an adapter and u is within the 16-bit type's range
+  // aside) share an adapter and fp16's terms, which are not scaled there, carry u: two of them are
+  // off by at most 2^-25 (half of fp16's smallest step), that is 2^-22 of a token's largest |u|
+  // from 2^-3 on, and the first one holds less than 2^15.  A token of u = 0 has nothing to carry.
   if (a.group && tid < share / 16) {
     const int g = rank * (share / 16) + tid, base = g * 16;
     if (t0 + base < a.T) {
       int id = s_id[base];
-      for (int i = 1; i < 16 && t0 + base + i < a.T; ++i) id = s_id[base + i] == s_id[base] ? id : kMixed;
-      a.group[t0 / 16 + g] = id >= 0 && s_big[g] ? kMixed : id;
+      bool fits = true;
+      for (int i = 0; i < 16 && t0 + base + i < a.T; ++i) {
+        id = s_id[base + i] == s_id[base] ? id : kMixed;
+        const uint32_t top = s_top[base + i];
+        fits = fits && (top == 0 || (top >= 0x3e000000u && top < 0x47000000u));   // 2^-3, 2^15
+      }
+      if (!std::is_same<TE, __nv_bfloat16>::value && id >= 0 && !fits) id = kMixed;
+      a.group[t0 / 16 + g] = id;
     }
   }
   if (!ok) {   // a wait gave up: leave the copies in flight time to land

@@ -1,0 +1,65 @@
+"""moe_adapter_linear's large batches (the persistent kernel) for what the small ones are tested for, and the
+accuracy of what an adapter adds.
+
+Tolerances of single elements are those of test_gpu_adapter_linear.py."""
+import pytest
+import torch
+
+from tests.helpers import load_lib
+from tests.test_gpu_adapter_linear import DT, _check, _data
+
+pytestmark = pytest.mark.gpu
+
+# 11 x 16 tiles of 128 x 128: past the SMs, so the persistent kernel for results of either kind
+T, N = 1300, 2048
+
+
+def _call(M, d, kind, **kw):
+    return M.moe_adapter_linear(d["x"], d["W"], d["A"], d["B"], d["ids"], d["c"], out_dtype=DT[kind], **kw)
+
+
+@pytest.mark.parametrize("T", [40, 1300])
+@pytest.mark.parametrize("out", ["f16", "f32"])
+@pytest.mark.parametrize("ids", ["runs", 0])
+@pytest.mark.parametrize("by", [1e-2, 1e-3, 1e-5])
+def test_adapter_linear_f16_below_its_range(T, out, ids, by):
+    # A x near and below fp16's smallest steps, brought back by B
+    M = load_lib()
+    d = _data(12, T, 256, N, 16, 3, "f16", ids)
+    d["A"] = (d["A"].float() * by).to(torch.float16)
+    d["B"] = (d["B"].float() * min(1 / by, 1e4)).to(torch.float16)
+    _check(M, d, "f16", out, rows=150)
+
+
+def test_adapter_linear_f16_small_and_ordinary_tokens_side_by_side():
+    # one group of 16 holds a token of tiny A x, one of none (x = 0) and ordinary ones
+    M = load_lib()
+    d = _data(13, T, 256, N, 16, 3, "f16", 0)
+    d["B"] = (d["B"].float() * 1e3).to(torch.float16)
+    d["x"][5::16] *= 2.0 ** -12
+    d["x"][6::16] = 0
+    _check(M, d, "f16", "f32", rows=400)
+
+
+@pytest.mark.parametrize("T", [5, 100, 1300])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+def test_adapter_linear_bits_of_a_x(T, dtype, ids):
+    """A picks single elements of x and B single ranks, by 1: a result is c x[j], whose product is rounded to fp32
+    (2^-24), cut to the terms' bits (none of bf16's 24; of f16's two 2^-22 of the token's largest) and added up from
+    them (2^-23)."""
+    M = load_lib()
+    d = _data(T, T, 256, N, 16, 4, dtype, ids)
+    for m in ("W", "A", "B"):
+        d[m].zero_()
+    pick = torch.randint(0, 256, (4, 16), device="cuda")
+    d["A"].scatter_(2, pick[..., None], 1.0)
+    rank = torch.arange(N, device="cuda") % 16
+    d["B"][:, torch.arange(N, device="cuda"), rank] = 1.0
+    got = _call(M, d, "f32").double()
+    a = d["ids"].long().clamp(min=0)
+    ref = torch.where(d["ids"][:, None] >= 0, d["c"].double()[a][:, None] * d["x"].double().gather(1, pick[a])[:, rank], 0.0)
+    tol = 2.0 ** -22 * ref.abs()
+    if dtype == "f16":
+        tol = tol + 2.0 ** -22 * ref.abs().amax(1, keepdim=True)
+    assert torch.all((got - ref).abs() <= tol)

@@ -706,14 +706,17 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
 // linear_split_kernel, the MMA's 128 rows being A rows: those of as many of the
 // adapters that the tokens name as fit (128 / R; a prompt's tokens name one or
 // two, more take another pass).  Every row meets every token; a token takes the
-// rows of its own adapter, so nothing else's values reach it.  Bound by reading x
+// rows of its own adapter, so nothing else's values reach it.  For fp32 results the
+// share of H goes through four accumulators of kF32Chunk steps, added up in
+// registers, as often as it takes.  Bound by reading x
 // (67 MB at 8192 x 4096: 20 us from HBM, rank 16; 33 MB at 4001: 15 us, rank 32).
 constexpr int kShrinkTokens = 128;
 constexpr int kShrinkStage = kATile + kShrinkTokens * 128;
 constexpr int kShrinkStages = 6;
 constexpr int kShrinkSmem = kShrinkStages * kShrinkStage + 1024;
+constexpr int kShrinkAcc = 512 / kShrinkTokens;   // accumulators for fp32 results
 
-template <typename TE>
+template <typename TE, bool F32>
 __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_constant__ CUtensorMap mA,
                                                              const __grid_constant__ CUtensorMap mX,
                                                              const LinearArgs a) {
@@ -726,6 +729,7 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = gridDim.x, rank = blockIdx.x, t0 = blockIdx.y * kShrinkTokens;
+  constexpr int cols = (F32 ? kShrinkAcc : 1) * kShrinkTokens;
   const int nk = (a.H + 63) / 64, k0 = (int)((long long)nk * rank / cs), k1 = (int)((long long)nk * (rank + 1) / cs);
   if (tid == 0) {
     prefetch_map(&mA);
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)),
-                 "r"(kShrinkTokens));
+                 "r"(cols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   __syncthreads();
@@ -805,47 +809,67 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
   const int share = kShrinkTokens / cs;
   for (int p = 0; p < total; p += per) {
     const int cnt = total - p < per ? total - p : per;
-    if (warp == 0) {
-      if (elect_one()) {
-        for (int k = k0; k < k1; ++k) {
-          if (wrapped && !wait_bar(&empty[r.stage], r.parity ^ 1, &s_err)) break;
-          uint8_t* st = sm + r.stage * kShrinkStage;
-          const bool have = p == 0 && k - k0 < early;
-          mbar_expect_tx(&full[r.stage], cnt * a.R * 128 + (have ? 0 : kShrinkTokens * 128));
-          for (int i = 0; i < cnt; ++i) tma_2d(st + i * a.R * 128, &mA, k * 64, s_list[p + i] * a.R, &full[r.stage]);
-          if (!have) tma_2d(st + kATile, &mX, k * 64, t0, &full[r.stage]);
-          r.next();
-          wrapped |= r.stage == 0;
+    float f[kShrinkTokens / 32][16];   // a warp's 32 rows, every other 16 tokens
+    for (int kb = k0, ke; kb < k1; kb = ke) {
+      ke = F32 && kb + kShrinkAcc * kF32Chunk < k1 ? kb + kShrinkAcc * kF32Chunk : k1;
+      if (warp == 0) {
+        if (elect_one()) {
+          for (int k = kb; k < ke; ++k) {
+            if (wrapped && !wait_bar(&empty[r.stage], r.parity ^ 1, &s_err)) break;
+            uint8_t* st = sm + r.stage * kShrinkStage;
+            const bool have = p == 0 && k - k0 < early;
+            mbar_expect_tx(&full[r.stage], cnt * a.R * 128 + (have ? 0 : kShrinkTokens * 128));
+            for (int i = 0; i < cnt; ++i) tma_2d(st + i * a.R * 128, &mA, k * 64, s_list[p + i] * a.R, &full[r.stage]);
+            if (!have) tma_2d(st + kATile, &mX, k * 64, t0, &full[r.stage]);
+            r.next();
+            wrapped |= r.stage == 0;
+          }
+        }
+      } else if (warp == 1) {
+        if (elect_one()) {
+          const uint32_t idesc = idesc_f16(kShrinkTokens, std::is_same<TE, __nv_bfloat16>::value);
+          const uint64_t d0 = umma_desc_sw128(su32(sm));
+          uint32_t d = tmem;
+          int in = 0;   // K steps in the accumulator
+          for (int k = kb; k < ke; ++k) {
+            if (!wait_bar(&full[r.stage], r.parity, &s_err)) break;
+            tc_fence_after();
+            const uint64_t da = d0 + (uint32_t)(r.stage * (kShrinkStage / 16)), db = da + kATile / 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma_k16(d, da + 2 * j, db + 2 * j, idesc, in || j);
+            mma_commit(&empty[r.stage]);
+            r.next();
+            if (++in == kF32Chunk && F32) in = 0, d += kShrinkTokens;
+          }
+          mma_commit(&done);
         }
       }
-    } else if (warp == 1) {
-      if (elect_one()) {
-        const uint32_t idesc = idesc_f16(kShrinkTokens, std::is_same<TE, __nv_bfloat16>::value);
-        const uint64_t d0 = umma_desc_sw128(su32(sm));
-        for (int k = k0; k < k1; ++k) {
-          if (!wait_bar(&full[r.stage], r.parity, &s_err)) break;
-          tc_fence_after();
-          const uint64_t da = d0 + (uint32_t)(r.stage * (kShrinkStage / 16)), db = da + kATile / 16;
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, wait_bar(&done, turn, &s_err)) && *(volatile int*)&s_err == MOE_OK;
+      turn ^= 1;
+      tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_k16(tmem, da + 2 * j, db + 2 * j, idesc, k != k0 || j);
-          mma_commit(&empty[r.stage]);
-          r.next();
+      for (int i = 0; i < kShrinkTokens / 32; ++i) {
+        const int ch = (warp >> 2) + 2 * i;
+        for (int b = 0; b == 0 || (F32 && b * kF32Chunk < ke - kb); ++b) {   // the accumulators in order
+          uint32_t v[16];
+          tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(b * kShrinkTokens + ch * 16), v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            f[i][j] = F32 && (b || kb > k0) ? f[i][j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
         }
-        mma_commit(&done);
+      }
+      if (F32 && ke < k1) {   // the accumulators are free again
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
       }
     }
-    __syncwarp();
-    ok = __all_sync(0xffffffffu, wait_bar(&done, turn, &s_err)) && *(volatile int*)&s_err == MOE_OK;
-    turn ^= 1;
-    tc_fence_after();
 #pragma unroll
-    for (int ch = warp >> 2; ch < kShrinkTokens / 16; ch += 2) {
-      uint32_t v[16];
-      tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(ch * 16), v);
+    for (int i = 0; i < kShrinkTokens / 32; ++i)
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        part[(ch * 16 + j) * kRows + (warp & 3) * 32 + lane] = ok ? __uint_as_float(v[j]) : NAN;
-    }
+        part[(((warp >> 2) + 2 * i) * 16 + j) * kRows + (warp & 3) * 32 + lane] = ok ? f[i][j] : NAN;
     tc_fence_before();
     __syncwarp();
     cluster_sync();
@@ -915,7 +939,7 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_consta
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kShrinkTokens));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
   }
   if (tid == 0 && s_err != MOE_OK && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
 }
@@ -1328,9 +1352,10 @@ static moe_status launch_shrink(const LinearArgs& a, int dtype, long long beside
   moe_status st = map_rows(&mA, a.A, dtype, a.H, (uint64_t)a.n * a.R, a.H, a.R);
   if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.H, a.T, a.ld_x, kShrinkTokens);
   if (st != MOE_OK) return st;
-  auto kernel = adapter_shrink_kernel<TE>;
-  static char allowed[64];
-  MOE_CUDA(allow_smem(kernel, kShrinkSmem, allowed));
+  const bool f32 = a.out_dtype == MOE_DT_F32;
+  auto kernel = f32 ? adapter_shrink_kernel<TE, true> : adapter_shrink_kernel<TE, false>;
+  static char allowed[2][64];
+  MOE_CUDA(allow_smem(kernel, kShrinkSmem, allowed[f32]));
   const int tiles = (a.T + kShrinkTokens - 1) / kShrinkTokens, nk = (a.H + 63) / 64;
   MOE_ARG(tiles <= 65535, "T too large");
   // as many blocks as leave the projection's room to run at the same time (1599 tokens to 378 outputs, H = 4744:

@@ -1,7 +1,11 @@
 """moe_adapter_linear's large batches (the persistent kernel) for what the small ones are tested for, and the
 accuracy of what an adapter adds.
 
-Tolerances of single elements are those of test_gpu_adapter_linear.py."""
+Tolerances of single elements are those of test_gpu_adapter_linear.py.  In the 2-norm, for fp32 results of normal
+data: a tensor-core step of 16 products cuts the accumulator's sum off at 24 bits, by 2^-24 of it on average and
+always towards zero.  Over the 32 steps of 512 products, the sum growing as their root, that is at most 2/3 x 32 x
+2^-24 = 1.3e-6 of an accumulator's sum, and of the whole as much (the accumulators are added in fp32).  What an
+adapter adds takes that from A x, and 2^-22 from A x's terms and the few steps of the second product: 1.6e-6."""
 import pytest
 import torch
 
@@ -63,3 +67,28 @@ def test_adapter_linear_bits_of_a_x(T, dtype, ids):
     if dtype == "f16":
         tol = tol + 2.0 ** -22 * ref.abs().amax(1, keepdim=True)
     assert torch.all((got - ref).abs() <= tol)
+
+
+def _norms(M, d, out):
+    """(error of the whole result, error of what the adapters add) in the 2-norm, against 64 bits."""
+    f = torch.float64
+    x, W = d["x"].to(f), d["W"].to(f)
+    low = torch.zeros(x.shape[0], W.shape[0], dtype=f, device="cuda")
+    for a in range(d["A"].shape[0]):
+        at = d["ids"] == a
+        low[at] = float(d["c"][a]) * ((x[at] @ d["A"][a].to(f).T) @ d["B"][a].to(f).T)
+    whole = x @ W.T + low
+    err = (_call(M, d, out).to(f) - whole).norm()
+    return float(err / whole.norm()), float(err / low.norm())
+
+
+@pytest.mark.parametrize("T,N", [(16, 256), (100, 640), (300, 640), (1300, 640), (1300, 2048), (16400, 100)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+def test_adapter_linear_accuracy_in_fp32(T, N, dtype, ids):
+    M = load_lib()
+    d = _data(T, T, 4096, N, 16, 4, dtype, ids)
+    assert _norms(M, d, "f32")[0] <= 1.6e-6
+    # what the adapters add by itself: no other term hides its error
+    d["W"].zero_()
+    assert _norms(M, d, "f32")[1] <= 1.6e-6

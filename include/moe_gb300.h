@@ -594,7 +594,9 @@ enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2 };
  *              ties to the lower group
  *   topk_ids   device int32 [T, k] out: the k largest keys in descending order,
  *              ties to the lower id; -1 where fewer than k experts are left
- *              (moe_slot_ensure and the expert forwards skip those)
+ *              (moe_slot_ensure skips those and leaves their slots as they
+ *              were: set them to -1 before it, as the expert forwards skip a
+ *              negative slot)
  *   topk_w     device fp32 [T, k] out: scale * s, renorm != 0: scale * s over
  *              the sum of the kept s (softmax: the softmax over the kept
  *              logits); 0 where the id is -1 or every kept s is 0

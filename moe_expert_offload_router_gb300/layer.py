@@ -248,12 +248,21 @@ class DecodeLayerRunner:
         if done != T:
             raise L.MoeError(L.MOE_ERR_CAPACITY, f"layer {layer_id}: single chunk expected, got {done}/{T}")
 
+    def _leave_out(self, ids, slots, stream):
+        # moe_slot_ensure writes the slots of non-negative ids only; where a Routing left -1, the
+        # slot of an earlier call must not stay (the default routing gives every token k experts)
+        if self.routing is not None:
+            with torch.cuda.stream(stream):
+                slots.copy_(ids, non_blocking=True)
+
     def _run_device(self, layer_id, T, ids, w, slots, x, y, stream, prefetch=None):
         v = self._views(T)
         k = self.k
         single = min(self.E, T * k) <= self.cache.S
         tb = 0
         while tb < T:
+            if tb == 0:
+                self._leave_out(ids, slots, stream)
             L.moe_slot_ensure(self.cache, layer_id, ids, slots, 0, k, L.MOE_FETCH_MARK_REST, tb,
                               v["keys4"], v["slots4"], v["count4"], v["done"], stream)
             overlap = self.overlap is True or (self.overlap == "auto" and T * k >= self.OVERLAP_MIN_PAIRS)
@@ -436,6 +445,8 @@ class DecodeLayerRunner:
         self.stats["calls"] += 1
         while tb < T:
             if self.ladder is None:
+                if tb == 0:
+                    self._leave_out(ids, slots, stream)
                 L.moe_slot_ensure(self.cache, layer_id, ids, slots, 0, k, L.MOE_FETCH, tb,
                                   v["keys4"], v["slots4"], v["count4"], v["done"], stream)
                 tags, wuse = None, w

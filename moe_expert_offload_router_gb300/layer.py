@@ -103,7 +103,8 @@ class DecodeLayerRunner:
     * ``graph``: replay single-chunk device-copy steps as CUDA graphs.
     * ``assume_resident``: every key has its slot (a cache of L * E slots);
       no copies, no host waits.
-    * ``int2_cache`` and ``ladder`` = (a, b): the precision ladder.
+    * ``int2_cache`` and ``ladder`` = (a, b): the precision ladder (its survivors' weights
+      sum to the Routing's scale; it takes none without ``renorm``).
     * ``routing``: a :class:`Routing`; None for softmax, top-k, renormalised.
     """
 
@@ -116,10 +117,10 @@ class DecodeLayerRunner:
                  ladder=None, assume_resident: bool = False, copy: str = "engine",
                  overlap=False, copy_ctas: int = 32, graph: bool = False, copy_parts: int = 1,
                  down_parts: int = 1, routing: Optional[Routing] = None):
-        self.routing = routing
         self.cache, self.views, self.E, self.k, self.T_max = cache, views, E, k, T_max
         self.dev = torch.device(device or "cuda")
         self.c2, self.ladder = int2_cache, ladder
+        self.routing = routing
         dev = self.dev
         P = T_max * k
         self.ids = torch.empty((T_max, k), dtype=torch.int32, device=dev)
@@ -248,12 +249,28 @@ class DecodeLayerRunner:
         if done != T:
             raise L.MoeError(L.MOE_ERR_CAPACITY, f"layer {layer_id}: single chunk expected, got {done}/{T}")
 
+    @property
+    def routing(self):
+        return self._routing
+
+    @routing.setter
+    def routing(self, r):
+        if r is not None and self.ladder is not None and not r.renorm:
+            raise ValueError("the ladder renormalises the survivors' weights: it takes a Routing with renorm")
+        self._routing = r
+
     def _leave_out(self, ids, slots, stream):
         # moe_slot_ensure writes the slots of non-negative ids only; where a Routing left -1, the
         # slot of an earlier call must not stay (the default routing gives every token k experts)
         if self.routing is not None:
             with torch.cuda.stream(stream):
                 slots.copy_(ids, non_blocking=True)
+
+    def _scale_survivors(self, w, stream):
+        # the ladder's weights sum to 1, a Routing's to its scale
+        if self.routing is not None and self.routing.scale != 1.0:
+            with torch.cuda.stream(stream):
+                w.mul_(self.routing.scale)
 
     def _run_device(self, layer_id, T, ids, w, slots, x, y, stream, prefetch=None):
         v = self._views(T)
@@ -340,6 +357,7 @@ class DecodeLayerRunner:
         tags, wuse = self.tags[:T], self.w2[:T]
         L.moe_ladder_classify(self.cache, self.c2, layer_id, ids, w, a, b, 0, slots, tags, wuse, v["keys4"],
                               v["slots4"], v["count4"], v["keys2"], v["slots2"], v["count2"], v["done"], stream)
+        self._scale_survivors(wuse, stream)
         with torch.cuda.stream(stream):
             self.status_h.copy_(self.info[0:4], non_blocking=True)
         self.status_ev.record(stream)
@@ -486,6 +504,8 @@ class DecodeLayerRunner:
                     self.stats["misses"] += n4 + n2
                     self.stats["bytes_copied"] += n4 * self.cache.B + (n2 * self.c2.B if n2 else 0)
             self.stats["chunks"] += 1
+            if self.ladder is not None:
+                self._scale_survivors(wuse[tb:done], stream)
             L.moe_expert_forward(self.views, x[tb:done], slots[tb:done],
                                  None if tags is None else tags[tb:done], wuse[tb:done], y[tb:done],
                                  self.ws, self.err, stream)

@@ -62,3 +62,47 @@ def test_tokens_with_fewer_experts_than_k(kw, T):
         assert np.isfinite(got).all()
         assert _off(got, moe_layer(x, ids, w, expert)) <= TOL
     cache.close()
+
+
+def _ladder(M, wl, routing, copy):
+    bank4, B4 = pinned_fp4_bank(wl, (0,))
+    B2 = M.moe_int2_expert_bytes(wl.H, wl.I)
+    bank2 = torch.empty(wl.E * B2, dtype=torch.uint8, pin_memory=True)
+    for e in range(wl.E):
+        bank2[e * B2:(e + 1) * B2] = torch.from_numpy(gen.int2_expert(wl, 0, e))
+    s4 = torch.empty(wl.S * B4, dtype=torch.uint8, device="cuda")
+    s2 = torch.empty(wl.S2 * B2, dtype=torch.uint8, device="cuda")
+    c4, c2 = M.moe_cache(wl.S, 1, wl.E, B4, s4, bank4), M.moe_cache(wl.S2, 1, wl.E, B2, s2, bank2)
+    views = M.make_views(wl.H, wl.I, s4, wl.S, s2, wl.S2, None)
+    runner = M.DecodeLayerRunner(c4, views, wl.E, wl.k, wl.T, int2_cache=c2, ladder=wl.ladder, copy=copy,
+                                 routing=routing)
+    return runner, (c4, c2)
+
+
+@pytest.mark.parametrize("copy,S", [("engine", 20), ("engine", 6), ("device", 20)])
+def test_ladder_keeps_the_routings_scale(copy, S):
+    # the survivors' weights sum to the scale, as the chosen experts' do without a ladder
+    M = load_lib()
+    wl = configs.scaled(configs.LADDER, H=256, I=128, T=8, S=S, S2=30)
+    out = []
+    for scale in (1.0, 2.5):
+        runner, caches = _ladder(M, wl, M.Routing(scale=scale), copy)
+        out.append([_run(runner, wl, gen.router_logits(wl, 0, step), gen.activations(wl, 0, step))
+                    for step in range(3)])
+        for c in caches:
+            c.close()
+    for one, more in zip(*out):
+        # two roundings to bf16, of values 2.5 apart
+        assert np.abs(one).max() > 0 and np.all(np.abs(more - 2.5 * one) <= 2.0 ** -8 * (np.abs(more) + 2.5 * np.abs(one)))
+
+
+def test_ladder_refuses_weights_that_are_not_renormalised():
+    M = load_lib()
+    wl = configs.scaled(configs.LADDER, H=256, I=128, T=8, S=20, S2=30)
+    with pytest.raises(ValueError, match="renorm"):
+        _ladder(M, wl, M.Routing(renorm=False), "device")
+    runner, caches = _ladder(M, wl, None, "device")
+    with pytest.raises(ValueError, match="renorm"):
+        runner.routing = M.Routing(renorm=False)
+    for c in caches:
+        c.close()

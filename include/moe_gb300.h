@@ -334,7 +334,8 @@ moe_status moe_debug_fail_copy(moe_cache* cache, int index);
  *   ids, w      device int32 / fp32 [T, k] (router output)
  *   slots_out   device int32 [T, k]: slot in the tagged pool, -1 if dropped
  *   tags_out    device int8  [T, k]: MOE_TAG_FP4 / MOE_TAG_INT2 / MOE_TAG_DROP
- *   w_out       device fp32  [T, k]: renormalised weights, 0 if dropped
+ *   w_out       device fp32  [T, k]: renormalised weights, 0 if dropped or if
+ *               the survivors' weights sum to 0
  *   miss lists and counts per pool as for moe_slot_ensure (counts negative on
  *   a device-detected error); d_tokens_done as for moe_slot_ensure.
  * Limits as moe_slot_ensure; 1 <= a <= b <= k.

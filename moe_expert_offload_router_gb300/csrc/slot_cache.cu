@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kEnsureThreads)
     }
     for (int j = 0; j < k; ++j) {
       const size_t i = (size_t)t * k + j;
-      w_out[i] = tags_out[i] == MOE_TAG_DROP ? 0.f : w[i] / sum;
+      w_out[i] = tags_out[i] == MOE_TAG_DROP || sum == 0.f ? 0.f : w[i] / sum;   // all weights 0: no 0 / 0
     }
   }
   if (threadIdx.x == 0) {

@@ -106,3 +106,16 @@ def test_ladder_refuses_weights_that_are_not_renormalised():
         runner.routing = M.Routing(renorm=False)
     for c in caches:
         c.close()
+
+
+def test_ladder_of_weights_that_are_all_zero():
+    # sigmoids that all underflow weigh nothing; a row's weights are then 0 and not 0 / 0
+    M = load_lib()
+    wl = configs.scaled(configs.LADDER, H=256, I=128, T=8, S=20, S2=30)
+    runner, caches = _ladder(M, wl, M.Routing(), "device")
+    lg = gen.router_logits(wl, 0, 0)
+    lg[3] -= 200
+    got = _run(runner, wl, lg, gen.activations(wl, 0, 0))
+    assert np.isfinite(got).all() and (got[3] == 0).all() and (got[[0, 1, 2, 4, 5, 6, 7]] != 0).any(1).all()
+    for c in caches:
+        c.close()

@@ -69,8 +69,15 @@ class Routing:
     scale: float = 1.0
     load: object = None
 
+    def _bias(self, layer: int):
+        return self.bias[layer] if isinstance(self.bias, (list, tuple)) else self.bias
+
+    def used(self, layer: int):
+        """The tensors that a call for `layer` reads and writes besides its arguments."""
+        return self._bias(layer), self.load[layer] if isinstance(self.load, (list, tuple)) else self.load
+
     def __call__(self, layer: int, logits, k: int, ids, w, stream):
-        bias = self.bias[layer] if isinstance(self.bias, (list, tuple)) else self.bias
+        bias = self._bias(layer)
         L.moe_route(logits, k, self.score, bias, self.n_group, self.topk_group, self.group_score, self.renorm,
                     self.scale, topk_ids=ids, topk_w=w, load=None if self.load is None else self.load[layer],
                     stream=stream)
@@ -100,7 +107,8 @@ class DecodeLayerRunner:
       into that many parts, each with its own pass.
     * ``copy_ctas``: the copy kernel's grid (each CTA keeps an SM from the
       grouped GEMM).
-    * ``graph``: replay single-chunk device-copy steps as CUDA graphs.
+    * ``graph``: replay single-chunk device-copy steps as CUDA graphs (captured again when the
+      Routing, its bias or its load is replaced; values changed in place need no capture).
     * ``assume_resident``: every key has its slot (a cache of L * E slots);
       no copies, no host waits.
     * ``int2_cache`` and ``ladder`` = (a, b): the precision ladder (its survivors' weights
@@ -373,6 +381,14 @@ class DecodeLayerRunner:
         return (self.graph and self.copy == "device" and self.ladder is None and not self.assume_resident
                 and prefetch is None and min(self.E, T * self.k) <= self.cache.S and not L.moe_profile_active())
 
+    @staticmethod
+    def _addresses(tensors):
+        return [None if t is None else t.data_ptr() for t in tensors]
+
+    def _same_routing(self, layer_id, used, at):
+        now = () if self.routing is None else self.routing.used(layer_id)
+        return all(a is b for a, b in zip(now, used)) and self._addresses(now) == at
+
     def _replay(self, layer_id, logits, x, y, stream):
         """Whole layer step as one CUDA graph: router, ensure, status read-back,
         device copies and the forward, replayed on static input and output buffers."""
@@ -380,7 +396,9 @@ class DecodeLayerRunner:
         key = (layer_id, T)
         if key not in self.graphs:
             return False
-        g, lg, xb, yb = self.graphs[key]
+        g, lg, xb, yb, routing, used, at = self.graphs[key]
+        if routing is not self.routing or not self._same_routing(layer_id, used, at):
+            return False   # run eagerly and captured again
         with torch.cuda.stream(stream):
             lg.copy_(logits, non_blocking=True)
             xb.copy_(x, non_blocking=True)
@@ -410,7 +428,9 @@ class DecodeLayerRunner:
             self._capturing = False
             self.pending = None
             self.stats["calls"], self.stats["chunks"] = calls, chunks
-        self.graphs[(layer_id, T)] = (g, lg, xb, yb)
+        # the graph holds the routing's parameters and its tensors' addresses: both are kept beside it
+        used = () if self.routing is None else self.routing.used(layer_id)
+        self.graphs[(layer_id, T)] = (g, lg, xb, yb, self.routing, used, self._addresses(used))
 
     def synchronize(self, stream=None):
         """Waits for the work enqueued on `stream` and raises what the device

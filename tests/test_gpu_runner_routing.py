@@ -119,3 +119,41 @@ def test_ladder_of_weights_that_are_all_zero():
     assert np.isfinite(got).all() and (got[3] == 0).all() and (got[[0, 1, 2, 4, 5, 6, 7]] != 0).any(1).all()
     for c in caches:
         c.close()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_routing_that_changes_between_calls(graph):
+    # a bias moved in place, a bias put in another's place, another count, another routing
+    M = load_lib()
+    wl = configs.scaled(configs.TINY, E=16, k=4, S=20, T=5)
+    rng = np.random.default_rng(0)
+
+    def bias():
+        return torch.from_numpy(np.round(rng.standard_normal(16) * 400).astype(np.float32) * 1e-3).cuda()
+    biases = [bias()]
+    load = torch.zeros(1, 16, dtype=torch.int32, device="cuda")
+    cache, _, runner, expert = _runner(M, wl, M.Routing(bias=biases, scale=1.5, load=load), copy="device", graph=graph)
+    lg, x = gen.router_logits(wl, 0, 0), gen.activations(wl, 0, 0)
+    old, counted, steps = [], 0, []
+
+    def step(score="sigmoid", b=None, scale=1.5):
+        got = _run(runner, wl, lg, x)
+        ids, w, margin = O.route(lg, 4, score, b, 1, 1, "top2", True, scale)
+        assert margin.min() > 4e-6
+        steps.append((np.array_equal(runner.ids.cpu().numpy(), ids), _off(got, moe_layer(x, ids, w, expert)) <= TOL))
+    for i in range(3):
+        step(b=biases[0].cpu().numpy())
+    biases[0].copy_(bias())
+    step(b=biases[0].cpu().numpy())
+    old.append(biases[0])            # held here: what is replaced is not freed in this test
+    biases[0] = bias()
+    step(b=biases[0].cpu().numpy())
+    step(b=biases[0].cpu().numpy())
+    counts = int(load.sum())
+    runner.routing = M.Routing(score=M.MOE_SCORE_SOFTMAX)
+    step("softmax", None, 1.0)
+    step("softmax", None, 1.0)
+    assert all(a and b for a, b in steps), steps
+    assert counts == 6 * 5 * 4 and int(load.sum()) == counts
+    assert len(runner.graphs) == int(graph)
+    cache.close()

@@ -591,8 +591,8 @@ enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2 };
  *              group, n_group <= 32 dividing E) only the topk_group groups of
  *              largest value take part: MOE_GROUP_MAX the largest key,
  *              MOE_GROUP_TOP2 the sum of the group's two largest s + bias (s
- *              without bias; the largest alone where only one is eligible);
- *              ties to the lower group
+ *              without bias; the largest alone where only one is eligible;
+ *              not below fp32's lowest finite value); ties to the lower group
  *   topk_ids   device int32 [T, k] out: the k largest keys in descending order,
  *              ties to the lower id; -1 where fewer than k experts are left
  *              (moe_slot_ensure skips those and leaves their slots as they

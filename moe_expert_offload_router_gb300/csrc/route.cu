@@ -85,6 +85,12 @@ __device__ __forceinline__ void load_row(const TL* row, int lane, int E, bool ve
   for (int i = 0; i < VPL; ++i) z[i] = fmaxf(z[i], -INFINITY);   // NaN: the other operand
 }
 
+// The two largest of a group as its worth; -inf is an empty group's, so two biases of fp32's lowest
+// value add up to that value.
+__device__ __forceinline__ float sum_of_two(float m1, float m2) {
+  return m2 > -INFINITY ? fmaxf(m1 + m2, -FLT_MAX) : m1;
+}
+
 // Lane g: what group g (of n_group times gs experts) is worth.  `lpg`: the lanes
 // of a group, where a lane's experts belong to one group and a group's lanes are
 // a power of two; else 0, and the groups are taken one after the other.
@@ -104,7 +110,7 @@ __device__ __forceinline__ float group_worth(const float (&val)[VPL], int lane, 
       m1 = fmaxf(m1, val[i]);
     }
     for (int o = 1; o < lpg; o <<= 1) join(o);
-    if (how == MOE_GROUP_TOP2 && m2 > -INFINITY) m1 += m2;
+    if (how == MOE_GROUP_TOP2) m1 = sum_of_two(m1, m2);
     return __shfl_sync(0xffffffffu, m1, lane * lpg & 31);
   }
   float worth = -INFINITY;
@@ -120,7 +126,7 @@ __device__ __forceinline__ float group_worth(const float (&val)[VPL], int lane, 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) join(o);
-    if (lane == g) worth = how == MOE_GROUP_TOP2 && m2 > -INFINITY ? m1 + m2 : m1;
+    if (lane == g) worth = how == MOE_GROUP_TOP2 ? sum_of_two(m1, m2) : m1;
   }
   return worth;
 }

@@ -9,6 +9,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <initializer_list>
@@ -143,13 +144,21 @@ struct Results {
   }
 };
 
-// A workspace for one call: freed for the call's own stream's later use.
-at::Tensor scratch(int64_t bytes, const at::Tensor& like, PyObject* stream_arg, cudaStream_t stream) {
-  at::Tensor ws = at::empty({bytes}, like.options().dtype(at::kByte));
-  if (stream_arg && stream_arg != Py_None && bytes)
-    c10::cuda::CUDACachingAllocator::recordStream(ws.storage().data_ptr(),
-                                                  c10::cuda::getStreamFromExternal(stream, ws.device().index()));
-  return ws;
+// A tensor that the caller did not bring, from the memory of the stream that the call runs on: what is
+// free there has no work of another stream before it.  A result is known to the current stream too,
+// where the caller takes it on (once that waits for the call's) and lets go of it.
+at::Tensor make(at::IntArrayRef shape, const at::TensorOptions& o, PyObject* stream_arg, bool result = true) {
+  if (!stream_arg || stream_arg == Py_None || !o.device().is_cuda()) return at::empty(shape, o);
+  const cudaStream_t s = stream_of(stream_arg);
+  const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(o.device().index());
+  if (s == now.stream()) return at::empty(shape, o);
+  at::Tensor t;
+  {
+    const c10::cuda::CUDAStreamGuard there(c10::cuda::getStreamFromExternal(s, o.device().index()));
+    t = at::empty(shape, o);
+  }
+  if (result && t.numel()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), now);
+  return t;
 }
 
 void check(moe_status st) {
@@ -179,9 +188,9 @@ PyObject* guarded(F f) {
 }
 
 const at::Tensor* either(PyObject* given, const char* what, at::Tensor& made, at::IntArrayRef shape,
-                         const at::TensorOptions& o) {
+                         const at::TensorOptions& o, PyObject* stream_arg) {
   if (const at::Tensor* t = tensor(given, what)) return t;
-  made = at::empty(shape, o);
+  made = make(shape, o, stream_arg);
   return &made;
 }
 
@@ -203,8 +212,8 @@ PyObject* route(PyObject*, PyObject* args, PyObject* kw) {
     const at::Tensor& lg = matrix(logits, "logits");
     const int T = to_int(lg.size(0), "T"), E = to_int(lg.size(1), "E"), d = dtype_code(lg);
     at::Tensor mi, mw;
-    const at::Tensor* ti = either(ids, "topk_ids", mi, {T, k}, lg.options().dtype(at::kInt));
-    const at::Tensor* tw = either(w, "topk_w", mw, {T, k}, lg.options().dtype(at::kFloat));
+    const at::Tensor* ti = either(ids, "topk_ids", mi, {T, k}, lg.options().dtype(at::kInt), st);
+    const at::Tensor* tw = either(w, "topk_w", mw, {T, k}, lg.options().dtype(at::kFloat), st);
     const Rows r = rows(&lg, T, E, "logits");
     auto* pb = (const float*)dense(tensor(bias, "bias"), {E}, at::kFloat, "bias");
     auto* pm = mask_ptr(mask, T);
@@ -232,7 +241,7 @@ PyObject* route_backward(PyObject*, PyObject* args, PyObject* kw) {
     const at::Tensor &lg = matrix(logits, "logits"), &ti = matrix(ids, "topk_ids");
     const int T = to_int(lg.size(0), "T"), E = to_int(lg.size(1), "E"), k = to_int(ti.size(1), "k"), d = dtype_code(lg);
     at::Tensor made;
-    const at::Tensor* td = either(dl, "d_logits", made, {T, E}, lg.options());
+    const at::Tensor* td = either(dl, "d_logits", made, {T, E}, lg.options(), st);
     same_type(td, lg.scalar_type(), "d_logits");
     const Rows r = rows(&lg, T, E, "logits"), rd = rows(td, T, E, "d_logits");
     auto* pm = mask_ptr(mask, T);
@@ -280,8 +289,8 @@ PyObject* block_norm(PyObject*, PyObject* args, PyObject* kw) {
     const at::Tensor *ty = tensor(y, "y"), *th = tensor(h, "h"), *txo = tensor(xo, "x_out");
     const at::Tensor& like = ty ? *ty : th ? *th : tx;
     at::Tensor mxo, mh;
-    if (!txo && ty) txo = &(mxo = at::empty({T, H}, tx.options()));
-    if (!th && w.tn) th = &(mh = at::empty({T, H}, like.options()));
+    if (!txo && ty) txo = &(mxo = make({T, H}, tx.options(), st));
+    if (!th && w.tn) th = &(mh = make({T, H}, like.options(), st));
     same_type(txo, tx.scalar_type(), "x_out");
     same_type(th, like.scalar_type(), "h");
     const int dx = dtype_code(tx), dy = dtype_code(like);
@@ -314,8 +323,8 @@ PyObject* block_norm_backward(PyObject*, PyObject* args, PyObject* kw) {
     const at::Tensor& like = ty ? *ty : tdh ? *tdh : tx;
     const auto f32 = tx.options().dtype(at::kFloat);
     at::Tensor mdx, mdy, mdp, mdg, mdn, mws;
-    const at::Tensor *tdx = either(dx, "d_x", mdx, {T, H}, tx.options()), *tdy = tensor(dy, "d_y");
-    if (!tdy && ty) tdy = &(mdy = at::empty({T, H}, ty->options()));
+    const at::Tensor *tdx = either(dx, "d_x", mdx, {T, H}, tx.options(), st), *tdy = tensor(dy, "d_y");
+    if (!tdy && ty) tdy = &(mdy = make({T, H}, ty->options(), st));
     same_type(tdu, tx.scalar_type(), "d_x_out");
     same_type(tdh, like.scalar_type(), "d_h");
     same_type(tdx, tx.scalar_type(), "d_x");
@@ -324,14 +333,14 @@ PyObject* block_norm_backward(PyObject*, PyObject* args, PyObject* kw) {
     const Rows rx = rows(&tx, T, H, "x"), ry = rows(ty, T, H, "y"), ru = rows(tdu, T, H, "d_x_out"),
                rh = rows(tdh, T, H, "d_h"), rdx = rows(tdx, T, H, "d_x"), rdy = rows(tdy, T, H, "d_y");
     float *pp = nullptr, *pg = nullptr, *pn = nullptr;
-    if (w.tp) pp = (float*)dense(either(dp, "d_post_weight", mdp, {H}, f32), {H}, at::kFloat, "d_post_weight");
-    if (w.mode == MOE_GATE_CHANNEL) pg = (float*)dense(either(dg, "d_gate", mdg, {H}, f32), {H}, at::kFloat, "d_gate");
+    if (w.tp) pp = (float*)dense(either(dp, "d_post_weight", mdp, {H}, f32, st), {H}, at::kFloat, "d_post_weight");
+    if (w.mode == MOE_GATE_CHANNEL) pg = (float*)dense(either(dg, "d_gate", mdg, {H}, f32, st), {H}, at::kFloat, "d_gate");
     if (w.mode == MOE_GATE_TOKEN)
-      pg = (float*)dense(either(dg, "d_gate", mdg, {T, 1}, f32), {T, 1}, at::kFloat, "d_gate");
-    if (w.tn) pn = (float*)dense(either(dn, "d_next_weight", mdn, {H}, f32), {H}, at::kFloat, "d_next_weight");
+      pg = (float*)dense(either(dg, "d_gate", mdg, {T, 1}, f32, st), {T, 1}, at::kFloat, "d_gate");
+    if (w.tn) pn = (float*)dense(either(dn, "d_next_weight", mdn, {H}, f32, st), {H}, at::kFloat, "d_next_weight");
     const cudaStream_t s = stream_of(st);
     const at::Tensor* tws = tensor(ws, "workspace");
-    if (!tws) tws = &(mws = scratch((int64_t)moe_block_norm_backward_workspace(T, H), tx, st, s));
+    if (!tws) tws = &(mws = make((int64_t)moe_block_norm_backward_workspace(T, H), tx.options().dtype(at::kByte), st, false));
     if (!tws->is_contiguous()) {
       PyErr_SetString(PyExc_ValueError, "workspace is not contiguous");
       throw Refused();
@@ -366,12 +375,6 @@ PyObject* adapter_linear(PyObject*, PyObject* args, PyObject* kw) {
     const float* ps = nullptr;
     size_t nb = 0;
     at::Tensor mws, mout;
-    cudaStream_t s = nullptr;
-    bool asked = false;
-    auto stream = [&] {   // once the arguments before it have passed
-      if (!asked) s = stream_of(st), asked = true;
-      return s;
-    };
     if (const at::Tensor* ta = tensor(la, "lora_a")) {
       if (ta->dim() != 3) {
         PyErr_Format(PyExc_ValueError, "lora_a must be [n, R, %d], got %s", H, shape_text(ta->sizes()).c_str());
@@ -383,7 +386,8 @@ PyObject* adapter_linear(PyObject*, PyObject* args, PyObject* kw) {
       pi = (const int32_t*)dense(&needed(ids, "adapter_ids"), {T}, at::kInt, "adapter_ids");
       ps = (const float*)dense(tensor(ls, "lora_scale"), {n}, at::kFloat, "lora_scale");
       const at::Tensor* tws = tensor(ws, "workspace");
-      if (!tws) tws = &(mws = scratch((int64_t)moe_adapter_linear_workspace(T, H, N, n, R), tx, st, stream()));
+      if (!tws)
+        tws = &(mws = make((int64_t)moe_adapter_linear_workspace(T, H, N, n, R), tx.options().dtype(at::kByte), st, false));
       if (!tws->is_contiguous()) {
         PyErr_SetString(PyExc_ValueError, "workspace is not contiguous");
         throw Refused();
@@ -397,12 +401,12 @@ PyObject* adapter_linear(PyObject*, PyObject* args, PyObject* kw) {
         throw Refused();
       }
       const at::ScalarType t = od && od != Py_None ? reinterpret_cast<THPDtype*>(od)->scalar_type : d;
-      to = &(mout = at::empty({T, N}, tx.options().dtype(t)));
+      to = &(mout = make({T, N}, tx.options().dtype(t), st));
     }
     const int xd = dtype_code(tx), ot = dtype_code(*to);
     const Rows ro = rows(to, T, N, "out");
     auto* pe = (int32_t*)dense(tensor(err, "d_error"), {1}, at::kInt, "d_error");
-    stream();
+    const cudaStream_t s = stream_of(st);
     check(unlocked([&] {
       return moe_adapter_linear(T, H, N, xd, ot, rx.p, rx.ld, rw.p, rw.ld, n, R, pa, pb, pi, ps, ro.p, ro.ld, pws, nb,
                                 pe, s);

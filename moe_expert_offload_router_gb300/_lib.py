@@ -502,7 +502,7 @@ def moe_rms_carry(y, eps: float, x_next, stream=None):
 # argument checks are compiled (csrc/binding.cpp) into functions of these names.
 from . import _binding  # noqa: E402  (needs torch's libraries and the library above loaded)
 
-_binding.set_check(_check)
+_binding.set_check(_check, MoeError)
 moe_route = _binding.moe_route
 moe_route_backward = _binding.moe_route_backward
 moe_block_norm = _binding.moe_block_norm

@@ -22,6 +22,16 @@ namespace {
 struct Refused {};   // the Python error is set
 
 PyObject* g_check = nullptr;   // _lib._check: raises MoeError for a status
+PyObject* g_error = nullptr;   // _lib.MoeError
+
+// Raises MoeError(MOE_ERR_INVALID, why).
+[[noreturn]] void refuse(const std::string& why) {
+  if (PyObject* e = PyObject_CallFunction(g_error, "is", (int)MOE_ERR_INVALID, why.c_str())) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+  throw Refused();
+}
 
 std::string shape_text(at::IntArrayRef s) {
   std::string r = "(";
@@ -74,12 +84,30 @@ void same_type(const at::Tensor* t, at::ScalarType d, const char* what) {
   }
 }
 
+// The tensors of a call, in the order in which they pass their own checks.
+struct Tensors {
+  const at::Tensor* t[20];
+  const char* what[20];
+  int n = 0;
+  void add(const at::Tensor* a, const char* name) {
+    if (n < 20) t[n] = a, what[n++] = name;
+  }
+  // Every tensor is on the first one's GPU: the kernels would read a host address as their own.
+  void on_one_gpu() const {
+    for (int i = 0; i < n; ++i) {
+      if (t[i]->is_cuda() && t[i]->device() == t[0]->device()) continue;
+      refuse(std::string(what[i]) + (t[i]->is_cuda() ? " is on another GPU than " + std::string(what[0])
+                                                     : " is not on a GPU (" + t[i]->device().str() + ")"));
+    }
+  }
+};
+
 struct Rows {
   void* p = nullptr;
   int64_t ld = 0;
 };
 // A [T, n] tensor whose rows may be strided (null: none).
-Rows rows(const at::Tensor* t, int64_t T, int64_t n, const char* what) {
+Rows rows(Tensors& all, const at::Tensor* t, int64_t T, int64_t n, const char* what) {
   if (!t) return {};
   if (t->dim() != 2 || t->size(0) != T || t->size(1) != n) {
     PyErr_Format(PyExc_ValueError, "%s must be [%lld, %lld], got %s", what, (long long)T, (long long)n,
@@ -99,10 +127,11 @@ Rows rows(const at::Tensor* t, int64_t T, int64_t n, const char* what) {
     }
     sr = n;
   }
+  all.add(t, what);
   return {t->data_ptr(), sr};
 }
 // A dense tensor of the given shape and type (null: none).
-void* dense(const at::Tensor* t, std::initializer_list<int64_t> shape, at::ScalarType d, const char* what) {
+void* dense(Tensors& all, const at::Tensor* t, std::initializer_list<int64_t> shape, at::ScalarType d, const char* what) {
   if (!t) return nullptr;
   const at::IntArrayRef want(shape.begin(), shape.size());
   if (t->sizes() != want || t->scalar_type() != d) {
@@ -115,6 +144,17 @@ void* dense(const at::Tensor* t, std::initializer_list<int64_t> shape, at::Scala
                  shape_text(t->sizes()).c_str(), shape_text(t->strides()).c_str());
     throw Refused();
   }
+  all.add(t, what);
+  return t->data_ptr();
+}
+// A workspace's address and bytes.
+void* space(Tensors& all, const at::Tensor* t, size_t& bytes) {
+  if (!t->is_contiguous()) {
+    PyErr_SetString(PyExc_ValueError, "workspace is not contiguous");
+    throw Refused();
+  }
+  all.add(t, "workspace");
+  bytes = t->nbytes();
   return t->data_ptr();
 }
 int to_int(int64_t v, const char* what) {
@@ -134,6 +174,17 @@ cudaStream_t stream_of(PyObject* o) {
   if (!p && PyErr_Occurred()) throw Refused();
   return (cudaStream_t)p;
 }
+
+// Where a call runs, once its arguments have passed their own checks: on its tensors' GPU.
+struct Place {
+  c10::cuda::OptionalCUDAGuard gpu;
+  cudaStream_t stream;
+  Place(const Tensors& all, PyObject* stream_arg) {
+    all.on_one_gpu();
+    gpu.set_device(all.t[0]->device());
+    stream = stream_of(stream_arg);
+  }
+};
 
 // Tensors that the caller did not bring: held, and handed out as results.
 struct Results {
@@ -194,9 +245,9 @@ const at::Tensor* either(PyObject* given, const char* what, at::Tensor& made, at
   return &made;
 }
 
-const uint8_t* mask_ptr(PyObject* o, int64_t T) {
+const uint8_t* mask_ptr(Tensors& all, PyObject* o, int64_t T) {
   const at::Tensor* m = tensor(o, "token_mask");
-  return (const uint8_t*)dense(m, {T}, m && m->scalar_type() == at::kBool ? at::kBool : at::kByte, "token_mask");
+  return (const uint8_t*)dense(all, m, {T}, m && m->scalar_type() == at::kBool ? at::kBool : at::kByte, "token_mask");
 }
 
 PyObject* route(PyObject*, PyObject* args, PyObject* kw) {
@@ -209,20 +260,21 @@ PyObject* route(PyObject*, PyObject* args, PyObject* kw) {
                                    &gs, &renorm, &scale, &mask, &ids, &w, &load, &st))
     return nullptr;
   return guarded([&] {
+    Tensors all;
     const at::Tensor& lg = matrix(logits, "logits");
     const int T = to_int(lg.size(0), "T"), E = to_int(lg.size(1), "E"), d = dtype_code(lg);
     at::Tensor mi, mw;
     const at::Tensor* ti = either(ids, "topk_ids", mi, {T, k}, lg.options().dtype(at::kInt), st);
     const at::Tensor* tw = either(w, "topk_w", mw, {T, k}, lg.options().dtype(at::kFloat), st);
-    const Rows r = rows(&lg, T, E, "logits");
-    auto* pb = (const float*)dense(tensor(bias, "bias"), {E}, at::kFloat, "bias");
-    auto* pm = mask_ptr(mask, T);
-    auto* pi = (int32_t*)dense(ti, {T, k}, at::kInt, "topk_ids");
-    auto* pw = (float*)dense(tw, {T, k}, at::kFloat, "topk_w");
-    auto* pl = (int32_t*)dense(tensor(load, "load"), {E}, at::kInt, "load");
-    const cudaStream_t s = stream_of(st);
+    const Rows r = rows(all, &lg, T, E, "logits");
+    auto* pb = (const float*)dense(all, tensor(bias, "bias"), {E}, at::kFloat, "bias");
+    auto* pm = mask_ptr(all, mask, T);
+    auto* pi = (int32_t*)dense(all, ti, {T, k}, at::kInt, "topk_ids");
+    auto* pw = (float*)dense(all, tw, {T, k}, at::kFloat, "topk_w");
+    auto* pl = (int32_t*)dense(all, tensor(load, "load"), {E}, at::kInt, "load");
+    const Place at(all, st);
     check(unlocked([&] {
-      return moe_route(r.p, d, r.ld, T, E, k, score, pb, ng, tg, gs, renorm, (float)scale, pm, pi, pw, pl, s);
+      return moe_route(r.p, d, r.ld, T, E, k, score, pb, ng, tg, gs, renorm, (float)scale, pm, pi, pw, pl, at.stream);
     }));
     return Py_BuildValue("(NN)", Results::of(ids, mi), Results::of(w, mw));
   });
@@ -238,18 +290,19 @@ PyObject* route_backward(PyObject*, PyObject* args, PyObject* kw) {
                                    &mask, &dl, &st))
     return nullptr;
   return guarded([&] {
+    Tensors all;
     const at::Tensor &lg = matrix(logits, "logits"), &ti = matrix(ids, "topk_ids");
     const int T = to_int(lg.size(0), "T"), E = to_int(lg.size(1), "E"), k = to_int(ti.size(1), "k"), d = dtype_code(lg);
     at::Tensor made;
     const at::Tensor* td = either(dl, "d_logits", made, {T, E}, lg.options(), st);
     same_type(td, lg.scalar_type(), "d_logits");
-    const Rows r = rows(&lg, T, E, "logits"), rd = rows(td, T, E, "d_logits");
-    auto* pm = mask_ptr(mask, T);
-    auto* pi = (const int32_t*)dense(&ti, {T, k}, at::kInt, "topk_ids");
-    auto* pd = (const float*)dense(&needed(dw, "d_w"), {T, k}, at::kFloat, "d_w");
-    const cudaStream_t s = stream_of(st);
+    const Rows r = rows(all, &lg, T, E, "logits"), rd = rows(all, td, T, E, "d_logits");
+    auto* pm = mask_ptr(all, mask, T);
+    auto* pi = (const int32_t*)dense(all, &ti, {T, k}, at::kInt, "topk_ids");
+    auto* pd = (const float*)dense(all, &needed(dw, "d_w"), {T, k}, at::kFloat, "d_w");
+    const Place at(all, st);
     check(unlocked([&] {
-      return moe_route_backward(r.p, d, r.ld, T, E, k, score, renorm, (float)scale, pm, pi, pd, rd.p, rd.ld, s);
+      return moe_route_backward(r.p, d, r.ld, T, E, k, score, renorm, (float)scale, pm, pi, pd, rd.p, rd.ld, at.stream);
     }));
     return Results::of(dl, made);
   });
@@ -260,16 +313,16 @@ struct NormWeights {
   int dtype = MOE_DT_F32, mode = MOE_GATE_NONE;
   const at::Tensor *tp, *tg, *tn;
   void *post, *gate, *next;
-  NormWeights(PyObject* p, PyObject* g, PyObject* n, int64_t T, int64_t H) {
+  NormWeights(Tensors& all, PyObject* p, PyObject* g, PyObject* n, int64_t T, int64_t H) {
     tp = tensor(p, "post_weight"), tg = tensor(g, "gate"), tn = tensor(n, "next_weight");
     const at::Tensor* first = tp ? tp : tg ? tg : tn;
     if (first) dtype = dtype_code(*first);
     const at::ScalarType d = first ? first->scalar_type() : at::kFloat;
-    post = dense(tp, {H}, d, "post_weight");
+    post = dense(all, tp, {H}, d, "post_weight");
     if (tg) mode = tg->dim() == 1 ? MOE_GATE_CHANNEL : MOE_GATE_TOKEN;   // [H]: each channel; [T, 1]: each token
-    gate = mode == MOE_GATE_TOKEN ? dense(tg, {T, 1}, d, "gate (of the weights' one type)")
-                                  : dense(tg, {H}, d, "gate (of the weights' one type)");
-    next = dense(tn, {H}, d, "next_weight (of the weights' one type)");
+    gate = mode == MOE_GATE_TOKEN ? dense(all, tg, {T, 1}, d, "gate (of the weights' one type)")
+                                  : dense(all, tg, {H}, d, "gate (of the weights' one type)");
+    next = dense(all, tn, {H}, d, "next_weight (of the weights' one type)");
   }
 };
 
@@ -283,9 +336,11 @@ PyObject* block_norm(PyObject*, PyObject* args, PyObject* kw) {
                                    &xo, &h, &st))
     return nullptr;
   return guarded([&] {
+    Tensors all;
     const at::Tensor& tx = matrix(x, "x");
     const int T = to_int(tx.size(0), "T"), H = to_int(tx.size(1), "H");
-    const NormWeights w(post, gate, next, T, H);
+    all.add(&tx, "x");   // first: the call runs on its GPU
+    const NormWeights w(all, post, gate, next, T, H);
     const at::Tensor *ty = tensor(y, "y"), *th = tensor(h, "h"), *txo = tensor(xo, "x_out");
     const at::Tensor& like = ty ? *ty : th ? *th : tx;
     at::Tensor mxo, mh;
@@ -294,12 +349,12 @@ PyObject* block_norm(PyObject*, PyObject* args, PyObject* kw) {
     same_type(txo, tx.scalar_type(), "x_out");
     same_type(th, like.scalar_type(), "h");
     const int dx = dtype_code(tx), dy = dtype_code(like);
-    const Rows rx = rows(&tx, T, H, "x"), ry = rows(ty, T, H, "y"), ro = rows(txo, T, H, "x_out"),
-               rh = rows(th, T, H, "h");
-    const cudaStream_t s = stream_of(st);
+    const Rows rx = rows(all, &tx, T, H, "x"), ry = rows(all, ty, T, H, "y"), ro = rows(all, txo, T, H, "x_out"),
+               rh = rows(all, th, T, H, "h");
+    const Place at(all, st);
     check(unlocked([&] {
       return moe_block_norm(T, H, dx, dy, w.dtype, rx.p, rx.ld, ry.p, ry.ld, w.post, w.gate, w.mode, (float)alpha,
-                            w.next, (float)eps, ro.p, ro.ld, rh.p, rh.ld, s);
+                            w.next, (float)eps, ro.p, ro.ld, rh.p, rh.ld, at.stream);
     }));
     return Py_BuildValue("(NN)", Results::of(xo, mxo), Results::of(h, mh));
   });
@@ -316,9 +371,11 @@ PyObject* block_norm_backward(PyObject*, PyObject* args, PyObject* kw) {
                                    &next, &eps, &dx, &dy, &dp, &dg, &dn, &ws, &st))
     return nullptr;
   return guarded([&] {
+    Tensors all;
     const at::Tensor& tx = matrix(x, "x");
     const int T = to_int(tx.size(0), "T"), H = to_int(tx.size(1), "H");
-    const NormWeights w(post, gate, next, T, H);
+    all.add(&tx, "x");   // first: the call runs on its GPU
+    const NormWeights w(all, post, gate, next, T, H);
     const at::Tensor *ty = tensor(y, "y"), *tdu = tensor(du, "d_x_out"), *tdh = tensor(dh, "d_h");
     const at::Tensor& like = ty ? *ty : tdh ? *tdh : tx;
     const auto f32 = tx.options().dtype(at::kFloat);
@@ -330,25 +387,24 @@ PyObject* block_norm_backward(PyObject*, PyObject* args, PyObject* kw) {
     same_type(tdx, tx.scalar_type(), "d_x");
     same_type(tdy, like.scalar_type(), "d_y");
     const int xd = dtype_code(tx), yd = dtype_code(like);
-    const Rows rx = rows(&tx, T, H, "x"), ry = rows(ty, T, H, "y"), ru = rows(tdu, T, H, "d_x_out"),
-               rh = rows(tdh, T, H, "d_h"), rdx = rows(tdx, T, H, "d_x"), rdy = rows(tdy, T, H, "d_y");
+    const Rows rx = rows(all, &tx, T, H, "x"), ry = rows(all, ty, T, H, "y"), ru = rows(all, tdu, T, H, "d_x_out"),
+               rh = rows(all, tdh, T, H, "d_h"), rdx = rows(all, tdx, T, H, "d_x"), rdy = rows(all, tdy, T, H, "d_y");
     float *pp = nullptr, *pg = nullptr, *pn = nullptr;
-    if (w.tp) pp = (float*)dense(either(dp, "d_post_weight", mdp, {H}, f32, st), {H}, at::kFloat, "d_post_weight");
-    if (w.mode == MOE_GATE_CHANNEL) pg = (float*)dense(either(dg, "d_gate", mdg, {H}, f32, st), {H}, at::kFloat, "d_gate");
+    if (w.tp) pp = (float*)dense(all, either(dp, "d_post_weight", mdp, {H}, f32, st), {H}, at::kFloat, "d_post_weight");
+    if (w.mode == MOE_GATE_CHANNEL) pg = (float*)dense(all, either(dg, "d_gate", mdg, {H}, f32, st), {H}, at::kFloat, "d_gate");
     if (w.mode == MOE_GATE_TOKEN)
-      pg = (float*)dense(either(dg, "d_gate", mdg, {T, 1}, f32, st), {T, 1}, at::kFloat, "d_gate");
-    if (w.tn) pn = (float*)dense(either(dn, "d_next_weight", mdn, {H}, f32, st), {H}, at::kFloat, "d_next_weight");
-    const cudaStream_t s = stream_of(st);
+      pg = (float*)dense(all, either(dg, "d_gate", mdg, {T, 1}, f32, st), {T, 1}, at::kFloat, "d_gate");
+    if (w.tn) pn = (float*)dense(all, either(dn, "d_next_weight", mdn, {H}, f32, st), {H}, at::kFloat, "d_next_weight");
+    const Place at(all, st);
     const at::Tensor* tws = tensor(ws, "workspace");
     if (!tws) tws = &(mws = make((int64_t)moe_block_norm_backward_workspace(T, H), tx.options().dtype(at::kByte), st, false));
-    if (!tws->is_contiguous()) {
-      PyErr_SetString(PyExc_ValueError, "workspace is not contiguous");
-      throw Refused();
-    }
+    size_t nb;
+    void* pws = space(all, tws, nb);
+    all.on_one_gpu();
     check(unlocked([&] {
       return moe_block_norm_backward(T, H, xd, yd, w.dtype, rx.p, rx.ld, ry.p, ry.ld, ru.p, ru.ld, rh.p, rh.ld, w.post,
                                      w.gate, w.mode, (float)alpha, w.next, (float)eps, rdx.p, rdx.ld, rdy.p, rdy.ld, pp,
-                                     pg, pn, tws->data_ptr(), tws->nbytes(), s);
+                                     pg, pn, pws, nb, at.stream);
     }));
     return Py_BuildValue("(NNNNN)", Results::of(dx, mdx), Results::of(dy, mdy), Results::of(w.tp ? dp : Py_None, mdp),
                          Results::of(w.tg ? dg : Py_None, mdg), Results::of(w.tn ? dn : Py_None, mdn));
@@ -364,10 +420,11 @@ PyObject* adapter_linear(PyObject*, PyObject* args, PyObject* kw) {
                                    &ws, &err, &st))
     return nullptr;
   return guarded([&] {
+    Tensors all;
     const at::Tensor &tx = matrix(x, "x"), &tw = matrix(wt, "weight");
     const int T = to_int(tx.size(0), "T"), H = to_int(tx.size(1), "H"), N = to_int(tw.size(0), "N");
     const at::ScalarType d = tx.scalar_type();
-    const Rows rx = rows(&tx, T, H, "x"), rw = rows(&tw, N, H, "weight");
+    const Rows rx = rows(all, &tx, T, H, "x"), rw = rows(all, &tw, N, H, "weight");
     same_type(&tw, d, "weight (as x)");
     int n = 0, R = 0;
     void *pa = nullptr, *pb = nullptr, *pws = nullptr;
@@ -381,18 +438,10 @@ PyObject* adapter_linear(PyObject*, PyObject* args, PyObject* kw) {
         throw Refused();
       }
       n = to_int(ta->size(0), "n"), R = to_int(ta->size(1), "R");
-      pa = dense(ta, {n, R, H}, d, "lora_a");
-      pb = dense(&needed(lb, "lora_b"), {n, N, R}, d, "lora_b");
-      pi = (const int32_t*)dense(&needed(ids, "adapter_ids"), {T}, at::kInt, "adapter_ids");
-      ps = (const float*)dense(tensor(ls, "lora_scale"), {n}, at::kFloat, "lora_scale");
-      const at::Tensor* tws = tensor(ws, "workspace");
-      if (!tws)
-        tws = &(mws = make((int64_t)moe_adapter_linear_workspace(T, H, N, n, R), tx.options().dtype(at::kByte), st, false));
-      if (!tws->is_contiguous()) {
-        PyErr_SetString(PyExc_ValueError, "workspace is not contiguous");
-        throw Refused();
-      }
-      pws = tws->data_ptr(), nb = tws->nbytes();
+      pa = dense(all, ta, {n, R, H}, d, "lora_a");
+      pb = dense(all, &needed(lb, "lora_b"), {n, N, R}, d, "lora_b");
+      pi = (const int32_t*)dense(all, &needed(ids, "adapter_ids"), {T}, at::kInt, "adapter_ids");
+      ps = (const float*)dense(all, tensor(ls, "lora_scale"), {n}, at::kFloat, "lora_scale");
     }
     const at::Tensor* to = tensor(out, "out");
     if (!to) {
@@ -404,19 +453,29 @@ PyObject* adapter_linear(PyObject*, PyObject* args, PyObject* kw) {
       to = &(mout = make({T, N}, tx.options().dtype(t), st));
     }
     const int xd = dtype_code(tx), ot = dtype_code(*to);
-    const Rows ro = rows(to, T, N, "out");
-    auto* pe = (int32_t*)dense(tensor(err, "d_error"), {1}, at::kInt, "d_error");
-    const cudaStream_t s = stream_of(st);
+    const Rows ro = rows(all, to, T, N, "out");
+    auto* pe = (int32_t*)dense(all, tensor(err, "d_error"), {1}, at::kInt, "d_error");
+    const Place at(all, st);
+    if (n) {
+      const at::Tensor* tws = tensor(ws, "workspace");
+      if (!tws)
+        tws = &(mws = make((int64_t)moe_adapter_linear_workspace(T, H, N, n, R), tx.options().dtype(at::kByte), st, false));
+      pws = space(all, tws, nb);
+      all.on_one_gpu();
+    }
     check(unlocked([&] {
       return moe_adapter_linear(T, H, N, xd, ot, rx.p, rx.ld, rw.p, rw.ld, n, R, pa, pb, pi, ps, ro.p, ro.ld, pws, nb,
-                                pe, s);
+                                pe, at.stream);
     }));
     return Results::of(out, mout);
   });
 }
 
-PyObject* set_check(PyObject*, PyObject* f) {
+PyObject* set_check(PyObject*, PyObject* args) {
+  PyObject *f, *e;
+  if (!PyArg_ParseTuple(args, "OO", &f, &e)) return nullptr;
   Py_XSETREF(g_check, Py_NewRef(f));
+  Py_XSETREF(g_error, Py_NewRef(e));
   Py_RETURN_NONE;
 }
 
@@ -448,7 +507,7 @@ PyMethodDef methods[] = {
      "out [T, N] = x weight^T + lora_scale[a] (x lora_a[a]^T) lora_b[a]^T, a = adapter_ids[t] (< 0: none).\n\n"
      "x [T, H] and weight [N, H] (rows may be strided), lora_a [n, R, H], lora_b [n, N, R], all bf16 or all f16; out\n"
      "of x's type or fp32.  Without lora_a the projection alone."},
-    {"set_check", set_check, METH_O, "The function that raises for a status other than MOE_OK."},
+    {"set_check", set_check, METH_VARARGS, "The function that raises for a status other than MOE_OK, and what it raises."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Compiled entry points of short calls.", -1, methods};
 

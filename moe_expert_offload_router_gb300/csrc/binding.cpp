@@ -120,12 +120,11 @@ Rows rows(Tensors& all, const at::Tensor* t, int64_t T, int64_t n, const char* w
                  shape_text(t->strides()).c_str());
     throw Refused();
   }
-  if (sr < n) {
-    if (T > 1) {
-      PyErr_Format(PyExc_ValueError, "%s: rows overlap (strides %s)", what, shape_text(t->strides()).c_str());
-      throw Refused();
-    }
-    sr = n;
+  if (T <= 1) {
+    sr = n;   // one row: the distance to the next is not used, whatever tensor it was taken from
+  } else if (sr < n) {
+    PyErr_Format(PyExc_ValueError, "%s: rows overlap (strides %s)", what, shape_text(t->strides()).c_str());
+    throw Refused();
   }
   all.add(t, what);
   return {t->data_ptr(), sr};

@@ -263,13 +263,14 @@ PyObject* route(PyObject*, PyObject* args, PyObject* kw) {
     const at::Tensor& lg = matrix(logits, "logits");
     const int T = to_int(lg.size(0), "T"), E = to_int(lg.size(1), "E"), d = dtype_code(lg);
     at::Tensor mi, mw;
-    const at::Tensor* ti = either(ids, "topk_ids", mi, {T, k}, lg.options().dtype(at::kInt), st);
-    const at::Tensor* tw = either(w, "topk_w", mw, {T, k}, lg.options().dtype(at::kFloat), st);
+    const int64_t made = k >= 0 && k <= E ? k : 0;   // any other k is refused by the library
+    const at::Tensor* ti = either(ids, "topk_ids", mi, {T, made}, lg.options().dtype(at::kInt), st);
+    const at::Tensor* tw = either(w, "topk_w", mw, {T, made}, lg.options().dtype(at::kFloat), st);
     const Rows r = rows(all, &lg, T, E, "logits");
     auto* pb = (const float*)dense(all, tensor(bias, "bias"), {E}, at::kFloat, "bias");
     auto* pm = mask_ptr(all, mask, T);
-    auto* pi = (int32_t*)dense(all, ti, {T, k}, at::kInt, "topk_ids");
-    auto* pw = (float*)dense(all, tw, {T, k}, at::kFloat, "topk_w");
+    auto* pi = (int32_t*)dense(all, ti, {T, mi.defined() ? made : k}, at::kInt, "topk_ids");
+    auto* pw = (float*)dense(all, tw, {T, mw.defined() ? made : k}, at::kFloat, "topk_w");
     auto* pl = (int32_t*)dense(all, tensor(load, "load"), {E}, at::kInt, "load");
     const Place at(all, st);
     check(unlocked([&] {

@@ -34,3 +34,10 @@ def test_route_groups_of_the_lowest_bias(E, G, score, group):
         rest = np.arange(gs) if t != 1 else 2 * gs + np.arange(gs)
         assert ids[t].tolist() == np.concatenate([first, rest])[:k].tolist()
     assert torch.isfinite(w).all()
+
+
+@pytest.mark.parametrize("k", [-1, 0, 17, 33, 2 ** 31 - 1])
+def test_route_refuses_a_k_out_of_range_as_the_library_does(k):
+    M = load_lib()
+    with pytest.raises(M.MoeError, match="k must be"):
+        M.moe_route(torch.zeros(4, 16, device="cuda"), k)

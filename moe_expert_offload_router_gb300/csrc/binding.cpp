@@ -5,6 +5,7 @@
 #include <Python.h>
 
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
@@ -231,8 +232,8 @@ PyObject* guarded(F f) {
   try {
     return f();
   } catch (const Refused&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {   // torch's own errors keep their Python types (out of memory among them)
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -45,3 +45,11 @@ def test_one_tensor_left_on_the_host(name):
             assert e.value.status == M.MOE_ERR_INVALID
     f(**good)
     torch.cuda.synchronize()
+
+
+def test_a_result_that_does_not_fit_raises_torchs_error():
+    # 4 TB of fp32 results
+    M = load_lib()
+    x, W = (torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda") for n in (1 << 20, 1 << 20))
+    with pytest.raises(torch.OutOfMemoryError):
+        M.moe_adapter_linear(x, W, out_dtype=torch.float32)

@@ -17,6 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 BINDING = os.path.join(PKG, "_binding.so")
+MADE_FOR = os.path.join(BUILD, "binding_made_for.txt")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -75,27 +76,47 @@ def _link_binding(obj: str):
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every source and link the shared libraries; returns the C library's path."""
-    srcs = sources()
-    hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hdrs.append(os.path.join(INCLUDE, "moe_gb300.h"))
-    if not force and os.path.exists(LIB) and os.path.exists(BINDING):
-        newest = max(os.path.getmtime(p) for p in srcs + hdrs + [os.path.join(CSRC, "binding.cpp"), __file__])
-        if min(os.path.getmtime(LIB), os.path.getmtime(BINDING)) >= newest:
-            return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
-        bound = ex.submit(_compile_binding)
-        objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding = bound.result()
+def _link(objs):
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libmoe_gb300.so", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def _made_for() -> str:
+    """The Python and the torch that a binding is compiled for (it uses their C and C++ interfaces)."""
+    import importlib.metadata as md
+    import importlib.util as iu
+    spec = iu.find_spec("torch")
+    return "\n".join([sys.version, md.version("torch"), spec.origin if spec else "", ""])
+
+
+def _newer(out: str, inputs) -> bool:
+    return os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(p) for p in inputs)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile every source and link the shared libraries; returns the C library's path."""
+    srcs = sources()
+    hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    hdrs.append(os.path.join(INCLUDE, "moe_gb300.h"))
+    made_for = _made_for()
+    lib = not force and _newer(LIB, srcs + hdrs + [__file__])
+    if (lib and _newer(BINDING, hdrs + [os.path.join(CSRC, "binding.cpp"), __file__, LIB])
+            and os.path.exists(MADE_FOR) and open(MADE_FOR).read() == made_for):
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
+        bound = ex.submit(_compile_binding)
+        objs = [] if lib else list(ex.map(lambda s: _compile(s, verbose), srcs))
+        binding = bound.result()
+    if not lib:
+        _link(objs)
     _link_binding(binding)
+    with open(MADE_FOR, "w") as f:
+        f.write(made_for)
     return LIB
 
 

@@ -45,28 +45,85 @@ def test_adapter_linear_f16_small_and_ordinary_tokens_side_by_side():
     _check(M, d, "f16", "f32", rows=400)
 
 
-@pytest.mark.parametrize("T", [5, 100, 1300])
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("ids", ["mixed", "runs"])
-def test_adapter_linear_bits_of_a_x(T, dtype, ids):
-    """A picks single elements of x and B single ranks, by 1: a result is c x[j], whose product is rounded to fp32
-    (2^-24), cut to the terms' bits (none of bf16's 24; of f16's two 2^-22 of the token's largest) and added up from
-    them (2^-23)."""
+def test_adapter_linear_nan_stays_with_its_adapter_large(out, ids):
     M = load_lib()
-    d = _data(T, T, 256, N, 16, 4, dtype, ids)
-    for m in ("W", "A", "B"):
-        d[m].zero_()
-    pick = torch.randint(0, 256, (4, 16), device="cuda")
-    d["A"].scatter_(2, pick[..., None], 1.0)
-    rank = torch.arange(N, device="cuda") % 16
-    d["B"][:, torch.arange(N, device="cuda"), rank] = 1.0
-    got = _call(M, d, "f32").double()
-    a = d["ids"].long().clamp(min=0)
-    ref = torch.where(d["ids"][:, None] >= 0, d["c"].double()[a][:, None] * d["x"].double().gather(1, pick[a])[:, rank], 0.0)
-    tol = 2.0 ** -22 * ref.abs()
-    if dtype == "f16":
-        tol = tol + 2.0 ** -22 * ref.abs().amax(1, keepdim=True)
-    assert torch.all((got - ref).abs() <= tol)
+    d = _data(4, T, 256, N, 16, 4, "bf16", ids)
+    want = _call(M, d, out)
+    d["A"][1] = float("nan")
+    d["B"][2] = float("inf")
+    got = _call(M, d, out)
+    ok = (d["ids"] != 1) & (d["ids"] != 2)
+    assert torch.equal(got[ok], want[ok]) and torch.isnan(got[d["ids"] == 1]).all()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+def test_adapter_linear_reports_an_id_out_of_range_large(out, ids):
+    M = load_lib()
+    d = _data(6, T, 256, N, 8, 3, "bf16", ids)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good = _call(M, d, out, d_error=err)
+    assert int(err) == M.MOE_OK
+    bad = d["ids"].clone()
+    bad[T // 2] = 3
+    got = _call(M, dict(d, ids=bad), out, d_error=err)
+    assert int(err) == M.MOE_ERR_INVALID
+    none = bad.clone()
+    none[T // 2] = -1
+    assert torch.equal(got, _call(M, dict(d, ids=none), out))
+    away = torch.arange(T, device="cuda") // 16 != T // 2 // 16   # its group is taken in another way
+    assert torch.equal(got[away], good[away])
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+def test_adapter_linear_strides_large(out, ids):
+    M = load_lib()
+    d = _data(5, T, 320, N, 16, 3, "bf16", ids, 16, 8)
+    want = _check(M, dict(d, x=d["x"].contiguous()), "bf16", out, rows=40)
+    wide_w = torch.zeros(N, 352, dtype=torch.bfloat16, device="cuda")
+    wide_w[:, 16:336] = d["W"]
+    wide = torch.full((T, N + 11), 3.0, dtype=DT[out], device="cuda")
+    M.moe_adapter_linear(d["x"], wide_w[:, 16:336], d["A"], d["B"], d["ids"], d["c"], out=wide[:, 7:N + 7])
+    assert torch.equal(wide[:, 7:N + 7], want)
+    assert (wide[:, :7] == 3).all() and (wide[:, N + 7:] == 3).all()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+def test_adapter_linear_on_another_stream_and_repeats_large(out, ids):
+    M = load_lib()
+    d = _data(7, T, 1024, N, 16, 5, "bf16", ids)
+    want = _call(M, d, out)
+    s = torch.cuda.Stream()
+    ws = torch.full((M.moe_adapter_linear_workspace(T, 1024, N, 5, 16),), 255, dtype=torch.uint8, device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    for w in (ws, ws):
+        got = torch.full_like(want, float("nan"))
+        s.wait_stream(torch.cuda.current_stream())
+        _call(M, d, out, out=got, workspace=w, stream=s)
+        s.synchronize()
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_adapter_linear_after_the_kernel_that_writes_x_large(out):
+    M = load_lib()
+    for ids in ("mixed", "runs"):
+        d = _data(8, T, 1024, N, 16, 8, "bf16", ids)
+        want = _call(M, d, out)
+        for _ in range(5):
+            late = dict(d, x=torch.zeros_like(d["x"]), ids=torch.full_like(d["ids"], -1))
+            got = torch.zeros_like(want)
+            torch.cuda._sleep(20000)
+            late["ids"].copy_(d["ids"])
+            late["x"].copy_(d["x"])
+            _call(M, late, out, out=got)
+            late["x"].zero_()
+            late["ids"].fill_(-1)
+            assert torch.equal(got, want)
 
 
 def _norms(M, d, out):
@@ -92,3 +149,27 @@ def test_adapter_linear_accuracy_in_fp32(T, N, dtype, ids):
     # what the adapters add by itself: no other term hides its error
     d["W"].zero_()
     assert _norms(M, d, "f32")[1] <= 1.6e-6
+
+
+@pytest.mark.parametrize("T", [5, 100, 1300])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+def test_adapter_linear_bits_of_a_x(T, dtype, ids):
+    """A picks single elements of x and B single ranks, by 1: a result is c x[j], whose product is rounded to fp32
+    (2^-24), cut to the terms' bits (none of bf16's 24; of f16's two 2^-22 of the token's largest) and added up from
+    them (2^-23)."""
+    M = load_lib()
+    d = _data(T, T, 256, N, 16, 4, dtype, ids)
+    for m in ("W", "A", "B"):
+        d[m].zero_()
+    pick = torch.randint(0, 256, (4, 16), device="cuda")
+    d["A"].scatter_(2, pick[..., None], 1.0)
+    rank = torch.arange(N, device="cuda") % 16
+    d["B"][:, torch.arange(N, device="cuda"), rank] = 1.0
+    got = _call(M, d, "f32").double()
+    a = d["ids"].long().clamp(min=0)
+    ref = torch.where(d["ids"][:, None] >= 0, d["c"].double()[a][:, None] * d["x"].double().gather(1, pick[a])[:, rank], 0.0)
+    tol = 2.0 ** -22 * ref.abs()
+    if dtype == "f16":
+        tol = tol + 2.0 ** -22 * ref.abs().amax(1, keepdim=True)
+    assert torch.all((got - ref).abs() <= tol)

@@ -717,7 +717,7 @@ constexpr int kShrinkSmem = kShrinkStages * kShrinkStage + 1024;
 constexpr int kShrinkAcc = 512 / kShrinkTokens;   // accumulators for fp32 results
 
 template <typename TE, bool F32>
-__global__ void __launch_bounds__(256) adapter_shrink_kernel(const __grid_constant__ CUtensorMap mA,
+__global__ void __launch_bounds__(256, 1) adapter_shrink_kernel(const __grid_constant__ CUtensorMap mA,
                                                              const __grid_constant__ CUtensorMap mX,
                                                              const LinearArgs a) {
   extern __shared__ uint8_t smem_raw[];

@@ -157,3 +157,22 @@ def test_routing_that_changes_between_calls(graph):
     assert counts == 6 * 5 * 4 and int(load.sum()) == counts
     assert len(runner.graphs) == int(graph)
     cache.close()
+
+
+def test_streamed_prefill_of_tokens_with_fewer_experts_than_k():
+    # padding is masked by logits of NaN or -inf: such a token takes part in nothing and its output is 0
+    M = load_lib()
+    wl = configs.scaled(configs.TINY, E=8, k=3, T=40, H=512, I=512)   # the grouped GEMM takes multiples of 512
+    bank, B = pinned_fp4_bank(wl, (0,))
+    ps = M.PrefillStreamer(bank, 1, 8, wl.H, wl.I, 3, 40, routing=M.Routing(scale=2.5))
+    ps.begin()
+    lg, x = gen.router_logits(wl, 0, 0, 40), gen.activations(wl, 0, 0, 40)
+    lg[::3] = np.nan
+    lg[1::6, 1:] = -np.inf
+    y = torch.full((40, wl.H), -1, dtype=torch.int16, device="cuda")
+    ps.run_layer(0, torch.from_numpy(lg).cuda(), torch.from_numpy(x.view(np.int16)).cuda(), y)
+    ps.synchronize()
+    ids, w, _ = O.route(lg, 3, "sigmoid", scale=2.5)
+    ref = moe_layer(x, ids, w, lambda e, tag: F.decode_fp4_expert(bank.numpy()[e * B:(e + 1) * B], wl.H, wl.I))
+    got = F.bf16_to_f64(y.cpu().numpy().view(np.uint16))
+    assert (got[::3] == 0).all() and _off(got, ref) <= TOL

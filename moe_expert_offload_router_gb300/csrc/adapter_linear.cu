@@ -3,8 +3,16 @@
 //
 // u (fp32 [T, R]) comes from a first kernel; the projection's kernel starts
 // beside it (programmatic dependent launch) and waits for it only before its
-// epilogue, where B[a] u is added in fp32 to the tokens that name a: an adapter touches
-// the tokens that name it and no others, whoever shares their tile.
+// epilogue or the steps that runs of one adapter add, where B[a] u is added to the
+// tokens that name a: an adapter touches the tokens that name it and no others,
+// whoever shares their tile.
+//
+// u enters that product as terms of x's type, its leading bits, the next ones, ...:
+// with fp16 two (22 bits of a token's largest value; scaled by a power of two, or
+// unscaled where they hold that many), with bf16 three (24 bits) for fp32 results and
+// two (16 bits) for 16-bit ones.  A third term there changes nothing that a bf16 result
+// can show: 4001 x 4096 x 4096, rank 32, is 1.662e-3 from 64 bits (its rounding) and
+// 1.46e-4 from the rounded exact result with two as with three, in 107.6 us and 109.6.
 //
 // The projection runs on tcgen05 (kind::f16, fp32 accumulators in tensor
 // memory) with the operands swapped: W's rows are the MMA's 128 rows and the
@@ -183,6 +191,10 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 // A tensor-core accumulator loses a little with every step (it truncates: 4.2e-6
 // of the result over 4096 products, 0.5e-6 over 512), so a result kept in fp32
 // takes at most this many 64-wide steps in one accumulator where there is room.
+// A 16-bit result takes one over all of H: 4.2e-6 is a four-hundredth of bf16's
+// rounding (1.66e-3) and a fiftieth of f16's (2.1e-4), while adding chunks up in
+// registers holds the persistent kernel's tiles to 128 tokens (4001 x 4096 x 4096
+// without adapters: fp32 results take 128 us, bf16 ones 80).
 constexpr int kF32Chunk = 8;
 constexpr int kRows = 128;          // outputs (W rows) of a tile
 constexpr int kATile = kRows * 128; // bytes of a 64-wide K step of W
@@ -554,7 +566,7 @@ __device__ __forceinline__ void adapter_tiles(const LinearArgs& a, AdapterTiles<
 // stages hold: with H / cluster <= 512 the whole share), multiplies it, puts its
 // fp32 sums into its own shared memory, and adds up the blocks' sums, in rank
 // order, for its share of the tokens.  64 tokens to 2048 outputs, H = 4096: 7.2 us
-// alone (19.5 MB), 11.9 with adapters; bound by what an SM takes in (W's 128 rows
+// alone (19.5 MB), 12.1 with adapters; bound by what an SM takes in (W's 128 rows
 // and x's 64 of 1024 columns: 390 KB) and the way there and back.
 template <typename TE, int NT>
 __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant__ CUtensorMap mW,
@@ -709,7 +721,8 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
 // rows of its own adapter, so nothing else's values reach it.  For fp32 results the
 // share of H goes through four accumulators of kF32Chunk steps, added up in
 // registers, as often as it takes.  Bound by reading x
-// (67 MB at 8192 x 4096: 20 us from HBM, rank 16; 33 MB at 4001: 15 us, rank 32).
+// (from a cold cache 67 MB at 8192 x 4096, rank 16, fp32 results: 23 us; 33 MB at
+// 4001, rank 32, 16-bit results: 17 us).
 constexpr int kShrinkTokens = 128;
 constexpr int kShrinkStage = kATile + kShrinkTokens * 128;
 constexpr int kShrinkStages = 6;
@@ -964,12 +977,10 @@ __global__ void __launch_bounds__(256, 1) adapter_shrink_kernel(const __grid_con
 //
 // Adapters: tokens come in groups of 16.  A run of groups that share one adapter
 // gets more K steps at the end of its tile, over that run's columns alone: B[a]
-// times u's leading bits, B[a] times the next ones (terms of 16-bit type: two carry
-// 16 significand bits of u with bf16, 22 with f16; an fp32 result takes three of
-// bf16, 24 bits).  A group of several adapters
-// is done in the epilogue (adapter_block), but with
-// CHUNKS, whose accumulators leave it no registers: adapter_mixed_kernel then adds
-// to the fp32 results.
+// times u's leading bits, B[a] times the next ones.  A group of several adapters, or
+// whose u fp16's terms do not carry unscaled, is done in the epilogue (adapter_block),
+// but with CHUNKS, whose accumulators leave it no registers: adapter_mixed_kernel
+// then adds to the fp32 results.
 constexpr int kStreamStages = 8;   // at most: as many as fit 208 KB
 constexpr int kStreamBytes = 208 * 1024;
 constexpr int kStreamSmem = kStreamBytes + 8 * 2048 + 1024;

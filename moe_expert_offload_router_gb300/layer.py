@@ -59,7 +59,10 @@ class Routing:
 
     ``bias``: one device fp32 [E] balance bias for every layer, or a sequence with
     one (or None) per layer.  ``load``: device int32 [layers, E], counts added per
-    call (cleared by the caller); what a bias is moved by."""
+    call (cleared by the caller); what a bias is moved by.
+
+    A token whose logits are all NaN or -inf (padding) takes part in nothing, and its
+    output is the shared expert's alone, 0 without one."""
     score: int = L.MOE_SCORE_SIGMOID
     bias: object = None
     n_group: int = 1

@@ -704,6 +704,78 @@ moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out_dtype, con
                               cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Tokens sorted by expert, and back.  topk_ids device int32 [T, k] (as moe_route
+ * writes them); a pair (t, j) takes part if 0 <= topk_ids[t, j] < E.
+ *
+ * moe_sort_rows:
+ *   offsets  device int32 [E + 1] out: offsets[e] is the number of pairs of experts
+ *            below e, offsets[E] of all pairs that take part
+ *   pos      device int32 [T, k] out: the pair's place among the pairs that take part,
+ *            stably sorted by expert (the order of moe_group_pairs), or -1
+ *   rows     device [T k, H] out: rows[pos[t, j]] = x[t], bit for bit; rows from
+ *            offsets[E] on are left as they were
+ *   An id >= E counts as none and, when d_error (device int32, may be NULL) is given,
+ *   sets *d_error to MOE_ERR_INVALID (the caller clears it).
+ * moe_sort_rows_backward: d_x[t] = sum_j d_rows[pos[t, j]].
+ *
+ * moe_combine_rows: y[t] = base[t] + sum_j w[t, j] rows[pos[t, j]]
+ *   w     device fp32 [T, k] or NULL (all 1)
+ *   base  device [T, H] of y's type or NULL (0); may be y itself (in place)
+ * moe_combine_rows_backward, with respect to rows and w:
+ *   d_rows[pos[t, j]] = w[t, j] d_y[t]   (rows that no pair names are left as they were)
+ *   d_w[t, j] = <d_y[t], rows[pos[t, j]]>, 0 where the pair has none; device fp32 [T, k]
+ *   or NULL: not wanted (rows is then not read).  d_rows may be rows itself (in place).
+ *
+ * A pos outside [0, n_rows) (n_rows: the rows of `rows`) counts as -1: nothing is read
+ * for it, so what rows past offsets[E] hold does not matter.  The pos of one call are
+ * distinct but for -1.  Sums are taken in fp32 in the order of j (d_w's over H in a fixed
+ * order), base last, and rounded once: equal calls give equal bits.
+ * x and rows of sort have one type; in combine y, base and d_y have y_dtype, rows and
+ * d_rows rows_dtype, which is y_dtype or MOE_DT_F32.  T >= 0, 1 <= k <= 64,
+ * 1 <= E <= 2048, H >= 1, T k < 2^31 - 32.  T == 0 writes only the offsets (0).
+ * ------------------------------------------------------------------------- */
+moe_status moe_sort_rows(int T, int k, int E, int H, int dtype, const void* x, int64_t ld_x,
+                         const int32_t* topk_ids, void* rows, int64_t ld_rows, int32_t* offsets, int32_t* pos,
+                         int32_t* d_error, cudaStream_t stream);
+moe_status moe_sort_rows_backward(int T, int k, int n_rows, int H, int dtype, const void* d_rows, int64_t ld_d_rows,
+                                  const int32_t* pos, void* d_x, int64_t ld_d_x, cudaStream_t stream);
+moe_status moe_combine_rows(int T, int k, int n_rows, int H, int rows_dtype, int y_dtype, const void* rows,
+                            int64_t ld_rows, const int32_t* pos, const float* w, const void* base, int64_t ld_base,
+                            void* y, int64_t ld_y, cudaStream_t stream);
+moe_status moe_combine_rows_backward(int T, int k, int n_rows, int H, int rows_dtype, int y_dtype, const void* d_y,
+                                     int64_t ld_d_y, const void* rows, int64_t ld_rows, const int32_t* pos,
+                                     const float* w, void* d_rows, int64_t ld_d_rows, float* d_w,
+                                     cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Products with 4-bit weights that share a scale in groups, for a dense projection or
+ * for the experts that sorted rows go to:
+ *   out[r, n] = sum_k x[r, k] (q[e, n, k] - z[e, n, k / group]) s[e, n, k / group]
+ * with e the expert of row r: offsets[e] <= r < offsets[e + 1].
+ *   x        device [P, K] of `dtype` (bf16 or f16)
+ *   codes    device uint8 [E, N, K / 2] dense: element 2j of a row in the low nibble of
+ *            byte j, 2j + 1 in the high one
+ *   scales   device [E, N, K / group] dense, of `dtype`
+ *   zeros    device uint8 [E, N, K / group] dense, values 0 to 127, or NULL (all 8)
+ *   offsets  device int32 [E + 1], ascending, as moe_sort_rows writes them, or NULL
+ *            (E == 1: all rows); rows of out from offsets[E] on are left as they were,
+ *            and so are rows before offsets[0]
+ *   swiglu   nonzero: the first N / 2 rows of a matrix are gates, the others ups (w1 and
+ *            w3 of an expert one after the other), and out [P, N / 2] is
+ *            silu(gate) * up, silu(v) = v / (1 + e^-v), from the fp32 sums
+ *   out      device [P, N] (or [P, N / 2]) of out_dtype: `dtype` or MOE_DT_F32
+ * q - z and its products with x are exact; a group's sum is taken in fp32 (tensor-core
+ * accumulators) and multiplied by its scale in fp32, and the groups are added in fp32.
+ * A row's values, NaN included, reach that row of out and no other.
+ * group 32, 64 or 128, K a multiple of it, x and codes 16-byte aligned, ld_x a multiple
+ * of 8; P >= 0, N >= 1 (even with swiglu), 1 <= E <= 65535, E N < 2^31.
+ * A wait that gave up sets *d_error (device int32, may be NULL) to MOE_ERR_TIMEOUT.
+ * ------------------------------------------------------------------------- */
+moe_status moe_w4_linear(int P, int N, int K, int E, int group, int dtype, int out_dtype, const void* x, int64_t ld_x,
+                         const uint8_t* codes, const void* scales, const uint8_t* zeros, const int32_t* offsets,
+                         int swiglu, void* out, int64_t ld_out, int32_t* d_error, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Per-kernel timing: when enabled, every kernel the library launches is
  * bracketed by two CUDA events recorded on its launching stream.
  * moe_profile_enable(1) clears the record and starts collecting; (0) stops.
@@ -719,7 +791,8 @@ moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out_dtype, con
 enum {
   MOE_K_ROUTER = 0, MOE_K_ENSURE, MOE_K_LADDER, MOE_K_GROUP, MOE_K_PLAN, MOE_K_GATEUP,
   MOE_K_DOWN, MOE_K_COMBINE, MOE_K_CARRY, MOE_K_GEMM_GATEUP, MOE_K_GEMM_DOWN, MOE_K_COPY,
-  MOE_K_ROUTE, MOE_K_ROUTE_BWD, MOE_K_NORM, MOE_K_NORM_BWD, MOE_K_LINEAR, MOE_K_COUNT
+  MOE_K_ROUTE, MOE_K_ROUTE_BWD, MOE_K_NORM, MOE_K_NORM_BWD, MOE_K_LINEAR,
+  MOE_K_SORT_ROWS, MOE_K_SORT_ROWS_BWD, MOE_K_COMBINE_ROWS, MOE_K_COMBINE_ROWS_BWD, MOE_K_W4, MOE_K_COUNT
 };
 moe_status moe_profile_enable(int enable);
 moe_status moe_profile_query(int kernel, double* total_ms, int* launches);

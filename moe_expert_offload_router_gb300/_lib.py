@@ -20,10 +20,12 @@ MOE_POOL_FP4, MOE_POOL_INT2, MOE_POOL_SHARED = 0, 1, 2
 MOE_W1, MOE_W3, MOE_W2 = 0, 1, 2
 (MOE_K_ROUTER, MOE_K_ENSURE, MOE_K_LADDER, MOE_K_GROUP, MOE_K_PLAN, MOE_K_GATEUP, MOE_K_DOWN,
  MOE_K_COMBINE, MOE_K_CARRY, MOE_K_GEMM_GATEUP, MOE_K_GEMM_DOWN, MOE_K_COPY, MOE_K_ROUTE, MOE_K_ROUTE_BWD, MOE_K_NORM, MOE_K_NORM_BWD,
- MOE_K_LINEAR, MOE_K_COUNT) = range(18)
+ MOE_K_LINEAR, MOE_K_SORT_ROWS, MOE_K_SORT_ROWS_BWD, MOE_K_COMBINE_ROWS, MOE_K_COMBINE_ROWS_BWD, MOE_K_W4,
+ MOE_K_COUNT) = range(23)
 KERNEL_NAMES = ["router", "ensure", "ladder", "group_pairs", "plan", "gateup", "down", "combine",
                 "rms_carry", "gemm_gateup", "gemm_down", "copy_device", "route", "route_backward", "block_norm",
-                "block_norm_backward", "adapter_linear"]
+                "block_norm_backward", "adapter_linear", "sort_rows", "sort_rows_backward", "combine_rows",
+                "combine_rows_backward", "w4_linear"]
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
@@ -113,6 +115,11 @@ _SIGS = {
     "moe_adapter_linear_workspace": (sz, [i32, i32, i32, i32, i32]),
     "moe_adapter_linear": (i32, [i32, i32, i32, i32, i32, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, i64, vp,
                                  sz, vp, vp]),
+    "moe_sort_rows": (i32, [i32, i32, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp]),
+    "moe_sort_rows_backward": (i32, [i32, i32, i32, i32, i32, vp, i64, vp, vp, i64, vp]),
+    "moe_combine_rows": (i32, [i32, i32, i32, i32, i32, i32, vp, i64, vp, vp, vp, i64, vp, i64, vp]),
+    "moe_combine_rows_backward": (i32, [i32, i32, i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp]),
+    "moe_w4_linear": (i32, [i32, i32, i32, i32, i32, i32, i32, vp, i64, vp, vp, vp, vp, i32, vp, i64, vp, vp]),
     "moe_selftest": (i32, []),
     "moe_debug_timeout_probe": (i32, [C.c_int64, vp, vp]),
     "moe_profile_enable": (i32, [i32]),
@@ -498,7 +505,7 @@ def moe_rms_carry(y, eps: float, x_next, stream=None):
     _check(_lib.moe_rms_carry(_p(y), T, H, eps, _p(x_next), _s(stream)))
 
 
-# Routing, block norms and the adapter projection: calls of microseconds, whose
+# Routing, block norms, projections and the rows around the experts: calls of microseconds, whose
 # argument checks are compiled (csrc/binding.cpp) into functions of these names.
 from . import _binding  # noqa: E402  (needs torch's libraries and the library above loaded)
 
@@ -508,6 +515,11 @@ moe_route_backward = _binding.moe_route_backward
 moe_block_norm = _binding.moe_block_norm
 moe_block_norm_backward = _binding.moe_block_norm_backward
 moe_adapter_linear = _binding.moe_adapter_linear
+moe_sort_rows = _binding.moe_sort_rows
+moe_sort_rows_backward = _binding.moe_sort_rows_backward
+moe_combine_rows = _binding.moe_combine_rows
+moe_combine_rows_backward = _binding.moe_combine_rows_backward
+moe_w4_linear = _binding.moe_w4_linear
 
 
 def moe_block_norm_backward_workspace(T: int, H: int) -> int:

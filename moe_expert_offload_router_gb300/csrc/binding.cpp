@@ -472,6 +472,179 @@ PyObject* adapter_linear(PyObject*, PyObject* args, PyObject* kw) {
   });
 }
 
+// Rows sorted by expert [n, H] and their pairs' places [T, k].
+struct SortedRows {
+  int T, k, n, H;
+  SortedRows(const at::Tensor& rows, const at::Tensor& pos)
+      : T(to_int(pos.size(0), "T")), k(to_int(pos.size(1), "k")), n(to_int(rows.size(0), "the number of rows")),
+        H(to_int(rows.size(1), "H")) {}
+};
+const int32_t* places(Tensors& all, const at::Tensor& t) {
+  return (const int32_t*)dense(all, &t, {t.size(0), t.size(1)}, at::kInt, "pos");
+}
+// The type of a result that the caller did not bring.
+at::ScalarType result_type(PyObject* o, at::ScalarType otherwise) {
+  if (!o || o == Py_None) return otherwise;
+  if (!THPDtype_Check(o)) {
+    PyErr_SetString(PyExc_TypeError, "out_dtype must be a torch.dtype");
+    throw Refused();
+  }
+  return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
+PyObject* sort_rows(PyObject*, PyObject* args, PyObject* kw) {
+  static const char* names[] = {"x", "topk_ids", "n_experts", "rows", "offsets", "pos", "d_error", "stream", nullptr};
+  PyObject *x, *ids, *rw = nullptr, *off = nullptr, *ps = nullptr, *err = nullptr, *st = nullptr;
+  int E;
+  if (!PyArg_ParseTupleAndKeywords(args, kw, "OOi|OOOOO", (char**)names, &x, &ids, &E, &rw, &off, &ps, &err, &st))
+    return nullptr;
+  return guarded([&] {
+    Tensors all;
+    const at::Tensor &tx = matrix(x, "x"), &ti = matrix(ids, "topk_ids");
+    const int T = to_int(tx.size(0), "T"), H = to_int(tx.size(1), "H"), k = to_int(ti.size(1), "k"), d = dtype_code(tx);
+    const int64_t P = (int64_t)T * k;
+    to_int(P, "T * k");
+    const auto i32 = tx.options().dtype(at::kInt);
+    at::Tensor mr, mo, mp;
+    const at::Tensor* to = either(off, "offsets", mo, {(E > 0 ? E : 0) + 1}, i32, st);
+    const at::Tensor* tp = either(ps, "pos", mp, {T, k}, i32, st);
+    const at::Tensor* tr = either(rw, "rows", mr, {P, H}, tx.options(), st);
+    same_type(tr, tx.scalar_type(), "rows (as x)");
+    const Rows rx = rows(all, &tx, T, H, "x"), rr = rows(all, tr, P, H, "rows");
+    auto* pi = (const int32_t*)dense(all, &ti, {T, k}, at::kInt, "topk_ids");
+    auto* po = (int32_t*)dense(all, to, {(E > 0 ? E : 0) + 1}, at::kInt, "offsets");
+    auto* pp = (int32_t*)dense(all, tp, {T, k}, at::kInt, "pos");
+    auto* pe = (int32_t*)dense(all, tensor(err, "d_error"), {1}, at::kInt, "d_error");
+    const Place at(all, st);
+    check(unlocked([&] {
+      return moe_sort_rows(T, k, E, H, d, rx.p, rx.ld, pi, rr.p, rr.ld, po, pp, pe, at.stream);
+    }));
+    return Py_BuildValue("(NNN)", Results::of(rw, mr), Results::of(off, mo), Results::of(ps, mp));
+  });
+}
+
+PyObject* sort_rows_backward(PyObject*, PyObject* args, PyObject* kw) {
+  static const char* names[] = {"d_rows", "pos", "d_x", "stream", nullptr};
+  PyObject *dr, *ps, *dx = nullptr, *st = nullptr;
+  if (!PyArg_ParseTupleAndKeywords(args, kw, "OO|OO", (char**)names, &dr, &ps, &dx, &st)) return nullptr;
+  return guarded([&] {
+    Tensors all;
+    const at::Tensor &tr = matrix(dr, "d_rows"), &tp = matrix(ps, "pos");
+    const SortedRows n(tr, tp);
+    at::Tensor made;
+    const at::Tensor* tx = either(dx, "d_x", made, {n.T, n.H}, tr.options(), st);
+    same_type(tx, tr.scalar_type(), "d_x (as d_rows)");
+    const int d = dtype_code(tr);
+    const Rows rr = rows(all, &tr, n.n, n.H, "d_rows"), rx = rows(all, tx, n.T, n.H, "d_x");
+    auto* pp = places(all, tp);
+    const Place at(all, st);
+    check(unlocked([&] {
+      return moe_sort_rows_backward(n.T, n.k, n.n, n.H, d, rr.p, rr.ld, pp, rx.p, rx.ld, at.stream);
+    }));
+    return Results::of(dx, made);
+  });
+}
+
+PyObject* combine_rows(PyObject*, PyObject* args, PyObject* kw) {
+  static const char* names[] = {"rows", "pos", "w", "base", "y", "out_dtype", "stream", nullptr};
+  PyObject *rw, *ps, *w = nullptr, *bs = nullptr, *y = nullptr, *od = nullptr, *st = nullptr;
+  if (!PyArg_ParseTupleAndKeywords(args, kw, "OO|OOOOO", (char**)names, &rw, &ps, &w, &bs, &y, &od, &st)) return nullptr;
+  return guarded([&] {
+    Tensors all;
+    const at::Tensor &tr = matrix(rw, "rows"), &tp = matrix(ps, "pos");
+    const SortedRows n(tr, tp);
+    const at::Tensor* tb = tensor(bs, "base");
+    at::Tensor made;
+    const at::Tensor* ty = either(y, "y", made, {n.T, n.H},
+                                  tr.options().dtype(result_type(od, tb ? tb->scalar_type() : tr.scalar_type())), st);
+    same_type(tb, ty->scalar_type(), "base (as y)");
+    const int dr = dtype_code(tr), dy = dtype_code(*ty);
+    const Rows rr = rows(all, &tr, n.n, n.H, "rows"), rb = rows(all, tb, n.T, n.H, "base"), ry = rows(all, ty, n.T, n.H, "y");
+    auto* pp = places(all, tp);
+    auto* pw = (const float*)dense(all, tensor(w, "w"), {n.T, n.k}, at::kFloat, "w");
+    const Place at(all, st);
+    check(unlocked([&] {
+      return moe_combine_rows(n.T, n.k, n.n, n.H, dr, dy, rr.p, rr.ld, pp, pw, rb.p, rb.ld, ry.p, ry.ld, at.stream);
+    }));
+    return Results::of(y, made);
+  });
+}
+
+PyObject* combine_rows_backward(PyObject*, PyObject* args, PyObject* kw) {
+  static const char* names[] = {"d_y", "rows", "pos", "w", "d_rows", "d_w", "want_d_w", "stream", nullptr};
+  PyObject *dy, *rw, *ps, *w = nullptr, *dr = nullptr, *dw = nullptr, *st = nullptr;
+  int want = 1;
+  if (!PyArg_ParseTupleAndKeywords(args, kw, "OOO|OOOpO", (char**)names, &dy, &rw, &ps, &w, &dr, &dw, &want, &st))
+    return nullptr;
+  return guarded([&] {
+    Tensors all;
+    const at::Tensor &ty = matrix(dy, "d_y"), &tr = matrix(rw, "rows"), &tp = matrix(ps, "pos");
+    const SortedRows n(tr, tp);
+    at::Tensor mr, mw;
+    const at::Tensor* td = either(dr, "d_rows", mr, {n.n, n.H}, tr.options(), st);
+    same_type(td, tr.scalar_type(), "d_rows (as rows)");
+    const at::Tensor* tw = want ? either(dw, "d_w", mw, {n.T, n.k}, tr.options().dtype(at::kFloat), st) : nullptr;
+    const int rd = dtype_code(tr), yd = dtype_code(ty);
+    const Rows ry = rows(all, &ty, n.T, n.H, "d_y"), rr = rows(all, &tr, n.n, n.H, "rows"), rdr = rows(all, td, n.n, n.H, "d_rows");
+    auto* pp = places(all, tp);
+    auto* pw = (const float*)dense(all, tensor(w, "w"), {n.T, n.k}, at::kFloat, "w");
+    auto* pdw = (float*)dense(all, tw, {n.T, n.k}, at::kFloat, "d_w");
+    const Place at(all, st);
+    check(unlocked([&] {
+      return moe_combine_rows_backward(n.T, n.k, n.n, n.H, rd, yd, ry.p, ry.ld, rr.p, rr.ld, pp, pw, rdr.p, rdr.ld, pdw,
+                                       at.stream);
+    }));
+    return Py_BuildValue("(NN)", Results::of(dr, mr), Results::of(want ? dw : Py_None, mw));
+  });
+}
+
+PyObject* w4_linear(PyObject*, PyObject* args, PyObject* kw) {
+  static const char* names[] = {"x", "codes", "scales", "zeros", "offsets", "swiglu", "out", "out_dtype", "d_error",
+                                "stream", nullptr};
+  PyObject *x, *cd, *sc, *zr = nullptr, *off = nullptr, *out = nullptr, *od = nullptr, *err = nullptr, *st = nullptr;
+  int swiglu = 0;
+  if (!PyArg_ParseTupleAndKeywords(args, kw, "OOO|OOpOOOO", (char**)names, &x, &cd, &sc, &zr, &off, &swiglu, &out, &od,
+                                   &err, &st))
+    return nullptr;
+  return guarded([&] {
+    Tensors all;
+    const at::Tensor &tx = matrix(x, "x"), &tc = needed(cd, "codes"), &ts = needed(sc, "scales");
+    const int P = to_int(tx.size(0), "the number of rows"), K = to_int(tx.size(1), "K");
+    const at::ScalarType d = tx.scalar_type();
+    const bool many = tc.dim() == 3;
+    if (!many && tc.dim() != 2) {
+      PyErr_Format(PyExc_ValueError, "codes must be [N, %d] or [E, N, %d], got %s", K / 2, K / 2, shape_text(tc.sizes()).c_str());
+      throw Refused();
+    }
+    const int E = many ? to_int(tc.size(0), "E") : 1, N = to_int(tc.size(many), "N");
+    const int64_t groups = ts.dim() ? ts.size(-1) : 0;
+    const int group = groups > 0 && K % groups == 0 ? (int)(K / groups) : 0;   // 0 is refused by the library
+    const Rows rx = rows(all, &tx, P, K, "x");
+    void *pc, *psc;
+    const uint8_t* pz;
+    if (many) {
+      pc = dense(all, &tc, {E, N, K / 2}, at::kByte, "codes"), psc = dense(all, &ts, {E, N, groups}, d, "scales (as x)");
+      pz = (const uint8_t*)dense(all, tensor(zr, "zeros"), {E, N, groups}, at::kByte, "zeros");
+    } else {
+      pc = dense(all, &tc, {N, K / 2}, at::kByte, "codes"), psc = dense(all, &ts, {N, groups}, d, "scales (as x)");
+      pz = (const uint8_t*)dense(all, tensor(zr, "zeros"), {N, groups}, at::kByte, "zeros");
+    }
+    auto* po = (const int32_t*)dense(all, tensor(off, "offsets"), {E + 1}, at::kInt, "offsets");
+    const int outs = swiglu ? N / 2 : N;
+    at::Tensor made;
+    const at::Tensor* to = either(out, "out", made, {P, outs}, tx.options().dtype(result_type(od, d)), st);
+    const int xd = dtype_code(tx), ot = dtype_code(*to);
+    const Rows ro = rows(all, to, P, outs, "out");
+    auto* pe = (int32_t*)dense(all, tensor(err, "d_error"), {1}, at::kInt, "d_error");
+    const Place at(all, st);
+    check(unlocked([&] {
+      return moe_w4_linear(P, N, K, E, group, xd, ot, rx.p, rx.ld, (const uint8_t*)pc, psc, pz, po, swiglu, ro.p, ro.ld,
+                           pe, at.stream);
+    }));
+    return Results::of(out, made);
+  });
+}
+
 PyObject* set_check(PyObject*, PyObject* args) {
   PyObject *f, *e;
   if (!PyArg_ParseTuple(args, "OO", &f, &e)) return nullptr;
@@ -508,6 +681,29 @@ PyMethodDef methods[] = {
      "out [T, N] = x weight^T + lora_scale[a] (x lora_a[a]^T) lora_b[a]^T, a = adapter_ids[t] (< 0: none).\n\n"
      "x [T, H] and weight [N, H] (rows may be strided), lora_a [n, R, H], lora_b [n, N, R], all bf16 or all f16; out\n"
      "of x's type or fp32.  Without lora_a the projection alone."},
+    {"moe_sort_rows", KW(sort_rows),
+     "moe_sort_rows(x, topk_ids, n_experts, rows=None, offsets=None, pos=None, d_error=None, stream=None)\n\n"
+     "(rows, offsets, pos): x's rows [T, H] sorted by the experts of topk_ids [T, k] (negative: none).\n\n"
+     "rows [T k, H] of x's type (from offsets[n_experts] on left as they were), offsets [n_experts + 1], pos [T, k]\n"
+     "(-1: the pair has no row)."},
+    {"moe_sort_rows_backward", KW(sort_rows_backward),
+     "moe_sort_rows_backward(d_rows, pos, d_x=None, stream=None)\n\n"
+     "d_x [T, H], the sum of a token's rows of d_rows."},
+    {"moe_combine_rows", KW(combine_rows),
+     "moe_combine_rows(rows, pos, w=None, base=None, y=None, out_dtype=None, stream=None)\n\n"
+     "y [T, H] = base + sum_j w[:, j] rows[pos[:, j]]; of out_dtype, else base's type or that of rows (which are of\n"
+     "y's type or fp32)."},
+    {"moe_combine_rows_backward", KW(combine_rows_backward),
+     "moe_combine_rows_backward(d_y, rows, pos, w=None, d_rows=None, d_w=None, want_d_w=True, stream=None)\n\n"
+     "(d_rows, d_w) of moe_combine_rows: rows' type and fp32; rows of d_rows that no pos names are left as they\n"
+     "were.  Without want_d_w, d_w is None."},
+    {"moe_w4_linear", KW(w4_linear),
+     "moe_w4_linear(x, codes, scales, zeros=None, offsets=None, swiglu=False, out=None, out_dtype=None, d_error=None, "
+     "stream=None)\n\n"
+     "out [P, N] = x ((codes - zeros) scales)^T, by the expert of each row where offsets [E + 1] are given.\n\n"
+     "x [P, K] bf16 or f16 (rows may be strided), codes uint8 [N, K / 2] or [E, N, K / 2] (even elements in the low\n"
+     "nibble), scales [..., N, K / group] of x's type, zeros uint8 of their shape (None: 8); group 32, 64 or 128.\n"
+     "swiglu: out [P, N / 2] = silu(first N / 2) * the others.  out of x's type or fp32."},
     {"set_check", set_check, METH_VARARGS, "The function that raises for a status other than MOE_OK, and what it raises."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Compiled entry points of short calls.", -1, methods};

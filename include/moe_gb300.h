@@ -768,7 +768,7 @@ moe_status moe_combine_rows_backward(int T, int k, int n_rows, int H, int rows_d
  * accumulators) and multiplied by its scale in fp32, and the groups are added in fp32.
  * A row's values, NaN included, reach that row of out and no other.
  * group 32, 64 or 128, K a multiple of it, x and codes 16-byte aligned, ld_x a multiple
- * of 8; P >= 0, N >= 1 (even with swiglu), 1 <= E <= 65535, E N < 2^31.
+ * of 8; P >= 0, N >= 1 (even with swiglu), 1 <= E <= 2048, E N < 2^31.
  * A wait that gave up sets *d_error (device int32, may be NULL) to MOE_ERR_TIMEOUT.
  * ------------------------------------------------------------------------- */
 moe_status moe_w4_linear(int P, int N, int K, int E, int group, int dtype, int out_dtype, const void* x, int64_t ld_x,

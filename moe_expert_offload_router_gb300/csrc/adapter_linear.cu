@@ -23,7 +23,7 @@
 #include <type_traits>
 
 #include "dtype.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_issue.cuh"
 
 namespace moe {
 
@@ -108,85 +108,6 @@ __global__ void __launch_bounds__(128) adapter_dot_kernel(const LinearArgs a) {
 }
 
 // -------------------------------------------------------------- projection --
-
-// Waits for the phase of parity `parity`, at most 2^26 polls (some seconds); a
-// wait that gives up says so in *err (the block's own word), and ends the block's
-// other waits.
-__device__ __forceinline__ bool test_wait(uint64_t* b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(su32(b)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-static __device__ __forceinline__ bool wait_bar(uint64_t* b, uint32_t parity, int* err) {
-  for (uint32_t i = 0; i < (1u << 26); ++i) {
-    if (test_wait(b, parity)) return true;
-    if ((i & 255) == 255 && *(volatile int*)err != MOE_OK) return false;
-  }
-  atomicExch(err, MOE_ERR_TIMEOUT);
-  return false;
-}
-
-// One thread of a warp issues all MMAs of a block.  Its loop has to stay short:
-// a K = 16 step of 128 x 128 takes 64 clocks and its issue alone about 54, so
-// stages and phases are counted, not divided out (with k % chunk in the loop a
-// 64-wide step of any width took 870 clocks; now 258 at n = 128, 514 at 256).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
-  return p != 0;
-}
-// D [128 x n] (fp32 in tensor memory) (+)= A [128 x 16] B [n x 16]^T.
-__device__ __forceinline__ void mma_k16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// Arrives on `bar` when the thread's MMAs so far have completed.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar)) : "memory");
-}
-// Bytes to come on `bar`, without an arrival.
-__device__ __forceinline__ void mbar_expect_only(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(su32(bar)), "r"(bytes) : "memory");
-}
-// A place in a ring of stages and the parity of its current pass.
-struct RingPos {
-  int stages, stage = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ explicit RingPos(int n) : stages(n) {}
-  __device__ __forceinline__ void next() {
-    if (++stage == stages) stage = 0, parity ^= 1;
-  }
-};
-// kind::f16, D fp32, A and B of one 16-bit type, both K-major, M = 128.
-__device__ __forceinline__ uint32_t idesc_f16(int n, bool bf16) {
-  const uint32_t t = bf16 ? 1u : 0u;
-  return (1u << 4) | (t << 7) | (t << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  float4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(r)
-               : "memory");
-  return v;
-}
-
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
-}
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // A tensor-core accumulator loses a little with every step (it truncates: 4.2e-6
 // of the result over 4096 products, 0.5e-6 over 512), so a result kept in fp32
@@ -993,39 +914,6 @@ struct StreamPlan {
   int blocks;
 };
 
-// The pair's forms: a copy into this block that completes on a barrier of the leader (a cluster
-// address), an MMA over both blocks' rows, its commit (arrives at the same barrier of both).
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(su32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3}], [%4];" ::"r"(su32(dst)),
-      "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void mma_k16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
-          su32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ uint32_t idesc_pair(int n, bool bf16) {   // M = 256
-  return (idesc_f16(n, bf16) & ~(31u << 24)) | (16u << 24);
-}
 template <typename TE, bool CHUNKS>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     linear_stream_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
@@ -1289,43 +1177,6 @@ __global__ void __launch_bounds__(256) adapter_mixed_kernel(const LinearArgs a) 
 }
 
 // --------------------------------------------------------------------- host --
-
-// rows x cols of 16-bit elements, `ld` apart: boxes of 64 columns x box_rows, 128-byte swizzle, zeros outside
-static moe_status map_rows(CUtensorMap* m, const void* base, int dtype, uint64_t cols, uint64_t rows, uint64_t ld,
-                           uint32_t box_rows) {
-  auto fn = tensor_map_encoder();
-  if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {ld * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  CUresult r = fn(m, dtype == MOE_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                  const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (projection) failed: %d", (int)r);
-  return MOE_OK;
-}
-
-// Clusters of cs blocks along x, started early (programmatic dependent launch).
-template <typename... KArgs, typename... Args>
-static moe_status launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int cs, size_t smem, cudaStream_t s,
-                                 const char* name, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cs, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-  if (e != cudaSuccess) return cuda_fail(e, name);
-  return check_launch(name);
-}
 
 // Blocks that split H, of a call of so many tiles: while the blocks still fit the SMs at once and each
 // keeps two steps; clusters of eight only where one of the eight GPCs takes each (16 of them: 13.4 us for

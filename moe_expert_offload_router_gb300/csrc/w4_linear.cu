@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "dtype.cuh"
+#include "tcgen05_issue.cuh"
 
 namespace moe {
 
@@ -22,7 +23,10 @@ struct W4Args {
   const void* scales;                 // [E][N][K / g] of x's type
   const int32_t* offsets;             // [E + 1] or null (all P rows are expert 0's)
   void* out;
+  int32_t* err;
 };
+
+constexpr int kMaxExperts = 2048;
 
 template <typename TE>
 struct W4;
@@ -227,7 +231,395 @@ __global__ void __launch_bounds__(256) w4_rows_kernel(const W4Args a, int swiglu
   }
 }
 
+
+// ------------------------------------------------------------- tiles, tcgen05 --
+
+// Waits for the phase of parity `parity`, at most a second; arrivals may come from the
+// pair's other block.  A wait that gives up says so in *err, and ends the block's other waits.
+__device__ __forceinline__ bool try_cluster(uint64_t* b, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __noinline__ bool wait_long(uint64_t* b, uint32_t parity, int* err) {
+  const uint64_t t0 = gtimer();
+  while (*(volatile int*)err == MOE_OK) {
+    if (try_cluster(b, parity, 100000)) return true;
+    if (gtimer() - t0 > 1000000000ull) atomicExch(err, MOE_ERR_TIMEOUT);
+  }
+  return false;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, int* err) {
+  return try_cluster(b, parity, 2000) || wait_long(b, parity, err);
+}
+
+// D [256 x n] over a pair of blocks (+)= A [256 x 16] (each block's 128 rows in its own tensor memory) B [n x 16]^T.
+__device__ __forceinline__ void mma_k16_pair_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+// unpack, in the codes' own order: (0, 1), (2, 3), (4, 5), (6, 7).
+template <typename TE>
+__device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t zero, uint32_t* v) {
+  const uint32_t odd = w >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = __byte_perm(w, odd, (uint32_t)(i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12)));
+    v[i] = W4<TE>::sub((u & 0x000f000fu) | W4<TE>::kMagic, zero);
+  }
+}
+
+// Many rows of x to a matrix: persistent pairs of blocks (cta_group::2, a block per SM)
+// over tiles of 256 rows of weights x NT rows of x.  A step is 128 products deep: each block
+// brings its 128 rows of codes and half of the x rows by TMA; eight warps turn the codes
+// into q - z straight into tensor memory, from where the MMAs read them as their A operand
+// (through shared memory they would take twice the bandwidth that there is); one thread
+// multiplies for both blocks into an accumulator for each group of the scales; and eight
+// warps multiply each accumulator by its scales - a scale belongs to a tensor memory lane -
+// and add it up in registers while the next ones fill.
+constexpr int kTileThreads = 576;   // 8 warps of codes, 8 of sums, TMA, MMA
+constexpr int kTileStages = 8, kAStages = 4, kCodeBytes = 128 * 64;
+constexpr int kExchange = 2 * 16 * 64 * 4;
+template <int NT>
+struct TileCfg {
+  static constexpr int kStage = kCodeBytes + NT / 2 * 256;
+  static constexpr int kBufs = 256 / NT;   // accumulators: half of tensor memory, A the other half
+  static constexpr int kRing = kTileStages * kStage;
+};
+static size_t tile_smem(int ring, int E) { return (size_t)ring + kExchange + 1024 + (size_t)(E + 1) * 8; }
+
+template <typename TE, int NT, int G>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    w4_tile_kernel(const __grid_constant__ CUtensorMap mC, const __grid_constant__ CUtensorMap mX,
+                   const __grid_constant__ W4Args a, int swiglu) {
+  using C = TileCfg<NT>;
+  extern __shared__ uint8_t tile_raw[];
+  __shared__ alignas(8) uint64_t full_c[kTileStages], full_x[kTileStages], empty[kTileStages], a_full[kAStages];
+  __shared__ alignas(8) uint64_t acc_full[C::kBufs], acc_empty[C::kBufs];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_err;
+  __shared__ int ws[34];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)tile_raw + 1023) & ~(uintptr_t)1023);
+  float* exchange = reinterpret_cast<float*>(sm + C::kRing);               // [half][16][64]
+  int* first = reinterpret_cast<int*>(sm + C::kRing + kExchange);          // [E + 1]: an expert's first row
+  int* cum = first + a.E + 1;                                              // [E + 1]: its first tile
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x & 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (tid == 0) {
+    prefetch_map(&mC);
+    prefetch_map(&mX);
+    for (int i = 0; i < kTileStages; ++i) {
+      mbar_init(&full_c[i], 1);
+      mbar_init(&full_x[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kAStages; ++i) mbar_init(&a_full[i], 16);          // the leader's: eight warps of each block
+    for (int i = 0; i < C::kBufs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 16);
+    }
+    s_err = MOE_OK;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 17) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  // the experts' tiles
+  const int per = swiglu ? 128 : 256, outs = swiglu ? a.N / 2 : a.N, row_tiles = (outs + per - 1) / per;
+  int tiles = 0;
+  for (int b = 0; b < a.E; b += kTileThreads) {
+    const int e = b + tid;
+    int n = 0, lo = 0, hi = a.P;
+    if (e < a.E) {
+      if (a.offsets) lo = min(max(a.offsets[e], 0), a.P), hi = min(max(a.offsets[e + 1], 0), a.P);
+      n = hi > lo ? (hi - lo + NT - 1) / NT * row_tiles : 0;
+    }
+    int all;
+    const int at = block_exclusive_scan(n, ws, &all);
+    if (e < a.E) {
+      first[e] = lo, cum[e] = tiles + at;
+      if (e == a.E - 1) first[a.E] = hi;
+    }
+    tiles += all;
+  }
+  if (tid == 0) cum[a.E] = tiles;
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();   // the barriers of both are there
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot, tmem_a = tmem + 256;
+  const int steps = (a.K + 127) / 128, groups = a.K / G;
+  bool ok = true;
+
+  int e = 0;
+  // a tile's rows of x and first output (of this block)
+  struct Tile {
+    int m0, m1, o0;
+  };
+  auto tile_at = [&](int tile) {
+    while (cum[e + 1] <= tile) ++e;
+    const int local = tile - cum[e], lo = first[e], hi = first[e + 1], tt = (hi - lo + NT - 1) / NT;
+    const int rt = local / tt, m0 = lo + (local - rt * tt) * NT;
+    return Tile{m0, hi < m0 + NT ? hi : m0 + NT, rt * per + rank * (per / 2)};
+  };
+
+  if (warp == 16) {
+    if (elect_one()) {
+      RingPos r(kTileStages);
+      bool wrapped = false;
+      for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        const Tile t = tile_at(tile);
+        const int row = e * a.N + t.o0, row2 = swiglu ? row + a.N / 2 : row + 64, x0 = t.m0 + rank * (NT / 2);
+        for (int k = 0; k < steps; ++k) {
+          if (wrapped && !(ok = wait_cluster(&empty[r.stage], r.parity ^ 1, &s_err))) break;
+          uint8_t* st = sm + r.stage * C::kStage;
+          mbar_expect_tx(&full_c[r.stage], kCodeBytes);
+          tma_2d(st, &mC, k * 64, row, &full_c[r.stage]);
+          tma_2d(st + kCodeBytes / 2, &mC, k * 64, row2, &full_c[r.stage]);
+          if (rank == 0) mbar_expect_tx(&full_x[r.stage], NT * 256);
+          const uint32_t bar = cluster_addr(&full_x[r.stage], 0);
+          tma_2d_pair(st + kCodeBytes, &mX, k * 128, x0, bar);
+          tma_2d_pair(st + kCodeBytes + NT / 2 * 128, &mX, k * 128 + 64, x0, bar);
+          r.next();
+          wrapped |= r.stage == 0;
+        }
+      }
+    }
+  } else if (warp == 17) {
+    if (rank == 0 && elect_one()) {
+      RingPos r(kTileStages), ar(kAStages), acc(C::kBufs);
+      int used = 0;
+      const uint32_t idesc = idesc_pair(NT, std::is_same<TE, __nv_bfloat16>::value);
+      const uint64_t d0 = umma_desc_sw128(su32(sm));
+      for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        for (int k = 0; k < steps && ok; ++k) {
+          if (!(ok = wait_cluster(&full_x[r.stage], r.parity, &s_err) && wait_cluster(&a_full[ar.stage], ar.parity, &s_err))) break;
+          tc_fence_after();
+          const uint64_t db = d0 + (uint32_t)((r.stage * C::kStage + kCodeBytes) / 16);
+          const uint32_t ta = tmem_a + ar.stage * 64;
+          const int left = a.K - k * 128;
+#pragma unroll
+          for (int g = 0; g < 128 / G; ++g) {
+            if (g * G >= left) break;
+            if (used >= C::kBufs && !(ok = wait_cluster(&acc_empty[acc.stage], acc.parity ^ 1, &s_err))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + acc.stage * NT;
+#pragma unroll
+            for (int i = 0; i < G / 16; ++i) {
+              const int j = g * (G / 16) + i;
+              mma_k16_pair_ta(d, ta + j * 8, db + (j >> 2) * (NT / 2 * 128 / 16) + (j & 3) * 2, idesc, i != 0);
+            }
+            // the stage's commit goes first: no arrival is under way once the last accumulator has been seen
+            if ((g + 1) * G >= left || g == 128 / G - 1) mma_commit_pair(&empty[r.stage]);
+            mma_commit_pair(&acc_full[acc.stage]);
+            acc.next();
+            ++used;
+          }
+          if (!ok) break;
+          r.next();
+          ar.next();
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // codes of row q * 32 + lane, K from h * 64 within the step
+    const int h = warp >> 2, q = warp & 3, row = q * 32 + lane;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    RingPos r(kTileStages), ar(kAStages);
+    int n = 0;   // steps so far
+    constexpr int kZeros = G == 32 ? 2 : 1;
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      const Tile t = tile_at(tile);
+      const int o = t.o0 + (swiglu ? row & 63 : row);
+      const long long wr = (long long)e * a.N + (swiglu && row >= 64 ? a.N / 2 : 0) + min(o, outs - 1);
+      const uint8_t* zp = a.zeros ? a.zeros + wr * groups : nullptr;
+      uint32_t z[kZeros];
+      auto zeros_of = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < kZeros; ++i) {
+          const int g = (k * 128 + h * 64 + i * 32) / G;
+          z[i] = zp && g < groups ? zp[g] : 8u;
+        }
+      };
+      zeros_of(0);
+      for (int k = 0; k < steps; ++k) {
+        uint32_t zero[kZeros];
+#pragma unroll
+        for (int i = 0; i < kZeros; ++i) zero[i] = W4<TE>::kMagic + z[i] * 0x00010001u;
+        zeros_of(k + 1);
+        if (!(ok = __all_sync(0xffffffffu, wait_cluster(&full_c[r.stage], r.parity, &s_err)))) break;
+        const uint8_t* st = sm + r.stage * C::kStage + row * 64;
+        uint32_t w[8], v[32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 u = *reinterpret_cast<const uint4*>(st + (((h * 2 + i) ^ ((row >> 1) & 3)) << 4));
+          w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) unpack_in_order<TE>(w[i], zero[kZeros == 2 ? i >> 2 : 0], v + 4 * i);
+        // the step that last used this A stage has been multiplied: its own ring stage was given back
+        if (n >= kAStages) {
+          const int p = n - kAStages;
+          if (!(ok = __all_sync(0xffffffffu, wait_cluster(&empty[p % kTileStages], (p / kTileStages) & 1, &s_err)))) break;
+          tc_fence_after();
+        }
+        tmem_st32(tmem_a + lanes + ar.stage * 64 + h * 32, v);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(cluster_addr(&a_full[ar.stage], 0));
+        r.next();
+        ar.next();
+        ++n;
+      }
+    }
+  } else {
+    // sums of row q * 32 + lane, columns from h * NT / 2
+    constexpr int kCols = NT / 2;
+    const int q = warp & 3, h = (warp - 8) >> 2, row = q * 32 + lane;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    RingPos acc(C::kBufs);
+    for (int tile = pair; tile < tiles; tile += pairs) {   // a wait that gave up: NaN to the end
+      const Tile t = tile_at(tile);
+      const int o = t.o0 + (swiglu ? row & 63 : row);
+      const long long wr = (long long)e * a.N + (swiglu && row >= 64 ? a.N / 2 : 0) + min(o, outs - 1);
+      const TE* sp = reinterpret_cast<const TE*>(a.scales) + wr * groups;
+      float sum[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
+      TE next = sp[0];
+      for (int g = 0; g < groups; ++g) {
+        const float s = to_f32(next);
+        if (g + 1 < groups) next = sp[g + 1];
+        ok = __all_sync(0xffffffffu, ok && wait_cluster(&acc_full[acc.stage], acc.parity, &s_err));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = tmem + lanes + acc.stage * NT + h * kCols;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          uint32_t u[32];
+          tmem_ld16_nw(at + c, u);
+          if (kCols >= 32) tmem_ld16_nw(at + c + 16, u + 16);
+          tmem_ld_wait16(u);
+          if (kCols >= 32) tmem_ld_fence16(u + 16);
+#pragma unroll
+          for (int i = 0; i < (kCols < 32 ? kCols : 32); ++i) sum[c + i] = fmaf(s, __uint_as_float(u[i]), sum[c + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(cluster_addr(&acc_empty[acc.stage], 0));
+        acc.next();
+      }
+      if (!ok)
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) sum[i] = NAN;
+      auto put = [&](int c, float v) {
+        const int m = t.m0 + h * kCols + c;
+        if (m >= t.m1 || o >= outs) return;
+        const long long at = m * a.ld_out + o;
+        if (a.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(a.out)[at] = v;
+        else reinterpret_cast<TE*>(a.out)[at] = from_f32<TE>(v);
+      };
+      if (!swiglu) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) put(i, sum[i]);
+      } else {
+        // ups (rows 64 on) to the gates' threads, 16 columns at a time
+        float* ex = exchange + h * 16 * 64 + (row & 63);
+        auto meet = [&] {   // the four warps of these columns
+          if (h) asm volatile("bar.sync 2, 128;" ::: "memory");
+          else asm volatile("bar.sync 1, 128;" ::: "memory");
+        };
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          if (q >= 2)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ex[i * 64] = sum[c + i];
+          meet();
+          if (q < 2)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) put(c + i, silu_times(sum[c + i], ex[i * 64]));
+          meet();
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (!ok) {   // a wait gave up: leave the copies in flight time to land
+    const uint64_t since = gtimer();
+    while (gtimer() - since < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();   // nothing of this block is used by the other any more
+  if (warp == 17) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+  if (tid == 0 && s_err != MOE_OK && a.err) atomicExch(a.err, MOE_ERR_TIMEOUT);
+}
+
 // --------------------------------------------------------------------- host --
+
+// codes: rows of K / 2 bytes, boxes of 64 bytes x 64 rows, 64-byte swizzle
+static moe_status map_codes(CUtensorMap* m, const W4Args& a) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[2] = {(cuuint64_t)a.K / 2, (cuuint64_t)a.E * a.N};
+  cuuint64_t strides[1] = {(cuuint64_t)a.K / 2};
+  cuuint32_t box[2] = {64, 64};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.codes), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (codes) failed: %d", (int)r);
+  return MOE_OK;
+}
+template <typename TE, int NT, int G>
+static moe_status launch_tiles(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {
+  CUtensorMap mC, mX;
+  moe_status st = map_codes(&mC, a);
+  if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.K, a.P, a.ld_x, NT / 2);
+  if (st != MOE_OK) return st;
+  auto kernel = w4_tile_kernel<TE, NT, G>;
+  static char allowed[64];
+  MOE_CUDA(allow_smem(kernel, tile_smem(TileCfg<NT>::kRing, kMaxExperts), allowed));
+  const int outs = swiglu ? a.N / 2 : a.N, per = swiglu ? 128 : 256;
+  // at most this many tiles: every expert's last one may be a part
+  const long long most = ((long long)a.P / NT + (a.E < a.P ? a.E : a.P)) * ((outs + per - 1) / per);
+  MOE_ARG(most <= 0x3fffffff, "too many tiles");
+  const int pairs = device_sms() / 2;
+  return launch_cluster(kernel, dim3(2 * (unsigned)(most < pairs ? most : pairs)), kTileThreads, 2,
+                        tile_smem(TileCfg<NT>::kRing, a.E), s, "w4_tile_kernel", mC, mX, a, swiglu);
+}
+template <typename TE, int G>
+static moe_status launch_tiles_of(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {
+  const int mean = a.P / a.E;
+  if (mean > 64) return launch_tiles<TE, 128, G>(a, dtype, swiglu, s);
+  if (mean > 32) return launch_tiles<TE, 64, G>(a, dtype, swiglu, s);
+  return launch_tiles<TE, 32, G>(a, dtype, swiglu, s);
+}
 
 template <typename TE, int WPL, int KS>
 static moe_status launch_rows_kernel(const W4Args& a, int swiglu, cudaStream_t s) {
@@ -250,8 +642,13 @@ static moe_status launch_split_rows(const W4Args& a, int swiglu, cudaStream_t s)
   return launch_rows_kernel<TE, WPL, 8>(a, swiglu, s);
 }
 template <typename TE>
-static moe_status launch_w4(const W4Args& a, int swiglu, cudaStream_t s) {
+static moe_status launch_w4(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {
   ProfScope ps(MOE_K_W4, s);
+  if (a.P / a.E >= 16) {
+    if (a.g == 128) return launch_tiles_of<TE, 128>(a, dtype, swiglu, s);
+    if (a.g == 64) return launch_tiles_of<TE, 64>(a, dtype, swiglu, s);
+    return launch_tiles_of<TE, 32>(a, dtype, swiglu, s);
+  }
   if (a.g == 128) return launch_split_rows<TE, 4>(a, swiglu, s);
   if (a.g == 64) return launch_split_rows<TE, 2>(a, swiglu, s);
   return launch_split_rows<TE, 1>(a, swiglu, s);
@@ -270,7 +667,7 @@ extern "C" moe_status moe_w4_linear(int P, int N, int K, int E, int group, int d
   MOE_ARG(N >= 1 && N <= 1 << 24, "N must be in [1, 2^24] (got %d)", N);
   MOE_ARG(group == 32 || group == 64 || group == 128, "the group must be 32, 64 or 128 (got %d)", group);
   MOE_ARG(K >= group && K <= 1 << 24 && K % group == 0, "K must be a multiple of the group, at most 2^24 (got %d)", K);
-  MOE_ARG(E >= 1 && E <= 65535, "E must be in [1, 65535] (got %d)", E);
+  MOE_ARG(E >= 1 && E <= kMaxExperts, "E must be in [1, %d] (got %d)", kMaxExperts, E);
   MOE_ARG((long long)E * N <= 0x7fffff00LL, "E * N must be below 2^31");
   MOE_ARG(dtype == MOE_DT_BF16 || dtype == MOE_DT_F16, "x must be bf16 or f16 (type %d)", dtype);
   MOE_ARG(out_dtype == dtype || out_dtype == MOE_DT_F32, "out must be of x's type or fp32 (type %d)", out_dtype);
@@ -281,7 +678,7 @@ extern "C" moe_status moe_w4_linear(int P, int N, int K, int E, int group, int d
   MOE_ARG(ld_x >= K && ld_out >= (swiglu ? N / 2 : N), "a row distance is below the row's length");
   MOE_ARG((uintptr_t)x % 16 == 0 && ld_x % 8 == 0, "x needs rows on 16-byte boundaries");
   MOE_ARG((uintptr_t)codes % 16 == 0 && (uintptr_t)scales % 2 == 0, "codes must be 16-byte aligned");
-  W4Args a = {P, N, K, E, group, out_dtype, x, ld_x, ld_out, codes, zeros, scales, offsets, out};
-  return dtype == MOE_DT_BF16 ? launch_w4<__nv_bfloat16>(a, swiglu ? 1 : 0, stream)
-                              : launch_w4<__half>(a, swiglu ? 1 : 0, stream);
+  W4Args a = {P, N, K, E, group, out_dtype, x, ld_x, ld_out, codes, zeros, scales, offsets, out, d_error};
+  return dtype == MOE_DT_BF16 ? launch_w4<__nv_bfloat16>(a, dtype, swiglu ? 1 : 0, stream)
+                              : launch_w4<__half>(a, dtype, swiglu ? 1 : 0, stream);
 }

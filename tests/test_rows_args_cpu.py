@@ -35,11 +35,11 @@ def test_combine_rows_refusals(L):   # noqa: F811
 def test_w4_linear_refusals(L):   # noqa: F811
     good = dict(P=4, N=48, K=256, E=3, g=128, dtype=1, out_dtype=1, x=ONE, ld_x=256, codes=ONE, scales=ONE, zeros=None,
                 offsets=ONE, swiglu=0, out=ONE, ld_out=48, err=None, stream=None)
-    _refused(L, "moe_w4_linear", good, P=[-1, (1 << 30) + 1], N=[0, 1 << 25], K=[0, 64, 192, 1 << 25], E=[0, 65536],
+    _refused(L, "moe_w4_linear", good, P=[-1, (1 << 30) + 1], N=[0, 1 << 25], K=[0, 64, 192, 1 << 25], E=[0, 2049],
              g=[0, 16, 96, 256], dtype=[0, 3], out_dtype=[2, 3], x=[None, 8], ld_x=[255, 260], codes=[None, 8],
              scales=None, offsets=None, out=None, ld_out=47)
     _refused(L, "moe_w4_linear", dict(good, swiglu=1, ld_out=24), N=47, ld_out=23)
-    _refused(L, "moe_w4_linear", dict(good, E=60000), N=1 << 20)
+    _refused(L, "moe_w4_linear", dict(good, E=2048), N=1 << 20)
     assert L.raw().moe_w4_linear(*dict(good, P=0, x=None, codes=None, out=None).values()) == L.MOE_OK
 
 

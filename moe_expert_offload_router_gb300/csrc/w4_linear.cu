@@ -234,27 +234,25 @@ __global__ void __launch_bounds__(256) w4_rows_kernel(const W4Args a, int swiglu
 
 // ------------------------------------------------------------- tiles, tcgen05 --
 
-// Waits for the phase of parity `parity`, at most a second; arrivals may come from the
-// pair's other block.  A wait that gives up says so in *err, and ends the block's other waits.
-__device__ __forceinline__ bool try_cluster(uint64_t* b, uint32_t parity, uint32_t hint_ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(su32(b)), "r"(parity), "r"(hint_ns)
-      : "memory");
-  return ok != 0;
-}
+// Waits for the phase of parity `parity`, at most a second.  A wait that gives up says so in
+// *err, and ends the block's other waits.
 static __device__ __noinline__ bool wait_long(uint64_t* b, uint32_t parity, int* err) {
   const uint64_t t0 = gtimer();
   while (*(volatile int*)err == MOE_OK) {
-    if (try_cluster(b, parity, 100000)) return true;
+    if (mbar_try_wait(b, parity, 100000)) return true;
     if (gtimer() - t0 > 1000000000ull) atomicExch(err, MOE_ERR_TIMEOUT);
   }
   return false;
 }
-__device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, int* err) {
-  return try_cluster(b, parity, 2000) || wait_long(b, parity, err);
+__device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, int* err) {
+  return test_wait(b, parity) || wait_long(b, parity, err);
+}
+// Arrives on a barrier of the pair.  What crosses the blocks here is in tensor memory, written or
+// read before a tcgen05 fence: nothing of the block's other memory goes with the arrival, and
+// a release at cluster scope, which waits for all of the thread's memory accesses, took 1300
+// clocks a step.
+__device__ __forceinline__ void arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // D [256 x n] over a pair of blocks (+)= A [256 x 16] (each block's 128 rows in its own tensor memory) B [n x 16]^T.
@@ -296,6 +294,46 @@ __device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t zero, uint3
 constexpr int kTileThreads = 576;   // 8 warps of codes, 8 of sums, TMA, MMA
 constexpr int kTileStages = 8, kAStages = 4, kCodeBytes = 128 * 64;
 constexpr int kExchange = 2 * 16 * 64 * 4;
+// Four neighbouring elements of B bytes of a row's array, fetched a batch ahead: a lane's row is
+// its own cache line, and a load of every element by itself takes the L1's time 32 times.
+// Rows start anywhere: the two aligned words that hold the four are loaded (one where they
+// are aligned themselves) and shifted.
+template <int B>
+struct Four {
+  using W = typename std::conditional<B == 2, uint64_t, uint32_t>::type;
+  const char *row, *end;
+  W lo = 0, hi = 0;
+  __device__ __forceinline__ Four(const void* p, int n) : row((const char*)p), end((const char*)p + (long long)n * B) {}
+  __device__ __forceinline__ void fetch(int batch) {   // elements 4 batch to 4 batch + 3, those that there are
+    const char* at = row + (long long)batch * (4 * B);
+    const W* w = reinterpret_cast<const W*>((uintptr_t)at & ~(uintptr_t)(4 * B - 1));
+    if (at < end) lo = __ldg(w);
+    if ((const char*)w != at && (const char*)(w + 1) < end) hi = __ldg(w + 1);
+  }
+  __device__ __forceinline__ W value(int batch) const {
+    const int sh = (int)((uintptr_t)(row + (long long)batch * (4 * B)) & (4 * B - 1)) * 8;
+    return sh ? lo >> sh | hi << (32 * B - sh) : lo;
+  }
+};
+struct F32x2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F32x2 pair_of(float a, float b) {
+  F32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves_of(F32x2 a) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(a.v));
+  return f;
+}
+__device__ __forceinline__ F32x2 fma_pair(F32x2 a, F32x2 b, F32x2 c) {
+  F32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 template <int NT>
 struct TileCfg {
   static constexpr int kStage = kCodeBytes + NT / 2 * 256;
@@ -329,7 +367,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&full_x[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kAStages; ++i) mbar_init(&a_full[i], 16);          // the leader's: eight warps of each block
+    for (int i = 0; i < kAStages; ++i) mbar_init(&a_full[i], 8);           // the leader's: four warps of each block
     for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 16);
@@ -391,7 +429,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const Tile t = tile_at(tile);
         const int row = e * a.N + t.o0, row2 = swiglu ? row + a.N / 2 : row + 64, x0 = t.m0 + rank * (NT / 2);
         for (int k = 0; k < steps; ++k) {
-          if (wrapped && !(ok = wait_cluster(&empty[r.stage], r.parity ^ 1, &s_err))) break;
+          if (wrapped && !(ok = wait_short(&empty[r.stage], r.parity ^ 1, &s_err))) break;
           uint8_t* st = sm + r.stage * C::kStage;
           mbar_expect_tx(&full_c[r.stage], kCodeBytes);
           tma_2d(st, &mC, k * 64, row, &full_c[r.stage]);
@@ -413,7 +451,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint64_t d0 = umma_desc_sw128(su32(sm));
       for (int tile = pair; tile < tiles && ok; tile += pairs) {
         for (int k = 0; k < steps && ok; ++k) {
-          if (!(ok = wait_cluster(&full_x[r.stage], r.parity, &s_err) && wait_cluster(&a_full[ar.stage], ar.parity, &s_err))) break;
+          if (!(ok = wait_short(&full_x[r.stage], r.parity, &s_err) && wait_short(&a_full[ar.stage], ar.parity, &s_err))) break;
           tc_fence_after();
           const uint64_t db = d0 + (uint32_t)((r.stage * C::kStage + kCodeBytes) / 16);
           const uint32_t ta = tmem_a + ar.stage * 64;
@@ -421,7 +459,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int g = 0; g < 128 / G; ++g) {
             if (g * G >= left) break;
-            if (used >= C::kBufs && !(ok = wait_cluster(&acc_empty[acc.stage], acc.parity ^ 1, &s_err))) break;
+            if (used >= C::kBufs && !(ok = wait_short(&acc_empty[acc.stage], acc.parity ^ 1, &s_err))) break;
             tc_fence_after();
             const uint32_t d = tmem + acc.stage * NT;
 #pragma unroll
@@ -442,55 +480,56 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
   } else if (warp < 8) {
-    // codes of row q * 32 + lane, K from h * 64 within the step
-    const int h = warp >> 2, q = warp & 3, row = q * 32 + lane;
+    // codes of row q * 32 + lane: four warps take the even steps, four the odd ones
+    const int set = warp >> 2, q = warp & 3, row = q * 32 + lane;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    RingPos r(kTileStages), ar(kAStages);
-    int n = 0;   // steps so far
-    constexpr int kZeros = G == 32 ? 2 : 1;
-    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+    constexpr int kGroups = 128 / G, kPer = 4 / kGroups;   // groups of a step, steps of four groups
+    int n0 = 0;   // steps before the tile
+    for (int tile = pair; tile < tiles && ok; tile += pairs, n0 += steps) {
       const Tile t = tile_at(tile);
       const int o = t.o0 + (swiglu ? row & 63 : row);
       const long long wr = (long long)e * a.N + (swiglu && row >= 64 ? a.N / 2 : 0) + min(o, outs - 1);
-      const uint8_t* zp = a.zeros ? a.zeros + wr * groups : nullptr;
-      uint32_t z[kZeros];
-      auto zeros_of = [&](int k) {
-#pragma unroll
-        for (int i = 0; i < kZeros; ++i) {
-          const int g = (k * 128 + h * 64 + i * 32) / G;
-          z[i] = zp && g < groups ? zp[g] : 8u;
+      Four<1> zeros(a.zeros ? a.zeros + wr * groups : nullptr, a.zeros ? groups : 0);
+      const int k0 = (n0 ^ set) & 1;   // these warps' first step of the tile
+      zeros.fetch(k0 / kPer);
+      int batch = -1;
+      uint32_t z4 = 0x08080808u;
+      for (int k = k0; k < steps; k += 2) {
+        if (k / kPer != batch) {
+          batch = k / kPer;
+          if (a.zeros) z4 = zeros.value(batch);
+          zeros.fetch(kPer == 1 ? batch + 2 : batch + 1);
         }
-      };
-      zeros_of(0);
-      for (int k = 0; k < steps; ++k) {
-        uint32_t zero[kZeros];
+        const int n = n0 + k, st = n % kTileStages, as = n % kAStages;
+        if (!(ok = __all_sync(0xffffffffu, wait_short(&full_c[st], (n / kTileStages) & 1, &s_err)))) break;
+        const uint8_t* codes = sm + st * C::kStage + row * 64;
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < kZeros; ++i) zero[i] = W4<TE>::kMagic + z[i] * 0x00010001u;
-        zeros_of(k + 1);
-        if (!(ok = __all_sync(0xffffffffu, wait_cluster(&full_c[r.stage], r.parity, &s_err)))) break;
-        const uint8_t* st = sm + r.stage * C::kStage + row * 64;
-        uint32_t w[8], v[32];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 u = *reinterpret_cast<const uint4*>(st + (((h * 2 + i) ^ ((row >> 1) & 3)) << 4));
+        for (int i = 0; i < 4; ++i) {
+          const uint4 u = *reinterpret_cast<const uint4*>(codes + ((i ^ ((row >> 1) & 3)) << 4));
           w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) unpack_in_order<TE>(w[i], zero[kZeros == 2 ? i >> 2 : 0], v + 4 * i);
         // the step that last used this A stage has been multiplied: its own ring stage was given back
         if (n >= kAStages) {
           const int p = n - kAStages;
-          if (!(ok = __all_sync(0xffffffffu, wait_cluster(&empty[p % kTileStages], (p / kTileStages) & 1, &s_err)))) break;
+          if (!(ok = __all_sync(0xffffffffu, wait_short(&empty[p % kTileStages], (p / kTileStages) & 1, &s_err)))) break;
           tc_fence_after();
         }
-        tmem_st32(tmem_a + lanes + ar.stage * 64 + h * 32, v);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int g = (h * 64 + i * 8) / G;   // within the step
+            const uint32_t z = z4 >> ((k % kPer * kGroups + g) * 8) & 255;
+            unpack_in_order<TE>(w[h * 8 + i], W4<TE>::kMagic + z * 0x00010001u, v + 4 * i);
+          }
+          tmem_st32(tmem_a + lanes + as * 64 + h * 32, v);
+        }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(cluster_addr(&a_full[ar.stage], 0));
-        r.next();
-        ar.next();
-        ++n;
+        if (lane == 0) arrive_pair(cluster_addr(&a_full[as], 0));
       }
     }
   } else {
@@ -503,32 +542,45 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const Tile t = tile_at(tile);
       const int o = t.o0 + (swiglu ? row & 63 : row);
       const long long wr = (long long)e * a.N + (swiglu && row >= 64 ? a.N / 2 : 0) + min(o, outs - 1);
-      const TE* sp = reinterpret_cast<const TE*>(a.scales) + wr * groups;
+      Four<2> scales(reinterpret_cast<const TE*>(a.scales) + wr * groups, groups);
+      scales.fetch(0);
+      F32x2 total[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) total[i].v = 0;
+      for (int b = 0; b * 4 < groups && ok; ++b) {
+        const uint64_t s4 = scales.value(b);
+        scales.fetch(b + 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (b * 4 + j >= groups) break;
+          const float s = W4<TE>::scale((uint32_t)(s4 >> (16 * j)) & 0xffff);
+          ok = __all_sync(0xffffffffu, ok && wait_short(&acc_full[acc.stage], acc.parity, &s_err));
+          if (!ok) break;
+          tc_fence_after();
+          const F32x2 by = pair_of(s, s);
+          const uint32_t at = tmem + lanes + acc.stage * NT + h * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            uint32_t u[32];
+            tmem_ld16_nw(at + c, u);
+            if (kCols >= 32) tmem_ld16_nw(at + c + 16, u + 16);
+            tmem_ld_wait16(u);
+            if (kCols >= 32) tmem_ld_fence16(u + 16);
+#pragma unroll
+            for (int i = 0; i < (kCols < 32 ? kCols : 32); i += 2)
+              total[(c + i) / 2] = fma_pair(by, pair_of(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), total[(c + i) / 2]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_pair(cluster_addr(&acc_empty[acc.stage], 0));
+          acc.next();
+        }
+      }
       float sum[kCols];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
-      TE next = sp[0];
-      for (int g = 0; g < groups; ++g) {
-        const float s = to_f32(next);
-        if (g + 1 < groups) next = sp[g + 1];
-        ok = __all_sync(0xffffffffu, ok && wait_cluster(&acc_full[acc.stage], acc.parity, &s_err));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t at = tmem + lanes + acc.stage * NT + h * kCols;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          uint32_t u[32];
-          tmem_ld16_nw(at + c, u);
-          if (kCols >= 32) tmem_ld16_nw(at + c + 16, u + 16);
-          tmem_ld_wait16(u);
-          if (kCols >= 32) tmem_ld_fence16(u + 16);
-#pragma unroll
-          for (int i = 0; i < (kCols < 32 ? kCols : 32); ++i) sum[c + i] = fmaf(s, __uint_as_float(u[i]), sum[c + i]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(cluster_addr(&acc_empty[acc.stage], 0));
-        acc.next();
+      for (int i = 0; i < kCols; i += 2) {
+        const float2 f = halves_of(total[i / 2]);
+        sum[i] = f.x, sum[i + 1] = f.y;
       }
       if (!ok)
 #pragma unroll

@@ -28,36 +28,56 @@ struct W4Args {
 
 constexpr int kMaxExperts = 2048;
 
+// A 16-bit float whose high bits are 0 is its low bits times the type's smallest number (2^-133 in
+// bf16, 2^-24 in f16; with the lowest bit of the exponent among them too).  So a code, in the
+// low four bits or the next four, is a number already, and one fused multiply-add brings it to
+// (q - z) kUnit, exactly: no conversion, no bits of an exponent to put in.  1 / kUnit goes
+// into the sums at the end.
 template <typename TE>
 struct W4;
 template <>
 struct W4<__nv_bfloat16> {
-  static constexpr uint32_t kMagic = 0x43004300u;   // 128: a nibble in its low bits is 128 + q
-  static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+  static constexpr float kUp = 64.f;                                       // 1 / kUnit
+  static constexpr uint32_t kLow = 0x7f007f00u, kHigh = 0x7d007d00u;       // 2^127, 2^123: codes in bits 0 to 3, 4 to 7
+  static constexpr uint32_t kBoth = 0x7d007f00u;                           // one of each
+  static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+  }
+  static __device__ __forceinline__ uint32_t offset(uint32_t z) {          // -z kUnit, twice
+    const uint32_t h = __float_as_uint((float)z * (-1.f / kUp));           // 8 bits: exact
+    return __byte_perm(h, h, 0x3232);
   }
   static __device__ __forceinline__ float scale(uint32_t packed) { return __uint_as_float(packed << 16); }
 };
 template <>
 struct W4<__half> {
-  static constexpr uint32_t kMagic = 0x64006400u;   // 1024
-  static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+  static constexpr float kUp = 512.f;
+  static constexpr uint32_t kLow = 0x78007800u, kHigh = 0x68006800u;       // 2^15, 2^11
+  static constexpr uint32_t kBoth = 0x68007800u;
+  static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+  }
+  static __device__ __forceinline__ uint32_t offset(uint32_t z) {
+    const __half2 h = __float2half2_rn((float)z * (-1.f / kUp));
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
   static __device__ __forceinline__ float scale(uint32_t packed) {
     return __half2float(__ushort_as_half((unsigned short)packed));
   }
 };
 
-// Eight codes of a word less the zero point (`zero`: kMagic + z in both halves), as the
-// pairs (0, 4), (1, 5), (2, 6), (3, 7): a nibble ORed into the mantissa of 128 (bf16) or
-// 1024 (f16) is that number plus the code.
+// Eight codes of a word less the zero point, times kUnit, as the pairs (0, 4), (1, 5), (2, 6), (3, 7).
 template <typename TE>
-__device__ __forceinline__ void unpack(uint32_t w, uint32_t zero, uint32_t (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = W4<TE>::sub(((w >> (4 * i)) & 0x000f000fu) | W4<TE>::kMagic, zero);
+__device__ __forceinline__ void unpack(uint32_t w, uint32_t offset, uint32_t (&v)[4]) {
+  const uint32_t up = w >> 8;
+  v[0] = W4<TE>::fma(w & 0x000f000fu, W4<TE>::kLow, offset);
+  v[1] = W4<TE>::fma(w & 0x00f000f0u, W4<TE>::kHigh, offset);
+  v[2] = W4<TE>::fma(up & 0x000f000fu, W4<TE>::kLow, offset);
+  v[3] = W4<TE>::fma(up & 0x00f000f0u, W4<TE>::kHigh, offset);
 }
 
 template <typename TE>
@@ -180,7 +200,7 @@ __global__ void __launch_bounds__(256) w4_rows_kernel(const W4Args a, int swiglu
         for (int j = 0; j < 4; ++j) {
           if (i + j >= i1) break;
           const uint32_t b0 = __shfl_sync(0xffffffffu, p0, (lane & ~3) | j), b1 = __shfl_sync(0xffffffffu, p1, (lane & ~3) | j);
-          const uint32_t k0 = W4<TE>::kMagic + (b0 >> 16) * 0x00010001u, k1 = W4<TE>::kMagic + (b1 >> 16) * 0x00010001u;
+          const uint32_t k0 = W4<TE>::offset(b0 >> 16), k1 = W4<TE>::offset(b1 >> 16);
           float d[4] = {};
 #pragma unroll
           for (int w = 0; w < WPL; ++w) {
@@ -213,6 +233,8 @@ __global__ void __launch_bounds__(256) w4_rows_kernel(const W4Args a, int swiglu
     }
     if (KS == 1 || ks == 0) {
 #pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] *= W4<TE>::kUp;
+#pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (2 * c + i >= m) continue;
         const long long o = (t0 + 2 * c + i) * a.ld_out + o0 + g;
@@ -234,7 +256,7 @@ __global__ void __launch_bounds__(256) w4_rows_kernel(const W4Args a, int swiglu
 
 // ------------------------------------------------------------- tiles, tcgen05 --
 
-// Waits for the phase of parity `parity`, at most a second.  A wait that gives up says so in
+// Waits for the phase of parity `parity`, at most a second or so.  A wait that gives up says so in
 // *err, and ends the block's other waits.
 static __device__ __noinline__ bool wait_long(uint64_t* b, uint32_t parity, int* err) {
   const uint64_t t0 = gtimer();
@@ -244,8 +266,10 @@ static __device__ __noinline__ bool wait_long(uint64_t* b, uint32_t parity, int*
   }
   return false;
 }
-__device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, int* err) {
-  return test_wait(b, parity) || wait_long(b, parity, err);
+// `ready`: what an earlier test_wait said.  A test takes some 150 clocks whatever it finds, and three
+// or four of them one after the other a third of a step: they are made early, under other work.
+__device__ __forceinline__ bool wait_unless(bool ready, uint64_t* b, uint32_t parity, int* err) {
+  return ready || mbar_try_wait(b, parity, 20000) || wait_long(b, parity, err);
 }
 // Arrives on a barrier of the pair.  What crosses the blocks here is in tensor memory, written or
 // read before a tcgen05 fence: nothing of the block's other memory goes with the arrival, and
@@ -262,7 +286,7 @@ __device__ __forceinline__ void mma_k16_pair_ta(uint32_t d, uint32_t a, uint64_t
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
@@ -272,15 +296,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
-// unpack, in the codes' own order: (0, 1), (2, 3), (4, 5), (6, 7).
+// The same in the codes' own order, (0, 1), (2, 3), (4, 5), (6, 7): a byte of the low codes, one of
+// the high ones, and zeros (the sign of a byte below 128) between them.
+template <int I>
+__device__ __forceinline__ uint32_t code_pair(uint32_t low, uint32_t high) {
+  uint32_t p;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(p) : "r"(low), "r"(high), "n"(I | 0x80 | (4 + I) << 8 | 0x8000));
+  return p;
+}
 template <typename TE>
-__device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t zero, uint32_t* v) {
-  const uint32_t odd = w >> 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = __byte_perm(w, odd, (uint32_t)(i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12)));
-    v[i] = W4<TE>::sub((u & 0x000f000fu) | W4<TE>::kMagic, zero);
-  }
+__device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t offset, uint32_t* v) {
+  const uint32_t low = w & 0x0f0f0f0fu, high = w & 0xf0f0f0f0u;
+  v[0] = W4<TE>::fma(code_pair<0>(low, high), W4<TE>::kBoth, offset);
+  v[1] = W4<TE>::fma(code_pair<1>(low, high), W4<TE>::kBoth, offset);
+  v[2] = W4<TE>::fma(code_pair<2>(low, high), W4<TE>::kBoth, offset);
+  v[3] = W4<TE>::fma(code_pair<3>(low, high), W4<TE>::kBoth, offset);
 }
 
 // Many rows of x to a matrix: persistent pairs of blocks (cta_group::2, a block per SM)
@@ -291,8 +321,9 @@ __device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t zero, uint3
 // multiplies for both blocks into an accumulator for each group of the scales; and eight
 // warps multiply each accumulator by its scales - a scale belongs to a tensor memory lane -
 // and add it up in registers while the next ones fill.
-constexpr int kTileThreads = 576;   // 8 warps of codes, 8 of sums, TMA, MMA
-constexpr int kTileStages = 8, kAStages = 4, kCodeBytes = 128 * 64;
+constexpr int kTileThreads = 640;   // TMA, MMA, two warps that only fill a group of four, 8 of codes, 8 of sums
+constexpr int kTileStages = 8, kCodeBytes = 128 * 64;
+constexpr int kAStages = 2, kACols = 384;   // A: two steps in the last 128 columns of tensor memory
 constexpr int kExchange = 2 * 16 * 64 * 4;
 // Four neighbouring elements of B bytes of a row's array, fetched a batch ahead: a lane's row is
 // its own cache line, and a load of every element by itself takes the L1's time 32 times.
@@ -337,7 +368,7 @@ __device__ __forceinline__ F32x2 fma_pair(F32x2 a, F32x2 b, F32x2 c) {
 template <int NT>
 struct TileCfg {
   static constexpr int kStage = kCodeBytes + NT / 2 * 256;
-  static constexpr int kBufs = 256 / NT;   // accumulators: half of tensor memory, A the other half
+  static constexpr int kBufs = kACols / NT;   // accumulators
   static constexpr int kRing = kTileStages * kStage;
 };
 static size_t tile_smem(int ring, int E) { return (size_t)ring + kExchange + 1024 + (size_t)(E + 1) * 8; }
@@ -375,7 +406,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     s_err = MOE_OK;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 17) {
+  if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_slot)),
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -405,7 +436,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncwarp();
   cluster_sync();   // the barriers of both are there
   tc_fence_after();
-  const uint32_t tmem = tmem_slot, tmem_a = tmem + 256;
+  const uint32_t tmem = tmem_slot, tmem_a = tmem + kACols;
   const int steps = (a.K + 127) / 128, groups = a.K / G;
   bool ok = true;
 
@@ -421,15 +452,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     return Tile{m0, hi < m0 + NT ? hi : m0 + NT, rt * per + rank * (per / 2)};
   };
 
-  if (warp == 16) {
-    if (elect_one()) {
+  if (warp < 4) {
+    if (warp == 0 && elect_one()) {
       RingPos r(kTileStages);
       bool wrapped = false;
       for (int tile = pair; tile < tiles && ok; tile += pairs) {
         const Tile t = tile_at(tile);
         const int row = e * a.N + t.o0, row2 = swiglu ? row + a.N / 2 : row + 64, x0 = t.m0 + rank * (NT / 2);
         for (int k = 0; k < steps; ++k) {
-          if (wrapped && !(ok = wait_short(&empty[r.stage], r.parity ^ 1, &s_err))) break;
+          if (wrapped && !(ok = wait_unless(false, &empty[r.stage], r.parity ^ 1, &s_err))) break;
           uint8_t* st = sm + r.stage * C::kStage;
           mbar_expect_tx(&full_c[r.stage], kCodeBytes);
           tma_2d(st, &mC, k * 64, row, &full_c[r.stage]);
@@ -443,23 +474,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
     }
-  } else if (warp == 17) {
-    if (rank == 0 && elect_one()) {
+    if (warp == 1 && rank == 0 && elect_one()) {
       RingPos r(kTileStages), ar(kAStages), acc(C::kBufs);
       int used = 0;
       const uint32_t idesc = idesc_pair(NT, std::is_same<TE, __nv_bfloat16>::value);
       const uint64_t d0 = umma_desc_sw128(su32(sm));
+      bool x_there = false, a_there = false, acc_free = false;
       for (int tile = pair; tile < tiles && ok; tile += pairs) {
         for (int k = 0; k < steps && ok; ++k) {
-          if (!(ok = wait_short(&full_x[r.stage], r.parity, &s_err) && wait_short(&a_full[ar.stage], ar.parity, &s_err))) break;
-          tc_fence_after();
+          const int last = min(a.K - k * 128, 128) / 16 - 1;
+          ok = wait_unless(x_there, &full_x[r.stage], r.parity, &s_err) &&
+               wait_unless(a_there, &a_full[ar.stage], ar.parity, &s_err);
           const uint64_t db = d0 + (uint32_t)((r.stage * C::kStage + kCodeBytes) / 16);
           const uint32_t ta = tmem_a + ar.stage * 64;
-          const int left = a.K - k * 128;
+          uint64_t* done = &empty[r.stage];
+          r.next();
+          ar.next();
 #pragma unroll
           for (int g = 0; g < 128 / G; ++g) {
-            if (g * G >= left) break;
-            if (used >= C::kBufs && !(ok = wait_short(&acc_empty[acc.stage], acc.parity ^ 1, &s_err))) break;
+            if (g * (G / 16) > last || !ok) break;
+            if (used >= C::kBufs && !(ok = wait_unless(acc_free, &acc_empty[acc.stage], acc.parity ^ 1, &s_err))) break;
             tc_fence_after();
             const uint32_t d = tmem + acc.stage * NT;
 #pragma unroll
@@ -467,23 +501,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               const int j = g * (G / 16) + i;
               mma_k16_pair_ta(d, ta + j * 8, db + (j >> 2) * (NT / 2 * 128 / 16) + (j & 3) * 2, idesc, i != 0);
             }
-            // the stage's commit goes first: no arrival is under way once the last accumulator has been seen
-            if ((g + 1) * G >= left || g == 128 / G - 1) mma_commit_pair(&empty[r.stage]);
-            mma_commit_pair(&acc_full[acc.stage]);
+            uint64_t* full = &acc_full[acc.stage];
             acc.next();
             ++used;
+            acc_free = mbar_test(&acc_empty[acc.stage], acc.parity ^ 1);
+            if ((g + 1) * (G / 16) > last) {
+              x_there = mbar_test(&full_x[r.stage], r.parity);
+              a_there = mbar_test(&a_full[ar.stage], ar.parity);
+              mma_commit_pair(done);   // first: no commit is under way once the last accumulator has been seen
+            }
+            mma_commit_pair(full);
           }
-          if (!ok) break;
-          r.next();
-          ar.next();
         }
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // codes of row q * 32 + lane: four warps take the even steps, four the odd ones
-    const int set = warp >> 2, q = warp & 3, row = q * 32 + lane;
-    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    const int set = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16, full_at = cluster_addr(&a_full[set], 0);
     constexpr int kGroups = 128 / G, kPer = 4 / kGroups;   // groups of a step, steps of four groups
+    const uint8_t* codes = sm + row * 64;
+    const int swizzle = ((row >> 1) & 3) << 4;
+    bool codes_there = false;
     int n0 = 0;   // steps before the tile
     for (int tile = pair; tile < tiles && ok; tile += pairs, n0 += steps) {
       const Tile t = tile_at(tile);
@@ -500,44 +539,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (a.zeros) z4 = zeros.value(batch);
           zeros.fetch(kPer == 1 ? batch + 2 : batch + 1);
         }
-        const int n = n0 + k, st = n % kTileStages, as = n % kAStages;
-        if (!(ok = __all_sync(0xffffffffu, wait_short(&full_c[st], (n / kTileStages) & 1, &s_err)))) break;
-        const uint8_t* codes = sm + st * C::kStage + row * 64;
-        uint32_t w[16];
+        const int n = n0 + k, st = n % kTileStages, p = n - kAStages;
+        ok = wait_unless(codes_there, &full_c[st], (n / kTileStages) & 1, &s_err);
+        // the step that last used this A stage: its own ring stage is given back once it has been multiplied
+        const bool free = p < 0 || mbar_test(&empty[p % kTileStages], (p / kTileStages) & 1);
+        uint32_t v[64];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 u = *reinterpret_cast<const uint4*>(codes + ((i ^ ((row >> 1) & 3)) << 4));
-          w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+          const uint4 w = *reinterpret_cast<const uint4*>(codes + st * C::kStage + ((i << 4) ^ swizzle));
+          const uint32_t offset = W4<TE>::offset(z4 >> ((k % kPer * kGroups + i * 32 / G) * 8) & 255);
+          unpack_in_order<TE>(w.x, offset, v + 16 * i);
+          unpack_in_order<TE>(w.y, offset, v + 16 * i + 4);
+          unpack_in_order<TE>(w.z, offset, v + 16 * i + 8);
+          unpack_in_order<TE>(w.w, offset, v + 16 * i + 12);
         }
-        // the step that last used this A stage has been multiplied: its own ring stage was given back
-        if (n >= kAStages) {
-          const int p = n - kAStages;
-          if (!(ok = __all_sync(0xffffffffu, wait_short(&empty[p % kTileStages], (p / kTileStages) & 1, &s_err)))) break;
-          tc_fence_after();
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int g = (h * 64 + i * 8) / G;   // within the step
-            const uint32_t z = z4 >> ((k % kPer * kGroups + g) * 8) & 255;
-            unpack_in_order<TE>(w[h * 8 + i], W4<TE>::kMagic + z * 0x00010001u, v + 4 * i);
-          }
-          tmem_st32(tmem_a + lanes + as * 64 + h * 32, v);
-        }
+        ok = ok && wait_unless(free, &empty[p % kTileStages], (p / kTileStages) & 1, &s_err);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        tmem_st32(tmem_a + lanes + set * 64, v);
+        tmem_st32(tmem_a + lanes + set * 64 + 32, v + 32);
+        codes_there = mbar_test(&full_c[(n + 2) % kTileStages], ((n + 2) / kTileStages) & 1);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_pair(cluster_addr(&a_full[as], 0));
+        if (lane == 0) arrive_pair(full_at);
       }
     }
   } else {
     // sums of row q * 32 + lane, columns from h * NT / 2
     constexpr int kCols = NT / 2;
-    const int q = warp & 3, h = (warp - 8) >> 2, row = q * 32 + lane;
+    const int q = warp & 3, h = (warp - 12) >> 2, row = q * 32 + lane;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    const uint32_t empty_at = cluster_addr(&acc_empty[0], 0);
     RingPos acc(C::kBufs);
+    bool sums_there = false;
     for (int tile = pair; tile < tiles; tile += pairs) {   // a wait that gave up: NaN to the end
       const Tile t = tile_at(tile);
       const int o = t.o0 + (swiglu ? row & 63 : row);
@@ -554,33 +589,38 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int j = 0; j < 4; ++j) {
           if (b * 4 + j >= groups) break;
           const float s = W4<TE>::scale((uint32_t)(s4 >> (16 * j)) & 0xffff);
-          ok = __all_sync(0xffffffffu, ok && wait_short(&acc_full[acc.stage], acc.parity, &s_err));
-          if (!ok) break;
+          ok = wait_unless(sums_there, &acc_full[acc.stage], acc.parity, &s_err);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
           const F32x2 by = pair_of(s, s);
-          const uint32_t at = tmem + lanes + acc.stage * NT + h * kCols;
-#pragma unroll
-          for (int c = 0; c < kCols; c += 32) {
-            uint32_t u[32];
-            tmem_ld16_nw(at + c, u);
-            if (kCols >= 32) tmem_ld16_nw(at + c + 16, u + 16);
-            tmem_ld_wait16(u);
-            if (kCols >= 32) tmem_ld_fence16(u + 16);
-#pragma unroll
-            for (int i = 0; i < (kCols < 32 ? kCols : 32); i += 2)
-              total[(c + i) / 2] = fma_pair(by, pair_of(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), total[(c + i) / 2]);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_pair(cluster_addr(&acc_empty[acc.stage], 0));
+          const uint32_t at = tmem + lanes + acc.stage * NT + h * kCols, free_at = empty_at + acc.stage * 8;
           acc.next();
+          uint32_t u[2][16];   // 16 columns are on their way while 16 are added
+          tmem_ld16_nw(at, u[0]);
+          tmem_ld_wait16(u[0]);
+#pragma unroll
+          for (int c = 0; c < kCols / 16; ++c) {
+            uint32_t* mine = u[c & 1];
+            if (c + 1 < kCols / 16) {
+              tmem_ld16_nw(at + (c + 1) * 16, u[(c + 1) & 1]);
+            } else {   // all of it is in registers
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) arrive_pair(free_at);
+              sums_there = mbar_test(&acc_full[acc.stage], acc.parity);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+              total[c * 8 + i / 2] = fma_pair(by, pair_of(__uint_as_float(mine[i]), __uint_as_float(mine[i + 1])), total[c * 8 + i / 2]);
+            if (c + 1 < kCols / 16) tmem_ld_wait16(u[(c + 1) & 1]);
+          }
         }
       }
       float sum[kCols];
 #pragma unroll
       for (int i = 0; i < kCols; i += 2) {
         const float2 f = halves_of(total[i / 2]);
-        sum[i] = f.x, sum[i + 1] = f.y;
+        sum[i] = f.x * W4<TE>::kUp, sum[i + 1] = f.y * W4<TE>::kUp;
       }
       if (!ok)
 #pragma unroll
@@ -625,7 +665,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_before();
   __syncwarp();
   cluster_sync();   // nothing of this block is used by the other any more
-  if (warp == 17) {
+  if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }

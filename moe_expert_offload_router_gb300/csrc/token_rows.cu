@@ -38,34 +38,40 @@ struct Bytes<2> {
   using T = uint16_t;
 };
 
-// V neighbouring elements of T as fp32 (fp32: pieces of at most 16 bytes).
+// V neighbouring elements of T, as they lie in memory (fp32: pieces of at most 16 bytes): loaded
+// first and converted later, so that many loads are under way in few registers.
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[V]) {
-  constexpr int B = V * (int)sizeof(T), P = B > 16 ? 16 : B, E = P / (int)sizeof(T);
+struct Vec {
+  static constexpr int B = V * (int)sizeof(T), P = B > 16 ? 16 : B, E = P / (int)sizeof(T), N = V / E;
   using W = typename Bytes<P>::T;
+  W w[N];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < V / E; ++i) {
-    const W w = reinterpret_cast<const W*>(p)[i];
-    T e[E];
-    memcpy(e, &w, P);
-#pragma unroll
-    for (int j = 0; j < E; ++j) f[i * E + j] = to_f32(e[j]);
+    for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const W*>(p)[i];
   }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
-  constexpr int B = V * (int)sizeof(T), P = B > 16 ? 16 : B, E = P / (int)sizeof(T);
-  using W = typename Bytes<P>::T;
+  __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-  for (int i = 0; i < V / E; ++i) {
-    T e[E];
-    W w;
-#pragma unroll
-    for (int j = 0; j < E; ++j) e[j] = from_f32<T>(f[i * E + j]);
-    memcpy(&w, e, P);
-    reinterpret_cast<W*>(p)[i] = w;
+    for (int i = 0; i < N; ++i) reinterpret_cast<W*>(p)[i] = w[i];
   }
-}
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      T e[E];
+      memcpy(e, &w[i], P);
+#pragma unroll
+      for (int j = 0; j < E; ++j) f[i * E + j] = to_f32(e[j]);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      T e[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) e[j] = from_f32<T>(f[i * E + j]);
+      memcpy(&w[i], e, P);
+    }
+  }
+};
 
 // ---------------------------------------------------------------------- plan --
 
@@ -212,6 +218,89 @@ __global__ void __launch_bounds__(256) sort_rows_kernel(const SortArgs a) {
   }
 }
 
+// Few pairs: one launch, each block placing the pairs of its own tokens by counting, a warp to a pair,
+// the pairs that come before it; the last block writes the offsets.  Latency: a launch and a
+// round trip to memory more than the copy.
+constexpr int kSmallPairs = 1024;
+struct SmallSortArgs {
+  SortArgs s;
+  int E;
+  const int32_t* ids;
+  int32_t *offsets, *pos, *err;
+};
+template <int VB>
+__global__ void __launch_bounds__(256) sort_small_kernel(const SmallSortArgs a) {
+  using W = typename Bytes<VB>::T;
+  __shared__ alignas(16) int ids[kSmallPairs];
+  __shared__ int place[kSmallPairs], cnt[kMaxE], ws[34];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, k = a.s.k, P = a.s.T * k;
+  pdl_wait();
+  pdl_launch_dependents();
+  const bool last = blockIdx.x == gridDim.x - 1;
+  const long long i0 = (long long)blockIdx.x * (256 * kItems);
+  const int t0 = last ? 0 : (int)(i0 / a.s.nv), v0 = (int)(i0 - (long long)t0 * a.s.nv);
+  W w[kItems];
+  int t[kItems], v[kItems];
+#pragma unroll
+  for (int u = 0; u < kItems; ++u) {
+    const unsigned at = (unsigned)v0 + u * 256 + tid, q = at / (unsigned)a.s.nv;
+    t[u] = last ? a.s.T : t0 + (int)min(q, (unsigned)a.s.T), v[u] = (int)(at - q * a.s.nv);
+    if (t[u] < a.s.T) w[u] = reinterpret_cast<const W*>(a.s.x + t[u] * a.s.ld_x)[v[u]];
+  }
+  bool bad = false;
+  for (int p = tid; p < kSmallPairs; p += 256) {
+    int e = p < P ? a.ids[p] : -1;
+    bad |= e >= a.E;
+    ids[p] = e >= 0 && e < a.E ? e : kMaxE;   // without an expert: after all others
+  }
+  if (last) {
+    if (bad && a.err) atomicExch(a.err, MOE_ERR_INVALID);
+    for (int e = tid; e < a.E; e += 256) cnt[e] = 0;
+  }
+  __syncthreads();
+  if (last) {
+    for (int p = tid; p < P; p += 256)
+      if (ids[p] < kMaxE) atomicAdd(&cnt[ids[p]], 1);
+    __syncthreads();
+    const int per = (a.E + 255) / 256, e0 = min(a.E, tid * per), e1 = min(a.E, e0 + per);
+    int sum = 0, all;
+    for (int e = e0; e < e1; ++e) sum += cnt[e];
+    int run = block_exclusive_scan(sum, ws, &all);
+    for (int e = e0; e < e1; ++e) {
+      a.offsets[e] = run;
+      run += cnt[e];
+    }
+    if (tid == 0) a.offsets[a.E] = all;
+    return;
+  }
+  const int t1 = (int)min((long long)a.s.T - 1, (i0 + 256 * kItems - 1) / a.s.nv), p0 = t0 * k, n = (t1 - t0 + 1) * k;
+  for (int i = warp; i < n; i += 8) {
+    const int p = p0 + i, e = ids[p];
+    int before = 0;
+    for (int q = lane * 4; q < P; q += 128) {   // past the pairs: kMaxE
+      const int4 o = *reinterpret_cast<const int4*>(ids + q);
+      before += (o.x < e || (o.x == e && q < p)) + (o.y < e || (o.y == e && q + 1 < p)) +
+                (o.z < e || (o.z == e && q + 2 < p)) + (o.w < e || (o.w == e && q + 3 < p));
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) {
+      place[i] = e < kMaxE ? before : -1;
+      if (v0 == 0 || i >= k) a.pos[p] = place[i];   // a token's first vector is this block's
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kItems; ++u) {
+    if (t[u] >= a.s.T) break;
+    const int* mine = place + (t[u] - t0) * k;
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) {
+      const int p = mine[j];
+      if (p >= 0) reinterpret_cast<W*>(a.s.rows + p * a.s.ld_rows)[v[u]] = w[u];
+    }
+  }
+}
+
 // ------------------------------------------------------------------- combine --
 
 struct CombineArgs {
@@ -236,31 +325,42 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const CombineArgs a) 
   const TR* rows = reinterpret_cast<const TR*>(a.rows) + c;
   const int32_t* pos = a.pos + t * a.k;
   const float* w = a.w ? a.w + t * a.k : nullptr;
+  Vec<TY, V> base;
+  if (a.base) base.load(reinterpret_cast<const TY*>(a.base) + t * a.ld_base + c);
   float s[V] = {};
 #pragma unroll 1
   for (int j0 = 0; j0 < a.k; j0 += 8) {
-    float f[8][V], by[8];
-    bool on[8];
+    Vec<TR, V> r[8];
+    float by[8];
+    int p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int p = j0 + j < a.k ? pos[j0 + j] : -1;
-      on[j] = p >= 0 && p < a.n_rows;
-      if (on[j]) load_vec<TR, V>(rows + p * a.ld_rows, f[j]);
-      by[j] = on[j] && w ? w[j0 + j] : 1.f;
+      p[j] = j0 + j < a.k ? pos[j0 + j] : -1;
+      by[j] = j0 + j < a.k && w ? w[j0 + j] : 1.f;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (on[j])
+    for (int j = 0; j < 8; ++j) {
+      if (p[j] >= a.n_rows) p[j] = -1;
+      if (p[j] >= 0) r[j].load(rows + p[j] * a.ld_rows);
+    }
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = fmaf(by[j], f[j][i], s[i]);
+    for (int j = 0; j < 8; ++j) {
+      float f[V];
+      r[j].get(f);
+      if (p[j] >= 0)
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = fmaf(by[j], f[i], s[i]);
+    }
   }
   if (a.base) {
     float b[V];
-    load_vec<TY, V>(reinterpret_cast<const TY*>(a.base) + t * a.ld_base + c, b);
+    base.get(b);
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] += b[i];
   }
-  store_vec<TY, V>(reinterpret_cast<TY*>(a.y) + t * a.ld_y + c, s);
+  Vec<TY, V> y;
+  y.set(s);
+  y.store(reinterpret_cast<TY*>(a.y) + t * a.ld_y + c);
 }
 
 // ---------------------------------------------------------- combine, backward --
@@ -274,6 +374,24 @@ struct CombineBwdArgs {
   const float* w;
   float* dw;
 };
+
+// Eight sums over a warp, halving: lane l comes out with sum l >> 2 (a lane's eight values are dealt out, four
+// to each half, then two, then one, 9 exchanges for 40).
+__device__ __forceinline__ float sum8(float (&s)[8]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 4; n > 0; n >>= 1) {
+    const bool up = lane & (n * 4);
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const float send = up ? s[j] : s[j + n], keep = up ? s[j + n] : s[j];
+      s[j] = keep + __shfl_xor_sync(0xffffffffu, send, n * 4);
+    }
+  }
+  float v = s[0];
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  return v + __shfl_xor_sync(0xffffffffu, v, 1);
+}
 
 // G threads to a token; its k products go eight at a time, each thread holding the eight
 // sums over its own columns.
@@ -290,53 +408,53 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdArgs a
   TR* d_rows = reinterpret_cast<TR*>(a.d_rows);
 #pragma unroll 1
   for (int j0 = 0; j0 < a.k; j0 += 8) {
-    long long p[8];
+    int p[8];
     float by[8], s[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int q = there && j0 + j < a.k ? a.pos[t * a.k + j0 + j] : -1;
-      p[j] = q < a.n_rows ? q : -1;
-      by[j] = p[j] >= 0 && a.w ? a.w[t * a.k + j0 + j] : 1.f;
+      p[j] = there && j0 + j < a.k ? a.pos[t * a.k + j0 + j] : -1;
+      by[j] = there && j0 + j < a.k && a.w ? a.w[t * a.k + j0 + j] : 1.f;
       s[j] = 0.f;
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (p[j] >= a.n_rows) p[j] = -1;
     if (there)
       for (int v = me; v < a.nv; v += G) {
-        float d[V], f[8][V];
+        Vec<TY, V> dv;
+        Vec<TR, V> r[8];
         const long long c = (long long)v * V;
-        load_vec<TY, V>(dy + c, d);
+        dv.load(dy + c);
         if (a.dw)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (p[j] >= 0) load_vec<TR, V>(rows + p[j] * a.ld_rows + c, f[j]);
+            if (p[j] >= 0) r[j].load(rows + p[j] * a.ld_rows + c);
+        float d[V];
+        dv.get(d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (p[j] < 0) continue;
+          if (a.dw) {
+            float f[V];
+            r[j].get(f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[j] = fmaf(d[i], f[i], s[j]);
+          }
           float o[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) o[i] = by[j] * d[i];
-          store_vec<TR, V>(d_rows + p[j] * a.ld_d_rows + c, o);
-          if (a.dw)
-#pragma unroll
-            for (int i = 0; i < V; ++i) s[j] = fmaf(d[i], f[j][i], s[j]);
+          r[j].set(o);
+          r[j].store(d_rows + p[j] * a.ld_d_rows + c);
         }
       }
     if (!a.dw) continue;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+    const float mine = sum8(s);
+    const int j = lane >> 2;
     if (G == 32) {
-      if (there && lane < 8 && j0 + lane < a.k) {
-        float v = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v = lane == j ? s[j] : v;
-        a.dw[t * a.k + j0 + lane] = v;
-      }
+      if (there && (lane & 3) == 0 && j0 + j < a.k) a.dw[t * a.k + j0 + j] = mine;
     } else {
       __syncthreads();
-      if (lane == 0)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) part[warp][j] = s[j];
+      if ((lane & 3) == 0) part[warp][j] = mine;
       __syncthreads();
       if (there && me < 8 && j0 + me < a.k) {
         float v = 0.f;
@@ -384,7 +502,8 @@ static moe_status launch_bwd_v(CombineBwdArgs a, int H, cudaStream_t s) {
   a.nv = H / V;
   const char* name = "combine_bwd_kernel";
   auto blocks = [&](int G) { return ((long long)a.T + 256 / G - 1) / (256 / G); };
-  if (a.nv <= 64) return launch_rows(combine_bwd_kernel<TR, TY, V, 32>, blocks(32), s, name, a);
+  if (a.nv <= 128) return launch_rows(combine_bwd_kernel<TR, TY, V, 32>, blocks(32), s, name, a);
+  if (a.nv <= 512) return launch_rows(combine_bwd_kernel<TR, TY, V, 128>, blocks(128), s, name, a);
   return launch_rows(combine_bwd_kernel<TR, TY, V, 256>, blocks(256), s, name, a);
 }
 template <typename TR, typename TY>
@@ -460,7 +579,21 @@ extern "C" moe_status moe_sort_rows(int T, int k, int E, int H, int dtype, const
   MOE_ARG(x && topk_ids && rows && pos, "null pointer");
   MOE_ARG(ld_x >= H && ld_rows >= H, "a row distance is below the row's length");
   ProfScope ps(MOE_K_SORT_ROWS, stream);
-  const int P = T * k, warps = plan_warps(E);
+  const int sz = (int)dtype_size(dtype);
+  SortArgs a = {T, k, 0, (const uint8_t*)x, (uint8_t*)rows, ld_x * sz, ld_rows * sz, pos};
+  const long long width = (long long)H * sz;
+  auto fits = [&](int v) { return splits(x, a.ld_x, width, v) && splits(rows, a.ld_rows, 0, v); };
+  const int v = fits(16) ? 16 : fits(4) ? 4 : 2, P = T * k;
+  a.nv = (int)(width / v);
+  const long long blocks = ((long long)T * a.nv + 256 * kItems - 1) / (256 * kItems);
+  if (P <= kSmallPairs) {
+    const SmallSortArgs m = {a, E, topk_ids, offsets, pos, d_error};
+    const char* name = "sort_small_kernel";
+    if (v == 16) return launch_rows(sort_small_kernel<16>, blocks + 1, stream, name, m);
+    if (v == 4) return launch_rows(sort_small_kernel<4>, blocks + 1, stream, name, m);
+    return launch_rows(sort_small_kernel<2>, blocks + 1, stream, name, m);
+  }
+  const int warps = plan_warps(E);
   const size_t smem = (size_t)(warps + 2) * E * 4;
   static char allowed[64];
   MOE_CUDA(allow_smem(sort_plan_kernel, (size_t)(16 + 2) * kMaxE * 4, allowed));   // more than 32 warps of 1024 experts
@@ -469,13 +602,6 @@ extern "C" moe_status moe_sort_rows(int T, int k, int E, int H, int dtype, const
   if (e != cudaSuccess) return cuda_fail(e, "sort_plan_kernel");
   st = check_launch("sort_plan_kernel");
   if (st != MOE_OK) return st;
-  const int sz = (int)dtype_size(dtype);
-  SortArgs a = {T, k, 0, (const uint8_t*)x, (uint8_t*)rows, ld_x * sz, ld_rows * sz, pos};
-  const long long width = (long long)H * sz;
-  auto fits = [&](int v) { return splits(x, a.ld_x, width, v) && splits(rows, a.ld_rows, 0, v); };
-  const int v = fits(16) ? 16 : fits(4) ? 4 : 2;
-  a.nv = (int)(width / v);
-  const long long blocks = ((long long)T * a.nv + 256 * kItems - 1) / (256 * kItems);
   const char* name = "sort_rows_kernel";
   if (v == 16) return launch_rows(sort_rows_kernel<16>, blocks, stream, name, a);
   if (v == 4) return launch_rows(sort_rows_kernel<4>, blocks, stream, name, a);

@@ -307,7 +307,13 @@ __global__ void __launch_bounds__(256) sort_rows_kernel(const SortArgs a) {
 // Few pairs: one launch, each block placing the pairs of its own tokens by counting, a warp to a pair,
 // the pairs that come before it; the last block writes the offsets.  Latency: a launch and a
 // round trip to memory more than the copy.
-constexpr int kSmallPairs = 1024, kItems = 2;   // pairs; vectors of a thread
+constexpr int kSmallPairs = 4096, kItems = 2;   // pairs; vectors of a thread
+// Whether counting is quicker than sort_plan_kernel (which takes some 5 us): a block compares each of its own
+// pairs with all of them.
+static bool counts_pairs(int P, int k, int nv) {
+  const long long own = (256 * kItems / nv + 1LL) * k;
+  return P <= kSmallPairs && own * P <= 131072;
+}
 struct SmallSortArgs {
   SortArgs s;
   int E;
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(256) sort_small_kernel(const SmallSortArgs a) 
     if (t[u] < a.s.T) w[u] = reinterpret_cast<const W*>(a.s.x + t[u] * a.s.ld_x)[v[u]];
   }
   bool bad = false;
-  for (int p = tid; p < kSmallPairs; p += 256) {
+  for (int p = tid; p < (P + 127) / 128 * 128; p += 256) {
     int e = p < P ? a.ids[p] : -1;
     bad |= e >= a.E;
     ids[p] = e >= 0 && e < a.E ? e : kMaxE;   // without an expert: after all others
@@ -414,6 +420,10 @@ __global__ void __launch_bounds__(256, V == 8 ? 4 : 3) combine_rows_kernel(const
   bool in[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) in[u] = v + u * step < a.nv;
+  Vec<TY, V> base[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    base[u].load(a.base && in[u], reinterpret_cast<const TY*>(a.base) + t * a.ld_base + (long long)(v + u * step) * V);
   float s[U][V] = {};
 #pragma unroll 1
   for (int j0 = 0; j0 < a.k; j0 += J) {
@@ -446,14 +456,10 @@ __global__ void __launch_bounds__(256, V == 8 ? 4 : 3) combine_rows_kernel(const
   for (int u = 0; u < U; ++u) {
     if (!in[u]) continue;
     const long long c = (long long)(v + u * step) * V;
-    if (a.base) {
-      Vec<TY, V> base;
-      float b[V];
-      base.load(reinterpret_cast<const TY*>(a.base) + t * a.ld_base + c);
-      base.get(b);
+    float b[V];   // 0 without a base
+    base[u].get(b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[u][i] += b[i];
-    }
+    for (int i = 0; i < V; ++i) s[u][i] += b[i];
     Vec<TY, V> y;
     y.set(s[u]);
     y.store(reinterpret_cast<TY*>(a.y) + t * a.ld_y + c);
@@ -711,7 +717,7 @@ extern "C" moe_status moe_sort_rows(int T, int k, int E, int H, int dtype, const
   const int v = fits(16) ? 16 : fits(4) ? 4 : 2, P = T * k;
   a.nv = (int)(width / v);
   const long long blocks = ((long long)T * a.nv + 256 * kItems - 1) / (256 * kItems);
-  if (P <= kSmallPairs) {
+  if (counts_pairs(P, k, a.nv)) {
     const SmallSortArgs m = {a, E, topk_ids, offsets, pos, d_error};
     const char* name = "sort_small_kernel";
     if (v == 16) return launch_rows(sort_small_kernel<16>, blocks + 1, stream, name, m);

@@ -504,10 +504,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             uint64_t* full = &acc_full[acc.stage];
             acc.next();
             ++used;
-            acc_free = mbar_test(&acc_empty[acc.stage], acc.parity ^ 1);
+            acc_free = test_wait(&acc_empty[acc.stage], acc.parity ^ 1);
             if ((g + 1) * (G / 16) > last) {
-              x_there = mbar_test(&full_x[r.stage], r.parity);
-              a_there = mbar_test(&a_full[ar.stage], ar.parity);
+              x_there = test_wait(&full_x[r.stage], r.parity);
+              a_there = test_wait(&a_full[ar.stage], ar.parity);
               mma_commit_pair(done);   // first: no commit is under way once the last accumulator has been seen
             }
             mma_commit_pair(full);
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int n = n0 + k, st = n % kTileStages, p = n - kAStages;
         ok = wait_unless(codes_there, &full_c[st], (n / kTileStages) & 1, &s_err);
         // the step that last used this A stage: its own ring stage is given back once it has been multiplied
-        const bool free = p < 0 || mbar_test(&empty[p % kTileStages], (p / kTileStages) & 1);
+        const bool free = p < 0 || test_wait(&empty[p % kTileStages], (p / kTileStages) & 1);
         uint32_t v[64];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_fence_after();
         tmem_st32(tmem_a + lanes + set * 64, v);
         tmem_st32(tmem_a + lanes + set * 64 + 32, v + 32);
-        codes_there = mbar_test(&full_c[(n + 2) % kTileStages], ((n + 2) / kTileStages) & 1);
+        codes_there = test_wait(&full_c[(n + 2) % kTileStages], ((n + 2) / kTileStages) & 1);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               tc_fence_before();
               __syncwarp();
               if (lane == 0) arrive_pair(free_at);
-              sums_there = mbar_test(&acc_full[acc.stage], acc.parity);
+              sums_there = test_wait(&acc_full[acc.stage], acc.parity);
             }
 #pragma unroll
             for (int i = 0; i < 16; i += 2)

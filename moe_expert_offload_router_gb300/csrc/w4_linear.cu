@@ -321,10 +321,8 @@ __device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t offset, uin
 // multiplies for both blocks into an accumulator for each group of the scales; and eight
 // warps multiply each accumulator by its scales - a scale belongs to a tensor memory lane -
 // and add it up in registers while the next ones fill.
-constexpr int kTileThreads = 640;   // TMA, MMA, two warps that only fill a group of four, 8 of codes, 8 of sums
 constexpr int kTileStages = 8, kCodeBytes = 128 * 64;
 constexpr int kAStages = 2, kACols = 384;   // A: two steps in the last 128 columns of tensor memory
-constexpr int kExchange = 2 * 16 * 64 * 4;
 // Four neighbouring elements of B bytes of a row's array, fetched a batch ahead: a lane's row is
 // its own cache line, and a load of every element by itself takes the L1's time 32 times.
 // Rows start anywhere: the two aligned words that hold the four are loaded (one where they
@@ -370,11 +368,19 @@ struct TileCfg {
   static constexpr int kStage = kCodeBytes + NT / 2 * 256;
   static constexpr int kBufs = kACols / NT;   // accumulators
   static constexpr int kRing = kTileStages * kStage;
+  // warps: TMA, MMA, two that only fill a group of four, 8 of codes, and 4 of sums for every kCols columns: 32, since 64
+  // a thread do not stay in its registers
+  static constexpr int kCols = NT == 128 ? 32 : NT / 2, kParts = NT / kCols;
+  static constexpr int kThreads = (12 + 4 * kParts) * 32;
+  static constexpr int kExchange = kParts * 16 * 64 * 4;
 };
-static size_t tile_smem(int ring, int E) { return (size_t)ring + kExchange + 1024 + (size_t)(E + 1) * 8; }
+template <int NT>
+static size_t tile_smem(int E) {
+  return (size_t)TileCfg<NT>::kRing + TileCfg<NT>::kExchange + 1024 + (size_t)(E + 1) * 8;
+}
 
 template <typename TE, int NT, int G>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
     w4_tile_kernel(const __grid_constant__ CUtensorMap mC, const __grid_constant__ CUtensorMap mX,
                    const __grid_constant__ W4Args a, int swiglu) {
   using C = TileCfg<NT>;
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ int ws[34];
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)tile_raw + 1023) & ~(uintptr_t)1023);
   float* exchange = reinterpret_cast<float*>(sm + C::kRing);               // [half][16][64]
-  int* first = reinterpret_cast<int*>(sm + C::kRing + kExchange);          // [E + 1]: an expert's first row
+  int* first = reinterpret_cast<int*>(sm + C::kRing + C::kExchange);          // [E + 1]: an expert's first row
   int* cum = first + a.E + 1;                                              // [E + 1]: its first tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x & 1;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int i = 0; i < kAStages; ++i) mbar_init(&a_full[i], 8);           // the leader's: four warps of each block
     for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 16);
+      mbar_init(&acc_empty[i], 8 * C::kParts);
     }
     s_err = MOE_OK;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // the experts' tiles
   const int per = swiglu ? 128 : 256, outs = swiglu ? a.N / 2 : a.N, row_tiles = (outs + per - 1) / per;
   int tiles = 0;
-  for (int b = 0; b < a.E; b += kTileThreads) {
+  for (int b = 0; b < a.E; b += C::kThreads) {
     const int e = b + tid;
     int n = 0, lo = 0, hi = a.P;
     if (e < a.E) {
@@ -543,21 +549,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = wait_unless(codes_there, &full_c[st], (n / kTileStages) & 1, &s_err);
         // the step that last used this A stage: its own ring stage is given back once it has been multiplied
         const bool free = p < 0 || test_wait(&empty[p % kTileStages], (p / kTileStages) & 1);
-        uint32_t v[64];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(codes + st * C::kStage + ((i << 4) ^ swizzle));
-          const uint32_t offset = W4<TE>::offset(z4 >> ((k % kPer * kGroups + i * 32 / G) * 8) & 255);
-          unpack_in_order<TE>(w.x, offset, v + 16 * i);
-          unpack_in_order<TE>(w.y, offset, v + 16 * i + 4);
-          unpack_in_order<TE>(w.z, offset, v + 16 * i + 8);
-          unpack_in_order<TE>(w.w, offset, v + 16 * i + 12);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(codes + st * C::kStage + (((h * 2 + i) << 4) ^ swizzle));
+            const uint32_t offset = W4<TE>::offset(z4 >> ((k % kPer * kGroups + (h * 2 + i) * 32 / G) * 8) & 255);
+            unpack_in_order<TE>(w.x, offset, v + 16 * i);
+            unpack_in_order<TE>(w.y, offset, v + 16 * i + 4);
+            unpack_in_order<TE>(w.z, offset, v + 16 * i + 8);
+            unpack_in_order<TE>(w.w, offset, v + 16 * i + 12);
+          }
+          if (h == 0) {
+            ok = __all_sync(0xffffffffu, ok && wait_unless(free, &empty[p % kTileStages], (p / kTileStages) & 1, &s_err));
+            tc_fence_after();
+          }
+          if (ok) tmem_st32(tmem_a + lanes + set * 64 + h * 32, v);
         }
-        ok = ok && wait_unless(free, &empty[p % kTileStages], (p / kTileStages) & 1, &s_err);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        tc_fence_after();
-        tmem_st32(tmem_a + lanes + set * 64, v);
-        tmem_st32(tmem_a + lanes + set * 64 + 32, v + 32);
+        if (!ok) break;
         codes_there = test_wait(&full_c[(n + 2) % kTileStages], ((n + 2) / kTileStages) & 1);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
@@ -566,8 +576,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
   } else {
-    // sums of row q * 32 + lane, columns from h * NT / 2
-    constexpr int kCols = NT / 2;
+    // sums of row q * 32 + lane, columns from h * kCols
+    constexpr int kCols = C::kCols;
     const int q = warp & 3, h = (warp - 12) >> 2, row = q * 32 + lane;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t empty_at = cluster_addr(&acc_empty[0], 0);
@@ -595,15 +605,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const F32x2 by = pair_of(s, s);
           const uint32_t at = tmem + lanes + acc.stage * NT + h * kCols, free_at = empty_at + acc.stage * 8;
           acc.next();
-          uint32_t u[2][16];   // 16 columns are on their way while 16 are added
-          tmem_ld16_nw(at, u[0]);
-          tmem_ld_wait16(u[0]);
 #pragma unroll
-          for (int c = 0; c < kCols / 16; ++c) {
-            uint32_t* mine = u[c & 1];
-            if (c + 1 < kCols / 16) {
-              tmem_ld16_nw(at + (c + 1) * 16, u[(c + 1) & 1]);
-            } else {   // all of it is in registers
+          for (int c = 0; c < kCols; c += 16) {
+            uint32_t u[16];
+            tmem_ld16(at + c, u);
+            if (c + 16 >= kCols) {   // all of it is in registers
               tc_fence_before();
               __syncwarp();
               if (lane == 0) arrive_pair(free_at);
@@ -611,46 +617,39 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
-              total[c * 8 + i / 2] = fma_pair(by, pair_of(__uint_as_float(mine[i]), __uint_as_float(mine[i + 1])), total[c * 8 + i / 2]);
-            if (c + 1 < kCols / 16) tmem_ld_wait16(u[(c + 1) & 1]);
+              total[(c + i) / 2] = fma_pair(by, pair_of(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), total[(c + i) / 2]);
           }
         }
       }
-      float sum[kCols];
-#pragma unroll
-      for (int i = 0; i < kCols; i += 2) {
+      auto sum = [&](int i) {
         const float2 f = halves_of(total[i / 2]);
-        sum[i] = f.x * W4<TE>::kUp, sum[i + 1] = f.y * W4<TE>::kUp;
-      }
-      if (!ok)
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) sum[i] = NAN;
-      auto put = [&](int c, float v) {
-        const int m = t.m0 + h * kCols + c;
-        if (m >= t.m1 || o >= outs) return;
-        const long long at = m * a.ld_out + o;
-        if (a.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(a.out)[at] = v;
-        else reinterpret_cast<TE*>(a.out)[at] = from_f32<TE>(v);
+        return ok ? (i & 1 ? f.y : f.x) * W4<TE>::kUp : NAN;
+      };
+      const int rows = o < outs ? t.m1 - t.m0 - h * kCols : 0;   // of out that are there, from this warp's first
+      long long at = (long long)(t.m0 + h * kCols) * a.ld_out + o;
+      auto put = [&](int i, float v) {
+        if (i < rows) {
+          if (a.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(a.out)[at] = v;
+          else reinterpret_cast<TE*>(a.out)[at] = from_f32<TE>(v);
+        }
+        at += a.ld_out;
       };
       if (!swiglu) {
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) put(i, sum[i]);
+        for (int i = 0; i < kCols; ++i) put(i, sum(i));
       } else {
         // ups (rows 64 on) to the gates' threads, 16 columns at a time
         float* ex = exchange + h * 16 * 64 + (row & 63);
-        auto meet = [&] {   // the four warps of these columns
-          if (h) asm volatile("bar.sync 2, 128;" ::: "memory");
-          else asm volatile("bar.sync 1, 128;" ::: "memory");
-        };
+        auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory"); };   // the four warps of these columns
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
           if (q >= 2)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ex[i * 64] = sum[c + i];
+            for (int i = 0; i < 16; ++i) ex[i * 64] = sum(c + i);
           meet();
           if (q < 2)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) put(c + i, silu_times(sum[c + i], ex[i * 64]));
+            for (int i = 0; i < 16; ++i) put(c + i, silu_times(sum(c + i), ex[i * 64]));
           meet();
         }
       }
@@ -696,14 +695,14 @@ static moe_status launch_tiles(const W4Args& a, int dtype, int swiglu, cudaStrea
   if (st != MOE_OK) return st;
   auto kernel = w4_tile_kernel<TE, NT, G>;
   static char allowed[64];
-  MOE_CUDA(allow_smem(kernel, tile_smem(TileCfg<NT>::kRing, kMaxExperts), allowed));
+  MOE_CUDA(allow_smem(kernel, tile_smem<NT>(kMaxExperts), allowed));
   const int outs = swiglu ? a.N / 2 : a.N, per = swiglu ? 128 : 256;
   // at most this many tiles: every expert's last one may be a part
   const long long most = ((long long)a.P / NT + (a.E < a.P ? a.E : a.P)) * ((outs + per - 1) / per);
   MOE_ARG(most <= 0x3fffffff, "too many tiles");
   const int pairs = device_sms() / 2;
-  return launch_cluster(kernel, dim3(2 * (unsigned)(most < pairs ? most : pairs)), kTileThreads, 2,
-                        tile_smem(TileCfg<NT>::kRing, a.E), s, "w4_tile_kernel", mC, mX, a, swiglu);
+  return launch_cluster(kernel, dim3(2 * (unsigned)(most < pairs ? most : pairs)), TileCfg<NT>::kThreads, 2,
+                        tile_smem<NT>(a.E), s, "w4_tile_kernel", mC, mX, a, swiglu);
 }
 template <typename TE, int G>
 static moe_status launch_tiles_of(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {

@@ -322,7 +322,7 @@ __device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t offset, uin
 // warps multiply each accumulator by its scales - a scale belongs to a tensor memory lane -
 // and add it up in registers while the next ones fill.
 constexpr int kTileStages = 8, kCodeBytes = 128 * 64;
-constexpr int kAStages = 2, kACols = 384;   // A: two steps in the last 128 columns of tensor memory
+constexpr int kAStages = 4, kACols = 256;   // A: four steps in the last 256 columns of tensor memory
 // Four neighbouring elements of B bytes of a row's array, fetched a batch ahead: a lane's row is
 // its own cache line, and a load of every element by itself takes the L1's time 32 times.
 // Rows start anywhere: the two aligned words that hold the four are loaded (one where they
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
   } else if (warp < 12) {
     // codes of row q * 32 + lane: four warps take the even steps, four the odd ones
     const int set = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
-    const uint32_t lanes = (uint32_t)(q * 32) << 16, full_at = cluster_addr(&a_full[set], 0);
+    const uint32_t lanes = (uint32_t)(q * 32) << 16, full_at = cluster_addr(&a_full[0], 0);
     constexpr int kGroups = 128 / G, kPer = 4 / kGroups;   // groups of a step, steps of four groups
     const uint8_t* codes = sm + row * 64;
     const int swizzle = ((row >> 1) & 3) << 4;
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
           if (a.zeros) z4 = zeros.value(batch);
           zeros.fetch(kPer == 1 ? batch + 2 : batch + 1);
         }
-        const int n = n0 + k, st = n % kTileStages, p = n - kAStages;
+        const int n = n0 + k, st = n % kTileStages, as = n % kAStages, p = n - kAStages;
         ok = wait_unless(codes_there, &full_c[st], (n / kTileStages) & 1, &s_err);
         // the step that last used this A stage: its own ring stage is given back once it has been multiplied
         const bool free = p < 0 || test_wait(&empty[p % kTileStages], (p / kTileStages) & 1);
@@ -565,14 +565,14 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
             ok = __all_sync(0xffffffffu, ok && wait_unless(free, &empty[p % kTileStages], (p / kTileStages) & 1, &s_err));
             tc_fence_after();
           }
-          if (ok) tmem_st32(tmem_a + lanes + set * 64 + h * 32, v);
+          if (ok) tmem_st32(tmem_a + lanes + as * 64 + h * 32, v);
         }
         if (!ok) break;
         codes_there = test_wait(&full_c[(n + 2) % kTileStages], ((n + 2) / kTileStages) & 1);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_pair(full_at);
+        if (lane == 0) arrive_pair(full_at + as * 8);
       }
     }
   } else {

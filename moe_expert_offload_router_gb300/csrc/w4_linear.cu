@@ -95,35 +95,67 @@ __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 16 bytes into another block's shared memory
+__device__ __forceinline__ void st_cluster4(uint32_t to, const float (&v)[4]) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
 __device__ __forceinline__ float silu_times(float gate, float up) { return gate / (1.f + expf(-gate)) * up; }
 
-// WPL words of codes of one row's group for a lane: c * WPL words into the group.
+// 16 bytes of weights, read once a launch; 0 where there are none
+__device__ __forceinline__ uint4 load_codes(bool in, const uint8_t* p) {
+  uint4 w;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "mov.u32 %3, 0;\n\t@q ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "=&r"(w.x), "=&r"(w.y), "=&r"(w.z), "=&r"(w.w)
+      : "l"(p), "r"((uint32_t)in));
+  return w;
+}
+
+// 128 codes of a row lie in four lanes, 16 bytes to each as they were loaded, WPL words of every group wanted:
+// lanes exchange words so that lane c holds WPL words of each group of 32 WPL, group by group.
 template <int WPL>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[WPL]) {
-  if constexpr (WPL == 4) {
-    const uint4 v = ld_stream_v4(p);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else if constexpr (WPL == 2) {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  } else {
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+__device__ __forceinline__ void deal_words(uint4 q, int c, uint32_t (&w)[4]) {
+  w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+  if (WPL <= 2) {   // halves: lanes 0 and 1 hold the first 64 codes, 2 and 3 the others
+    const bool up = c & 2;
+    const uint32_t a = __shfl_xor_sync(0xffffffffu, up ? w[0] : w[2], 2), b = __shfl_xor_sync(0xffffffffu, up ? w[1] : w[3], 2);
+    if (up) w[0] = a, w[1] = b;
+    else w[2] = a, w[3] = b;
   }
+  if (WPL == 1) {   // quarters
+    const bool up = c & 1;
+    const uint32_t a = __shfl_xor_sync(0xffffffffu, up ? w[0] : w[1], 1), b = __shfl_xor_sync(0xffffffffu, up ? w[2] : w[3], 1);
+    if (up) w[0] = a, w[2] = b;
+    else w[1] = a, w[3] = b;
+  }
+}
+// Where x's values of word `in` of a step's 16 go: (word of the lane) * 32 + the lane's c.
+template <int WPL>
+__device__ __forceinline__ int word_place(int in) {
+  if (WPL == 4) return (in & 3) * 32 + (in >> 2);
+  if (WPL == 1) return (in >> 2) * 32 + (in & 3);
+  const int lane = in >> 2 & 1, half = in >> 1 & 1;   // of the group's eight words: lanes 0, 2, 1, 3 hold two each
+  return ((in >> 3) * 2 + (in & 1)) * 32 + lane + 2 * half;
 }
 
 // Few rows of x to a matrix.  A warp multiplies 16 rows of weights by up to 8 rows of x
-// (m16n8k16): lane (g, c) holds codes of rows g and g + 8, WPL words (8 WPL neighbouring
-// codes) of each group, loaded straight from memory four groups ahead; which k a lane's
-// codes are does not matter as long as x's fragment holds the same ones.  x lies in
-// shared memory in the fragments' order.  The block's warps split the rows and, KS ways,
-// the groups; the KS sums are added in order at the end.
-constexpr int kChunkBytes = 64 * 1024;   // of x at a time
+// (m16n8k16), 128 products a step: lane (g, c) loads 16 bytes of codes of rows g and g + 8
+// straight from memory, four steps ahead; which k a lane's codes are does not matter as
+// long as x's fragment holds the same ones.  x lies in shared memory in the fragments'
+// order.  Where the rows of weights alone would not fill the GPU, a cluster of `splits`
+// blocks shares the steps, and its first block adds their sums in order.
+constexpr int kChunk = 32, kChunkBytes = kChunk * 2048;   // steps of x at a time
+constexpr int kMaxSplits = 8;
 
 template <typename TE, int WPL, int KS>
-__global__ void __launch_bounds__(256) w4_rows_kernel(const W4Args a, int swiglu) {
+__global__ void __launch_bounds__(256, KS == 8 ? 2 : 3) w4_rows_kernel(const W4Args a, int swiglu, int lg, int x_bytes) {
   extern __shared__ __align__(16) uint8_t w4_smem[];
-  constexpr int kRowWarps = 8 / KS, kGroup = 32 * WPL;
+  constexpr int GP = 4 / WPL, kRowWarps = 8 / KS;   // groups of a step
+  constexpr int D = WPL == 4 ? 4 : 2, NB = D * GP / 4;   // steps under way, scales of a lane for them
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int rw = warp % kRowWarps, ks = warp / kRowWarps;
+  const int splits = 1 << lg, split = (int)blockIdx.x & (splits - 1), tile = (int)blockIdx.x >> lg;
   pdl_wait();
   pdl_launch_dependents();
   // the expert: with fewer rows than experts the y-th that has any
@@ -149,110 +181,139 @@ __global__ void __launch_bounds__(256) w4_rows_kernel(const W4Args a, int swiglu
     }
     m0 = max(a.offsets[e], 0), m1 = min(a.offsets[e + 1], a.P);
   }
-  if (m0 >= m1) return;
+  if (m0 >= m1) return;   // all blocks of a cluster
+  if (splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int half = swiglu ? a.N / 2 : 8, outs = swiglu ? a.N / 2 : a.N;   // distance of a lane's two rows
-  const int o0 = (blockIdx.x * kRowWarps + rw) * (swiglu ? 8 : 16);       // the warp's first output
-  const int groups = a.K / kGroup, chunk = kChunkBytes / (kGroup * 16) & ~3;   // groups of x at a time
+  const int o0 = (tile * kRowWarps + rw) * (swiglu ? 8 : 16);             // the warp's first output
+  const int groups = a.K / (32 * WPL), all_steps = (a.K + 127) / 128;
+  const int sb = all_steps * split >> lg, se = all_steps * (split + 1) >> lg;
   const int r0 = min(o0 + g, a.N - 1), r1 = min(o0 + g + half, a.N - 1);
   const long long row0 = (long long)e * a.N + r0, row1 = (long long)e * a.N + r1;
-  const uint8_t* w0 = a.codes + row0 * (a.K / 2) + c * (WPL * 4);
-  const uint8_t* w1 = a.codes + row1 * (a.K / 2) + c * (WPL * 4);
-  const unsigned short* s0 = reinterpret_cast<const unsigned short*>(a.scales) + row0 * groups;
-  const unsigned short* s1 = reinterpret_cast<const unsigned short*>(a.scales) + row1 * groups;
-  const uint8_t* z0 = a.zeros ? a.zeros + row0 * groups : nullptr;
-  const uint8_t* z1 = a.zeros ? a.zeros + row1 * groups : nullptr;
-  float* sums = reinterpret_cast<float*>(w4_smem);   // [KS - 1][rows warps][32][4], after the last chunk
+  const uint8_t* w0 = a.codes + row0 * (a.K / 2) + c * 16;
+  const uint8_t* w1 = a.codes + row1 * (a.K / 2) + c * 16;
+  const long long g0 = row0 * groups + c, g1 = row1 * groups + c;
+  float* sums = reinterpret_cast<float*>(w4_smem + x_bytes);   // [splits * KS - 1][kRowWarps][32][4]
 
   for (int t0 = m0; t0 < m1; t0 += 8) {
     const int m = min(8, m1 - t0);
     float acc[4] = {};
-    for (int gb = 0; gb < groups; gb += chunk) {
-      const int ge = min(groups, gb + chunk);
-      // x's fragments: [group][word][lane] of 16 bytes, lane 4 i + c for row i of x
+    for (int cb = sb; cb < se; cb += kChunk) {
+      const int ce = min(se, cb + kChunk), ib = cb + (ce - cb) * ks / KS, ie = cb + (ce - cb) * (ks + 1) / KS;   // this warp's
+      uint4 q0[D], q1[D];
+      auto codes = [&](int i, int j) {   // 0 past the row's end, where x is 0 too
+        if constexpr (WPL == 4) {
+          q0[j] = ld_stream_v4(w0 + (long long)i * 64);
+          q1[j] = ld_stream_v4(w1 + (long long)i * 64);
+        } else {
+          const bool in = i * 128 + c * 32 < a.K;
+          q0[j] = load_codes(in, w0 + (long long)i * 64);
+          q1[j] = load_codes(in, w1 + (long long)i * 64);
+        }
+      };
+      // scales and zero points of four steps' groups, every fourth one to a lane c, loaded four steps ahead
+      uint32_t p0[NB], p1[NB], n0[NB], n1[NB];
+      auto scales = [&](int i) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int at = i * GP + 4 * b;
+          n0[b] = n1[b] = 0;
+          if (at + c < groups && i < ie) {
+            const unsigned short* s = reinterpret_cast<const unsigned short*>(a.scales) + at;
+            n0[b] = s[g0] | (a.zeros ? (uint32_t)a.zeros[g0 + at] : 8u) << 16;
+            n1[b] = s[g1] | (a.zeros ? (uint32_t)a.zeros[g1 + at] : 8u) << 16;
+          }
+        }
+      };
+      // x's fragments: [step][word of a lane][lane] of 16 bytes, lane 4 i + c for row i of x
       __syncthreads();
-      const int pieces = (ge - gb) * 4 * WPL;   // of 8 values
+      const int pieces = (ce - cb) * 16;   // of 8 values
       for (int i = tid; i < pieces * m; i += 256) {
-        const int t = i / pieces, q = i - t * pieces, in = q % (4 * WPL);
-        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const TE*>(a.x) + (t0 + t) * a.ld_x +
-                                                        (long long)gb * kGroup + q * 8);
+        const int t = i / pieces, q = i - t * pieces;
+        const long long k = (long long)cb * 128 + q * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (k < a.K) v = *reinterpret_cast<const uint4*>(reinterpret_cast<const TE*>(a.x) + (t0 + t) * a.ld_x + k);
         uint4 f;   // (0, 4), (1, 5), (2, 6), (3, 7)
         f.x = __byte_perm(v.x, v.z, 0x5410), f.y = __byte_perm(v.x, v.z, 0x7632);
         f.z = __byte_perm(v.y, v.w, 0x5410), f.w = __byte_perm(v.y, v.w, 0x7632);
-        *reinterpret_cast<uint4*>(w4_smem + ((q / (4 * WPL) * WPL + in % WPL) * 32 + t * 4 + in / WPL) * 16) = f;
+        *reinterpret_cast<uint4*>(w4_smem + ((q >> 4) * 128 + word_place<WPL>(q & 15) + t * 4) * 16) = f;
       }
       __syncthreads();
-      const int n = ge - gb, i0 = gb + n * ks / KS, i1 = gb + n * (ks + 1) / KS;   // this warp's groups
-      uint32_t q0[4][WPL], q1[4][WPL];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i0 + j < i1) {
-          load_words<WPL>(w0 + (long long)(i0 + j) * (kGroup / 2), q0[j]);
-          load_words<WPL>(w1 + (long long)(i0 + j) * (kGroup / 2), q1[j]);
-        }
-      for (int i = i0; i < i1; i += 4) {
-        // scales and zero points of four groups, one to a lane c
-        uint32_t p0 = 0, p1 = 0;
-        if (i + c < i1) {
-          p0 = s0[i + c] | (z0 ? (uint32_t)z0[i + c] : 8u) << 16;
-          p1 = s1[i + c] | (z1 ? (uint32_t)z1[i + c] : 8u) << 16;
-        }
+      for (int j = 0; j < D; ++j)
+        if (ib + j < ie) codes(ib + j, j);
+      scales(ib);
+      for (int i = ib; i < ie; i += D) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (i + j >= i1) break;
-          const uint32_t b0 = __shfl_sync(0xffffffffu, p0, (lane & ~3) | j), b1 = __shfl_sync(0xffffffffu, p1, (lane & ~3) | j);
-          const uint32_t k0 = W4<TE>::offset(b0 >> 16), k1 = W4<TE>::offset(b1 >> 16);
-          float d[4] = {};
+        for (int b = 0; b < NB; ++b) p0[b] = n0[b], p1[b] = n1[b];
+        scales(i + D);
 #pragma unroll
-          for (int w = 0; w < WPL; ++w) {
-            uint32_t u[4], v[4];
-            unpack<TE>(q0[j][w], k0, u);
-            unpack<TE>(q1[j][w], k1, v);
-            const uint4 f = *reinterpret_cast<const uint4*>(w4_smem + (((i + j - gb) * WPL + w) * 32 + lane) * 16);
-            w4_mma<TE>(d, u[0], v[0], u[1], v[1], f.x, f.y);
-            w4_mma<TE>(d, u[2], v[2], u[3], v[3], f.z, f.w);
+        for (int j = 0; j < D; ++j) {
+          if (i + j >= ie) break;
+          uint32_t c0[4], c1[4];
+          deal_words<WPL>(q0[j], c, c0);
+          deal_words<WPL>(q1[j], c, c1);
+#pragma unroll
+          for (int h = 0; h < GP; ++h) {
+            const int from = (lane & ~3) | ((j * GP + h) & 3);
+            const uint32_t b0 = __shfl_sync(0xffffffffu, p0[(j * GP + h) / 4], from);
+            const uint32_t b1 = __shfl_sync(0xffffffffu, p1[(j * GP + h) / 4], from);
+            const uint32_t k0 = W4<TE>::offset(b0 >> 16), k1 = W4<TE>::offset(b1 >> 16);
+            float d[4] = {};
+#pragma unroll
+            for (int w = h * WPL; w < (h + 1) * WPL; ++w) {
+              uint32_t u[4], v[4];
+              unpack<TE>(c0[w], k0, u);
+              unpack<TE>(c1[w], k1, v);
+              const uint4 f = *reinterpret_cast<const uint4*>(w4_smem + (((i + j - cb) * 4 + w) * 32 + lane) * 16);
+              w4_mma<TE>(d, u[0], v[0], u[1], v[1], f.x, f.y);
+              w4_mma<TE>(d, u[2], v[2], u[3], v[3], f.z, f.w);
+            }
+            const float f0 = W4<TE>::scale(b0 & 0xffff), f1 = W4<TE>::scale(b1 & 0xffff);
+            acc[0] = fmaf(f0, d[0], acc[0]), acc[1] = fmaf(f0, d[1], acc[1]);
+            acc[2] = fmaf(f1, d[2], acc[2]), acc[3] = fmaf(f1, d[3], acc[3]);
           }
-          const float f0 = W4<TE>::scale(b0 & 0xffff), f1 = W4<TE>::scale(b1 & 0xffff);
-          acc[0] = fmaf(f0, d[0], acc[0]), acc[1] = fmaf(f0, d[1], acc[1]);
-          acc[2] = fmaf(f1, d[2], acc[2]), acc[3] = fmaf(f1, d[3], acc[3]);
-          if (i + j + 4 < i1) {
-            load_words<WPL>(w0 + (long long)(i + j + 4) * (kGroup / 2), q0[j]);
-            load_words<WPL>(w1 + (long long)(i + j + 4) * (kGroup / 2), q1[j]);
-          }
+          if (i + j + D < ie) codes(i + j + D, j);
         }
       }
     }
-    if (KS > 1) {
-      __syncthreads();
-      if (ks) *reinterpret_cast<float4*>(sums + ((ks - 1) * kRowWarps + rw) * 128 + lane * 4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      __syncthreads();
-      if (ks == 0)
-        for (int j = 1; j < KS; ++j) {
-          const float4 o = *reinterpret_cast<const float4*>(sums + ((j - 1) * kRowWarps + rw) * 128 + lane * 4);
-          acc[0] += o.x, acc[1] += o.y, acc[2] += o.z, acc[3] += o.w;
-        }
+    if (splits > 1 || KS > 1) {
+      float* to = sums + ((split * KS + ks - 1) * kRowWarps + rw) * 128 + lane * 4;
+      if (splits > 1) {
+        // into the first block's memory: once it has started, and once it has read the sums of the rows before
+        if (t0 == m0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        else cluster_sync();
+        if (split) st_cluster4(cluster_addr(to, 0), acc);
+        cluster_sync();
+      } else {
+        __syncthreads();
+        if (ks) *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        __syncthreads();
+      }
+      if (split || ks) continue;
+      for (int j = 0; j < splits * KS - 1; ++j) {
+        const float4 o = *reinterpret_cast<const float4*>(sums + (j * kRowWarps + rw) * 128 + lane * 4);
+        acc[0] += o.x, acc[1] += o.y, acc[2] += o.z, acc[3] += o.w;
+      }
     }
-    if (KS == 1 || ks == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] *= W4<TE>::kUp;
+    for (int i = 0; i < 4; ++i) acc[i] *= W4<TE>::kUp;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (2 * c + i >= m) continue;
-        const long long o = (t0 + 2 * c + i) * a.ld_out + o0 + g;
-        auto put = [&](long long at, float v) {
-          if (a.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(a.out)[at] = v;
-          else reinterpret_cast<TE*>(a.out)[at] = from_f32<TE>(v);
-        };
-        if (swiglu) {
-          if (o0 + g < outs) put(o, silu_times(acc[i], acc[i + 2]));
-        } else {
-          if (o0 + g < outs) put(o, acc[i]);
-          if (o0 + g + 8 < outs) put(o + 8, acc[i + 2]);
-        }
+    for (int i = 0; i < 2; ++i) {
+      if (2 * c + i >= m) continue;
+      const long long o = (t0 + 2 * c + i) * a.ld_out + o0 + g;
+      auto put = [&](long long at, float v) {
+        if (a.out_dtype == MOE_DT_F32) reinterpret_cast<float*>(a.out)[at] = v;
+        else reinterpret_cast<TE*>(a.out)[at] = from_f32<TE>(v);
+      };
+      if (swiglu) {
+        if (o0 + g < outs) put(o, silu_times(acc[i], acc[i + 2]));
+      } else {
+        if (o0 + g < outs) put(o, acc[i]);
+        if (o0 + g + 8 < outs) put(o + 8, acc[i + 2]);
       }
     }
   }
 }
-
 
 // ------------------------------------------------------------- tiles, tcgen05 --
 
@@ -713,24 +774,33 @@ static moe_status launch_tiles_of(const W4Args& a, int dtype, int swiglu, cudaSt
 }
 
 template <typename TE, int WPL, int KS>
-static moe_status launch_rows_kernel(const W4Args& a, int swiglu, cudaStream_t s) {
+static moe_status launch_rows_kernel(const W4Args& a, int swiglu, int lg, cudaStream_t s) {
   auto kernel = w4_rows_kernel<TE, WPL, KS>;
   static char allowed[64];
-  MOE_CUDA(allow_smem(kernel, kChunkBytes, allowed));
+  MOE_CUDA(allow_smem(kernel, kChunkBytes + (kMaxSplits - 1) * 4096, allowed));
   const int outs = swiglu ? a.N / 2 : a.N, per = 8 / KS * (swiglu ? 8 : 16), tiles = (outs + per - 1) / per;
-  const int experts = a.offsets && a.P < a.E ? a.P : a.E;
-  const long long x = (long long)a.K * 16;   // 8 rows
-  const size_t smem = x < 4096 ? 4096 : x < kChunkBytes ? (size_t)x : kChunkBytes;
-  cudaError_t e = launch_pdl(kernel, dim3(tiles, experts), dim3(256), smem, s, a, swiglu);
+  const int experts = a.offsets && a.P < a.E ? a.P : a.E, steps = (a.K + 127) / 128;
+  const int splits = 1 << lg, mine = (steps + splits - 1) / splits, x_bytes = (mine < kChunk ? mine : kChunk) * 2048;
+  const size_t smem = x_bytes + (splits * KS - 1) * (8 / KS) * 512;
+  MOE_ARG((long long)tiles * splits <= 0x7fffffffLL, "too many tiles");
+  if (splits > 1)
+    return launch_cluster(kernel, dim3(tiles * splits, experts), 256, splits, smem, s, "w4_rows_kernel", a, swiglu, lg, x_bytes);
+  cudaError_t e = launch_pdl(kernel, dim3(tiles, experts), dim3(256), smem, s, a, swiglu, 0, x_bytes);
   if (e != cudaSuccess) return cuda_fail(e, "w4_rows_kernel");
   return check_launch("w4_rows_kernel");
 }
 template <typename TE, int WPL>
 static moe_status launch_split_rows(const W4Args& a, int swiglu, cudaStream_t s) {
-  // few tiles: the groups are split over a block's warps, so that more blocks share the rows
+  // Blocks of 128 rows fill the GPU.  Else, with few rows of x, blocks of 16 whose warps split the groups (4096 x 4096,
+  // one row: 4.8 us, clusters 6.4); with more of them a block would load more of x than of codes, so clusters share the
+  // groups of 128 rows (8 rows: 6.5 us, blocks of 16 8.5; 8192 x 8192: 16 and 30).
   const long long tiles = ((long long)a.N + 127) / 128 * (a.offsets && a.P < a.E ? a.P : a.E);
-  if (tiles * 2 >= device_sms() * 3) return launch_rows_kernel<TE, WPL, 1>(a, swiglu, s);
-  return launch_rows_kernel<TE, WPL, 8>(a, swiglu, s);
+  if (tiles >= device_sms()) return launch_rows_kernel<TE, WPL, 1>(a, swiglu, 0, s);
+  if (a.P < a.E * 4) return launch_rows_kernel<TE, WPL, 8>(a, swiglu, 0, s);
+  const int steps = (a.K + 127) / 128;
+  int lg = 0;
+  while (1 << lg < kMaxSplits && tiles << lg < device_sms() && steps >= 4 << lg) ++lg;
+  return launch_rows_kernel<TE, WPL, 1>(a, swiglu, lg, s);
 }
 template <typename TE>
 static moe_status launch_w4(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {

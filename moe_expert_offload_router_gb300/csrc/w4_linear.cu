@@ -99,6 +99,11 @@ __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 __device__ __forceinline__ void st_cluster4(uint32_t to, const float (&v)[4]) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
 }
+__device__ __forceinline__ float ld_cluster(uint32_t from) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from) : "memory");
+  return v;
+}
 __device__ __forceinline__ float silu_times(float gate, float up) { return gate / (1.f + expf(-gate)) * up; }
 
 // 16 bytes of weights, read once a launch; 0 where there are none
@@ -347,6 +352,13 @@ __device__ __forceinline__ void mma_k16_pair_ta(uint32_t d, uint32_t a, uint64_t
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// Arrives on `bar` of the blocks of `mask` once this thread's MMAs so far have completed.
+__device__ __forceinline__ void mma_commit_to(uint64_t* bar, uint32_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(su32(bar)),
+      "h"((uint16_t)mask)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -443,7 +455,7 @@ static size_t tile_smem(int E) {
 template <typename TE, int NT, int G>
 __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
     w4_tile_kernel(const __grid_constant__ CUtensorMap mC, const __grid_constant__ CUtensorMap mX,
-                   const __grid_constant__ W4Args a, int swiglu) {
+                   const __grid_constant__ W4Args a, int swiglu, int lg) {
   using C = TileCfg<NT>;
   extern __shared__ uint8_t tile_raw[];
   __shared__ alignas(8) uint64_t full_c[kTileStages], full_x[kTileStages], empty[kTileStages], a_full[kAStages];
@@ -456,7 +468,8 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
   int* first = reinterpret_cast<int*>(sm + C::kRing + C::kExchange);          // [E + 1]: an expert's first row
   int* cum = first + a.E + 1;                                              // [E + 1]: its first tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x & 1;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int splits = 1 << lg, split = (int)(blockIdx.x >> 1) & (splits - 1), leader = split * 2;   // places in the cluster
+  const int pair = blockIdx.x >> (1 + lg), pairs = gridDim.x >> (1 + lg);   // of all that share a tile
   if (tid == 0) {
     prefetch_map(&mC);
     prefetch_map(&mX);
@@ -499,12 +512,14 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
     tiles += all;
   }
   if (tid == 0) cum[a.E] = tiles;
+  if (lg) tiles = min(tiles, pairs);   // one each (the host counts them; offsets that do not ascend could make more)
   tc_fence_before();
   __syncwarp();
   cluster_sync();   // the barriers of both are there
   tc_fence_after();
   const uint32_t tmem = tmem_slot, tmem_a = tmem + kACols;
-  const int steps = (a.K + 127) / 128, groups = a.K / G;
+  const int all_steps = (a.K + 127) / 128, groups = a.K / G;
+  const int sb = all_steps * split >> lg, se = all_steps * (split + 1) >> lg, steps = se - sb;   // this pair's
   bool ok = true;
 
   int e = 0;
@@ -526,14 +541,14 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
       for (int tile = pair; tile < tiles && ok; tile += pairs) {
         const Tile t = tile_at(tile);
         const int row = e * a.N + t.o0, row2 = swiglu ? row + a.N / 2 : row + 64, x0 = t.m0 + rank * (NT / 2);
-        for (int k = 0; k < steps; ++k) {
+        for (int k = sb; k < se; ++k) {
           if (wrapped && !(ok = wait_unless(false, &empty[r.stage], r.parity ^ 1, &s_err))) break;
           uint8_t* st = sm + r.stage * C::kStage;
           mbar_expect_tx(&full_c[r.stage], kCodeBytes);
           tma_2d(st, &mC, k * 64, row, &full_c[r.stage]);
           tma_2d(st + kCodeBytes / 2, &mC, k * 64, row2, &full_c[r.stage]);
           if (rank == 0) mbar_expect_tx(&full_x[r.stage], NT * 256);
-          const uint32_t bar = cluster_addr(&full_x[r.stage], 0);
+          const uint32_t bar = cluster_addr(&full_x[r.stage], leader);
           tma_2d_pair(st + kCodeBytes, &mX, k * 128, x0, bar);
           tma_2d_pair(st + kCodeBytes + NT / 2 * 128, &mX, k * 128 + 64, x0, bar);
           r.next();
@@ -546,9 +561,10 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
       int used = 0;
       const uint32_t idesc = idesc_pair(NT, std::is_same<TE, __nv_bfloat16>::value);
       const uint64_t d0 = umma_desc_sw128(su32(sm));
+      const uint32_t both = 3u << leader;
       bool x_there = false, a_there = false, acc_free = false;
       for (int tile = pair; tile < tiles && ok; tile += pairs) {
-        for (int k = 0; k < steps && ok; ++k) {
+        for (int k = sb; k < se && ok; ++k) {
           const int last = min(a.K - k * 128, 128) / 16 - 1;
           ok = wait_unless(x_there, &full_x[r.stage], r.parity, &s_err) &&
                wait_unless(a_there, &a_full[ar.stage], ar.parity, &s_err);
@@ -575,17 +591,19 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
             if ((g + 1) * (G / 16) > last) {
               x_there = test_wait(&full_x[r.stage], r.parity);
               a_there = test_wait(&a_full[ar.stage], ar.parity);
-              mma_commit_pair(done);   // first: no commit is under way once the last accumulator has been seen
+              mma_commit_to(done, both);   // first: no commit is under way once the last accumulator has been seen
             }
-            mma_commit_pair(full);
+            mma_commit_to(full, both);
           }
         }
       }
     }
+    __syncwarp();
+    if (lg && pair < tiles) cluster_sync();   // the sums are there
   } else if (warp < 12) {
     // codes of row q * 32 + lane: four warps take the even steps, four the odd ones
     const int set = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
-    const uint32_t lanes = (uint32_t)(q * 32) << 16, full_at = cluster_addr(&a_full[0], 0);
+    const uint32_t lanes = (uint32_t)(q * 32) << 16, full_at = cluster_addr(&a_full[0], leader);
     constexpr int kGroups = 128 / G, kPer = 4 / kGroups;   // groups of a step, steps of four groups
     const uint8_t* codes = sm + row * 64;
     const int swizzle = ((row >> 1) & 3) << 4;
@@ -596,17 +614,17 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
       const int o = t.o0 + (swiglu ? row & 63 : row);
       const long long wr = (long long)e * a.N + (swiglu && row >= 64 ? a.N / 2 : 0) + min(o, outs - 1);
       Four<1> zeros(a.zeros ? a.zeros + wr * groups : nullptr, a.zeros ? groups : 0);
-      const int k0 = (n0 ^ set) & 1;   // these warps' first step of the tile
+      const int k0 = sb + ((n0 ^ set) & 1);   // these warps' first step of the tile
       zeros.fetch(k0 / kPer);
       int batch = -1;
       uint32_t z4 = 0x08080808u;
-      for (int k = k0; k < steps; k += 2) {
+      for (int k = k0; k < se; k += 2) {
         if (k / kPer != batch) {
           batch = k / kPer;
           if (a.zeros) z4 = zeros.value(batch);
           zeros.fetch(kPer == 1 ? batch + 2 : batch + 1);
         }
-        const int n = n0 + k, st = n % kTileStages, as = n % kAStages, p = n - kAStages;
+        const int n = n0 + k - sb, st = n % kTileStages, as = n % kAStages, p = n - kAStages;
         ok = wait_unless(codes_there, &full_c[st], (n / kTileStages) & 1, &s_err);
         // the step that last used this A stage: its own ring stage is given back once it has been multiplied
         const bool free = p < 0 || test_wait(&empty[p % kTileStages], (p / kTileStages) & 1);
@@ -636,29 +654,32 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
         if (lane == 0) arrive_pair(full_at + as * 8);
       }
     }
+    __syncwarp();
+    if (lg && pair < tiles) cluster_sync();   // the sums are there
   } else {
     // sums of row q * 32 + lane, columns from h * kCols
     constexpr int kCols = C::kCols;
     const int q = warp & 3, h = (warp - 12) >> 2, row = q * 32 + lane;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    const uint32_t empty_at = cluster_addr(&acc_empty[0], 0);
+    const uint32_t empty_at = cluster_addr(&acc_empty[0], leader);
+    const int g0 = sb * (128 / G), mine = min(groups, se * (128 / G)) - g0;   // groups
     RingPos acc(C::kBufs);
     bool sums_there = false;
     for (int tile = pair; tile < tiles; tile += pairs) {   // a wait that gave up: NaN to the end
       const Tile t = tile_at(tile);
       const int o = t.o0 + (swiglu ? row & 63 : row);
       const long long wr = (long long)e * a.N + (swiglu && row >= 64 ? a.N / 2 : 0) + min(o, outs - 1);
-      Four<2> scales(reinterpret_cast<const TE*>(a.scales) + wr * groups, groups);
+      Four<2> scales(reinterpret_cast<const TE*>(a.scales) + wr * groups + g0, mine);
       scales.fetch(0);
       F32x2 total[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) total[i].v = 0;
-      for (int b = 0; b * 4 < groups && ok; ++b) {
+      for (int b = 0; b * 4 < mine && ok; ++b) {
         const uint64_t s4 = scales.value(b);
         scales.fetch(b + 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (b * 4 + j >= groups) break;
+          if (b * 4 + j >= mine) break;
           const float s = W4<TE>::scale((uint32_t)(s4 >> (16 * j)) & 0xffff);
           ok = wait_unless(sums_there, &acc_full[acc.stage], acc.parity, &s_err);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -695,7 +716,26 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
         }
         at += a.ld_out;
       };
-      if (!swiglu) {
+      if (lg) {
+        // sums into the ring's memory, which the last accumulator's products were the last to use: [column][row]; then
+        // each pair reads a share of the columns from all, in order
+        float* mem = reinterpret_cast<float*>(sm) + h * kCols * 128 + row;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) mem[i * 128] = sum(i);
+        cluster_sync();
+        const int per = kCols >> lg;
+        at += (long long)split * per * a.ld_out;
+        for (int i = split * per; i < (split + 1) * per; ++i) {
+          float v = 0.f, up = 0.f;
+          for (int j = 0; j < splits; ++j) {
+            const uint32_t f = cluster_addr(mem + i * 128, j * 2 + rank);
+            v += ld_cluster(f);
+            if (swiglu && q < 2) up += ld_cluster(f + 64 * 4);
+          }
+          if (!swiglu) put(i, v);
+          else if (q < 2) put(i, silu_times(v, up));
+        }
+      } else if (!swiglu) {
 #pragma unroll
         for (int i = 0; i < kCols; ++i) put(i, sum(i));
       } else {
@@ -748,6 +788,53 @@ static moe_status map_codes(CUtensorMap* m, const W4Args& a) {
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (codes) failed: %d", (int)r);
   return MOE_OK;
 }
+// At most this many tiles: every expert's last one may be a part.
+static long long most_tiles(const W4Args& a, int swiglu, int NT) {
+  const int outs = swiglu ? a.N / 2 : a.N, per = swiglu ? 128 : 256;
+  const long long of_x = a.offsets ? (long long)a.P / NT + (a.E < a.P ? a.E : a.P) : ((long long)a.P + NT - 1) / NT;
+  return of_x * ((outs + per - 1) / per);
+}
+template <typename TE, int NT, int G>
+static cudaError_t allow_tiles() {
+  static char allowed[64];
+  return allow_smem(w4_tile_kernel<TE, NT, G>, tile_smem<NT>(kMaxExperts), allowed);
+}
+// How many clusters of 2 << lg of the blocks, one to an SM, the device runs at once: a cluster's SMs are
+// neighbours, and fewer fit than the SMs' number says (of eight 15, not 19).
+static cudaError_t clusters_at_once(const void* kernel, int lg, int threads, size_t smem, int* n) {
+  static int known[64][3];   // + 1; every instance fills an SM, so it is the same for all
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int k = dev < 64 ? __atomic_load_n(&known[dev][lg], __ATOMIC_RELAXED) : 0;
+  if (k == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2u << lg), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2u << lg, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr, cfg.numAttrs = 1;
+    int got = 0;
+    e = cudaOccupancyMaxActiveClusters(&got, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    k = got + 1;
+    if (dev < 64) __atomic_store_n(&known[dev][lg], k, __ATOMIC_RELAXED);
+  }
+  *n = k - 1;
+  return cudaSuccess;
+}
+// Few tiles: clusters of two or four pairs (1 << lg) share the steps of one each, where all of them run at once.  Measured,
+// 57 rows of x, 4096 x 2048: 11.6 us by four, 18.7 by two, 23.4 by pairs.
+static cudaError_t splits_of(const W4Args& a, long long most, const void* kernel, int threads, size_t smem, int* lg) {
+  const int steps = (a.K + 127) / 128;
+  for (*lg = 0; *lg < 2 && steps >= 4 << *lg; ++*lg) {   // two steps each at least
+    int fit;
+    const cudaError_t e = clusters_at_once(kernel, *lg + 1, threads, smem, &fit);
+    if (e != cudaSuccess) return e;
+    if (most > fit) break;
+  }
+  return cudaSuccess;
+}
 template <typename TE, int NT, int G>
 static moe_status launch_tiles(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {
   CUtensorMap mC, mX;
@@ -755,21 +842,46 @@ static moe_status launch_tiles(const W4Args& a, int dtype, int swiglu, cudaStrea
   if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.K, a.P, a.ld_x, NT / 2);
   if (st != MOE_OK) return st;
   auto kernel = w4_tile_kernel<TE, NT, G>;
-  static char allowed[64];
-  MOE_CUDA(allow_smem(kernel, tile_smem<NT>(kMaxExperts), allowed));
-  const int outs = swiglu ? a.N / 2 : a.N, per = swiglu ? 128 : 256;
-  // at most this many tiles: every expert's last one may be a part
-  const long long most = ((long long)a.P / NT + (a.E < a.P ? a.E : a.P)) * ((outs + per - 1) / per);
+  const cudaError_t allowed = allow_tiles<TE, NT, G>();
+  MOE_CUDA(allowed);
+  const long long most = most_tiles(a, swiglu, NT);
   MOE_ARG(most <= 0x3fffffff, "too many tiles");
   const int pairs = device_sms() / 2;
-  return launch_cluster(kernel, dim3(2 * (unsigned)(most < pairs ? most : pairs)), TileCfg<NT>::kThreads, 2,
-                        tile_smem<NT>(a.E), s, "w4_tile_kernel", mC, mX, a, swiglu);
+  int lg;
+  MOE_CUDA(splits_of(a, most, (const void*)kernel, TileCfg<NT>::kThreads, tile_smem<NT>(kMaxExperts), &lg));
+  return launch_cluster(kernel, dim3((unsigned)(lg || most < pairs ? most : pairs) << (lg + 1)), TileCfg<NT>::kThreads, 2 << lg,
+                        tile_smem<NT>(a.E), s, "w4_tile_kernel", mC, mX, a, swiglu, lg);
 }
 template <typename TE, int G>
 static moe_status launch_tiles_of(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {
-  const int mean = a.P / a.E;
-  if (mean > 64) return launch_tiles<TE, 128, G>(a, dtype, swiglu, s);
-  if (mean > 32) return launch_tiles<TE, 64, G>(a, dtype, swiglu, s);
+  int nt = 128;
+  if (a.offsets) {   // an expert's rows in one tile, most of the time
+    const int mean = a.P / a.E;
+    nt = mean > 64 ? 128 : mean > 32 ? 64 : 32;
+  } else {
+    // Rounds of tiles times steps times what a step of the width takes (5, 7 and 10 parts: measured 0.64, 0.9 and 1.26 us
+    // in groups of 64), and 70 parts for the exchange of a split.  4096 x 4096: 64 rows 13.6 us at a width of 32, 16.2 at
+    // 64, 20.3 at 128; 256 rows 30, 18.8 and 21.2.
+    const int steps = (a.K + 127) / 128, pairs = device_sms() / 2;
+    long long least = 0;
+    auto consider = [&](auto width, int part) {
+      constexpr int NT = decltype(width)::value;
+      const long long most = most_tiles(a, swiglu, NT);
+      int lg;
+      cudaError_t e = allow_tiles<TE, NT, G>();
+      if (e == cudaSuccess)
+        e = splits_of(a, most, (const void*)w4_tile_kernel<TE, NT, G>, TileCfg<NT>::kThreads, tile_smem<NT>(kMaxExperts), &lg);
+      if (e != cudaSuccess) return e;
+      const long long rounds = lg ? 1 : (most + pairs - 1) / pairs, cost = rounds * ((steps + (1 << lg) - 1) >> lg) * part + (lg ? 70 : 0);
+      if (least == 0 || cost < least) least = cost, nt = NT;
+      return cudaSuccess;
+    };
+    MOE_CUDA(consider(std::integral_constant<int, 32>(), 5));
+    MOE_CUDA(consider(std::integral_constant<int, 64>(), 7));
+    MOE_CUDA(consider(std::integral_constant<int, 128>(), 10));
+  }
+  if (nt == 128) return launch_tiles<TE, 128, G>(a, dtype, swiglu, s);
+  if (nt == 64) return launch_tiles<TE, 64, G>(a, dtype, swiglu, s);
   return launch_tiles<TE, 32, G>(a, dtype, swiglu, s);
 }
 
@@ -796,7 +908,7 @@ static moe_status launch_split_rows(const W4Args& a, int swiglu, cudaStream_t s)
   // groups of 128 rows (8 rows: 6.5 us, blocks of 16 8.5; 8192 x 8192: 16 and 30).
   const long long tiles = ((long long)a.N + 127) / 128 * (a.offsets && a.P < a.E ? a.P : a.E);
   if (tiles >= device_sms()) return launch_rows_kernel<TE, WPL, 1>(a, swiglu, 0, s);
-  if (a.P < a.E * 4) return launch_rows_kernel<TE, WPL, 8>(a, swiglu, 0, s);
+  if (a.P < (long long)a.E * 3) return launch_rows_kernel<TE, WPL, 8>(a, swiglu, 0, s);
   const int steps = (a.K + 127) / 128;
   int lg = 0;
   while (1 << lg < kMaxSplits && tiles << lg < device_sms() && steps >= 4 << lg) ++lg;
@@ -805,7 +917,9 @@ static moe_status launch_split_rows(const W4Args& a, int swiglu, cudaStream_t s)
 template <typename TE>
 static moe_status launch_w4(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {
   ProfScope ps(MOE_K_W4, s);
-  if (a.P / a.E >= 16) {
+  // Up to eight rows of x the kernel for few reads the codes once; experts have more than the mean too: 2048 x 2048, 256
+  // experts, 8 rows to each 165 us (201 by tiles), 12 rows 219 (201).
+  if (a.P >= (long long)a.E * (a.offsets ? 11 : 9)) {
     if (a.g == 128) return launch_tiles_of<TE, 128>(a, dtype, swiglu, s);
     if (a.g == 64) return launch_tiles_of<TE, 64>(a, dtype, swiglu, s);
     return launch_tiles_of<TE, 32>(a, dtype, swiglu, s);

@@ -728,7 +728,7 @@ moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out_dtype, con
  *
  * A pos outside [0, n_rows) (n_rows: the rows of `rows`) counts as -1: nothing is read
  * for it, so what rows past offsets[E] hold does not matter.  The pos of one call are
- * distinct but for -1.  Sums are taken in fp32 in the order of j (d_w's over H in a fixed
+ * distinct but for -1.  But for the two named, results must not overlap what a call reads.  Sums are taken in fp32 in the order of j (d_w's over H in a fixed
  * order), base last, and rounded once: equal calls give equal bits.
  * x and rows of sort have one type; in combine y, base and d_y have y_dtype, rows and
  * d_rows rows_dtype, which is y_dtype or MOE_DT_F32.  T >= 0, 1 <= k <= 64,
@@ -766,7 +766,9 @@ moe_status moe_combine_rows_backward(int T, int k, int n_rows, int H, int rows_d
  *   out      device [P, N] (or [P, N / 2]) of out_dtype: `dtype` or MOE_DT_F32
  * q - z and its products with x are exact; a group's sum is taken in fp32 (tensor-core
  * accumulators) and multiplied by its scale in fp32, and the groups are added in fp32.
- * A row's values, NaN included, reach that row of out and no other.
+ * A row's values, NaN included, reach that row of out and no other.  out must not overlap
+ * what the call reads.  Equal calls give equal bits; the order of a sum's parts goes by the
+ * sizes (P, N, K, E), so a row's last bits may differ between batches of different sizes.
  * group 32, 64 or 128, K a multiple of it, x and codes 16-byte aligned, ld_x a multiple
  * of 8; P >= 0, N >= 1 (even with swiglu), 1 <= E <= 2048, E N < 2^31.
  * A wait that gave up sets *d_error (device int32, may be NULL) to MOE_ERR_TIMEOUT.

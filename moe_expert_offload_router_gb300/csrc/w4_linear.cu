@@ -148,8 +148,15 @@ __device__ __forceinline__ int word_place(int in) {
 // (m16n8k16), 128 products a step: lane (g, c) loads 16 bytes of codes of rows g and g + 8
 // straight from memory, four steps ahead; which k a lane's codes are does not matter as
 // long as x's fragment holds the same ones.  x lies in shared memory in the fragments'
-// order.  Where the rows of weights alone would not fill the GPU, a cluster of `splits`
-// blocks shares the steps, and its first block adds their sums in order.
+// order.  Where the rows of weights alone would not fill the GPU, KS of the block's warps
+// or a cluster of `splits` blocks share the steps, and the sums are added in order.
+//
+// Bound by HBM where there are codes enough: 512 rows of 256 experts, 4096 x 4096 (gates and
+// ups) 365 us, 5.35 TB/s; one row of 4096 x 4096 4.7 us with the codes in the L2 and 7 to 9
+// from HBM, latency: x, the codes and a sum over the warps after each other.  Groups of 32
+// take twice the instructions of groups of 128 (scales, zero points and sums for each): the
+// same experts 615 us, 2.9 TB/s.  Scales come four steps ahead as the codes do; 80
+// registers keep three blocks on an SM, more of them under way cost the third (556 us).
 constexpr int kChunk = 32, kChunkBytes = kChunk * 2048;   // steps of x at a time
 constexpr int kMaxSplits = 8;
 
@@ -394,6 +401,13 @@ __device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t offset, uin
 // multiplies for both blocks into an accumulator for each group of the scales; and eight
 // warps multiply each accumulator by its scales - a scale belongs to a tensor memory lane -
 // and add it up in registers while the next ones fill.
+//
+// What bounds it is the way of a step through its four hands: codes, MMA, sums and back, each
+// waiting on the other's barrier.  4001 x 4096 x 4096 in groups of 128 takes 146 us (0.92
+// PFLOP/s), 0.65 us a step whose MMAs take some 0.27; without the sums 123.  Smaller groups hand
+// over more accumulators: 220 us in groups of 64, 390 in groups of 32.  Two accumulators and
+// four steps of codes in tensor memory were faster than three and two; a third set of four
+// warps for the codes slower (174 us), and so were 64 columns of sums a thread.
 constexpr int kTileStages = 8, kCodeBytes = 128 * 64;
 constexpr int kAStages = 4, kACols = 256;   // A: four steps in the last 256 columns of tensor memory
 // Four neighbouring elements of B bytes of a row's array, fetched a batch ahead: a lane's row is

@@ -633,9 +633,15 @@ static moe_status launch_bwd_v(CombineBwdArgs a, int H, cudaStream_t s) {
   // Single elements (fp32, 1021 tokens of 5 rows of 1001): 13.3 by warps, 11.7 by halves of a block, 15 by blocks.
   const int sms = device_sms();
   if (a.T >= 16 * sms || a.nv <= 32) return run(integral_constant<int, 32>(), integral_constant<int, V == 8 ? 2 : 4>());
-  if (V < 8) return run(integral_constant<int, 128>(), integral_constant<int, 4>());
-  if (a.T >= 2 * sms) return run(integral_constant<int, 256>(), integral_constant<int, 1>());
-  return run(integral_constant<int, 256>(), integral_constant<int, 2>());
+  if constexpr (V < 8) {
+    return run(integral_constant<int, 128>(), integral_constant<int, 4>());
+  } else {
+    // 32 bytes of an fp32 row are two loads already: 64 tokens of 8 rows of 4096 6.7 us (7.3 with a second vector), 200 13.4
+    // (15.8).  By warps the second one pays for fp32 too: 4096 tokens of 6 rows 131 us, 141 without.
+    if constexpr (sizeof(TR) == 2)
+      if (a.T < 2 * sms) return run(integral_constant<int, 256>(), integral_constant<int, 2>());
+    return run(integral_constant<int, 256>(), integral_constant<int, 1>());
+  }
 }
 template <typename TR, typename TY>
 static moe_status launch_bwd(const CombineBwdArgs& a, int H, cudaStream_t s) {

@@ -24,6 +24,7 @@ struct W4Args {
   const int32_t* offsets;             // [E + 1] or null (all P rows are expert 0's)
   void* out;
   int32_t* err;
+  int few;                            // experts of up to so many rows are w4_rows_kernel's, those of more w4_tile_kernel's
 };
 
 constexpr int kMaxExperts = 2048;
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(256, KS == 8 ? 2 : 3) w4_rows_kernel(const W4A
     }
     m0 = max(a.offsets[e], 0), m1 = min(a.offsets[e + 1], a.P);
   }
-  if (m0 >= m1) return;   // all blocks of a cluster
+  if (m0 >= m1 || m1 - m0 > a.few) return;   // all blocks of a cluster
   if (splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int half = swiglu ? a.N / 2 : 8, outs = swiglu ? a.N / 2 : a.N;   // distance of a lane's two rows
   const int o0 = (tile * kRowWarps + rw) * (swiglu ? 8 : 16);             // the warp's first output
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
     int n = 0, lo = 0, hi = a.P;
     if (e < a.E) {
       if (a.offsets) lo = min(max(a.offsets[e], 0), a.P), hi = min(max(a.offsets[e + 1], 0), a.P);
-      n = hi > lo ? (hi - lo + NT - 1) / NT * row_tiles : 0;
+      n = hi - lo > a.few ? (hi - lo + NT - 1) / NT * row_tiles : 0;
     }
     int all;
     const int at = block_exclusive_scan(n, ws, &all);
@@ -805,7 +806,7 @@ static moe_status map_codes(CUtensorMap* m, const W4Args& a) {
 // At most this many tiles: every expert's last one may be a part.
 static long long most_tiles(const W4Args& a, int swiglu, int NT) {
   const int outs = swiglu ? a.N / 2 : a.N, per = swiglu ? 128 : 256;
-  const long long of_x = a.offsets ? (long long)a.P / NT + (a.E < a.P ? a.E : a.P) : ((long long)a.P + NT - 1) / NT;
+  const long long of_x = a.offsets ? (long long)a.P / NT + (a.E < a.P / (a.few + 1) ? a.E : a.P / (a.few + 1)) : ((long long)a.P + NT - 1) / NT;
   return of_x * ((outs + per - 1) / per);
 }
 template <typename TE, int NT, int G>
@@ -871,7 +872,7 @@ static moe_status launch_tiles_of(const W4Args& a, int dtype, int swiglu, cudaSt
   int nt = 128;
   if (a.offsets) {   // an expert's rows in one tile, most of the time
     const int mean = a.P / a.E;
-    nt = mean > 64 ? 128 : mean > 32 ? 64 : 32;
+    nt = mean > 64 ? 128 : mean > 32 || a.few ? 64 : 32;
   } else {
     // Rounds of tiles times steps times what a step of the width takes (5, 7 and 10 parts: measured 0.64, 0.9 and 1.26 us
     // in groups of 64), and 70 parts for the exchange of a split.  4096 x 4096: 64 rows 13.6 us at a width of 32, 16.2 at
@@ -928,19 +929,27 @@ static moe_status launch_split_rows(const W4Args& a, int swiglu, cudaStream_t s)
   while (1 << lg < kMaxSplits && tiles << lg < device_sms() && steps >= 4 << lg) ++lg;
   return launch_rows_kernel<TE, WPL, 1>(a, swiglu, lg, s);
 }
+// Few rows to an expert on average can still be many to some, and w4_rows_kernel reads the codes again for every eight: such
+// experts go to a launch of tiles behind it.  1802 rows of 2048 to 4096, 1500 of them one expert's of 256: 78 us, 1263
+// without; where no expert has so many the launch costs 2 to 5 us (512 rows of 256 experts 185 us, 180 without), which a
+// call of up to kFewInAll rows is spared.
+constexpr int kFewRows = 24, kFewInAll = 64;
 template <typename TE>
 static moe_status launch_w4(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {
   ProfScope ps(MOE_K_W4, s);
   // Up to eight rows of x the kernel for few reads the codes once; experts have more than the mean too: 2048 x 2048, 256
   // experts, 8 rows to each 165 us (201 by tiles), 12 rows 219 (201).
-  if (a.P >= (long long)a.E * (a.offsets ? 11 : 9)) {
-    if (a.g == 128) return launch_tiles_of<TE, 128>(a, dtype, swiglu, s);
-    if (a.g == 64) return launch_tiles_of<TE, 64>(a, dtype, swiglu, s);
-    return launch_tiles_of<TE, 32>(a, dtype, swiglu, s);
+  W4Args b = a;
+  b.few = a.P >= (long long)a.E * (a.offsets ? 11 : 9) ? 0 : a.offsets && a.P > kFewInAll ? kFewRows : a.P;
+  if (b.few) {
+    const moe_status st = a.g == 128  ? launch_split_rows<TE, 4>(b, swiglu, s)
+                          : a.g == 64 ? launch_split_rows<TE, 2>(b, swiglu, s)
+                                      : launch_split_rows<TE, 1>(b, swiglu, s);
+    if (st != MOE_OK || b.few == a.P) return st;
   }
-  if (a.g == 128) return launch_split_rows<TE, 4>(a, swiglu, s);
-  if (a.g == 64) return launch_split_rows<TE, 2>(a, swiglu, s);
-  return launch_split_rows<TE, 1>(a, swiglu, s);
+  if (a.g == 128) return launch_tiles_of<TE, 128>(b, dtype, swiglu, s);
+  if (a.g == 64) return launch_tiles_of<TE, 64>(b, dtype, swiglu, s);
+  return launch_tiles_of<TE, 32>(b, dtype, swiglu, s);
 }
 
 }  // namespace moe
@@ -967,7 +976,7 @@ extern "C" moe_status moe_w4_linear(int P, int N, int K, int E, int group, int d
   MOE_ARG(ld_x >= K && ld_out >= (swiglu ? N / 2 : N), "a row distance is below the row's length");
   MOE_ARG((uintptr_t)x % 16 == 0 && ld_x % 8 == 0, "x needs rows on 16-byte boundaries");
   MOE_ARG((uintptr_t)codes % 16 == 0 && (uintptr_t)scales % 2 == 0, "codes must be 16-byte aligned");
-  W4Args a = {P, N, K, E, group, out_dtype, x, ld_x, ld_out, codes, zeros, scales, offsets, out, d_error};
+  W4Args a = {P, N, K, E, group, out_dtype, x, ld_x, ld_out, codes, zeros, scales, offsets, out, d_error, 0};
   return dtype == MOE_DT_BF16 ? launch_w4<__nv_bfloat16>(a, dtype, swiglu ? 1 : 0, stream)
                               : launch_w4<__half>(a, dtype, swiglu ? 1 : 0, stream);
 }

@@ -148,3 +148,26 @@ def test_a_layer_and_its_gradients(T, k, E, H, I, dtype):
     eager = layer(M, h, router, w13, w2, E, k, dtype, shared)
     for name in eager:
         assert torch.equal(bufs[name], eager[name]), name
+
+
+@pytest.mark.parametrize("group,swiglu", [(128, False), (64, True), (32, False)])
+def test_a_batch_that_goes_to_few_of_many_experts(group, swiglu):
+    """Some experts have many rows, most none: both ways are taken side by side."""
+    M = load_lib()
+    counts = [0] * 64
+    for e, n in ((0, 24), (1, 25), (2, 1), (7, 300), (30, 8), (31, 9), (62, 64), (63, 26)):
+        counts[e] = n
+    E, P, N, K = 64, sum(counts) + 2, 192, 640
+    g = torch.Generator(device="cuda").manual_seed(group)
+    x = normal(g, P, K, BF16)
+    x[P - 2:] = float("nan")
+    codes, scales, z = weights(g, E, N, K, group, BF16)
+    offsets = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    got = torch.full((P, N // 2 if swiglu else N), 7.0, dtype=F32, device="cuda")
+    M.moe_w4_linear(x, codes, scales, z, offsets, swiglu=swiglu, out=got)
+    check(got, x, codes, scales, z, offsets, swiglu)
+    assert (got[P - 2:] == 7).all()
+    again = torch.full_like(got, 7.0)
+    for _ in range(10):
+        M.moe_w4_linear(x, codes, scales, z, offsets, swiglu=swiglu, out=again)
+    assert torch.equal(again, got)

@@ -12,6 +12,7 @@
 
 #include "dtype.cuh"
 #include "tcgen05_issue.cuh"
+#include "w4_tile.h"
 
 namespace moe {
 
@@ -26,8 +27,6 @@ struct W4Args {
   int32_t* err;
   int few;                            // experts of up to so many rows are w4_rows_kernel's, those of more w4_tile_kernel's
 };
-
-constexpr int kMaxExperts = 2048;
 
 // A 16-bit float whose high bits are 0 is its low bits times the type's smallest number (2^-133 in
 // bf16, 2^-24 in f16; with the lowest bit of the exponent among them too).  So a code, in the
@@ -409,8 +408,6 @@ __device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t offset, uin
 // over more accumulators: 220 us in groups of 64, 390 in groups of 32.  Two accumulators and
 // four steps of codes in tensor memory were faster than three and two; a third set of four
 // warps for the codes slower (174 us), and so were 64 columns of sums a thread.
-constexpr int kTileStages = 8, kCodeBytes = 128 * 64;
-constexpr int kAStages = 4, kACols = 256;   // A: four steps in the last 256 columns of tensor memory
 // Four neighbouring elements of B bytes of a row's array, fetched a batch ahead: a lane's row is
 // its own cache line, and a load of every element by itself takes the L1's time 32 times.
 // Rows start anywhere: the two aligned words that hold the four are loaded (one where they
@@ -449,22 +446,6 @@ __device__ __forceinline__ F32x2 fma_pair(F32x2 a, F32x2 b, F32x2 c) {
   F32x2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
-}
-
-template <int NT>
-struct TileCfg {
-  static constexpr int kStage = kCodeBytes + NT / 2 * 256;
-  static constexpr int kBufs = kACols / NT;   // accumulators
-  static constexpr int kRing = kTileStages * kStage;
-  // warps: TMA, MMA, two that only fill a group of four, 8 of codes, and 4 of sums for every kCols columns: 32, since 64
-  // a thread do not stay in its registers
-  static constexpr int kCols = NT == 128 ? 32 : NT / 2, kParts = NT / kCols;
-  static constexpr int kThreads = (12 + 4 * kParts) * 32;
-  static constexpr int kExchange = kParts * 16 * 64 * 4;
-};
-template <int NT>
-static size_t tile_smem(int E) {
-  return (size_t)TileCfg<NT>::kRing + TileCfg<NT>::kExchange + 1024 + (size_t)(E + 1) * 8;
 }
 
 template <typename TE, int NT, int G>
@@ -507,7 +488,6 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   pdl_wait();
-  pdl_launch_dependents();
   // the experts' tiles
   const int per = swiglu ? 128 : 256, outs = swiglu ? a.N / 2 : a.N, row_tiles = (outs + per - 1) / per;
   int tiles = 0;
@@ -532,6 +512,7 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
   __syncwarp();
   cluster_sync();   // the barriers of both are there
   tc_fence_after();
+  pdl_launch_dependents();   // both have their tensor memory: no launch behind this one can come between
   const uint32_t tmem = tmem_slot, tmem_a = tmem + kACols;
   const int all_steps = (a.K + 127) / 128, groups = a.K / G;
   const int sb = all_steps * split >> lg, se = all_steps * (split + 1) >> lg, steps = se - sb;   // this pair's
@@ -817,7 +798,7 @@ static cudaError_t allow_tiles() {
 // How many clusters of 2 << lg of the blocks, one to an SM, the device runs at once: a cluster's SMs are
 // neighbours, and fewer fit than the SMs' number says (of eight 15, not 19).
 static cudaError_t clusters_at_once(const void* kernel, int lg, int threads, size_t smem, int* n) {
-  static int known[64][3];   // + 1; every instance fills an SM, so it is the same for all
+  static int known[64][3];   // + 1; every instance has its SM to itself (kAloneBytes), so it is the same for all
   int dev;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "dtype.cuh"
+#include "four_of_row.h"
 #include "tcgen05_issue.cuh"
 #include "w4_tile.h"
 
@@ -22,6 +23,7 @@ struct W4Args {
   long long ld_x, ld_out;             // elements
   const uint8_t *codes, *zeros;       // [E][N][K / 2]; [E][N][K / g] or null (8)
   const void* scales;                 // [E][N][K / g] of x's type
+  const void *scales_end, *zeros_end;
   const int32_t* offsets;             // [E + 1] or null (all P rows are expert 0's)
   void* out;
   int32_t* err;
@@ -408,25 +410,10 @@ __device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t offset, uin
 // over more accumulators: 220 us in groups of 64, 390 in groups of 32.  Two accumulators and
 // four steps of codes in tensor memory were faster than three and two; a third set of four
 // warps for the codes slower (174 us), and so were 64 columns of sums a thread.
-// Four neighbouring elements of B bytes of a row's array, fetched a batch ahead: a lane's row is
-// its own cache line, and a load of every element by itself takes the L1's time 32 times.
-// Rows start anywhere: the two aligned words that hold the four are loaded (one where they
-// are aligned themselves) and shifted.
-template <int B>
-struct Four {
-  using W = typename std::conditional<B == 2, uint64_t, uint32_t>::type;
-  const char *row, *end;
-  W lo = 0, hi = 0;
-  __device__ __forceinline__ Four(const void* p, int n) : row((const char*)p), end((const char*)p + (long long)n * B) {}
-  __device__ __forceinline__ void fetch(int batch) {   // elements 4 batch to 4 batch + 3, those that there are
-    const char* at = row + (long long)batch * (4 * B);
-    const W* w = reinterpret_cast<const W*>((uintptr_t)at & ~(uintptr_t)(4 * B - 1));
-    if (at < end) lo = __ldg(w);
-    if ((const char*)w != at && (const char*)(w + 1) < end) hi = __ldg(w + 1);
-  }
-  __device__ __forceinline__ W value(int batch) const {
-    const int sh = (int)((uintptr_t)(row + (long long)batch * (4 * B)) & (4 * B - 1)) * 8;
-    return sh ? lo >> sh | hi << (32 * B - sh) : lo;
+struct LoadNc {
+  template <typename T>
+  __device__ __forceinline__ T operator()(const T* p) const {
+    return __ldg(p);
   }
 };
 struct F32x2 {
@@ -448,7 +435,11 @@ __device__ __forceinline__ F32x2 fma_pair(F32x2 a, F32x2 b, F32x2 c) {
   return r;
 }
 
-template <typename TE, int NT, int G>
+// CUTS: rows of scales and zero points may be cut by their array's ends (Four).  At a width of 128 the second loops cost
+// the first ones registers (4001 x 4096 x 4096 in groups of 128, 64 and 32: 149, 236 and 410 us with them, 146, 222 and
+// 388 without), so arrays that start and end on whole words have an instance of their own; at 32 and 64 there is no
+// difference.  Scales off an 8-byte boundary: 158, 273 and 497 us.
+template <typename TE, int NT, int G, bool CUTS>
 __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
     w4_tile_kernel(const __grid_constant__ CUtensorMap mC, const __grid_constant__ CUtensorMap mX,
                    const __grid_constant__ W4Args a, int swiglu, int lg) {
@@ -609,46 +600,53 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
       const Tile t = tile_at(tile);
       const int o = t.o0 + (swiglu ? row & 63 : row);
       const long long wr = (long long)e * a.N + (swiglu && row >= 64 ? a.N / 2 : 0) + min(o, outs - 1);
-      Four<1> zeros(a.zeros ? a.zeros + wr * groups : nullptr, a.zeros ? groups : 0);
+      const uint8_t* z_row = a.zeros ? a.zeros + wr * groups : nullptr;
+      const int zs = a.zeros ? groups : 0;
       const int k0 = sb + ((n0 ^ set) & 1);   // these warps' first step of the tile
-      zeros.fetch(k0 / kPer);
-      int batch = -1;
-      uint32_t z4 = 0x08080808u;
-      for (int k = k0; k < se; k += 2) {
-        if (k / kPer != batch) {
-          batch = k / kPer;
-          if (a.zeros) z4 = zeros.value(batch);
-          zeros.fetch(kPer == 1 ? batch + 2 : batch + 1);
-        }
-        const int n = n0 + k - sb, st = n % kTileStages, as = n % kAStages, p = n - kAStages;
-        ok = wait_unless(codes_there, &full_c[st], (n / kTileStages) & 1, &s_err);
-        // the step that last used this A stage: its own ring stage is given back once it has been multiplied
-        const bool free = p < 0 || test_wait(&empty[p % kTileStages], (p / kTileStages) & 1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4*>(codes + st * C::kStage + (((h * 2 + i) << 4) ^ swizzle));
-            const uint32_t offset = W4<TE>::offset(z4 >> ((k % kPer * kGroups + (h * 2 + i) * 32 / G) * 8) & 255);
-            unpack_in_order<TE>(w.x, offset, v + 16 * i);
-            unpack_in_order<TE>(w.y, offset, v + 16 * i + 4);
-            unpack_in_order<TE>(w.z, offset, v + 16 * i + 8);
-            unpack_in_order<TE>(w.w, offset, v + 16 * i + 12);
+      auto tile_codes = [&](auto zeros) {
+        zeros.fetch(k0 / kPer, LoadNc());
+        int batch = -1;
+        uint32_t z4 = 0x08080808u;
+        for (int k = k0; k < se; k += 2) {
+          if (k / kPer != batch) {
+            batch = k / kPer;
+            if (a.zeros) z4 = zeros.value(batch, LoadNc());
+            zeros.fetch(kPer == 1 ? batch + 2 : batch + 1, LoadNc());
           }
-          if (h == 0) {
-            ok = __all_sync(0xffffffffu, ok && wait_unless(free, &empty[p % kTileStages], (p / kTileStages) & 1, &s_err));
-            tc_fence_after();
+          const int n = n0 + k - sb, st = n % kTileStages, as = n % kAStages, p = n - kAStages;
+          ok = wait_unless(codes_there, &full_c[st], (n / kTileStages) & 1, &s_err);
+          // the step that last used this A stage: its own ring stage is given back once it has been multiplied
+          const bool free = p < 0 || test_wait(&empty[p % kTileStages], (p / kTileStages) & 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 w = *reinterpret_cast<const uint4*>(codes + st * C::kStage + (((h * 2 + i) << 4) ^ swizzle));
+              const uint32_t offset = W4<TE>::offset(z4 >> ((k % kPer * kGroups + (h * 2 + i) * 32 / G) * 8) & 255);
+              unpack_in_order<TE>(w.x, offset, v + 16 * i);
+              unpack_in_order<TE>(w.y, offset, v + 16 * i + 4);
+              unpack_in_order<TE>(w.z, offset, v + 16 * i + 8);
+              unpack_in_order<TE>(w.w, offset, v + 16 * i + 12);
+            }
+            if (h == 0) {
+              ok = __all_sync(0xffffffffu, ok && wait_unless(free, &empty[p % kTileStages], (p / kTileStages) & 1, &s_err));
+              tc_fence_after();
+            }
+            if (ok) tmem_st32(tmem_a + lanes + as * 64 + h * 32, v);
           }
-          if (ok) tmem_st32(tmem_a + lanes + as * 64 + h * 32, v);
+          if (!ok) return;
+          codes_there = test_wait(&full_c[(n + 2) % kTileStages], ((n + 2) / kTileStages) & 1);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_pair(full_at + as * 8);
         }
-        if (!ok) break;
-        codes_there = test_wait(&full_c[(n + 2) % kTileStages], ((n + 2) / kTileStages) & 1);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_pair(full_at + as * 8);
-      }
+      };
+      if (CUTS && __any_sync(0xffffffffu, Four<1>(z_row, zs).cut(a.zeros, a.zeros_end)))
+        tile_codes(Four<1, CUTS>(z_row, zs));
+      else
+        tile_codes(Four<1>(z_row, zs));
     }
     __syncwarp();
     if (lg && pair < tiles) cluster_sync();   // the sums are there
@@ -665,40 +663,46 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
       const Tile t = tile_at(tile);
       const int o = t.o0 + (swiglu ? row & 63 : row);
       const long long wr = (long long)e * a.N + (swiglu && row >= 64 ? a.N / 2 : 0) + min(o, outs - 1);
-      Four<2> scales(reinterpret_cast<const TE*>(a.scales) + wr * groups + g0, mine);
-      scales.fetch(0);
+      const TE* s_row = reinterpret_cast<const TE*>(a.scales) + wr * groups + g0;
       F32x2 total[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) total[i].v = 0;
-      for (int b = 0; b * 4 < mine && ok; ++b) {
-        const uint64_t s4 = scales.value(b);
-        scales.fetch(b + 1);
+      auto tile_sums = [&](auto scales) {
+        scales.fetch(0, LoadNc());
+        for (int b = 0; b * 4 < mine && ok; ++b) {
+          const uint64_t s4 = scales.value(b, LoadNc());
+          scales.fetch(b + 1, LoadNc());
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (b * 4 + j >= mine) break;
-          const float s = W4<TE>::scale((uint32_t)(s4 >> (16 * j)) & 0xffff);
-          ok = wait_unless(sums_there, &acc_full[acc.stage], acc.parity, &s_err);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          tc_fence_after();
-          const F32x2 by = pair_of(s, s);
-          const uint32_t at = tmem + lanes + acc.stage * NT + h * kCols, free_at = empty_at + acc.stage * 8;
-          acc.next();
+          for (int j = 0; j < 4; ++j) {
+            if (b * 4 + j >= mine) break;
+            const float s = W4<TE>::scale((uint32_t)(s4 >> (16 * j)) & 0xffff);
+            ok = wait_unless(sums_there, &acc_full[acc.stage], acc.parity, &s_err);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            const F32x2 by = pair_of(s, s);
+            const uint32_t at = tmem + lanes + acc.stage * NT + h * kCols, free_at = empty_at + acc.stage * 8;
+            acc.next();
 #pragma unroll
-          for (int c = 0; c < kCols; c += 16) {
-            uint32_t u[16];
-            tmem_ld16(at + c, u);
-            if (c + 16 >= kCols) {   // all of it is in registers
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) arrive_pair(free_at);
-              sums_there = test_wait(&acc_full[acc.stage], acc.parity);
+            for (int c = 0; c < kCols; c += 16) {
+              uint32_t u[16];
+              tmem_ld16(at + c, u);
+              if (c + 16 >= kCols) {   // all of it is in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_pair(free_at);
+                sums_there = test_wait(&acc_full[acc.stage], acc.parity);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; i += 2)
+                total[(c + i) / 2] = fma_pair(by, pair_of(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), total[(c + i) / 2]);
             }
-#pragma unroll
-            for (int i = 0; i < 16; i += 2)
-              total[(c + i) / 2] = fma_pair(by, pair_of(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), total[(c + i) / 2]);
           }
         }
-      }
+      };
+      if (CUTS && __any_sync(0xffffffffu, Four<2>(s_row, mine).cut(a.scales, a.scales_end)))
+        tile_sums(Four<2, CUTS>(s_row, mine));
+      else
+        tile_sums(Four<2>(s_row, mine));
       auto sum = [&](int i) {
         const float2 f = halves_of(total[i / 2]);
         return ok ? (i & 1 ? f.y : f.x) * W4<TE>::kUp : NAN;
@@ -790,10 +794,10 @@ static long long most_tiles(const W4Args& a, int swiglu, int NT) {
   const long long of_x = a.offsets ? (long long)a.P / NT + (a.E < a.P / (a.few + 1) ? a.E : a.P / (a.few + 1)) : ((long long)a.P + NT - 1) / NT;
   return of_x * ((outs + per - 1) / per);
 }
-template <typename TE, int NT, int G>
+template <typename TE, int NT, int G, bool CUTS>
 static cudaError_t allow_tiles() {
   static char allowed[64];
-  return allow_smem(w4_tile_kernel<TE, NT, G>, tile_smem<NT>(kMaxExperts), allowed);
+  return allow_smem(w4_tile_kernel<TE, NT, G, CUTS>, tile_smem<NT>(kMaxExperts), allowed);
 }
 // How many clusters of 2 << lg of the blocks, one to an SM, the device runs at once: a cluster's SMs are
 // neighbours, and fewer fit than the SMs' number says (of eight 15, not 19).
@@ -831,14 +835,14 @@ static cudaError_t splits_of(const W4Args& a, long long most, const void* kernel
   }
   return cudaSuccess;
 }
-template <typename TE, int NT, int G>
+template <typename TE, int NT, int G, bool CUTS>
 static moe_status launch_tiles(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {
   CUtensorMap mC, mX;
   moe_status st = map_codes(&mC, a);
   if (st == MOE_OK) st = map_rows(&mX, a.x, dtype, a.K, a.P, a.ld_x, NT / 2);
   if (st != MOE_OK) return st;
-  auto kernel = w4_tile_kernel<TE, NT, G>;
-  const cudaError_t allowed = allow_tiles<TE, NT, G>();
+  auto kernel = w4_tile_kernel<TE, NT, G, CUTS>;
+  const cudaError_t allowed = allow_tiles<TE, NT, G, CUTS>();
   MOE_CUDA(allowed);
   const long long most = most_tiles(a, swiglu, NT);
   MOE_ARG(most <= 0x3fffffff, "too many tiles");
@@ -864,9 +868,9 @@ static moe_status launch_tiles_of(const W4Args& a, int dtype, int swiglu, cudaSt
       constexpr int NT = decltype(width)::value;
       const long long most = most_tiles(a, swiglu, NT);
       int lg;
-      cudaError_t e = allow_tiles<TE, NT, G>();
+      cudaError_t e = allow_tiles<TE, NT, G, true>();
       if (e == cudaSuccess)
-        e = splits_of(a, most, (const void*)w4_tile_kernel<TE, NT, G>, TileCfg<NT>::kThreads, tile_smem<NT>(kMaxExperts), &lg);
+        e = splits_of(a, most, (const void*)w4_tile_kernel<TE, NT, G, true>, TileCfg<NT>::kThreads, tile_smem<NT>(kMaxExperts), &lg);
       if (e != cudaSuccess) return e;
       const long long rounds = lg ? 1 : (most + pairs - 1) / pairs, cost = rounds * ((steps + (1 << lg) - 1) >> lg) * part + (lg ? 70 : 0);
       if (least == 0 || cost < least) least = cost, nt = NT;
@@ -876,9 +880,11 @@ static moe_status launch_tiles_of(const W4Args& a, int dtype, int swiglu, cudaSt
     MOE_CUDA(consider(std::integral_constant<int, 64>(), 7));
     MOE_CUDA(consider(std::integral_constant<int, 128>(), 10));
   }
-  if (nt == 128) return launch_tiles<TE, 128, G>(a, dtype, swiglu, s);
-  if (nt == 64) return launch_tiles<TE, 64, G>(a, dtype, swiglu, s);
-  return launch_tiles<TE, 32, G>(a, dtype, swiglu, s);
+  if (nt == 64) return launch_tiles<TE, 64, G, true>(a, dtype, swiglu, s);
+  if (nt == 32) return launch_tiles<TE, 32, G, true>(a, dtype, swiglu, s);
+  const long long n_groups = (long long)a.E * a.N * (a.K / G);
+  const bool cuts = ends_cut(a.scales, n_groups, 2) || (a.zeros && ends_cut(a.zeros, n_groups, 1));
+  return cuts ? launch_tiles<TE, 128, G, true>(a, dtype, swiglu, s) : launch_tiles<TE, 128, G, false>(a, dtype, swiglu, s);
 }
 
 template <typename TE, int WPL, int KS>
@@ -957,7 +963,9 @@ extern "C" moe_status moe_w4_linear(int P, int N, int K, int E, int group, int d
   MOE_ARG(ld_x >= K && ld_out >= (swiglu ? N / 2 : N), "a row distance is below the row's length");
   MOE_ARG((uintptr_t)x % 16 == 0 && ld_x % 8 == 0, "x needs rows on 16-byte boundaries");
   MOE_ARG((uintptr_t)codes % 16 == 0 && (uintptr_t)scales % 2 == 0, "codes must be 16-byte aligned");
-  W4Args a = {P, N, K, E, group, out_dtype, x, ld_x, ld_out, codes, zeros, scales, offsets, out, d_error, 0};
+  const long long n_groups = (long long)E * N * (K / group);
+  W4Args a = {P, N, K, E, group, out_dtype, x, ld_x, ld_out, codes, zeros, scales, (const char*)scales + n_groups * 2,
+              zeros ? zeros + n_groups : nullptr, offsets, out, d_error, 0};
   return dtype == MOE_DT_BF16 ? launch_w4<__nv_bfloat16>(a, dtype, swiglu ? 1 : 0, stream)
                               : launch_w4<__half>(a, dtype, swiglu ? 1 : 0, stream);
 }

@@ -18,3 +18,7 @@ def test_a_tile_s_block_has_its_sm_to_itself(tmp_path):
     """The kernel takes all of an SM's tensor memory, for a pair of blocks at once: two blocks on an SM would wait for one
     another's."""
     run_host_program("w4_tile_alone", tmp_path)
+
+
+def test_scales_and_zero_points_are_read_inside_their_arrays(tmp_path):
+    run_host_program("four_of_row", tmp_path)

@@ -506,13 +506,14 @@ PyObject* sort_rows(PyObject*, PyObject* args, PyObject* kw) {
     to_int(P, "T * k");
     const auto i32 = tx.options().dtype(at::kInt);
     at::Tensor mr, mo, mp;
-    const at::Tensor* to = either(off, "offsets", mo, {(E > 0 ? E : 0) + 1}, i32, st);
+    const int64_t made = E >= 1 && E <= 2048 ? E : 0;   // any other E is refused by the library
+    const at::Tensor* to = either(off, "offsets", mo, {made + 1}, i32, st);
     const at::Tensor* tp = either(ps, "pos", mp, {T, k}, i32, st);
     const at::Tensor* tr = either(rw, "rows", mr, {P, H}, tx.options(), st);
     same_type(tr, tx.scalar_type(), "rows (as x)");
     const Rows rx = rows(all, &tx, T, H, "x"), rr = rows(all, tr, P, H, "rows");
     auto* pi = (const int32_t*)dense(all, &ti, {T, k}, at::kInt, "topk_ids");
-    auto* po = (int32_t*)dense(all, to, {(E > 0 ? E : 0) + 1}, at::kInt, "offsets");
+    auto* po = (int32_t*)dense(all, to, {(mo.defined() ? made : E > 0 ? (int64_t)E : 0) + 1}, at::kInt, "offsets");
     auto* pp = (int32_t*)dense(all, tp, {T, k}, at::kInt, "pos");
     auto* pe = (int32_t*)dense(all, tensor(err, "d_error"), {1}, at::kInt, "d_error");
     const Place at(all, st);

@@ -728,8 +728,9 @@ moe_status moe_adapter_linear(int T, int H, int N, int dtype, int out_dtype, con
  *
  * A pos outside [0, n_rows) (n_rows: the rows of `rows`) counts as -1: nothing is read
  * for it, so what rows past offsets[E] hold does not matter.  The pos of one call are
- * distinct but for -1.  But for the two named, results must not overlap what a call reads.  Sums are taken in fp32 in the order of j (d_w's over H in a fixed
- * order), base last, and rounded once: equal calls give equal bits.
+ * distinct but for -1.  But for the two named, results must not overlap what a call reads.
+ * Sums are taken in fp32 in the order of j (d_w's over H in a fixed order), base last, and
+ * rounded once: equal calls give equal bits.
  * x and rows of sort have one type; in combine y, base and d_y have y_dtype, rows and
  * d_rows rows_dtype, which is y_dtype or MOE_DT_F32.  T >= 0, 1 <= k <= 64,
  * 1 <= E <= 2048, H >= 1, T k < 2^31 - 32.  T == 0 writes only the offsets (0).
@@ -756,7 +757,7 @@ moe_status moe_combine_rows_backward(int T, int k, int n_rows, int H, int rows_d
  *   codes    device uint8 [E, N, K / 2] dense: element 2j of a row in the low nibble of
  *            byte j, 2j + 1 in the high one
  *   scales   device [E, N, K / group] dense, of `dtype`
- *   zeros    device uint8 [E, N, K / group] dense, values 0 to 127, or NULL (all 8)
+ *   zeros    device uint8 [E, N, K / group] dense, values 0 to 255, or NULL (all 8)
  *   offsets  device int32 [E + 1], ascending, as moe_sort_rows writes them, or NULL
  *            (E == 1: all rows); rows of out from offsets[E] on are left as they were,
  *            and so are rows before offsets[0]
@@ -770,7 +771,9 @@ moe_status moe_combine_rows_backward(int T, int k, int n_rows, int H, int rows_d
  * what the call reads.  Equal calls give equal bits; the order of a sum's parts goes by the
  * sizes (P, N, K, E), so a row's last bits may differ between batches of different sizes.
  * group 32, 64 or 128, K a multiple of it, x and codes 16-byte aligned, ld_x a multiple
- * of 8; P >= 0, N >= 1 (even with swiglu), 1 <= E <= 2048, E N < 2^31.
+ * of 8; scales 2-byte aligned, zeros anywhere (hundreds of rows take 3 to 28 % longer where
+ * scales do not start on 8 bytes, zeros not on 4, or E N K / group is no multiple of 4);
+ * P >= 0, N >= 1 (even with swiglu), 1 <= E <= 2048, E N < 2^31.
  * A wait that gave up sets *d_error (device int32, may be NULL) to MOE_ERR_TIMEOUT.
  * ------------------------------------------------------------------------- */
 moe_status moe_w4_linear(int P, int N, int K, int E, int group, int dtype, int out_dtype, const void* x, int64_t ld_x,

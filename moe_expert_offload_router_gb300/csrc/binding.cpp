@@ -703,7 +703,8 @@ PyMethodDef methods[] = {
      "stream=None)\n\n"
      "out [P, N] = x ((codes - zeros) scales)^T, by the expert of each row where offsets [E + 1] are given.\n\n"
      "x [P, K] bf16 or f16 (rows may be strided), codes uint8 [N, K / 2] or [E, N, K / 2] (even elements in the low\n"
-     "nibble), scales [..., N, K / group] of x's type, zeros uint8 of their shape (None: 8); group 32, 64 or 128.\n"
+     "nibble), scales [..., N, K / group] of x's type, zeros uint8 of their shape (0 to 255, None: 8); group 32, 64 or\n"
+     "128.\n"
      "swiglu: out [P, N / 2] = silu(first N / 2) * the others.  out of x's type or fp32."},
     {"set_check", set_check, METH_VARARGS, "The function that raises for a status other than MOE_OK, and what it raises."},
     {nullptr, nullptr, 0, nullptr}};

@@ -148,16 +148,16 @@ __device__ __forceinline__ int word_place(int in) {
 
 // Few rows of x to a matrix.  A warp multiplies 16 rows of weights by up to 8 rows of x
 // (m16n8k16), 128 products a step: lane (g, c) loads 16 bytes of codes of rows g and g + 8
-// straight from memory, four steps ahead; which k a lane's codes are does not matter as
-// long as x's fragment holds the same ones.  x lies in shared memory in the fragments'
+// straight from memory, D steps ahead (four in groups of 128, two in smaller ones); which k a lane's codes
+// are does not matter as long as x's fragment holds the same ones.  x lies in shared memory in the fragments'
 // order.  Where the rows of weights alone would not fill the GPU, KS of the block's warps
 // or a cluster of `splits` blocks share the steps, and the sums are added in order.
 //
 // Bound by HBM where there are codes enough: 512 rows of 256 experts, 4096 x 4096 (gates and
-// ups) 365 us, 5.35 TB/s; one row of 4096 x 4096 4.7 us with the codes in the L2 and 7 to 9
+// ups) 369 us with the launch of tiles behind it, 5.3 TB/s; one row of 4096 x 4096 4.7 us with the codes in the L2 and 7 to 9
 // from HBM, latency: x, the codes and a sum over the warps after each other.  Groups of 32
 // take twice the instructions of groups of 128 (scales, zero points and sums for each): the
-// same experts 615 us, 2.9 TB/s.  Scales come four steps ahead as the codes do; 80
+// same experts 618 us, 3.6 TB/s.  Scales come D steps ahead as the codes do; 80
 // registers keep three blocks on an SM, more of them under way cost the third (556 us).
 constexpr int kChunk = 32, kChunkBytes = kChunk * 2048;   // steps of x at a time
 constexpr int kMaxSplits = 8;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(256, KS == 8 ? 2 : 3) w4_rows_kernel(const W4A
           q1[j] = load_codes(in, w1 + (long long)i * 64);
         }
       };
-      // scales and zero points of four steps' groups, every fourth one to a lane c, loaded four steps ahead
+      // scales and zero points of D steps' groups, every fourth one to a lane c, loaded D steps ahead
       uint32_t p0[NB], p1[NB], n0[NB], n1[NB];
       auto scales = [&](int i) {
 #pragma unroll
@@ -401,13 +401,13 @@ __device__ __forceinline__ void unpack_in_order(uint32_t w, uint32_t offset, uin
 // into q - z straight into tensor memory, from where the MMAs read them as their A operand
 // (through shared memory they would take twice the bandwidth that there is); one thread
 // multiplies for both blocks into an accumulator for each group of the scales; and eight
-// warps multiply each accumulator by its scales - a scale belongs to a tensor memory lane -
-// and add it up in registers while the next ones fill.
+// warps (sixteen at a width of 128) multiply each accumulator by its scales - a scale belongs to a tensor memory
+// lane - and add it up in registers while the next ones fill.
 //
 // What bounds it is the way of a step through its four hands: codes, MMA, sums and back, each
 // waiting on the other's barrier.  4001 x 4096 x 4096 in groups of 128 takes 146 us (0.92
 // PFLOP/s), 0.65 us a step whose MMAs take some 0.27; without the sums 123.  Smaller groups hand
-// over more accumulators: 220 us in groups of 64, 390 in groups of 32.  Two accumulators and
+// over more accumulators: 222 us in groups of 64, 388 in groups of 32.  Two accumulators and
 // four steps of codes in tensor memory were faster than three and two; a third set of four
 // warps for the codes slower (174 us), and so were 64 columns of sums a thread.
 struct LoadNc {
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(TileCfg<NT>::kThreads, 1)
   __shared__ int s_err;
   __shared__ int ws[34];
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)tile_raw + 1023) & ~(uintptr_t)1023);
-  float* exchange = reinterpret_cast<float*>(sm + C::kRing);               // [half][16][64]
+  float* exchange = reinterpret_cast<float*>(sm + C::kRing);               // [kParts][16][64]
   int* first = reinterpret_cast<int*>(sm + C::kRing + C::kExchange);          // [E + 1]: an expert's first row
   int* cum = first + a.E + 1;                                              // [E + 1]: its first tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x & 1;
@@ -860,8 +860,10 @@ static moe_status launch_tiles_of(const W4Args& a, int dtype, int swiglu, cudaSt
     nt = mean > 64 ? 128 : mean > 32 || a.few ? 64 : 32;
   } else {
     // Rounds of tiles times steps times what a step of the width takes (5, 7 and 10 parts: measured 0.64, 0.9 and 1.26 us
-    // in groups of 64), and 70 parts for the exchange of a split.  4096 x 4096: 64 rows 13.6 us at a width of 32, 16.2 at
-    // 64, 20.3 at 128; 256 rows 30, 18.8 and 21.2.
+    // in groups of 64), and 70 parts for the exchange of a split.  4096 x 4096 at widths of 32, 64 and 128, groups of 128:
+    // 64 rows 13.6, 16.5 and 20.5 us, 128 rows 17.2, 17.1 and 20.8, 256 rows 29.7, 19.0 and 21.4, 512 rows 55, 33 and
+    // 25.  The parts' ratios are near enough in groups of 128; in groups of 32 a narrow width can cost up to a seventh
+    // more than the best one (100 rows 29.3 us at 32, which is taken, 25.7 at 64).
     const int steps = (a.K + 127) / 128, pairs = device_sms() / 2;
     long long least = 0;
     auto consider = [&](auto width, int part) {
@@ -919,7 +921,8 @@ static moe_status launch_split_rows(const W4Args& a, int swiglu, cudaStream_t s)
 // Few rows to an expert on average can still be many to some, and w4_rows_kernel reads the codes again for every eight: such
 // experts go to a launch of tiles behind it.  1802 rows of 2048 to 4096, 1500 of them one expert's of 256: 78 us, 1263
 // without; where no expert has so many the launch costs 2 to 5 us (512 rows of 256 experts 185 us, 180 without), which a
-// call of up to kFewInAll rows is spared.
+// call of up to kFewInAll rows is spared: 64 rows that are all one expert's read its codes eight times, 119 us for 4096 x
+// 4096 (13.6 as a dense product).
 constexpr int kFewRows = 24, kFewInAll = 64;
 template <typename TE>
 static moe_status launch_w4(const W4Args& a, int dtype, int swiglu, cudaStream_t s) {

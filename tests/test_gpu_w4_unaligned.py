@@ -40,6 +40,23 @@ def test_dense(P, N, K, group, at):
     check(got, x, codes, scales, None, None, False)
 
 
+@pytest.mark.parametrize("N,K,group,dtype", [(2050, 1056, 32, BF16), (2050, 1088, 64, F16), (2050, 1152, 128, BF16)])
+def test_wide_tiles(N, K, group, dtype):
+    """600 rows: tiles of 128, whose rows an array's end cuts only in the first and the last of them."""
+    M = load_lib()
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = normal(g, 600, K, dtype)
+    codes, scales, z = (t[0] for t in weights(g, 1, N, K, group, dtype))
+    first = {}
+    for at in (0, 1, 3):
+        s, zz = inside(scales, at, float("nan")), inside(z, 3 * at, 255)
+        for swiglu in (False, True):
+            got = M.moe_w4_linear(x, codes, s, zz, swiglu=swiglu, out_dtype=F32)
+            check(got, x, codes, scales, z, None, swiglu, rows=[0, 127, 128, 300, 599])
+            assert torch.isfinite(got).all()
+            assert torch.equal(first.setdefault(swiglu, got), got)   # the same sums in the same order
+
+
 @pytest.mark.parametrize("counts", [[3, 0, 1], [70, 5, 150], [40, 41, 0, 30], [200] + [0] * 40 + [3] * 15])
 @pytest.mark.parametrize("N,K,group", [(130, 128, 128), (66, 96, 32), (300, 320, 64)])
 def test_experts(counts, N, K, group):
